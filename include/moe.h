@@ -204,6 +204,101 @@ moe_status_t moe_combine(const void *y_sorted, moe_dtype_t dtype, int64_t n_toke
                          int32_t hidden, int32_t topk, const moe_routing_t *routing, void *out,
                          void *stream);
 
+/* ---- Rows into sorted order and back, with gradients ----------------------------
+ * For expert products that run outside this library (a training step, experts
+ * with adapters): the dispatch into expert-sorted rows and the weighted sum
+ * back, which moe_experts fuses into its GEMMs, as calls of their own, and the
+ * gradients down to the router logits.  The order is moe_route's (or
+ * moe_route_ep's): row p of a sorted array belongs to the entry f with
+ * row_sorted[f] = p, slot f % topk of token f / topk.  Slots whose row_sorted
+ * is outside [0, n_tokens * topk) (-1: outside an expert share) move nothing,
+ * add nothing and get a zero weight gradient, and sorted rows that no slot
+ * points to are left as they were.  dtype and routing->w_dtype are independent.
+ * Deterministic, no atomics, no workspace; limits as moe_combine.  Outputs must
+ * not overlap inputs.
+ *
+ * moe_dispatch: x_sorted [N*topk, hidden]; x_sorted[row_sorted[t*topk + j]] =
+ *   x[t].  Reads routing->row_sorted only.  Its gradient with respect to x is
+ *   moe_combine of the gradient of x_sorted.
+ * moe_combine_weighted: out[t] = sum over j of topk_w[t][j] *
+ *   y_sorted[row_sorted[t*topk + j]], in slot order with fp32 accumulation and
+ *   one rounding.  Reads routing->row_sorted and topk_w.
+ * moe_combine_weighted_backward: from d_out [N, hidden], the gradient of the
+ *   step above: d_y_sorted[row_sorted[t*topk + j]] = topk_w[t][j] * d_out[t],
+ *   rounded once to `dtype`, and d_topk_w [N, topk] fp32, the dot products
+ *   <d_out[t], y_sorted[row_sorted[t*topk + j]]> summed in fp32.
+ * moe_route_backward: the gradient of topk_w with respect to the logits:
+ *   d_logits [N, n_experts] in routing->w_dtype, d_logits[t][topk_idx[t][j]] =
+ *   topk_w[t][j] * (d_topk_w[t][j] - sum_i topk_w[t][i] * d_topk_w[t][i]) and 0
+ *   for every expert that was not selected (the selection itself has no
+ *   gradient).  n_experts is the layer's expert count, an expert share's
+ *   included.  Reads routing->topk_idx and topk_w.  It is linear in d_topk_w:
+ *   the shares of an expert-parallel group may each call it on their own
+ *   d_topk_w and add the results. */
+moe_status_t moe_dispatch(const void *x, moe_dtype_t dtype, int64_t n_tokens, int32_t hidden,
+                          int32_t topk, const moe_routing_t *routing, void *x_sorted,
+                          void *stream);
+moe_status_t moe_combine_weighted(const void *y_sorted, moe_dtype_t dtype, int64_t n_tokens,
+                                  int32_t hidden, int32_t topk, const moe_routing_t *routing,
+                                  void *out, void *stream);
+moe_status_t moe_combine_weighted_backward(const void *d_out, const void *y_sorted,
+                                           moe_dtype_t dtype, int64_t n_tokens, int32_t hidden,
+                                           int32_t topk, const moe_routing_t *routing,
+                                           void *d_y_sorted, float *d_topk_w, void *stream);
+moe_status_t moe_route_backward(const float *d_topk_w, int64_t n_tokens, int32_t n_experts,
+                                int32_t topk, const moe_routing_t *routing, void *d_logits,
+                                void *stream);
+
+/* ---- Norms around a block ------------------------------------------------------
+ * The RMS norms that a transformer puts around this layer, with the gate and
+ * the residual sum, in one pass over the token rows:
+ *
+ *   z     = y * rstd(y) * w_post,   rstd(u) = 1 / sqrt(mean(u^2) + eps)
+ *   x_out = x + residual_scale * gate * z
+ *   n_out = x_out * rstd(x_out) * w_pre
+ *
+ * x is the residual stream ahead of a block, y the block's output, w_post the
+ * weight of the norm after the block and w_pre that of the norm ahead of the
+ * next one.  Parts that are absent drop out: without w_post z is y, without y
+ * x_out is x (and is not written), without w_pre there is no n_out; the gate is
+ * absent, one value a token or one a channel.  Everything is fp32 between the
+ * loads and the one rounding of each output; n_out is the norm of x_out ahead
+ * of its rounding. */
+typedef enum { MOE_GATE_NONE = 0, MOE_GATE_TOKEN = 1, MOE_GATE_CHANNEL = 2 } moe_gate_kind_t;
+typedef struct {
+  const void *w_post;    /* [hidden] or NULL                                   */
+  const void *w_pre;     /* [hidden] or NULL                                   */
+  const void *gate;      /* [N] or [hidden] by gate_kind                       */
+  int32_t gate_kind;     /* moe_gate_kind_t                                    */
+  float residual_scale;  /* finite                                             */
+  float eps;             /* > 0, finite                                        */
+} moe_block_norm_t;
+
+/* moe_block_norm: x [N, hidden], y [N, hidden] or NULL, weights and gate in
+ *   `dtype`; x_out [N, hidden] (with y; may be x itself), n_out [N, hidden]
+ *   (with w_pre), rstd_post [N] and rstd_pre [N] fp32, which the gradient reads
+ *   (each NULL if it is not wanted; without w_post or w_pre not written).
+ *   Needs y or w_pre; w_post and a gate need y.  hidden a multiple of 8 up to
+ *   16384, N below 2^31.
+ * moe_block_norm_backward: from d_x_out [N, hidden] (NULL: zero, allowed with
+ *   w_pre) and d_n_out [N, hidden] (with w_pre), the forward call's x, y, norm
+ *   and rstds (not its x_out, which may have replaced x only if x was kept),
+ *   d_x [N, hidden] (may be d_x_out itself), d_y [N, hidden] (with y), and fp32
+ *   d_w_post [hidden], d_w_pre [hidden], d_gate [N] or [hidden] as far as the
+ *   call has them.  The sums over tokens are added in a fixed order
+ *   (deterministic); with N = 0 they are written as zeros.  workspace: at
+ *   least moe_block_norm_workspace_bytes(n_tokens, hidden, dtype). */
+size_t moe_block_norm_workspace_bytes(int64_t n_tokens, int32_t hidden, moe_dtype_t dtype);
+moe_status_t moe_block_norm(const void *x, const void *y, moe_dtype_t dtype, int64_t n_tokens,
+                            int32_t hidden, const moe_block_norm_t *norm, void *x_out,
+                            void *n_out, float *rstd_post, float *rstd_pre, void *stream);
+moe_status_t moe_block_norm_backward(const void *d_x_out, const void *d_n_out, const void *x,
+                                     const void *y, moe_dtype_t dtype, int64_t n_tokens,
+                                     int32_t hidden, const moe_block_norm_t *norm,
+                                     const float *rstd_post, const float *rstd_pre, void *d_x,
+                                     void *d_y, float *d_w_post, float *d_w_pre, float *d_gate,
+                                     void *workspace, size_t ws_bytes, void *stream);
+
 /* moe_route on `logits` (dtype `dtype`) into *routing_out, then moe_experts. */
 moe_status_t moe_forward(const void *x, const void *logits, moe_dtype_t dtype,
                          int64_t n_tokens, int32_t hidden, const void *w13, const void *w2,

@@ -19,6 +19,9 @@ Python binding, and imports neither.
 * both also give one GPU's expert-parallel share (``route_ep``,
   ``moe_ffn_share``): the selected experts remapped to local ids, -1 outside.
 
+* :mod:`oracle.block` -- rows into expert-sorted order and back with the routing
+  weights, the norms around a block, and the gradients of both.
+
 Every function is pinned by ``tests/test_oracle_*.py`` against brute force,
 library routines, closed forms, invariants and the hand-derived fixtures in
 ``tests/golden/``; the one part with no such pin (the SwiGLU-OAI formula relative
@@ -28,6 +31,8 @@ from .routing import (RoutingRef, bitmatrix, gate_logits, histogram, offsets_fro
                       remap_to_share, route, route_ep, route_gate, round_to_dtype, sorted_indices,
                       topk_select, topk_softmax)
 from .quant import dequantize_mxfp4, e2m1_decode, e2m1_encode, quantize_mxfp4
+from .block import (block_norm, block_norm_grad, combine_weighted, combine_weighted_grad,
+                    dispatch, rms_norm, topk_weight_grad)
 from .ffn import (activation, moe_ffn, moe_ffn_share, moe_ffn_sorted,
                   moe_ffn_weighted_input, split_gate_up)
 
@@ -37,5 +42,6 @@ __all__ = [
     "gate_logits", "route_gate",
     "activation", "split_gate_up", "moe_ffn", "moe_ffn_sorted", "moe_ffn_share",
     "moe_ffn_weighted_input", "quantize_mxfp4", "dequantize_mxfp4", "e2m1_encode",
-    "e2m1_decode",
+    "e2m1_decode", "dispatch", "combine_weighted", "combine_weighted_grad", "topk_weight_grad",
+    "rms_norm", "block_norm", "block_norm_grad",
 ]

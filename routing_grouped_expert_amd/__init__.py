@@ -24,6 +24,23 @@ outputs over the group's shares gives the layer output:
     routing = moe_route_ep(logits, topk, lo, n)
     out = moe_experts_ep(x, w13, w2, routing, act="silu")
     out, routing = moe_forward_ep(x, logits, w13, w2, topk, lo, act="silu")
+
+Expert products that run elsewhere (a training step) take their rows from
+``moe_dispatch`` and give them back to ``moe_combine_weighted``; the gradients
+are calls of their own (this package registers nothing with autograd):
+
+    x_sorted = moe_dispatch(x, routing)                  # rows by expert
+    out = moe_combine_weighted(y_sorted, routing)        # topk_w applied
+    d_y_sorted, d_topk_w = moe_combine_weighted_backward(d_out, y_sorted, routing)
+    d_logits = moe_route_backward(d_topk_w, routing)
+    d_x = moe_combine(d_x_sorted, routing)               # gradient of the dispatch
+
+The norms around the layer, with the gate and the residual sum, are one call:
+
+    s = moe_block_norm(x, y, w_post=w_post, gate=gate, w_pre=w_next, residual_scale=0.22)
+    g = moe_block_norm_backward(d_x_out, d_n_out, x, y, w_post=w_post, gate=gate, w_pre=w_next,
+                                residual_scale=0.22, rstd_post=s.rstd_post,
+                                rstd_pre=s.rstd_pre)
 """
 from __future__ import annotations
 
@@ -45,6 +62,11 @@ __all__ = ["Routing", "MoeError", "Prepared", "moe_route", "moe_experts", "moe_e
            "prepare_gate_route", "prepare_gate_forward", "moe_experts_weighted_input",
            "prepare_experts_weighted_input", "moe_quantize_mxfp4", "moe_experts_mxfp4",
            "moe_forward_mxfp4", "prepare_experts_mxfp4", "prepare_forward_mxfp4",
+           "moe_dispatch", "moe_combine_weighted", "moe_combine_weighted_backward",
+           "moe_route_backward", "prepare_dispatch", "prepare_combine_weighted",
+           "prepare_combine_weighted_backward", "prepare_route_backward", "BlockNorm",
+           "BlockNormGrads", "moe_block_norm", "moe_block_norm_backward", "prepare_block_norm",
+           "prepare_block_norm_backward", "moe_block_norm_workspace_bytes",
            "moe_workspace_bytes", "moe_status_str", "ACTS", "LAYOUTS"]
 
 _DT = {torch.float32: N.MOE_F32, torch.bfloat16: N.MOE_BF16}
@@ -751,3 +773,316 @@ def moe_forward_mxfp4(x: torch.Tensor, logits: torch.Tensor, w13_q: torch.Tensor
     """Routing then the MXFP4-weight experts on one stream; returns ``(out, routing)``."""
     return prepare_forward_mxfp4(x, logits, w13_q, w13_s, w2_q, w2_s, topk, act, layout, params,
                                  out=out, routing=routing, workspace=workspace, stream=stream)()
+
+
+# ------------------------------------------------- rows into sorted order and back
+
+class _DevicePrepared(Prepared):
+    """A Prepared whose launches go to the device of its tensors, whichever
+    device is current when it is called."""
+
+    def __init__(self, dev, name: str, args: tuple, keep: tuple, result):
+        super().__init__(name, args, keep, result)
+        self._dev = dev
+
+    def __call__(self):
+        if torch.cuda.current_device() == self._dev.index:
+            return super().__call__()
+        with torch.cuda.device(self._dev):
+            return super().__call__()
+
+
+def _empty(shape, dtype, dev, stream) -> torch.Tensor:
+    """Uninitialised memory that belongs to the stream the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _given(t, shape, dtype, dev, stream, name: str) -> torch.Tensor:
+    """The caller's output tensor, checked, or a new one."""
+    if t is None:
+        return _empty(shape, dtype, dev, stream)
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous() \
+            or t.device != dev:
+        raise ValueError(f"{name} must be contiguous {tuple(shape)} {dtype} on {dev}")
+    return t
+
+
+def _row_routing(routing: Routing, dev, fields_):
+    """The routing fields a row call reads; returns (N, k)."""
+    n, k = routing.topk_idx.shape
+    for f in fields_:
+        t = getattr(routing, f)
+        if t.numel() != n * k or not t.is_contiguous() or t.device != dev:
+            raise ValueError(f"routing.{f} must be contiguous with N*k = {n * k} entries on {dev}")
+        if f != "topk_w" and t.dtype != torch.int32:
+            raise TypeError(f"routing.{f} must be int32")
+    return n, k
+
+
+def prepare_dispatch(x, routing: Routing, *, x_sorted=None, stream=None) -> Prepared:
+    dev = _dev(x)
+    n, k = _row_routing(routing, dev, ("row_sorted",))
+    if x.dim() != 2 or x.shape[0] != n:
+        raise ValueError("x must be [N, hidden] with the routing's N")
+    hidden = x.shape[1]
+    x_sorted = _given(x_sorted, (n * k, hidden), x.dtype, dev, stream, "x_sorted")
+    r = routing.as_c()
+    args = (x.data_ptr(), _dt(x), n, hidden, k, ctypes.byref(r), x_sorted.data_ptr(),
+            _stream(dev, stream))
+    return _DevicePrepared(dev, "moe_dispatch", args, (r, x, x_sorted, routing), x_sorted)
+
+
+def moe_dispatch(x: torch.Tensor, routing: Routing, *, x_sorted: Optional[torch.Tensor] = None,
+                 stream=None) -> torch.Tensor:
+    """Token rows into expert-sorted order: ``x_sorted[row_sorted[t*k + j]] = x[t]``
+    (``[N*k, hidden]``; rows that no slot points to are left as they were).  The
+    gradient with respect to ``x`` is ``moe_combine(d_x_sorted, routing)``."""
+    return prepare_dispatch(x, routing, x_sorted=x_sorted, stream=stream)()
+
+
+def prepare_combine_weighted(y_sorted, routing: Routing, *, out=None, stream=None) -> Prepared:
+    dev = _dev(y_sorted)
+    n, k = _row_routing(routing, dev, ("row_sorted", "topk_w"))
+    if y_sorted.dim() != 2 or y_sorted.shape[0] != n * k:
+        raise ValueError("y_sorted must be [N*k, hidden]")
+    hidden = y_sorted.shape[1]
+    out = _given(out, (n, hidden), y_sorted.dtype, dev, stream, "out")
+    r = routing.as_c()
+    args = (y_sorted.data_ptr(), _dt(y_sorted), n, hidden, k, ctypes.byref(r), out.data_ptr(),
+            _stream(dev, stream))
+    return _DevicePrepared(dev, "moe_combine_weighted", args, (r, y_sorted, out, routing), out)
+
+
+def moe_combine_weighted(y_sorted: torch.Tensor, routing: Routing, *,
+                         out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Expert rows back into token order with the routing weights applied:
+    ``out[t] = sum_j topk_w[t, j] * y_sorted[row_sorted[t*k + j]]`` (slot order,
+    fp32 sum, one rounding; slots with row_sorted = -1 skipped)."""
+    return prepare_combine_weighted(y_sorted, routing, out=out, stream=stream)()
+
+
+def prepare_combine_weighted_backward(d_out, y_sorted, routing: Routing, *, d_y_sorted=None,
+                                      d_topk_w=None, stream=None) -> Prepared:
+    dev = _dev(d_out, y_sorted)
+    n, k = _row_routing(routing, dev, ("row_sorted", "topk_w"))
+    if y_sorted.dim() != 2 or y_sorted.shape[0] != n * k:
+        raise ValueError("y_sorted must be [N*k, hidden]")
+    hidden = y_sorted.shape[1]
+    if tuple(d_out.shape) != (n, hidden) or d_out.dtype != y_sorted.dtype:
+        raise ValueError("d_out must be [N, hidden] in the dtype of y_sorted")
+    d_y_sorted = _given(d_y_sorted, (n * k, hidden), y_sorted.dtype, dev, stream, "d_y_sorted")
+    d_topk_w = _given(d_topk_w, (n, k), torch.float32, dev, stream, "d_topk_w")
+    r = routing.as_c()
+    args = (d_out.data_ptr(), y_sorted.data_ptr(), _dt(y_sorted), n, hidden, k, ctypes.byref(r),
+            d_y_sorted.data_ptr(), d_topk_w.data_ptr(), _stream(dev, stream))
+    return _DevicePrepared(dev, "moe_combine_weighted_backward", args,
+                           (r, d_out, y_sorted, d_y_sorted, d_topk_w, routing),
+                           (d_y_sorted, d_topk_w))
+
+
+def moe_combine_weighted_backward(d_out: torch.Tensor, y_sorted: torch.Tensor, routing: Routing,
+                                  *, d_y_sorted: Optional[torch.Tensor] = None,
+                                  d_topk_w: Optional[torch.Tensor] = None, stream=None):
+    """Gradient of moe_combine_weighted: returns ``(d_y_sorted [N*k, hidden],
+    d_topk_w [N, k] fp32)``; rows that no slot points to are left as they were and
+    skipped slots get a zero weight gradient (see moe.h)."""
+    return prepare_combine_weighted_backward(d_out, y_sorted, routing, d_y_sorted=d_y_sorted,
+                                             d_topk_w=d_topk_w, stream=stream)()
+
+
+def prepare_route_backward(d_topk_w, routing: Routing, n_experts: Optional[int] = None, *,
+                           d_logits=None, stream=None) -> Prepared:
+    dev = _dev(d_topk_w)
+    n, k = _row_routing(routing, dev, ("topk_idx", "topk_w"))
+    if tuple(d_topk_w.shape) != (n, k) or d_topk_w.dtype != torch.float32:
+        raise ValueError("d_topk_w must be fp32 [N, k]")
+    e = routing.n_experts if n_experts is None else n_experts
+    d_logits = _given(d_logits, (n, e), routing.topk_w.dtype, dev, stream, "d_logits")
+    r = routing.as_c()
+    args = (d_topk_w.data_ptr(), n, e, k, ctypes.byref(r), d_logits.data_ptr(),
+            _stream(dev, stream))
+    return _DevicePrepared(dev, "moe_route_backward", args, (r, d_topk_w, d_logits, routing),
+                           d_logits)
+
+
+def moe_route_backward(d_topk_w: torch.Tensor, routing: Routing,
+                       n_experts: Optional[int] = None, *,
+                       d_logits: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Gradient of the routing weights with respect to the router logits
+    ``[N, E]`` (zeros for experts that were not selected).  ``n_experts``: the
+    layer's expert count, needed with the routing of an expert share, whose
+    ``col_sum`` holds the share's experts only."""
+    return prepare_route_backward(d_topk_w, routing, n_experts, d_logits=d_logits,
+                                  stream=stream)()
+
+
+# ------------------------------------------------- norms around a block
+
+@dataclass
+class BlockNorm:
+    """Outputs of moe_block_norm; None for what the call does not have."""
+
+    x_out: Optional[torch.Tensor]      # [N, H]
+    n_out: Optional[torch.Tensor]      # [N, H]
+    rstd_post: Optional[torch.Tensor]  # [N] fp32
+    rstd_pre: Optional[torch.Tensor]   # [N] fp32
+
+
+@dataclass
+class BlockNormGrads:
+    """Outputs of moe_block_norm_backward; None for what the call does not have."""
+
+    d_x: torch.Tensor                  # [N, H]
+    d_y: Optional[torch.Tensor]        # [N, H]
+    d_w_post: Optional[torch.Tensor]   # [H] fp32
+    d_w_pre: Optional[torch.Tensor]    # [H] fp32
+    d_gate: Optional[torch.Tensor]     # fp32 in the shape of the gate
+
+
+def moe_block_norm_workspace_bytes(n_tokens: int, hidden: int,
+                                   dtype: torch.dtype = torch.bfloat16) -> int:
+    b = N.load().moe_block_norm_workspace_bytes(n_tokens, hidden, _DT[dtype])
+    if b == 0:
+        raise MoeError(N.MOE_ERR_SHAPE, "moe_block_norm_workspace_bytes")
+    return b
+
+
+def _block_norm_args(x, y, w_post, w_pre, gate, residual_scale, eps):
+    """Checks what both directions take; returns (device, the C struct)."""
+    here = [t for t in (x, y, w_post, w_pre, gate) if t is not None]
+    dev = _dev(*here)
+    if x.dim() != 2:
+        raise ValueError("x must be [N, hidden]")
+    if any(t.dtype != x.dtype for t in here):
+        raise TypeError("x, y, the weights and the gate must share a dtype")
+    n, hidden = x.shape
+    if y is not None and y.shape != x.shape:
+        raise ValueError("y must have the shape of x")
+    for name, w in (("w_post", w_post), ("w_pre", w_pre)):
+        if w is not None and tuple(w.shape) != (hidden,):
+            raise ValueError(f"{name} must be [hidden]")
+    kind = N.MOE_GATE_NONE
+    if gate is not None:
+        if tuple(gate.shape) not in ((n, 1), (hidden,)):
+            raise ValueError("gate must be [N, 1] (a value per token) or [hidden] (per channel)")
+        kind = N.MOE_GATE_CHANNEL if gate.dim() == 1 else N.MOE_GATE_TOKEN
+    if y is None and (w_post is not None or gate is not None):
+        raise ValueError("w_post and gate need the block's output y")
+    if y is None and w_pre is None:
+        raise ValueError("nothing to do without y and w_pre")
+    c = N.MoeBlockNorm(None if w_post is None else w_post.data_ptr(),
+                       None if w_pre is None else w_pre.data_ptr(),
+                       None if gate is None else gate.data_ptr(), kind, residual_scale, eps)
+    return dev, c
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def prepare_block_norm(x, y=None, *, w_post=None, w_pre=None, gate=None,
+                       residual_scale: float = 1.0, eps: float = 1e-6, x_out=None, n_out=None,
+                       rstd_post=None, rstd_pre=None, stream=None) -> Prepared:
+    dev, c = _block_norm_args(x, y, w_post, w_pre, gate, residual_scale, eps)
+    n, hidden = x.shape
+    for name, t, have in (("x_out", x_out, y), ("n_out", n_out, w_pre),
+                          ("rstd_post", rstd_post, w_post), ("rstd_pre", rstd_pre, w_pre)):
+        if t is not None and have is None:
+            raise ValueError(f"the call has no {name}")
+    f32 = torch.float32
+    res = BlockNorm(
+        None if y is None else _given(x_out, (n, hidden), x.dtype, dev, stream, "x_out"),
+        None if w_pre is None else _given(n_out, (n, hidden), x.dtype, dev, stream, "n_out"),
+        None if w_post is None else _given(rstd_post, (n,), f32, dev, stream, "rstd_post"),
+        None if w_pre is None else _given(rstd_pre, (n,), f32, dev, stream, "rstd_pre"))
+    args = (x.data_ptr(), _ptr(y), _dt(x), n, hidden, ctypes.byref(c), _ptr(res.x_out),
+            _ptr(res.n_out), _ptr(res.rstd_post), _ptr(res.rstd_pre), _stream(dev, stream))
+    return _DevicePrepared(dev, "moe_block_norm", args, (c, x, y, w_post, w_pre, gate, res), res)
+
+
+def moe_block_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, *,
+                   w_post: Optional[torch.Tensor] = None, w_pre: Optional[torch.Tensor] = None,
+                   gate: Optional[torch.Tensor] = None, residual_scale: float = 1.0,
+                   eps: float = 1e-6, x_out: Optional[torch.Tensor] = None,
+                   n_out: Optional[torch.Tensor] = None,
+                   rstd_post: Optional[torch.Tensor] = None,
+                   rstd_pre: Optional[torch.Tensor] = None, stream=None) -> BlockNorm:
+    """Norms around a block in one pass: ``x_out = x + residual_scale * gate *
+    rmsnorm(y, w_post)`` and ``n_out = rmsnorm(x_out, w_pre)``, the input of the
+    next block.  Without ``y`` it is the norm ahead of a block alone, without
+    ``w_pre`` the step after a block alone, without ``w_post`` the block's output
+    enters unnormed.  ``gate``: ``[N, 1]`` (a value per token) or ``[hidden]``
+    (per channel).  ``x_out`` may be ``x`` (see moe.h)."""
+    return prepare_block_norm(x, y, w_post=w_post, w_pre=w_pre, gate=gate,
+                              residual_scale=residual_scale, eps=eps, x_out=x_out, n_out=n_out,
+                              rstd_post=rstd_post, rstd_pre=rstd_pre, stream=stream)()
+
+
+def prepare_block_norm_backward(d_x_out, d_n_out, x, y=None, *, w_post=None, w_pre=None,
+                                gate=None, residual_scale: float = 1.0, rstd_post=None,
+                                rstd_pre=None, d_x=None, d_y=None, d_w_post=None, d_w_pre=None,
+                                d_gate=None, workspace=None, stream=None) -> Prepared:
+    # the gradient takes the saved rstds, so eps no longer matters
+    dev, c = _block_norm_args(x, y, w_post, w_pre, gate, residual_scale, 1.0)
+    n, hidden = x.shape
+    if d_x_out is None and w_pre is None:
+        raise ValueError("no gradient flows in: d_x_out or w_pre with d_n_out is needed")
+    if (d_n_out is None) != (w_pre is None):
+        raise ValueError("d_n_out goes with w_pre")
+    f32 = torch.float32
+    for name, t, shape, dtype, need in (
+            ("d_x_out", d_x_out, (n, hidden), x.dtype, False),
+            ("d_n_out", d_n_out, (n, hidden), x.dtype, False),
+            ("rstd_post", rstd_post, (n,), f32, w_post is not None),
+            ("rstd_pre", rstd_pre, (n,), f32, w_pre is not None)):
+        if t is None and need:
+            raise ValueError(f"{name} of the forward call is needed")
+        if t is not None:
+            _given(t, shape, dtype, dev, stream, name)
+    for name, t, have in (("d_y", d_y, y), ("d_w_post", d_w_post, w_post),
+                          ("d_w_pre", d_w_pre, w_pre), ("d_gate", d_gate, gate)):
+        if t is not None and have is None:
+            raise ValueError(f"the call has no {name}")
+    res = BlockNormGrads(
+        _given(d_x, (n, hidden), x.dtype, dev, stream, "d_x"),
+        None if y is None else _given(d_y, (n, hidden), x.dtype, dev, stream, "d_y"),
+        None if w_post is None else _given(d_w_post, (hidden,), f32, dev, stream, "d_w_post"),
+        None if w_pre is None else _given(d_w_pre, (hidden,), f32, dev, stream, "d_w_pre"),
+        None if gate is None else _given(d_gate, gate.shape, f32, dev, stream, "d_gate"))
+    need = moe_block_norm_workspace_bytes(n, hidden, x.dtype)
+    ws = _empty((need,), torch.uint8, dev, stream) if workspace is None \
+        else _workspace(workspace, need, dev)
+    _dev(ws)
+    args = (_ptr(d_x_out), _ptr(d_n_out), x.data_ptr(), _ptr(y), _dt(x), n, hidden,
+            ctypes.byref(c), _ptr(rstd_post), _ptr(rstd_pre), res.d_x.data_ptr(), _ptr(res.d_y),
+            _ptr(res.d_w_post), _ptr(res.d_w_pre), _ptr(res.d_gate), ws.data_ptr(), _nbytes(ws),
+            _stream(dev, stream))
+    return _DevicePrepared(dev, "moe_block_norm_backward", args,
+                           (c, d_x_out, d_n_out, x, y, w_post, w_pre, gate, rstd_post, rstd_pre,
+                            res, ws), res)
+
+
+def moe_block_norm_backward(d_x_out: Optional[torch.Tensor], d_n_out: Optional[torch.Tensor],
+                            x: torch.Tensor, y: Optional[torch.Tensor] = None, *,
+                            w_post: Optional[torch.Tensor] = None,
+                            w_pre: Optional[torch.Tensor] = None,
+                            gate: Optional[torch.Tensor] = None, residual_scale: float = 1.0,
+                            rstd_post: Optional[torch.Tensor] = None,
+                            rstd_pre: Optional[torch.Tensor] = None,
+                            d_x: Optional[torch.Tensor] = None,
+                            d_y: Optional[torch.Tensor] = None,
+                            d_w_post: Optional[torch.Tensor] = None,
+                            d_w_pre: Optional[torch.Tensor] = None,
+                            d_gate: Optional[torch.Tensor] = None,
+                            workspace: Optional[torch.Tensor] = None,
+                            stream=None) -> BlockNormGrads:
+    """Gradient of moe_block_norm from the gradients of ``x_out`` (None: zero) and
+    ``n_out`` (with ``w_pre``), the forward call's arguments and its rstds.  The
+    gradients of the weights and the gate are fp32 (see moe.h)."""
+    return prepare_block_norm_backward(
+        d_x_out, d_n_out, x, y, w_post=w_post, w_pre=w_pre, gate=gate,
+        residual_scale=residual_scale, rstd_post=rstd_post, rstd_pre=rstd_pre, d_x=d_x, d_y=d_y,
+        d_w_post=d_w_post, d_w_pre=d_w_pre, d_gate=d_gate, workspace=workspace, stream=stream)()

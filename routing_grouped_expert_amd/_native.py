@@ -18,6 +18,8 @@ MOE_NOALLOC_SCRATCH_BYTES = 64 << 20
 MOE_F32, MOE_BF16 = 0, 1
 MOE_ACT_SILU, MOE_ACT_SWIGLU_OAI, MOE_ACT_RELU2 = 0, 1, 2
 MOE_W13_PACKED, MOE_W13_INTERLEAVED = 0, 1
+# moe_gate_kind_t
+MOE_GATE_NONE, MOE_GATE_TOKEN, MOE_GATE_CHANNEL = 0, 1, 2
 MOE_PARAM_ALPHA, MOE_PARAM_BETA, MOE_PARAM_LIMIT = 1, 2, 4
 
 
@@ -31,7 +33,13 @@ class MoeRouting(ctypes.Structure):
                 ("gate_scal", c_vp), ("w_dtype", c_i32)]
 
 
+class MoeBlockNorm(ctypes.Structure):
+    _fields_ = [("w_post", c_vp), ("w_pre", c_vp), ("gate", c_vp), ("gate_kind", c_i32),
+                ("residual_scale", c_f), ("eps", c_f)]
+
+
 _P_ROUTING = ctypes.POINTER(MoeRouting)
+_P_NORM = ctypes.POINTER(MoeBlockNorm)
 _P_PARAMS = ctypes.POINTER(MoeActParams)
 
 # name -> (restype, argtypes); every function include/moe.h declares
@@ -73,6 +81,17 @@ SIGNATURES = {
     "moe_forward_mxfp4": (c_i32, [c_vp, c_vp, c_i32, c_i64, c_i32, c_vp, c_vp, c_vp, c_vp, c_i32,
                                   c_i32, c_i32, c_i32, c_i32, _P_PARAMS, _P_ROUTING, c_vp, c_vp,
                                   c_sz, c_vp]),
+    "moe_dispatch": (c_i32, [c_vp, c_i32, c_i64, c_i32, c_i32, _P_ROUTING, c_vp, c_vp]),
+    "moe_combine_weighted": (c_i32, [c_vp, c_i32, c_i64, c_i32, c_i32, _P_ROUTING, c_vp, c_vp]),
+    "moe_combine_weighted_backward": (c_i32, [c_vp, c_vp, c_i32, c_i64, c_i32, c_i32, _P_ROUTING,
+                                              c_vp, c_vp, c_vp]),
+    "moe_route_backward": (c_i32, [c_vp, c_i64, c_i32, c_i32, _P_ROUTING, c_vp, c_vp]),
+    "moe_block_norm_workspace_bytes": (c_sz, [c_i64, c_i32, c_i32]),
+    "moe_block_norm": (c_i32, [c_vp, c_vp, c_i32, c_i64, c_i32, _P_NORM, c_vp, c_vp, c_vp, c_vp,
+                               c_vp]),
+    "moe_block_norm_backward": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_i32, c_i64, c_i32, _P_NORM,
+                                        c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_sz,
+                                        c_vp]),
     "moe_status_str": (ctypes.c_char_p, [c_i32]),
 }
 

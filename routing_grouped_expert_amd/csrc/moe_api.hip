@@ -112,6 +112,59 @@ moe_status_t check_ptrs(std::initializer_list<const void *> ptrs) {
   return MOE_OK;
 }
 
+// Sizes and types of the calls that move rows between token and sorted order.
+moe_status_t check_rows(moe_dtype_t dtype, int64_t n, int32_t hidden, int32_t k,
+                        const moe_routing_t *routing, bool weights) {
+  moe_status_t st = check_sizes(n, kCombineAnyExperts, k, false);
+  if (st != MOE_OK) return st;
+  if (check_ffn_sizes(hidden, 8) != MOE_OK) return MOE_ERR_SHAPE;
+  if (!dtype_ok(dtype)) return MOE_ERR_DTYPE;
+  // one thread per 16-byte chunk of a token row: below 2^31 workgroups of 256
+  if (n * hidden * (int64_t)dsize(dtype) / 16 > 0x7fffffffLL * 256) return MOE_ERR_SHAPE;
+  if (!routing) return MOE_ERR_NULL;
+  return weights && !dtype_ok(routing->w_dtype) ? MOE_ERR_DTYPE : MOE_OK;
+}
+
+// Operands of the block norm, either direction: which of them a call has
+// follows from y, w_post, w_pre and the gate.
+moe_status_t check_block_norm(const void *x, const void *y, moe_dtype_t dtype, int64_t n,
+                              int32_t hidden, const moe_block_norm_t *norm) {
+  if (n < 0 || n > 0x7fffffffLL || hidden < 8 || hidden % 8 || hidden > moe::kMaxNormHidden)
+    return MOE_ERR_SHAPE;
+  if (!dtype_ok(dtype)) return MOE_ERR_DTYPE;
+  if (!norm) return MOE_ERR_NULL;
+  if (!(norm->eps > 0.f) || !isfinite(norm->eps) || !isfinite(norm->residual_scale))
+    return MOE_ERR_SHAPE;
+  if (norm->gate_kind != MOE_GATE_NONE && norm->gate_kind != MOE_GATE_TOKEN &&
+      norm->gate_kind != MOE_GATE_CHANNEL)
+    return MOE_ERR_UNSUPPORTED;
+  // a norm or a gate of the block's output needs that output; a call without
+  // it must have the norm ahead of a block to do
+  if (n > 0 && !y && (norm->w_post || norm->gate_kind != MOE_GATE_NONE || !norm->w_pre))
+    return MOE_ERR_NULL;
+  if (n > 0 && !x) return MOE_ERR_NULL;
+  if (norm->gate_kind != MOE_GATE_NONE && n > 0 && !norm->gate) return MOE_ERR_NULL;
+  for (const void *p : {x, y, norm->w_post, norm->w_pre, norm->gate})
+    if (!aligned16(p)) return MOE_ERR_ALIGN;
+  return MOE_OK;
+}
+
+moe::BlockNormArgs block_norm_args(const void *x, const void *y, int64_t n, int32_t hidden,
+                                   const moe_block_norm_t *norm) {
+  moe::BlockNormArgs g{};
+  g.x = x;
+  g.y = y;
+  g.w_post = norm->w_post;
+  g.w_pre = norm->w_pre;
+  g.gate = norm->gate;
+  g.gate_kind = norm->gate_kind;
+  g.n_tokens = n;
+  g.hidden = hidden;
+  g.residual_scale = norm->residual_scale;
+  g.eps = norm->eps;
+  return g;
+}
+
 moe_status_t check_ws(const void *ws, size_t have, size_t need) {
   if (need == 0) return MOE_OK;
   if (!ws) return MOE_ERR_WORKSPACE;
@@ -379,6 +432,66 @@ moe_status_t moe_combine(const void *y_sorted, moe_dtype_t dtype, int64_t n_toke
              : MOE_ERR_HIP;
 }
 
+moe_status_t moe_dispatch(const void *x, moe_dtype_t dtype, int64_t n_tokens, int32_t hidden,
+                          int32_t topk, const moe_routing_t *routing, void *x_sorted,
+                          void *stream) {
+  moe_status_t st = check_rows(dtype, n_tokens, hidden, topk, routing, false);
+  if (st != MOE_OK || n_tokens == 0) return st;
+  if ((st = check_ptrs({x, routing->row_sorted, x_sorted})) != MOE_OK) return st;
+  return moe::launch_dispatch(x, routing->row_sorted, x_sorted, dtype, n_tokens, topk, hidden,
+                              (hipStream_t)stream) == hipSuccess
+             ? MOE_OK
+             : MOE_ERR_HIP;
+}
+
+moe_status_t moe_combine_weighted(const void *y_sorted, moe_dtype_t dtype, int64_t n_tokens,
+                                  int32_t hidden, int32_t topk, const moe_routing_t *routing,
+                                  void *out, void *stream) {
+  moe_status_t st = check_rows(dtype, n_tokens, hidden, topk, routing, true);
+  if (st != MOE_OK || n_tokens == 0) return st;
+  if ((st = check_ptrs({y_sorted, routing->row_sorted, routing->topk_w, out})) != MOE_OK)
+    return st;
+  return moe::launch_combine_weighted(y_sorted, routing->row_sorted, routing->topk_w,
+                                      (moe_dtype_t)routing->w_dtype, out, dtype, n_tokens, topk,
+                                      hidden, (hipStream_t)stream) == hipSuccess
+             ? MOE_OK
+             : MOE_ERR_HIP;
+}
+
+moe_status_t moe_combine_weighted_backward(const void *d_out, const void *y_sorted,
+                                           moe_dtype_t dtype, int64_t n_tokens, int32_t hidden,
+                                           int32_t topk, const moe_routing_t *routing,
+                                           void *d_y_sorted, float *d_topk_w, void *stream) {
+  moe_status_t st = check_rows(dtype, n_tokens, hidden, topk, routing, true);
+  if (st != MOE_OK || n_tokens == 0) return st;
+  if ((st = check_ptrs({d_out, y_sorted, routing->row_sorted, routing->topk_w, d_y_sorted,
+                        d_topk_w})) != MOE_OK)
+    return st;
+  return moe::launch_combine_weighted_backward(
+             d_out, y_sorted, routing->row_sorted, routing->topk_w, (moe_dtype_t)routing->w_dtype,
+             d_y_sorted, d_topk_w, dtype, n_tokens, topk, hidden,
+             (hipStream_t)stream) == hipSuccess
+             ? MOE_OK
+             : MOE_ERR_HIP;
+}
+
+moe_status_t moe_route_backward(const float *d_topk_w, int64_t n_tokens, int32_t n_experts,
+                                int32_t topk, const moe_routing_t *routing, void *d_logits,
+                                void *stream) {
+  moe_status_t st = check_sizes(n_tokens, n_experts, topk);
+  if (st != MOE_OK) return st;
+  if (!routing) return MOE_ERR_NULL;
+  if (!dtype_ok(routing->w_dtype)) return MOE_ERR_DTYPE;
+  if (n_tokens == 0) return MOE_OK;
+  if ((st = check_ptrs({d_topk_w, routing->topk_idx, routing->topk_w, d_logits})) != MOE_OK)
+    return st;
+  return moe::launch_route_backward(d_topk_w, routing->topk_idx, routing->topk_w, d_logits,
+                                    (moe_dtype_t)routing->w_dtype, n_tokens, n_experts, topk,
+                                    (hipStream_t)stream) == hipSuccess
+             ? MOE_OK
+             : MOE_ERR_HIP;
+}
+
 moe_status_t moe_forward(const void *x, const void *logits, moe_dtype_t dtype, int64_t n_tokens,
                          int32_t hidden, const void *w13, const void *w2, int32_t n_experts,
                          int32_t inter, int32_t topk, moe_act_t act, moe_w13_layout_t layout,
@@ -624,6 +737,74 @@ moe_status_t moe_forward_mxfp4(const void *x, const void *logits, moe_dtype_t dt
     return MOE_ERR_HIP;
   return run_experts(x, dtype, n_tokens, hidden, w13_q, w2_q, n_experts, inter, topk, act, layout,
                      prm, routing_out, out, workspace, s, false, w13_s, w2_s);
+}
+
+size_t moe_block_norm_workspace_bytes(int64_t n_tokens, int32_t hidden, moe_dtype_t dtype) {
+  if (n_tokens < 0 || n_tokens > 0x7fffffffLL || hidden < 8 || hidden % 8 ||
+      hidden > moe::kMaxNormHidden || !dtype_ok(dtype))
+    return 0;
+  const size_t b = align256(moe::block_norm_scratch_bytes(n_tokens, hidden, dtype));
+  return b ? b : 256;
+}
+
+moe_status_t moe_block_norm(const void *x, const void *y, moe_dtype_t dtype, int64_t n_tokens,
+                            int32_t hidden, const moe_block_norm_t *norm, void *x_out,
+                            void *n_out, float *rstd_post, float *rstd_pre, void *stream) {
+  moe_status_t st = check_block_norm(x, y, dtype, n_tokens, hidden, norm);
+  if (st != MOE_OK || n_tokens == 0) return st;
+  if ((y && !x_out) || (norm->w_pre && !n_out)) return MOE_ERR_NULL;
+  for (const void *p : {(const void *)x_out, (const void *)n_out, (const void *)rstd_post,
+                        (const void *)rstd_pre})
+    if (!aligned16(p)) return MOE_ERR_ALIGN;
+  moe::BlockNormArgs g = block_norm_args(x, y, n_tokens, hidden, norm);
+  g.x_out = x_out;
+  g.n_out = n_out;
+  g.rstd_post = rstd_post;
+  g.rstd_pre = rstd_pre;
+  return moe::launch_block_norm(g, dtype, (hipStream_t)stream) == hipSuccess ? MOE_OK
+                                                                             : MOE_ERR_HIP;
+}
+
+moe_status_t moe_block_norm_backward(const void *d_x_out, const void *d_n_out, const void *x,
+                                     const void *y, moe_dtype_t dtype, int64_t n_tokens,
+                                     int32_t hidden, const moe_block_norm_t *norm,
+                                     const float *rstd_post, const float *rstd_pre, void *d_x,
+                                     void *d_y, float *d_w_post, float *d_w_pre, float *d_gate,
+                                     void *workspace, size_t ws_bytes, void *stream) {
+  moe_status_t st = check_block_norm(x, y, dtype, n_tokens, hidden, norm);
+  if (st != MOE_OK) return st;
+  const bool token_gate = norm->gate_kind == MOE_GATE_TOKEN;
+  if (n_tokens > 0) {
+    // something flows back, and everything it flows through is there
+    if ((!d_x_out && !norm->w_pre) || !d_x || (y && !d_y)) return MOE_ERR_NULL;
+    if (norm->w_pre && (!d_n_out || !rstd_pre)) return MOE_ERR_NULL;
+    if (norm->w_post && !rstd_post) return MOE_ERR_NULL;
+    if (token_gate && !d_gate) return MOE_ERR_NULL;
+  }
+  if ((norm->w_pre && !d_w_pre) || (norm->w_post && !d_w_post) ||
+      (norm->gate_kind == MOE_GATE_CHANNEL && !d_gate))
+    return MOE_ERR_NULL;
+  for (const void *p : {d_x_out, d_n_out, (const void *)rstd_post, (const void *)rstd_pre,
+                        (const void *)d_x, (const void *)d_y, (const void *)d_w_post,
+                        (const void *)d_w_pre, (const void *)d_gate})
+    if (!aligned16(p)) return MOE_ERR_ALIGN;
+  if ((st = check_ws(workspace, ws_bytes,
+                     moe::block_norm_scratch_bytes(n_tokens, hidden, dtype))) != MOE_OK)
+    return st;
+  moe::BlockNormArgs g = block_norm_args(x, y, n_tokens, hidden, norm);
+  g.d_x_out = d_x_out;
+  g.d_n_out = d_n_out;
+  g.rstd_post = const_cast<float *>(rstd_post);
+  g.rstd_pre = const_cast<float *>(rstd_pre);
+  g.d_x = d_x;
+  g.d_y = d_y;
+  g.d_gate = token_gate ? d_gate : nullptr;
+  g.partial = reinterpret_cast<float *>(workspace);
+  const moe::ColumnSums sums{norm->w_pre ? d_w_pre : nullptr, norm->w_post ? d_w_post : nullptr,
+                             norm->gate_kind == MOE_GATE_CHANNEL ? d_gate : nullptr};
+  return moe::launch_block_norm_backward(g, sums, dtype, (hipStream_t)stream) == hipSuccess
+             ? MOE_OK
+             : MOE_ERR_HIP;
 }
 
 const char *moe_status_str(moe_status_t status) {

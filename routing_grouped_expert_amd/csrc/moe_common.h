@@ -120,4 +120,50 @@ hipError_t launch_quantize_mxfp4(const void *w, moe_dtype_t dt, int n_experts, i
 // topk == 1: out[t] = 0 where row_sorted[t] = -1.
 hipError_t launch_zero_unrouted(const int32_t *row_sorted, void *out, moe_dtype_t dt,
                                 int64_t n_tokens, int hidden, hipStream_t s);
+
+// x_sorted[row_sorted[t*topk + j]] = x[t]; slots with row_sorted = -1 skipped
+// (as in the three that follow).
+hipError_t launch_dispatch(const void *x, const int32_t *row_sorted, void *x_sorted,
+                           moe_dtype_t dt, int64_t n_tokens, int topk, int hidden, hipStream_t s);
+// out[t] = sum_j topk_w[t, j] * y_sorted[row_sorted[t*topk + j]] (fp32, slot order).
+hipError_t launch_combine_weighted(const void *y_sorted, const int32_t *row_sorted,
+                                   const void *topk_w, moe_dtype_t w_dt, void *out, moe_dtype_t dt,
+                                   int64_t n_tokens, int topk, int hidden, hipStream_t s);
+// d_y_sorted[p] = topk_w[t, j] * d_out[t], d_topk_w[t, j] = <d_out[t], y_sorted[p]>
+// (0 for a skipped slot).
+hipError_t launch_combine_weighted_backward(const void *d_out, const void *y_sorted,
+                                            const int32_t *row_sorted, const void *topk_w,
+                                            moe_dtype_t w_dt, void *d_y_sorted, float *d_topk_w,
+                                            moe_dtype_t dt, int64_t n_tokens, int topk, int hidden,
+                                            hipStream_t s);
+// Gradient of the softmax over the selected logits, zeros elsewhere.
+hipError_t launch_route_backward(const float *d_topk_w, const int32_t *topk_idx,
+                                 const void *topk_w, void *d_logits, moe_dtype_t w_dt,
+                                 int64_t n_tokens, int n_experts, int topk, hipStream_t s);
+
+// Norms around a block (block_norm.hip): the operands of both directions; NULL
+// where a call has none.
+struct BlockNormArgs {
+  const void *x, *y;               // [n_tokens, hidden]
+  const void *w_post, *w_pre;      // [hidden]
+  const void *gate;                // [n_tokens] or [hidden] by gate_kind
+  const void *d_x_out, *d_n_out;   // backward
+  void *x_out, *n_out;             // forward
+  void *d_x, *d_y;                 // backward
+  float *rstd_post, *rstd_pre;     // [n_tokens]: written forward, read backward
+  float *d_gate;                   // [n_tokens] (a gate per token, backward)
+  float *partial;                  // [3, workgroups, hidden] column sums (backward)
+  int64_t n_tokens;
+  int hidden, gate_kind;
+  float residual_scale, eps;
+};
+// [hidden] gradients summed over the tokens (NULL: not wanted).
+struct ColumnSums {
+  float *d_w_pre, *d_w_post, *d_gate;
+};
+constexpr int kMaxNormHidden = 16384;
+size_t block_norm_scratch_bytes(int64_t n_tokens, int hidden, moe_dtype_t dt);
+hipError_t launch_block_norm(const BlockNormArgs &g, moe_dtype_t dt, hipStream_t s);
+hipError_t launch_block_norm_backward(const BlockNormArgs &g, const ColumnSums &sums,
+                                      moe_dtype_t dt, hipStream_t s);
 }  // namespace moe
