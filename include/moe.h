@@ -478,6 +478,62 @@ moe_status_t moe_forward_mxfp4(const void *x, const void *logits, moe_dtype_t dt
                                const moe_routing_t *routing_out, void *out, void *workspace,
                                size_t ws_bytes, void *stream);
 
+/* ---- 4-bit expert weights with group scales ------------------------------------
+ * Weights of 4-bit codes with one scale and one zero point per group of 32, 64
+ * or 128 consecutive weights along K:
+ *
+ *   w[e][r][k] = scales[e][k / group][r] * (code[e][r][k] - zeros[e][k / group][r])
+ *
+ * q [n_experts, rows, k / 2]: codes 0 .. 15, two to a byte, the even element in
+ * the low nibble.  scales [n_experts, k / group, rows] bf16.  zeros the same
+ * shape, bytes 0 .. 15 (larger ones are outside the contract), or NULL:
+ * symmetric codes, zero point 8. */
+typedef struct {
+  const void *q;
+  const void *scales;
+  const void *zeros; /* NULL: 8 */
+} moe_int4_weights_t;
+
+/* moe_quantize_int4: w [n_experts, rows, k] in `dtype` (finite) -> q, scales and
+ *   zeros (NULL: symmetric).  Symmetric: scale = max|w| / 7; otherwise scale =
+ *   (max(w, 0) - min(w, 0)) / 15 and zero = round(-min(w, 0) / scale); both
+ *   scales rounded to bf16 before they are used, code = round(w / scale) + zero
+ *   limited to [0, 15]; IEEE fp32 division, rounding to nearest, ties to even.
+ *   A group of zeros gets scale 0.  k a multiple of group.  Deterministic.
+ * moe_dequantize_int4: the weights in bf16, each rounded once, for the entry
+ *   points that take bf16 weights (prompts, see moe_experts_int4). */
+moe_status_t moe_quantize_int4(const void *w, moe_dtype_t dtype, int32_t n_experts, int32_t rows,
+                               int32_t k, int32_t group, void *q, void *scales, void *zeros,
+                               void *stream);
+moe_status_t moe_dequantize_int4(const moe_int4_weights_t *w, int32_t n_experts, int32_t rows,
+                                 int32_t k, int32_t group, void *out, void *stream);
+
+/* moe_experts_int4 / moe_forward_int4: moe_experts / moe_forward of a bf16 layer
+ *   with 4-bit weights: w13 [E, w13 rows, hidden] and w2 [E, hidden, inter] as
+ *   above, with one group size for both (hidden and inter multiples of it).
+ *   The products of codes and activations are exact and summed in fp32, the
+ *   scales enter in fp32; the activation rows are rounded to bf16 as in
+ *   moe_experts, the weighted expert rows stay fp32 and the output is rounded
+ *   once.  x must be finite (an infinity becomes NaN in its token's row).
+ *   Deterministic.
+ *   Any batch is right; the kernel is shaped for decode-sized ones, a few rows
+ *   an expert.  For prompts, moe_dequantize_int4 once and moe_experts are
+ *   faster.  workspace: moe_int4_workspace_bytes(...). */
+size_t moe_int4_workspace_bytes(int64_t n_tokens, int32_t n_experts, int32_t topk, int32_t hidden,
+                                int32_t inter);
+moe_status_t moe_experts_int4(const void *x, int64_t n_tokens, int32_t hidden,
+                              const moe_int4_weights_t *w13, const moe_int4_weights_t *w2,
+                              int32_t n_experts, int32_t inter, int32_t topk, int32_t group,
+                              moe_act_t act, moe_w13_layout_t layout,
+                              const moe_act_params_t *params, const moe_routing_t *routing,
+                              void *out, void *workspace, size_t ws_bytes, void *stream);
+moe_status_t moe_forward_int4(const void *x, const void *logits, int64_t n_tokens, int32_t hidden,
+                              const moe_int4_weights_t *w13, const moe_int4_weights_t *w2,
+                              int32_t n_experts, int32_t inter, int32_t topk, int32_t group,
+                              moe_act_t act, moe_w13_layout_t layout,
+                              const moe_act_params_t *params, const moe_routing_t *routing_out,
+                              void *out, void *workspace, size_t ws_bytes, void *stream);
+
 /* Static, human-readable name of a status code. */
 const char *moe_status_str(moe_status_t status);
 

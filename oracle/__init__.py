@@ -13,7 +13,8 @@ Python binding, and imports neither.
 * :mod:`oracle.ffn` also gives the layer with the routing weight on the input
   rows (``moe_ffn_weighted_input``).
 * :mod:`oracle.quant` -- MXFP4 expert weights: E2M1 codes with one E8M0 scale
-  per 32 weights along K (quantise, dequantise).
+  per 32 weights along K (quantise, dequantise), and 4-bit codes with a scale and
+  a zero point per group of weights.
 * :mod:`oracle.routing` also gives the router logits from the gate weight
   (``gate_logits``, ``route_gate``).
 * both also give one GPU's expert-parallel share (``route_ep``,
@@ -30,7 +31,8 @@ to the pages) is marked "parity unpinned" where it is defined.
 from .routing import (RoutingRef, bitmatrix, gate_logits, histogram, offsets_from_hist,
                       remap_to_share, route, route_ep, route_gate, round_to_dtype, sorted_indices,
                       topk_select, topk_softmax)
-from .quant import dequantize_mxfp4, e2m1_decode, e2m1_encode, quantize_mxfp4
+from .quant import (dequantize_int4, dequantize_mxfp4, e2m1_decode, e2m1_encode, quantize_int4,
+                    quantize_mxfp4)
 from .block import (block_norm, block_norm_grad, combine_weighted, combine_weighted_grad,
                     dispatch, rms_norm, topk_weight_grad)
 from .ffn import (activation, moe_ffn, moe_ffn_share, moe_ffn_sorted,
@@ -43,5 +45,5 @@ __all__ = [
     "activation", "split_gate_up", "moe_ffn", "moe_ffn_sorted", "moe_ffn_share",
     "moe_ffn_weighted_input", "quantize_mxfp4", "dequantize_mxfp4", "e2m1_encode",
     "e2m1_decode", "dispatch", "combine_weighted", "combine_weighted_grad", "topk_weight_grad",
-    "rms_norm", "block_norm", "block_norm_grad",
+    "rms_norm", "block_norm", "block_norm_grad", "quantize_int4", "dequantize_int4",
 ]

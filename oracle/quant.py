@@ -83,3 +83,45 @@ def dequantize_mxfp4(q: np.ndarray, s: np.ndarray) -> np.ndarray:
     vals = e2m1_decode(codes).reshape(*q.shape[:-1], k // BLOCK, BLOCK)
     scale = np.exp2(s.astype(np.float64) - 127.0)
     return (vals * scale[..., None]).reshape(*q.shape[:-1], k)
+
+
+# 4-bit codes with a bf16 scale and a zero point per group of weights along K:
+# w = s * (q - z).  Symmetric: z = 8, s = max|w| / 7; else s = (hi - lo) / 15 and
+# z = round(-lo / s) with lo = min(w, 0), hi = max(w, 0).  The division and the
+# rounding are defined in fp32 (round to nearest, ties to even), so the codes
+# are exact.
+
+def _to_bf16(v: np.ndarray) -> np.ndarray:
+    u = np.ascontiguousarray(v, dtype=np.float32).view(np.uint32)
+    u = (u + np.uint32(0x7fff) + ((u >> np.uint32(16)) & np.uint32(1))) & np.uint32(0xffff0000)
+    return u.view(np.float32)
+
+
+def quantize_int4(w, group: int, zeros: bool):
+    """``w [..., K]`` -> packed codes ``[..., K/2]`` uint8, scales ``[..., K/group]``
+    (fp32 holding bf16 values) and zero points ``[..., K/group]`` uint8."""
+    import torch
+    w = w.detach().to("cpu", torch.float32).numpy()
+    k = w.shape[-1]
+    g = w.reshape(*w.shape[:-1], k // group, group)
+    lo, hi = np.minimum(g.min(-1), 0), np.maximum(g.max(-1), 0)
+    f32 = np.float32
+    s = _to_bf16((hi - lo) / f32(15) if zeros else np.maximum(hi, -lo) / f32(7))
+    safe = np.where(s > 0, s, f32(1))
+    if zeros:
+        z = np.where(s > 0, np.clip(np.rint(-lo / safe), 0, 15), f32(0))
+    else:
+        z = np.full(s.shape, 8, dtype=f32)
+    q = np.where((s > 0)[..., None], np.rint(g / safe[..., None]), f32(0))
+    q = np.clip(q + z[..., None], 0, 15).astype(np.uint8).reshape(w.shape)
+    return (q[..., 0::2] | (q[..., 1::2] << 4)).astype(np.uint8), s, z.astype(np.uint8)
+
+
+def dequantize_int4(q: np.ndarray, s: np.ndarray, z, group: int) -> np.ndarray:
+    """Float64 weights ``[..., K]``; ``z`` None: 8."""
+    q = np.asarray(q, dtype=np.uint8)
+    codes = np.stack([q & 15, q >> 4], axis=-1).reshape(*q.shape[:-1], q.shape[-1] * 2)
+    k = codes.shape[-1]
+    v = codes.astype(np.float64).reshape(*q.shape[:-1], k // group, group)
+    zero = 8.0 if z is None else np.asarray(z, dtype=np.float64)[..., None]
+    return (np.asarray(s, dtype=np.float64)[..., None] * (v - zero)).reshape(codes.shape)

@@ -66,7 +66,9 @@ __all__ = ["Routing", "MoeError", "Prepared", "moe_route", "moe_experts", "moe_e
            "moe_route_backward", "prepare_dispatch", "prepare_combine_weighted",
            "prepare_combine_weighted_backward", "prepare_route_backward", "BlockNorm",
            "BlockNormGrads", "moe_block_norm", "moe_block_norm_backward", "prepare_block_norm",
-           "prepare_block_norm_backward", "moe_block_norm_workspace_bytes",
+           "prepare_block_norm_backward", "moe_block_norm_workspace_bytes", "moe_quantize_int4",
+           "moe_dequantize_int4", "moe_experts_int4", "moe_forward_int4", "prepare_experts_int4",
+           "prepare_forward_int4", "moe_int4_workspace_bytes",
            "moe_workspace_bytes", "moe_status_str", "ACTS", "LAYOUTS"]
 
 _DT = {torch.float32: N.MOE_F32, torch.bfloat16: N.MOE_BF16}
@@ -1086,3 +1088,152 @@ def moe_block_norm_backward(d_x_out: Optional[torch.Tensor], d_n_out: Optional[t
         d_x_out, d_n_out, x, y, w_post=w_post, w_pre=w_pre, gate=gate,
         residual_scale=residual_scale, rstd_post=rstd_post, rstd_pre=rstd_pre, d_x=d_x, d_y=d_y,
         d_w_post=d_w_post, d_w_pre=d_w_pre, d_gate=d_gate, workspace=workspace, stream=stream)()
+
+
+# ------------------------------------------------- 4-bit expert weights with group scales
+
+def moe_quantize_int4(w: torch.Tensor, group: int = 128, *, zeros: bool = True, stream=None):
+    """4-bit weights from ``w [E, rows, K]`` (K a multiple of ``group``, 32, 64 or
+    128): returns ``(q [E, rows, K/2] uint8, scales [E, K/group, rows] bf16,
+    zeros [E, K/group, rows] uint8)``; the last is None without ``zeros``
+    (symmetric codes, see moe.h)."""
+    dev = _dev(w)
+    if w.dim() != 3:
+        raise ValueError("expected w [E, rows, K]")
+    e, rows, k = w.shape
+    if group not in (32, 64, 128) or k % group:
+        raise ValueError("group must be 32, 64 or 128 and divide K")
+    q = _empty((e, rows, k // 2), torch.uint8, dev, stream)
+    s = _empty((e, k // group, rows), torch.bfloat16, dev, stream)
+    z = _empty((e, k // group, rows), torch.uint8, dev, stream) if zeros else None
+    args = (w.data_ptr(), _dt(w), e, rows, k, group, q.data_ptr(), s.data_ptr(), _ptr(z),
+            _stream(dev, stream))
+    return _DevicePrepared(dev, "moe_quantize_int4", args, (w,), (q, s, z))()
+
+
+def _int4_weights(q, s, z, name: str):
+    """Checks one weight array; returns (E, rows, K, group, the C struct)."""
+    if q.dtype != torch.uint8 or s.dtype != torch.bfloat16 or q.dim() != 3 or s.dim() != 3:
+        raise TypeError(f"{name}: expected uint8 codes [E, rows, K/2] and bf16 scales "
+                        f"[E, K/group, rows]")
+    e, rows, k = q.shape[0], q.shape[1], 2 * q.shape[2]
+    group = k // s.shape[1] if s.shape[1] else 0
+    if group not in (32, 64, 128) or tuple(s.shape) != (e, k // group, rows) or k % group:
+        raise ValueError(f"{name}: scales {tuple(s.shape)} do not give groups of 32, 64 or 128 "
+                         f"of codes {tuple(q.shape)}")
+    if z is not None and (z.dtype != torch.uint8 or z.shape != s.shape):
+        raise ValueError(f"{name}: zeros must be uint8 in the shape of the scales")
+    return e, rows, k, group, N.MoeInt4Weights(q.data_ptr(), s.data_ptr(), _ptr(z))
+
+
+def moe_dequantize_int4(q: torch.Tensor, scales: torch.Tensor,
+                        zeros: Optional[torch.Tensor] = None, *,
+                        out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """bf16 weights ``[E, rows, K]`` of 4-bit codes, scales and zero points."""
+    dev = _dev(*(t for t in (q, scales, zeros) if t is not None))
+    e, rows, k, group, c = _int4_weights(q, scales, zeros, "w")
+    out = _given(out, (e, rows, k), torch.bfloat16, dev, stream, "out")
+    args = (ctypes.byref(c), e, rows, k, group, out.data_ptr(), _stream(dev, stream))
+    return _DevicePrepared(dev, "moe_dequantize_int4", args, (c, q, scales, zeros), out)()
+
+
+def moe_int4_workspace_bytes(n_tokens: int, n_experts: int, topk: int, hidden: int,
+                             inter: int) -> int:
+    b = N.load().moe_int4_workspace_bytes(n_tokens, n_experts, topk, hidden, inter)
+    if b == 0:
+        raise MoeError(N.MOE_ERR_SHAPE, "moe_int4_workspace_bytes")
+    return b
+
+
+def _int4_args(x, w13, w2, act, layout):
+    """Checks the layer; returns (device, n, hidden, E, inter, group, structs)."""
+    dev = _dev(x, *(t for t in (*w13, *w2) if t is not None))
+    if act not in ACTS:
+        raise ValueError(f"unknown activation {act!r}")
+    if layout not in LAYOUTS:
+        raise ValueError(f"unknown w13 layout {layout!r}")
+    if x.dim() != 2 or x.dtype != torch.bfloat16:
+        raise TypeError("4-bit weights run a bf16 layer: x must be bf16 [N, hidden]")
+    n, hidden = x.shape
+    e, rows, k, group, c13 = _int4_weights(*w13, "w13")
+    e2, h2, inter, group2, c2 = _int4_weights(*w2, "w2")
+    if k != hidden or h2 != hidden or e2 != e or rows != (inter if act == "relu2" else 2 * inter):
+        raise ValueError(f"w13 [{e}, {rows}, {k}] / w2 [{e2}, {h2}, {inter}] do not match "
+                         f"x {tuple(x.shape)} and act {act!r}")
+    if group != group2:
+        raise ValueError(f"w13 and w2 must share a group size, got {group} and {group2}")
+    return dev, n, hidden, e, inter, group, c13, c2
+
+
+def prepare_experts_int4(x, w13_q, w13_s, w13_z, w2_q, w2_s, w2_z, routing: Routing, act: str,
+                         layout: str = "packed", params: Optional[dict] = None, *, out=None,
+                         workspace=None, stream=None) -> Prepared:
+    w13, w2 = (w13_q, w13_s, w13_z), (w2_q, w2_s, w2_z)
+    k = routing.topk
+    dev, n, hidden, e, inter, group, c13, c2 = _int4_args(x, w13, w2, act, layout)
+    _check_routing(routing, n, e, k)
+    _dev(x, routing.offsets, routing.col_sorted, routing.row_sorted, routing.gate_scal)
+    out = _given(out, (n, hidden), x.dtype, dev, stream, "out")
+    need = moe_int4_workspace_bytes(n, e, k, hidden, inter)
+    ws = _empty((need,), torch.uint8, dev, stream) if workspace is None \
+        else _workspace(workspace, need, dev)
+    r = routing.as_c()
+    p = _params(params)
+    args = (x.data_ptr(), n, hidden, ctypes.byref(c13), ctypes.byref(c2), e, inter, k, group,
+            ACTS[act], LAYOUTS[layout], ctypes.byref(p) if p else None, ctypes.byref(r),
+            out.data_ptr(), ws.data_ptr(), _nbytes(ws), _stream(dev, stream))
+    return _DevicePrepared(dev, "moe_experts_int4", args,
+                           (r, p, c13, c2, x, w13, w2, out, ws, routing), out)
+
+
+def moe_experts_int4(x: torch.Tensor, w13_q: torch.Tensor, w13_s: torch.Tensor,
+                     w13_z: Optional[torch.Tensor], w2_q: torch.Tensor, w2_s: torch.Tensor,
+                     w2_z: Optional[torch.Tensor], routing: Routing, act: str,
+                     layout: str = "packed", params: Optional[dict] = None, *,
+                     out: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """moe_experts with 4-bit expert weights (codes, scales and zero points as
+    moe_quantize_int4 gives them, zeros None for symmetric codes); bf16 layer,
+    shaped for decode-sized batches (see moe.h)."""
+    return prepare_experts_int4(x, w13_q, w13_s, w13_z, w2_q, w2_s, w2_z, routing, act, layout,
+                                params, out=out, workspace=workspace, stream=stream)()
+
+
+def prepare_forward_int4(x, logits, w13_q, w13_s, w13_z, w2_q, w2_s, w2_z, topk: int, act: str,
+                         layout: str = "packed", params: Optional[dict] = None, *, out=None,
+                         routing=None, workspace=None, stream=None) -> Prepared:
+    w13, w2 = (w13_q, w13_s, w13_z), (w2_q, w2_s, w2_z)
+    dev, n, hidden, e, inter, group, c13, c2 = _int4_args(x, w13, w2, act, layout)
+    _dev(x, logits)
+    if logits.dtype != x.dtype or tuple(logits.shape) != (n, e):
+        raise ValueError("logits must be [N, E] in the layer dtype")
+    if routing is None:
+        if stream is None:
+            routing = Routing.empty(n, e, topk, x.dtype, dev)
+        else:
+            with torch.cuda.stream(stream):
+                routing = Routing.empty(n, e, topk, x.dtype, dev)
+    _check_routing(routing, n, e, topk)
+    out = _given(out, (n, hidden), x.dtype, dev, stream, "out")
+    need = moe_int4_workspace_bytes(n, e, topk, hidden, inter)
+    ws = _empty((need,), torch.uint8, dev, stream) if workspace is None \
+        else _workspace(workspace, need, dev)
+    r = routing.as_c()
+    p = _params(params)
+    args = (x.data_ptr(), logits.data_ptr(), n, hidden, ctypes.byref(c13), ctypes.byref(c2), e,
+            inter, topk, group, ACTS[act], LAYOUTS[layout], ctypes.byref(p) if p else None,
+            ctypes.byref(r), out.data_ptr(), ws.data_ptr(), _nbytes(ws), _stream(dev, stream))
+    return _DevicePrepared(dev, "moe_forward_int4", args,
+                           (r, p, c13, c2, x, logits, w13, w2, out, ws, routing), (out, routing))
+
+
+def moe_forward_int4(x: torch.Tensor, logits: torch.Tensor, w13_q: torch.Tensor,
+                     w13_s: torch.Tensor, w13_z: Optional[torch.Tensor], w2_q: torch.Tensor,
+                     w2_s: torch.Tensor, w2_z: Optional[torch.Tensor], topk: int, act: str,
+                     layout: str = "packed", params: Optional[dict] = None, *,
+                     out: Optional[torch.Tensor] = None, routing: Optional[Routing] = None,
+                     workspace: Optional[torch.Tensor] = None, stream=None):
+    """Routing then the 4-bit experts on one stream; returns ``(out, routing)``."""
+    return prepare_forward_int4(x, logits, w13_q, w13_s, w13_z, w2_q, w2_s, w2_z, topk, act,
+                                layout, params, out=out, routing=routing, workspace=workspace,
+                                stream=stream)()

@@ -38,7 +38,12 @@ class MoeBlockNorm(ctypes.Structure):
                 ("residual_scale", c_f), ("eps", c_f)]
 
 
+class MoeInt4Weights(ctypes.Structure):
+    _fields_ = [("q", c_vp), ("scales", c_vp), ("zeros", c_vp)]
+
+
 _P_ROUTING = ctypes.POINTER(MoeRouting)
+_P_INT4 = ctypes.POINTER(MoeInt4Weights)
 _P_NORM = ctypes.POINTER(MoeBlockNorm)
 _P_PARAMS = ctypes.POINTER(MoeActParams)
 
@@ -92,6 +97,15 @@ SIGNATURES = {
     "moe_block_norm_backward": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_i32, c_i64, c_i32, _P_NORM,
                                         c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_sz,
                                         c_vp]),
+    "moe_int4_workspace_bytes": (c_sz, [c_i64, c_i32, c_i32, c_i32, c_i32]),
+    "moe_quantize_int4": (c_i32, [c_vp, c_i32, c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp,
+                                  c_vp]),
+    "moe_dequantize_int4": (c_i32, [_P_INT4, c_i32, c_i32, c_i32, c_i32, c_vp, c_vp]),
+    "moe_experts_int4": (c_i32, [c_vp, c_i64, c_i32, _P_INT4, _P_INT4, c_i32, c_i32, c_i32, c_i32,
+                                 c_i32, c_i32, _P_PARAMS, _P_ROUTING, c_vp, c_vp, c_sz, c_vp]),
+    "moe_forward_int4": (c_i32, [c_vp, c_vp, c_i64, c_i32, _P_INT4, _P_INT4, c_i32, c_i32, c_i32,
+                                 c_i32, c_i32, c_i32, _P_PARAMS, _P_ROUTING, c_vp, c_vp, c_sz,
+                                 c_vp]),
     "moe_status_str": (ctypes.c_char_p, [c_i32]),
 }
 

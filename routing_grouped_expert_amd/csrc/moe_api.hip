@@ -739,6 +739,134 @@ moe_status_t moe_forward_mxfp4(const void *x, const void *logits, moe_dtype_t dt
                      prm, routing_out, out, workspace, s, false, w13_s, w2_s);
 }
 
+namespace {
+bool group_ok(int32_t g) { return g == 32 || g == 64 || g == 128; }
+
+// Scratch of the 4-bit experts: activation rows a[M, inter] bf16, then (topk >
+// 1) the weighted expert rows y[M, hidden] in fp32.
+size_t int4_act_bytes(int64_t n, int32_t k, int32_t inter) {
+  return align256((size_t)n * k * inter * 2);
+}
+size_t int4_ws_bytes(int64_t n, int32_t k, int32_t hidden, int32_t inter) {
+  return int4_act_bytes(n, k, inter) + (k > 1 ? align256((size_t)n * k * hidden * 4) : 0);
+}
+
+moe_status_t check_int4_weights(const moe_int4_weights_t *w) {
+  if (!w || !w->q || !w->scales) return MOE_ERR_NULL;
+  if (!aligned16(w->q) || !aligned16(w->scales) || !aligned16(w->zeros)) return MOE_ERR_ALIGN;
+  return MOE_OK;
+}
+
+moe_status_t check_int4(const void *x, int64_t n, int32_t hidden, const moe_int4_weights_t *w13,
+                        const moe_int4_weights_t *w2, int32_t e, int32_t inter, int32_t k,
+                        int32_t group, moe_act_t act, moe_w13_layout_t layout,
+                        const moe_act_params_t *params, const moe_routing_t *routing, void *out,
+                        void *ws, size_t ws_bytes, ActParams *prm) {
+  moe_status_t st = check_expert_args(MOE_BF16, n, hidden, e, inter, k, act, layout, params,
+                                      routing, prm);
+  if (st != MOE_OK) return st;
+  if (!group_ok(group) || hidden % group || inter % group) return MOE_ERR_SHAPE;
+  if (n == 0) return MOE_OK;
+  if ((st = check_int4_weights(w13)) != MOE_OK || (st = check_int4_weights(w2)) != MOE_OK)
+    return st;
+  if ((st = check_ptrs({x, out})) != MOE_OK) return st;
+  return check_ws(ws, ws_bytes, int4_ws_bytes(n, k, hidden, inter));
+}
+
+moe_status_t run_int4(const void *x, int64_t n, int32_t hidden, const moe_int4_weights_t *w13,
+                      const moe_int4_weights_t *w2, int32_t e, int32_t inter, int32_t k,
+                      int32_t group, moe_act_t act, moe_w13_layout_t layout, const ActParams &prm,
+                      const moe_routing_t *routing, void *out, void *ws, hipStream_t s) {
+  char *base = reinterpret_cast<char *>(ws);
+  return moe::launch_experts_int4({w13->q, w13->scales, w13->zeros}, {w2->q, w2->scales, w2->zeros},
+                                  x, routing, out, base, base + int4_act_bytes(n, k, inter), n, k,
+                                  e, hidden, inter, group, act, layout, prm, s) == hipSuccess
+             ? MOE_OK
+             : MOE_ERR_HIP;
+}
+
+moe_status_t check_int4_array(int32_t e, int32_t rows, int32_t k, int32_t group) {
+  if (e < 1 || rows < 1 || k < 1 || k > (1 << 24) || !group_ok(group) || k % group)
+    return MOE_ERR_SHAPE;
+  // one thread per eight weights at most: below 2^31 workgroups of 256
+  if ((int64_t)e * rows > 0x7fffffffLL * 256 / (k / 8)) return MOE_ERR_SHAPE;
+  return MOE_OK;
+}
+}  // namespace
+
+size_t moe_int4_workspace_bytes(int64_t n_tokens, int32_t n_experts, int32_t topk, int32_t hidden,
+                                int32_t inter) {
+  if (check_sizes(n_tokens, n_experts, topk) != MOE_OK ||
+      check_ffn_sizes(hidden, inter) != MOE_OK)
+    return 0;
+  // the expert scratch reuses the routing's once the routing has run
+  const size_t route = moe::route_scratch_bytes(n_tokens, n_experts, topk);
+  const size_t ffn = int4_ws_bytes(n_tokens, topk, hidden, inter);
+  const size_t b = route > ffn ? route : ffn;
+  return b ? b : 256;
+}
+
+moe_status_t moe_quantize_int4(const void *w, moe_dtype_t dtype, int32_t n_experts, int32_t rows,
+                               int32_t k, int32_t group, void *q, void *scales, void *zeros,
+                               void *stream) {
+  if (!dtype_ok(dtype)) return MOE_ERR_DTYPE;
+  moe_status_t st = check_int4_array(n_experts, rows, k, group);
+  if (st != MOE_OK) return st;
+  if ((st = check_ptrs({w, q, scales})) != MOE_OK) return st;
+  if (!aligned16(zeros)) return MOE_ERR_ALIGN;
+  return moe::launch_quantize_int4(w, dtype, n_experts, rows, k, group, {q, scales, zeros},
+                                   (hipStream_t)stream) == hipSuccess
+             ? MOE_OK
+             : MOE_ERR_HIP;
+}
+
+moe_status_t moe_dequantize_int4(const moe_int4_weights_t *w, int32_t n_experts, int32_t rows,
+                                 int32_t k, int32_t group, void *out, void *stream) {
+  moe_status_t st = check_int4_array(n_experts, rows, k, group);
+  if (st != MOE_OK) return st;
+  if ((st = check_int4_weights(w)) != MOE_OK) return st;
+  if ((st = check_ptrs({out})) != MOE_OK) return st;
+  return moe::launch_dequantize_int4({w->q, w->scales, w->zeros}, n_experts, rows, k, group, out,
+                                     (hipStream_t)stream) == hipSuccess
+             ? MOE_OK
+             : MOE_ERR_HIP;
+}
+
+moe_status_t moe_experts_int4(const void *x, int64_t n_tokens, int32_t hidden,
+                              const moe_int4_weights_t *w13, const moe_int4_weights_t *w2,
+                              int32_t n_experts, int32_t inter, int32_t topk, int32_t group,
+                              moe_act_t act, moe_w13_layout_t layout,
+                              const moe_act_params_t *params, const moe_routing_t *routing,
+                              void *out, void *workspace, size_t ws_bytes, void *stream) {
+  ActParams prm;
+  moe_status_t st = check_int4(x, n_tokens, hidden, w13, w2, n_experts, inter, topk, group, act,
+                               layout, params, routing, out, workspace, ws_bytes, &prm);
+  if (st != MOE_OK || n_tokens == 0) return st;
+  return run_int4(x, n_tokens, hidden, w13, w2, n_experts, inter, topk, group, act, layout, prm,
+                  routing, out, workspace, (hipStream_t)stream);
+}
+
+moe_status_t moe_forward_int4(const void *x, const void *logits, int64_t n_tokens, int32_t hidden,
+                              const moe_int4_weights_t *w13, const moe_int4_weights_t *w2,
+                              int32_t n_experts, int32_t inter, int32_t topk, int32_t group,
+                              moe_act_t act, moe_w13_layout_t layout,
+                              const moe_act_params_t *params, const moe_routing_t *routing_out,
+                              void *out, void *workspace, size_t ws_bytes, void *stream) {
+  ActParams prm;
+  moe_status_t st = check_route(logits, MOE_BF16, n_tokens, n_experts, topk, routing_out,
+                                workspace, ws_bytes);
+  if (st != MOE_OK) return st;
+  st = check_int4(x, n_tokens, hidden, w13, w2, n_experts, inter, topk, group, act, layout,
+                  params, routing_out, out, workspace, ws_bytes, &prm);
+  if (st != MOE_OK || n_tokens == 0) return st;
+  hipStream_t s = (hipStream_t)stream;
+  if (moe::launch_route(logits, MOE_BF16, n_tokens, n_experts, topk, 0, n_experts, routing_out,
+                        workspace, s) != hipSuccess)
+    return MOE_ERR_HIP;
+  return run_int4(x, n_tokens, hidden, w13, w2, n_experts, inter, topk, group, act, layout, prm,
+                  routing_out, out, workspace, s);
+}
+
 size_t moe_block_norm_workspace_bytes(int64_t n_tokens, int32_t hidden, moe_dtype_t dtype) {
   if (n_tokens < 0 || n_tokens > 0x7fffffffLL || hidden < 8 || hidden % 8 ||
       hidden > moe::kMaxNormHidden || !dtype_ok(dtype))

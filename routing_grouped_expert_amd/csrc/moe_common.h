@@ -141,6 +141,22 @@ hipError_t launch_route_backward(const float *d_topk_w, const int32_t *topk_idx,
                                  const void *topk_w, void *d_logits, moe_dtype_t w_dt,
                                  int64_t n_tokens, int n_experts, int topk, hipStream_t s);
 
+// 4-bit weights with group scales (expert_int4.hip): codes [E, rows, K / 2],
+// bf16 scales and byte zero points (NULL: 8) [E, K / group, rows].
+struct Int4Weights {
+  const void *q, *s, *z;
+};
+// The expert FFN: act [M, inter] bf16 and y [M, hidden] fp32 (topk > 1) are scratch.
+hipError_t launch_experts_int4(const Int4Weights &w13, const Int4Weights &w2, const void *x,
+                               const moe_routing_t *r, void *out, void *act, void *y,
+                               int64_t n_tokens, int topk, int n_experts, int hidden, int inter,
+                               int group, moe_act_t kind, moe_w13_layout_t layout, ActParams prm,
+                               hipStream_t s);
+hipError_t launch_quantize_int4(const void *w, moe_dtype_t dt, int n_experts, int rows, int k,
+                                int group, const Int4Weights &out, hipStream_t s);
+hipError_t launch_dequantize_int4(const Int4Weights &in, int n_experts, int rows, int k, int group,
+                                  void *w, hipStream_t s);
+
 // Norms around a block (block_norm.hip): the operands of both directions; NULL
 // where a call has none.
 struct BlockNormArgs {

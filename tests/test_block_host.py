@@ -137,3 +137,60 @@ def test_python_side_refuses_host_tensors():
                  lambda: moe.moe_block_norm_backward(x, x, x, w_pre=x[0], rstd_pre=x[0])):
         with pytest.raises(ValueError, match="GPU"):
             call()
+
+
+def int4(q=FAKE, s=FAKE, z=FAKE):
+    return ctypes.byref(N.MoeInt4Weights(q, s, z))
+
+
+def test_int4_calls(lib):
+    def experts(x=FAKE, n=33, h=128, w13=None, w2=None, e=8, i=256, k=2, g=64,
+                act=N.MOE_ACT_SILU, layout=N.MOE_W13_PACKED, r=None, o=FAKE, ws=FAKE,
+                wsb=1 << 30):
+        return lib.moe_experts_int4(x, n, h, w13 or int4(), w2 or int4(z=None), e, i, k, g, act,
+                                    layout, None, r or routing(), o, ws, wsb, None)
+
+    def forward(x=FAKE, n=33, h=128, w13=None, w2=None, e=8, i=256, k=2, g=64,
+                act=N.MOE_ACT_SILU, layout=N.MOE_W13_PACKED, r=None, o=FAKE, ws=FAKE,
+                wsb=1 << 30):
+        return lib.moe_forward_int4(x, FAKE, n, h, w13 or int4(), w2 or int4(z=None), e, i, k, g,
+                                    act, layout, None, r or routing(), o, ws, wsb, None)
+
+    for call in (experts, forward):
+        assert call(None, n=0, o=None) == N.MOE_OK
+        assert call(None) == N.MOE_ERR_NULL
+        assert call(MISALIGNED) == N.MOE_ERR_ALIGN
+        assert call(o=None) == N.MOE_ERR_NULL
+        assert call(w13=int4(q=None)) == N.MOE_ERR_NULL
+        assert call(w2=int4(s=None)) == N.MOE_ERR_NULL
+        assert call(w2=int4(z=MISALIGNED)) == N.MOE_ERR_ALIGN
+        for bad in ({"g": 16}, {"g": 0}, {"g": 96}, {"h": 96}, {"i": 96}, {"h": 0}, {"k": 9},
+                    {"e": 257}, {"n": -1}, {"n": 1 << 24, "h": 1024}):
+            assert call(**bad) == N.MOE_ERR_SHAPE, bad
+        assert call(act=5) == N.MOE_ERR_UNSUPPORTED
+        assert call(act=N.MOE_ACT_RELU2, layout=N.MOE_W13_INTERLEAVED) == N.MOE_ERR_UNSUPPORTED
+        assert call(r=routing({"offsets": None})) == N.MOE_ERR_NULL
+        assert call(ws=None) == N.MOE_ERR_WORKSPACE
+        assert call(wsb=1024) == N.MOE_ERR_WORKSPACE
+    need = lib.moe_int4_workspace_bytes(33, 8, 2, 128, 256)
+    assert need >= 66 * 256 * 2 + 66 * 128 * 4
+    assert lib.moe_int4_workspace_bytes(33, 8, 9, 128, 256) == 0
+    assert lib.moe_int4_workspace_bytes(33, 8, 2, 100, 256) == 0
+
+    def quantize(w=FAKE, dt=N.MOE_F32, e=4, rows=33, k=128, g=64, q=FAKE, s=FAKE, z=None):
+        return lib.moe_quantize_int4(w, dt, e, rows, k, g, q, s, z, None)
+    assert quantize(None) == N.MOE_ERR_NULL
+    assert quantize(q=None) == N.MOE_ERR_NULL
+    assert quantize(s=MISALIGNED) == N.MOE_ERR_ALIGN
+    assert quantize(z=MISALIGNED) == N.MOE_ERR_ALIGN
+    assert quantize(dt=4) == N.MOE_ERR_DTYPE
+    for bad in ({"e": 0}, {"rows": 0}, {"k": 96}, {"k": 0}, {"g": 48}, {"g": 0},
+                {"e": 1 << 30, "rows": 1 << 20}):
+        assert quantize(**bad) == N.MOE_ERR_SHAPE, bad
+
+    def dequantize(w=None, e=4, rows=33, k=128, g=64, o=FAKE):
+        return lib.moe_dequantize_int4(w or int4(), e, rows, k, g, o, None)
+    assert dequantize(int4(q=None)) == N.MOE_ERR_NULL
+    assert dequantize(int4(z=MISALIGNED)) == N.MOE_ERR_ALIGN
+    assert dequantize(o=None) == N.MOE_ERR_NULL
+    assert dequantize(k=100) == N.MOE_ERR_SHAPE
