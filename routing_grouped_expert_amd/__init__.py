@@ -778,63 +778,126 @@ def moe_forward_mxfp4(x: torch.Tensor, logits: torch.Tensor, w13_q: torch.Tensor
 
 
 # ------------------------------------------------- rows into sorted order and back
+#
+# The calls below marshal their arguments once for both forms: moe_X runs them
+# right away, prepare_X keeps them in a Prepared.  A decoding step is a chain of
+# kernels of a few microseconds, so what moe_X does on the host is kept short:
+# raw device indexes and stream handles instead of torch's objects for them.
+
+class _Call:
+    """One checked C call: its device, name, arguments, and what they refer to."""
+
+    __slots__ = ("dev", "name", "args", "keep", "result")
+
+    def __init__(self, dev: int, name: str, args: tuple, keep: tuple, result):
+        self.dev, self.name, self.args, self.keep, self.result = dev, name, args, keep, result
+
+    def run(self):
+        fn = getattr(N.load(), self.name)
+        if torch._C._cuda_getDevice() == self.dev:
+            st = fn(*self.args)
+        else:
+            with torch.cuda.device(self.dev):
+                st = fn(*self.args)
+        if st != N.MOE_OK:
+            raise MoeError(st, self.name)
+        return self.result
+
+    def prepared(self) -> Prepared:
+        return _DevicePrepared(self.dev, self.name, self.args, self.keep, self.result)
+
 
 class _DevicePrepared(Prepared):
     """A Prepared whose launches go to the device of its tensors, whichever
     device is current when it is called."""
 
-    def __init__(self, dev, name: str, args: tuple, keep: tuple, result):
+    def __init__(self, dev: int, name: str, args: tuple, keep: tuple, result):
         super().__init__(name, args, keep, result)
         self._dev = dev
 
     def __call__(self):
-        if torch.cuda.current_device() == self._dev.index:
+        if torch.cuda.current_device() == self._dev:
             return super().__call__()
         with torch.cuda.device(self._dev):
             return super().__call__()
 
 
-def _empty(shape, dtype, dev, stream) -> torch.Tensor:
-    """Uninitialised memory that belongs to the stream the call runs on."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+def _index(*ts: torch.Tensor) -> int:
+    """Device index of tensors that must be contiguous on one GPU."""
+    dev = ts[0].get_device()
+    for t in ts:
+        if dev < 0 or t.get_device() != dev:
+            raise ValueError("all tensors must be on the same GPU")
+        if not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+    return dev
 
 
-def _given(t, shape, dtype, dev, stream, name: str) -> torch.Tensor:
-    """The caller's output tensor, checked, or a new one."""
+def _raw_stream(dev: int, stream) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _output(t, like: torch.Tensor, shape, dtype, stream, name: str) -> torch.Tensor:
+    """The caller's output tensor, checked, or new memory that belongs to the
+    stream the call runs on."""
     if t is None:
-        return _empty(shape, dtype, dev, stream)
+        if stream is None:
+            return like.new_empty(shape, dtype=dtype)
+        with torch.cuda.stream(stream):
+            return like.new_empty(shape, dtype=dtype)
     if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous() \
-            or t.device != dev:
-        raise ValueError(f"{name} must be contiguous {tuple(shape)} {dtype} on {dev}")
+            or t.device != like.device:
+        raise ValueError(f"{name} must be contiguous {tuple(shape)} {dtype} on {like.device}")
     return t
 
 
-def _row_routing(routing: Routing, dev, fields_):
-    """The routing fields a row call reads; returns (N, k)."""
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _scratch(ws, like: torch.Tensor, nbytes: int, stream) -> torch.Tensor:
+    if ws is None:
+        return _output(None, like, (nbytes,), torch.uint8, stream, "workspace")
+    _index(like, ws)
+    return _workspace(ws, nbytes, None)
+
+
+def _row_routing(routing: Routing, dev: int, order: str, weights: bool):
+    """The routing fields a row call reads (`order`: row_sorted or topk_idx);
+    returns (N, k, the C struct with just these)."""
+    idx = getattr(routing, order)
     n, k = routing.topk_idx.shape
-    for f in fields_:
-        t = getattr(routing, f)
-        if t.numel() != n * k or not t.is_contiguous() or t.device != dev:
-            raise ValueError(f"routing.{f} must be contiguous with N*k = {n * k} entries on {dev}")
-        if f != "topk_w" and t.dtype != torch.int32:
-            raise TypeError(f"routing.{f} must be int32")
-    return n, k
+    if idx.numel() != n * k or idx.get_device() != dev or not idx.is_contiguous():
+        raise ValueError(f"routing.{order} must be contiguous with N*k = {n * k} entries on the "
+                         f"GPU of the rows")
+    if idx.dtype != torch.int32:
+        raise TypeError(f"routing.{order} must be int32")
+    w = routing.topk_w
+    r = N.MoeRouting()
+    setattr(r, order, idx.data_ptr())
+    if weights:
+        if w.shape != (n, k) or w.get_device() != dev or not w.is_contiguous():
+            raise ValueError("routing.topk_w must be contiguous [N, k] on the GPU of the rows")
+        r.topk_w = w.data_ptr()
+        r.w_dtype = _dt(w)
+    return n, k, r
 
 
-def prepare_dispatch(x, routing: Routing, *, x_sorted=None, stream=None) -> Prepared:
-    dev = _dev(x)
-    n, k = _row_routing(routing, dev, ("row_sorted",))
+def _dispatch(x, routing, x_sorted, stream) -> _Call:
+    dev = _index(x)
+    n, k, r = _row_routing(routing, dev, "row_sorted", False)
     if x.dim() != 2 or x.shape[0] != n:
         raise ValueError("x must be [N, hidden] with the routing's N")
     hidden = x.shape[1]
-    x_sorted = _given(x_sorted, (n * k, hidden), x.dtype, dev, stream, "x_sorted")
-    r = routing.as_c()
+    x_sorted = _output(x_sorted, x, (n * k, hidden), x.dtype, stream, "x_sorted")
     args = (x.data_ptr(), _dt(x), n, hidden, k, ctypes.byref(r), x_sorted.data_ptr(),
-            _stream(dev, stream))
-    return _DevicePrepared(dev, "moe_dispatch", args, (r, x, x_sorted, routing), x_sorted)
+            _raw_stream(dev, stream))
+    return _Call(dev, "moe_dispatch", args, (r, x, x_sorted, routing), x_sorted)
+
+
+def prepare_dispatch(x: torch.Tensor, routing: Routing, *,
+                     x_sorted: Optional[torch.Tensor] = None, stream=None) -> Prepared:
+    return _dispatch(x, routing, x_sorted, stream).prepared()
 
 
 def moe_dispatch(x: torch.Tensor, routing: Routing, *, x_sorted: Optional[torch.Tensor] = None,
@@ -842,20 +905,24 @@ def moe_dispatch(x: torch.Tensor, routing: Routing, *, x_sorted: Optional[torch.
     """Token rows into expert-sorted order: ``x_sorted[row_sorted[t*k + j]] = x[t]``
     (``[N*k, hidden]``; rows that no slot points to are left as they were).  The
     gradient with respect to ``x`` is ``moe_combine(d_x_sorted, routing)``."""
-    return prepare_dispatch(x, routing, x_sorted=x_sorted, stream=stream)()
+    return _dispatch(x, routing, x_sorted, stream).run()
 
 
-def prepare_combine_weighted(y_sorted, routing: Routing, *, out=None, stream=None) -> Prepared:
-    dev = _dev(y_sorted)
-    n, k = _row_routing(routing, dev, ("row_sorted", "topk_w"))
+def _combine_weighted(y_sorted, routing, out, stream) -> _Call:
+    dev = _index(y_sorted)
+    n, k, r = _row_routing(routing, dev, "row_sorted", True)
     if y_sorted.dim() != 2 or y_sorted.shape[0] != n * k:
         raise ValueError("y_sorted must be [N*k, hidden]")
     hidden = y_sorted.shape[1]
-    out = _given(out, (n, hidden), y_sorted.dtype, dev, stream, "out")
-    r = routing.as_c()
+    out = _output(out, y_sorted, (n, hidden), y_sorted.dtype, stream, "out")
     args = (y_sorted.data_ptr(), _dt(y_sorted), n, hidden, k, ctypes.byref(r), out.data_ptr(),
-            _stream(dev, stream))
-    return _DevicePrepared(dev, "moe_combine_weighted", args, (r, y_sorted, out, routing), out)
+            _raw_stream(dev, stream))
+    return _Call(dev, "moe_combine_weighted", args, (r, y_sorted, out, routing), out)
+
+
+def prepare_combine_weighted(y_sorted: torch.Tensor, routing: Routing, *,
+                             out: Optional[torch.Tensor] = None, stream=None) -> Prepared:
+    return _combine_weighted(y_sorted, routing, out, stream).prepared()
 
 
 def moe_combine_weighted(y_sorted: torch.Tensor, routing: Routing, *,
@@ -863,26 +930,33 @@ def moe_combine_weighted(y_sorted: torch.Tensor, routing: Routing, *,
     """Expert rows back into token order with the routing weights applied:
     ``out[t] = sum_j topk_w[t, j] * y_sorted[row_sorted[t*k + j]]`` (slot order,
     fp32 sum, one rounding; slots with row_sorted = -1 skipped)."""
-    return prepare_combine_weighted(y_sorted, routing, out=out, stream=stream)()
+    return _combine_weighted(y_sorted, routing, out, stream).run()
 
 
-def prepare_combine_weighted_backward(d_out, y_sorted, routing: Routing, *, d_y_sorted=None,
-                                      d_topk_w=None, stream=None) -> Prepared:
-    dev = _dev(d_out, y_sorted)
-    n, k = _row_routing(routing, dev, ("row_sorted", "topk_w"))
+def _combine_weighted_backward(d_out, y_sorted, routing, d_y_sorted, d_topk_w, stream) -> _Call:
+    dev = _index(d_out, y_sorted)
+    n, k, r = _row_routing(routing, dev, "row_sorted", True)
     if y_sorted.dim() != 2 or y_sorted.shape[0] != n * k:
         raise ValueError("y_sorted must be [N*k, hidden]")
     hidden = y_sorted.shape[1]
     if tuple(d_out.shape) != (n, hidden) or d_out.dtype != y_sorted.dtype:
         raise ValueError("d_out must be [N, hidden] in the dtype of y_sorted")
-    d_y_sorted = _given(d_y_sorted, (n * k, hidden), y_sorted.dtype, dev, stream, "d_y_sorted")
-    d_topk_w = _given(d_topk_w, (n, k), torch.float32, dev, stream, "d_topk_w")
-    r = routing.as_c()
+    d_y_sorted = _output(d_y_sorted, y_sorted, (n * k, hidden), y_sorted.dtype, stream,
+                         "d_y_sorted")
+    d_topk_w = _output(d_topk_w, y_sorted, (n, k), torch.float32, stream, "d_topk_w")
     args = (d_out.data_ptr(), y_sorted.data_ptr(), _dt(y_sorted), n, hidden, k, ctypes.byref(r),
-            d_y_sorted.data_ptr(), d_topk_w.data_ptr(), _stream(dev, stream))
-    return _DevicePrepared(dev, "moe_combine_weighted_backward", args,
-                           (r, d_out, y_sorted, d_y_sorted, d_topk_w, routing),
-                           (d_y_sorted, d_topk_w))
+            d_y_sorted.data_ptr(), d_topk_w.data_ptr(), _raw_stream(dev, stream))
+    return _Call(dev, "moe_combine_weighted_backward", args,
+                 (r, d_out, y_sorted, d_y_sorted, d_topk_w, routing), (d_y_sorted, d_topk_w))
+
+
+def prepare_combine_weighted_backward(d_out: torch.Tensor, y_sorted: torch.Tensor,
+                                      routing: Routing, *,
+                                      d_y_sorted: Optional[torch.Tensor] = None,
+                                      d_topk_w: Optional[torch.Tensor] = None,
+                                      stream=None) -> Prepared:
+    return _combine_weighted_backward(d_out, y_sorted, routing, d_y_sorted, d_topk_w,
+                                      stream).prepared()
 
 
 def moe_combine_weighted_backward(d_out: torch.Tensor, y_sorted: torch.Tensor, routing: Routing,
@@ -891,23 +965,26 @@ def moe_combine_weighted_backward(d_out: torch.Tensor, y_sorted: torch.Tensor, r
     """Gradient of moe_combine_weighted: returns ``(d_y_sorted [N*k, hidden],
     d_topk_w [N, k] fp32)``; rows that no slot points to are left as they were and
     skipped slots get a zero weight gradient (see moe.h)."""
-    return prepare_combine_weighted_backward(d_out, y_sorted, routing, d_y_sorted=d_y_sorted,
-                                             d_topk_w=d_topk_w, stream=stream)()
+    return _combine_weighted_backward(d_out, y_sorted, routing, d_y_sorted, d_topk_w,
+                                      stream).run()
 
 
-def prepare_route_backward(d_topk_w, routing: Routing, n_experts: Optional[int] = None, *,
-                           d_logits=None, stream=None) -> Prepared:
-    dev = _dev(d_topk_w)
-    n, k = _row_routing(routing, dev, ("topk_idx", "topk_w"))
+def _route_backward(d_topk_w, routing, n_experts, d_logits, stream) -> _Call:
+    dev = _index(d_topk_w)
+    n, k, r = _row_routing(routing, dev, "topk_idx", True)
     if tuple(d_topk_w.shape) != (n, k) or d_topk_w.dtype != torch.float32:
         raise ValueError("d_topk_w must be fp32 [N, k]")
     e = routing.n_experts if n_experts is None else n_experts
-    d_logits = _given(d_logits, (n, e), routing.topk_w.dtype, dev, stream, "d_logits")
-    r = routing.as_c()
+    d_logits = _output(d_logits, d_topk_w, (n, e), routing.topk_w.dtype, stream, "d_logits")
     args = (d_topk_w.data_ptr(), n, e, k, ctypes.byref(r), d_logits.data_ptr(),
-            _stream(dev, stream))
-    return _DevicePrepared(dev, "moe_route_backward", args, (r, d_topk_w, d_logits, routing),
-                           d_logits)
+            _raw_stream(dev, stream))
+    return _Call(dev, "moe_route_backward", args, (r, d_topk_w, d_logits, routing), d_logits)
+
+
+def prepare_route_backward(d_topk_w: torch.Tensor, routing: Routing,
+                           n_experts: Optional[int] = None, *,
+                           d_logits: Optional[torch.Tensor] = None, stream=None) -> Prepared:
+    return _route_backward(d_topk_w, routing, n_experts, d_logits, stream).prepared()
 
 
 def moe_route_backward(d_topk_w: torch.Tensor, routing: Routing,
@@ -917,8 +994,7 @@ def moe_route_backward(d_topk_w: torch.Tensor, routing: Routing,
     ``[N, E]`` (zeros for experts that were not selected).  ``n_experts``: the
     layer's expert count, needed with the routing of an expert share, whose
     ``col_sum`` holds the share's experts only."""
-    return prepare_route_backward(d_topk_w, routing, n_experts, d_logits=d_logits,
-                                  stream=stream)()
+    return _route_backward(d_topk_w, routing, n_experts, d_logits, stream).run()
 
 
 # ------------------------------------------------- norms around a block
@@ -953,56 +1029,66 @@ def moe_block_norm_workspace_bytes(n_tokens: int, hidden: int,
 
 
 def _block_norm_args(x, y, w_post, w_pre, gate, residual_scale, eps):
-    """Checks what both directions take; returns (device, the C struct)."""
+    """Checks what both directions take; returns (device, n, hidden, C struct)."""
     here = [t for t in (x, y, w_post, w_pre, gate) if t is not None]
-    dev = _dev(*here)
+    dev = _index(*here)
     if x.dim() != 2:
         raise ValueError("x must be [N, hidden]")
-    if any(t.dtype != x.dtype for t in here):
-        raise TypeError("x, y, the weights and the gate must share a dtype")
+    dtype = x.dtype
+    for t in here:
+        if t.dtype != dtype:
+            raise TypeError("x, y, the weights and the gate must share a dtype")
     n, hidden = x.shape
     if y is not None and y.shape != x.shape:
         raise ValueError("y must have the shape of x")
-    for name, w in (("w_post", w_post), ("w_pre", w_pre)):
-        if w is not None and tuple(w.shape) != (hidden,):
-            raise ValueError(f"{name} must be [hidden]")
+    if w_post is not None and w_post.shape != (hidden,):
+        raise ValueError("w_post must be [hidden]")
+    if w_pre is not None and w_pre.shape != (hidden,):
+        raise ValueError("w_pre must be [hidden]")
     kind = N.MOE_GATE_NONE
     if gate is not None:
-        if tuple(gate.shape) not in ((n, 1), (hidden,)):
+        if gate.shape != (n, 1) and gate.shape != (hidden,):
             raise ValueError("gate must be [N, 1] (a value per token) or [hidden] (per channel)")
         kind = N.MOE_GATE_CHANNEL if gate.dim() == 1 else N.MOE_GATE_TOKEN
     if y is None and (w_post is not None or gate is not None):
         raise ValueError("w_post and gate need the block's output y")
     if y is None and w_pre is None:
         raise ValueError("nothing to do without y and w_pre")
-    c = N.MoeBlockNorm(None if w_post is None else w_post.data_ptr(),
-                       None if w_pre is None else w_pre.data_ptr(),
-                       None if gate is None else gate.data_ptr(), kind, residual_scale, eps)
-    return dev, c
+    c = N.MoeBlockNorm(_ptr(w_post), _ptr(w_pre), _ptr(gate), kind, residual_scale, eps)
+    return dev, n, hidden, c
 
 
-def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
-
-
-def prepare_block_norm(x, y=None, *, w_post=None, w_pre=None, gate=None,
-                       residual_scale: float = 1.0, eps: float = 1e-6, x_out=None, n_out=None,
-                       rstd_post=None, rstd_pre=None, stream=None) -> Prepared:
-    dev, c = _block_norm_args(x, y, w_post, w_pre, gate, residual_scale, eps)
-    n, hidden = x.shape
+def _block_norm(x, y, w_post, w_pre, gate, residual_scale, eps, x_out, n_out, rstd_post, rstd_pre,
+                stream) -> _Call:
+    dev, n, hidden, c = _block_norm_args(x, y, w_post, w_pre, gate, residual_scale, eps)
     for name, t, have in (("x_out", x_out, y), ("n_out", n_out, w_pre),
                           ("rstd_post", rstd_post, w_post), ("rstd_pre", rstd_pre, w_pre)):
         if t is not None and have is None:
             raise ValueError(f"the call has no {name}")
-    f32 = torch.float32
-    res = BlockNorm(
-        None if y is None else _given(x_out, (n, hidden), x.dtype, dev, stream, "x_out"),
-        None if w_pre is None else _given(n_out, (n, hidden), x.dtype, dev, stream, "n_out"),
-        None if w_post is None else _given(rstd_post, (n,), f32, dev, stream, "rstd_post"),
-        None if w_pre is None else _given(rstd_pre, (n,), f32, dev, stream, "rstd_pre"))
-    args = (x.data_ptr(), _ptr(y), _dt(x), n, hidden, ctypes.byref(c), _ptr(res.x_out),
-            _ptr(res.n_out), _ptr(res.rstd_post), _ptr(res.rstd_pre), _stream(dev, stream))
-    return _DevicePrepared(dev, "moe_block_norm", args, (c, x, y, w_post, w_pre, gate, res), res)
+    dtype, f32 = x.dtype, torch.float32
+    if y is not None:
+        x_out = _output(x_out, x, (n, hidden), dtype, stream, "x_out")
+    if w_pre is not None:
+        n_out = _output(n_out, x, (n, hidden), dtype, stream, "n_out")
+        rstd_pre = _output(rstd_pre, x, (n,), f32, stream, "rstd_pre")
+    if w_post is not None:
+        rstd_post = _output(rstd_post, x, (n,), f32, stream, "rstd_post")
+    args = (x.data_ptr(), _ptr(y), _dt(x), n, hidden, ctypes.byref(c), _ptr(x_out), _ptr(n_out),
+            _ptr(rstd_post), _ptr(rstd_pre), _raw_stream(dev, stream))
+    res = BlockNorm(x_out, n_out, rstd_post, rstd_pre)
+    return _Call(dev, "moe_block_norm", args, (c, x, y, w_post, w_pre, gate, res), res)
+
+
+def prepare_block_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, *,
+                       w_post: Optional[torch.Tensor] = None,
+                       w_pre: Optional[torch.Tensor] = None,
+                       gate: Optional[torch.Tensor] = None, residual_scale: float = 1.0,
+                       eps: float = 1e-6, x_out: Optional[torch.Tensor] = None,
+                       n_out: Optional[torch.Tensor] = None,
+                       rstd_post: Optional[torch.Tensor] = None,
+                       rstd_pre: Optional[torch.Tensor] = None, stream=None) -> Prepared:
+    return _block_norm(x, y, w_post, w_pre, gate, residual_scale, eps, x_out, n_out, rstd_post,
+                       rstd_pre, stream).prepared()
 
 
 def moe_block_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, *,
@@ -1018,53 +1104,70 @@ def moe_block_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, *,
     ``w_pre`` the step after a block alone, without ``w_post`` the block's output
     enters unnormed.  ``gate``: ``[N, 1]`` (a value per token) or ``[hidden]``
     (per channel).  ``x_out`` may be ``x`` (see moe.h)."""
-    return prepare_block_norm(x, y, w_post=w_post, w_pre=w_pre, gate=gate,
-                              residual_scale=residual_scale, eps=eps, x_out=x_out, n_out=n_out,
-                              rstd_post=rstd_post, rstd_pre=rstd_pre, stream=stream)()
+    return _block_norm(x, y, w_post, w_pre, gate, residual_scale, eps, x_out, n_out, rstd_post,
+                       rstd_pre, stream).run()
 
 
-def prepare_block_norm_backward(d_x_out, d_n_out, x, y=None, *, w_post=None, w_pre=None,
-                                gate=None, residual_scale: float = 1.0, rstd_post=None,
-                                rstd_pre=None, d_x=None, d_y=None, d_w_post=None, d_w_pre=None,
-                                d_gate=None, workspace=None, stream=None) -> Prepared:
+def _block_norm_backward(d_x_out, d_n_out, x, y, w_post, w_pre, gate, residual_scale, rstd_post,
+                         rstd_pre, d_x, d_y, d_w_post, d_w_pre, d_gate, workspace,
+                         stream) -> _Call:
     # the gradient takes the saved rstds, so eps no longer matters
-    dev, c = _block_norm_args(x, y, w_post, w_pre, gate, residual_scale, 1.0)
-    n, hidden = x.shape
+    dev, n, hidden, c = _block_norm_args(x, y, w_post, w_pre, gate, residual_scale, 1.0)
     if d_x_out is None and w_pre is None:
         raise ValueError("no gradient flows in: d_x_out or w_pre with d_n_out is needed")
     if (d_n_out is None) != (w_pre is None):
         raise ValueError("d_n_out goes with w_pre")
-    f32 = torch.float32
-    for name, t, shape, dtype, need in (
-            ("d_x_out", d_x_out, (n, hidden), x.dtype, False),
-            ("d_n_out", d_n_out, (n, hidden), x.dtype, False),
-            ("rstd_post", rstd_post, (n,), f32, w_post is not None),
-            ("rstd_pre", rstd_pre, (n,), f32, w_pre is not None)):
-        if t is None and need:
-            raise ValueError(f"{name} of the forward call is needed")
+    dtype, f32 = x.dtype, torch.float32
+    for name, t, shape, dt, need in (("d_x_out", d_x_out, (n, hidden), dtype, None),
+                                     ("d_n_out", d_n_out, (n, hidden), dtype, w_pre),
+                                     ("rstd_post", rstd_post, (n,), f32, w_post),
+                                     ("rstd_pre", rstd_pre, (n,), f32, w_pre)):
         if t is not None:
-            _given(t, shape, dtype, dev, stream, name)
+            _output(t, x, shape, dt, stream, name)
+        elif need is not None:
+            raise ValueError(f"{name} of the forward call is needed")
     for name, t, have in (("d_y", d_y, y), ("d_w_post", d_w_post, w_post),
                           ("d_w_pre", d_w_pre, w_pre), ("d_gate", d_gate, gate)):
         if t is not None and have is None:
             raise ValueError(f"the call has no {name}")
-    res = BlockNormGrads(
-        _given(d_x, (n, hidden), x.dtype, dev, stream, "d_x"),
-        None if y is None else _given(d_y, (n, hidden), x.dtype, dev, stream, "d_y"),
-        None if w_post is None else _given(d_w_post, (hidden,), f32, dev, stream, "d_w_post"),
-        None if w_pre is None else _given(d_w_pre, (hidden,), f32, dev, stream, "d_w_pre"),
-        None if gate is None else _given(d_gate, gate.shape, f32, dev, stream, "d_gate"))
-    need = moe_block_norm_workspace_bytes(n, hidden, x.dtype)
-    ws = _empty((need,), torch.uint8, dev, stream) if workspace is None \
-        else _workspace(workspace, need, dev)
-    _dev(ws)
+    d_x = _output(d_x, x, (n, hidden), dtype, stream, "d_x")
+    if y is not None:
+        d_y = _output(d_y, x, (n, hidden), dtype, stream, "d_y")
+    if w_post is not None:
+        d_w_post = _output(d_w_post, x, (hidden,), f32, stream, "d_w_post")
+    if w_pre is not None:
+        d_w_pre = _output(d_w_pre, x, (hidden,), f32, stream, "d_w_pre")
+    if gate is not None:
+        d_gate = _output(d_gate, x, gate.shape, f32, stream, "d_gate")
+    ws = _scratch(workspace, x, moe_block_norm_workspace_bytes(n, hidden, dtype), stream)
     args = (_ptr(d_x_out), _ptr(d_n_out), x.data_ptr(), _ptr(y), _dt(x), n, hidden,
-            ctypes.byref(c), _ptr(rstd_post), _ptr(rstd_pre), res.d_x.data_ptr(), _ptr(res.d_y),
-            _ptr(res.d_w_post), _ptr(res.d_w_pre), _ptr(res.d_gate), ws.data_ptr(), _nbytes(ws),
-            _stream(dev, stream))
-    return _DevicePrepared(dev, "moe_block_norm_backward", args,
-                           (c, d_x_out, d_n_out, x, y, w_post, w_pre, gate, rstd_post, rstd_pre,
-                            res, ws), res)
+            ctypes.byref(c), _ptr(rstd_post), _ptr(rstd_pre), d_x.data_ptr(), _ptr(d_y),
+            _ptr(d_w_post), _ptr(d_w_pre), _ptr(d_gate), ws.data_ptr(), _nbytes(ws),
+            _raw_stream(dev, stream))
+    res = BlockNormGrads(d_x, d_y, d_w_post, d_w_pre, d_gate)
+    return _Call(dev, "moe_block_norm_backward", args,
+                 (c, d_x_out, d_n_out, x, y, w_post, w_pre, gate, rstd_post, rstd_pre, res, ws),
+                 res)
+
+
+def prepare_block_norm_backward(d_x_out: Optional[torch.Tensor], d_n_out: Optional[torch.Tensor],
+                                x: torch.Tensor, y: Optional[torch.Tensor] = None, *,
+                                w_post: Optional[torch.Tensor] = None,
+                                w_pre: Optional[torch.Tensor] = None,
+                                gate: Optional[torch.Tensor] = None,
+                                residual_scale: float = 1.0,
+                                rstd_post: Optional[torch.Tensor] = None,
+                                rstd_pre: Optional[torch.Tensor] = None,
+                                d_x: Optional[torch.Tensor] = None,
+                                d_y: Optional[torch.Tensor] = None,
+                                d_w_post: Optional[torch.Tensor] = None,
+                                d_w_pre: Optional[torch.Tensor] = None,
+                                d_gate: Optional[torch.Tensor] = None,
+                                workspace: Optional[torch.Tensor] = None,
+                                stream=None) -> Prepared:
+    return _block_norm_backward(d_x_out, d_n_out, x, y, w_post, w_pre, gate, residual_scale,
+                                rstd_post, rstd_pre, d_x, d_y, d_w_post, d_w_pre, d_gate,
+                                workspace, stream).prepared()
 
 
 def moe_block_norm_backward(d_x_out: Optional[torch.Tensor], d_n_out: Optional[torch.Tensor],
@@ -1084,31 +1187,33 @@ def moe_block_norm_backward(d_x_out: Optional[torch.Tensor], d_n_out: Optional[t
     """Gradient of moe_block_norm from the gradients of ``x_out`` (None: zero) and
     ``n_out`` (with ``w_pre``), the forward call's arguments and its rstds.  The
     gradients of the weights and the gate are fp32 (see moe.h)."""
-    return prepare_block_norm_backward(
-        d_x_out, d_n_out, x, y, w_post=w_post, w_pre=w_pre, gate=gate,
-        residual_scale=residual_scale, rstd_post=rstd_post, rstd_pre=rstd_pre, d_x=d_x, d_y=d_y,
-        d_w_post=d_w_post, d_w_pre=d_w_pre, d_gate=d_gate, workspace=workspace, stream=stream)()
+    return _block_norm_backward(d_x_out, d_n_out, x, y, w_post, w_pre, gate, residual_scale,
+                                rstd_post, rstd_pre, d_x, d_y, d_w_post, d_w_pre, d_gate,
+                                workspace, stream).run()
 
 
 # ------------------------------------------------- 4-bit expert weights with group scales
+
+_INT4_GROUPS = (32, 64, 128)
+
 
 def moe_quantize_int4(w: torch.Tensor, group: int = 128, *, zeros: bool = True, stream=None):
     """4-bit weights from ``w [E, rows, K]`` (K a multiple of ``group``, 32, 64 or
     128): returns ``(q [E, rows, K/2] uint8, scales [E, K/group, rows] bf16,
     zeros [E, K/group, rows] uint8)``; the last is None without ``zeros``
     (symmetric codes, see moe.h)."""
-    dev = _dev(w)
+    dev = _index(w)
     if w.dim() != 3:
         raise ValueError("expected w [E, rows, K]")
     e, rows, k = w.shape
-    if group not in (32, 64, 128) or k % group:
+    if group not in _INT4_GROUPS or k % group:
         raise ValueError("group must be 32, 64 or 128 and divide K")
-    q = _empty((e, rows, k // 2), torch.uint8, dev, stream)
-    s = _empty((e, k // group, rows), torch.bfloat16, dev, stream)
-    z = _empty((e, k // group, rows), torch.uint8, dev, stream) if zeros else None
+    q = _output(None, w, (e, rows, k // 2), torch.uint8, stream, "q")
+    s = _output(None, w, (e, k // group, rows), torch.bfloat16, stream, "scales")
+    z = _output(None, w, (e, k // group, rows), torch.uint8, stream, "zeros") if zeros else None
     args = (w.data_ptr(), _dt(w), e, rows, k, group, q.data_ptr(), s.data_ptr(), _ptr(z),
-            _stream(dev, stream))
-    return _DevicePrepared(dev, "moe_quantize_int4", args, (w,), (q, s, z))()
+            _raw_stream(dev, stream))
+    return _Call(dev, "moe_quantize_int4", args, (w,), (q, s, z)).run()
 
 
 def _int4_weights(q, s, z, name: str):
@@ -1116,9 +1221,10 @@ def _int4_weights(q, s, z, name: str):
     if q.dtype != torch.uint8 or s.dtype != torch.bfloat16 or q.dim() != 3 or s.dim() != 3:
         raise TypeError(f"{name}: expected uint8 codes [E, rows, K/2] and bf16 scales "
                         f"[E, K/group, rows]")
-    e, rows, k = q.shape[0], q.shape[1], 2 * q.shape[2]
-    group = k // s.shape[1] if s.shape[1] else 0
-    if group not in (32, 64, 128) or tuple(s.shape) != (e, k // group, rows) or k % group:
+    e, rows, half = q.shape
+    ng, k = s.shape[1], 2 * half
+    group = k // ng if ng else 0
+    if group not in _INT4_GROUPS or k != ng * group or s.shape != (e, ng, rows):
         raise ValueError(f"{name}: scales {tuple(s.shape)} do not give groups of 32, 64 or 128 "
                          f"of codes {tuple(q.shape)}")
     if z is not None and (z.dtype != torch.uint8 or z.shape != s.shape):
@@ -1130,11 +1236,11 @@ def moe_dequantize_int4(q: torch.Tensor, scales: torch.Tensor,
                         zeros: Optional[torch.Tensor] = None, *,
                         out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """bf16 weights ``[E, rows, K]`` of 4-bit codes, scales and zero points."""
-    dev = _dev(*(t for t in (q, scales, zeros) if t is not None))
+    dev = _index(q, scales) if zeros is None else _index(q, scales, zeros)
     e, rows, k, group, c = _int4_weights(q, scales, zeros, "w")
-    out = _given(out, (e, rows, k), torch.bfloat16, dev, stream, "out")
-    args = (ctypes.byref(c), e, rows, k, group, out.data_ptr(), _stream(dev, stream))
-    return _DevicePrepared(dev, "moe_dequantize_int4", args, (c, q, scales, zeros), out)()
+    out = _output(out, q, (e, rows, k), torch.bfloat16, stream, "out")
+    args = (ctypes.byref(c), e, rows, k, group, out.data_ptr(), _raw_stream(dev, stream))
+    return _Call(dev, "moe_dequantize_int4", args, (c, q, scales, zeros), out).run()
 
 
 def moe_int4_workspace_bytes(n_tokens: int, n_experts: int, topk: int, hidden: int,
@@ -1145,9 +1251,9 @@ def moe_int4_workspace_bytes(n_tokens: int, n_experts: int, topk: int, hidden: i
     return b
 
 
-def _int4_args(x, w13, w2, act, layout):
+def _int4_layer(x, w13, w2, act, layout):
     """Checks the layer; returns (device, n, hidden, E, inter, group, structs)."""
-    dev = _dev(x, *(t for t in (*w13, *w2) if t is not None))
+    dev = _index(x, *(t for t in (*w13, *w2) if t is not None))
     if act not in ACTS:
         raise ValueError(f"unknown activation {act!r}")
     if layout not in LAYOUTS:
@@ -1165,25 +1271,36 @@ def _int4_args(x, w13, w2, act, layout):
     return dev, n, hidden, e, inter, group, c13, c2
 
 
-def prepare_experts_int4(x, w13_q, w13_s, w13_z, w2_q, w2_s, w2_z, routing: Routing, act: str,
-                         layout: str = "packed", params: Optional[dict] = None, *, out=None,
-                         workspace=None, stream=None) -> Prepared:
-    w13, w2 = (w13_q, w13_s, w13_z), (w2_q, w2_s, w2_z)
+def _experts_int4(x, w13, w2, routing, act, layout, params, out, workspace, stream) -> _Call:
+    dev, n, hidden, e, inter, group, c13, c2 = _int4_layer(x, w13, w2, act, layout)
     k = routing.topk
-    dev, n, hidden, e, inter, group, c13, c2 = _int4_args(x, w13, w2, act, layout)
-    _check_routing(routing, n, e, k)
-    _dev(x, routing.offsets, routing.col_sorted, routing.row_sorted, routing.gate_scal)
-    out = _given(out, (n, hidden), x.dtype, dev, stream, "out")
-    need = moe_int4_workspace_bytes(n, e, k, hidden, inter)
-    ws = _empty((need,), torch.uint8, dev, stream) if workspace is None \
-        else _workspace(workspace, need, dev)
-    r = routing.as_c()
+    m = n * k
+    for f, size in (("offsets", e + 1), ("col_sorted", m), ("row_sorted", m), ("gate_scal", m)):
+        t = getattr(routing, f)
+        if t.shape != (size,) or t.get_device() != dev or not t.is_contiguous():
+            raise ValueError(f"routing.{f} must be contiguous [{size}] on the GPU of x")
+        if f != "gate_scal" and t.dtype != torch.int32:
+            raise TypeError(f"routing.{f} must be int32")
+    out = _output(out, x, (n, hidden), x.dtype, stream, "out")
+    ws = _scratch(workspace, x, moe_int4_workspace_bytes(n, e, k, hidden, inter), stream)
+    r = N.MoeRouting(None, None, None, None, routing.offsets.data_ptr(),
+                     routing.col_sorted.data_ptr(), routing.row_sorted.data_ptr(),
+                     routing.gate_scal.data_ptr(), _dt(routing.gate_scal))
     p = _params(params)
     args = (x.data_ptr(), n, hidden, ctypes.byref(c13), ctypes.byref(c2), e, inter, k, group,
             ACTS[act], LAYOUTS[layout], ctypes.byref(p) if p else None, ctypes.byref(r),
-            out.data_ptr(), ws.data_ptr(), _nbytes(ws), _stream(dev, stream))
-    return _DevicePrepared(dev, "moe_experts_int4", args,
-                           (r, p, c13, c2, x, w13, w2, out, ws, routing), out)
+            out.data_ptr(), ws.data_ptr(), _nbytes(ws), _raw_stream(dev, stream))
+    return _Call(dev, "moe_experts_int4", args, (r, p, c13, c2, x, w13, w2, out, ws, routing), out)
+
+
+def prepare_experts_int4(x: torch.Tensor, w13_q: torch.Tensor, w13_s: torch.Tensor,
+                         w13_z: Optional[torch.Tensor], w2_q: torch.Tensor, w2_s: torch.Tensor,
+                         w2_z: Optional[torch.Tensor], routing: Routing, act: str,
+                         layout: str = "packed", params: Optional[dict] = None, *,
+                         out: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None, stream=None) -> Prepared:
+    return _experts_int4(x, (w13_q, w13_s, w13_z), (w2_q, w2_s, w2_z), routing, act, layout,
+                         params, out, workspace, stream).prepared()
 
 
 def moe_experts_int4(x: torch.Tensor, w13_q: torch.Tensor, w13_s: torch.Tensor,
@@ -1195,36 +1312,43 @@ def moe_experts_int4(x: torch.Tensor, w13_q: torch.Tensor, w13_s: torch.Tensor,
     """moe_experts with 4-bit expert weights (codes, scales and zero points as
     moe_quantize_int4 gives them, zeros None for symmetric codes); bf16 layer,
     shaped for decode-sized batches (see moe.h)."""
-    return prepare_experts_int4(x, w13_q, w13_s, w13_z, w2_q, w2_s, w2_z, routing, act, layout,
-                                params, out=out, workspace=workspace, stream=stream)()
+    return _experts_int4(x, (w13_q, w13_s, w13_z), (w2_q, w2_s, w2_z), routing, act, layout,
+                         params, out, workspace, stream).run()
 
 
-def prepare_forward_int4(x, logits, w13_q, w13_s, w13_z, w2_q, w2_s, w2_z, topk: int, act: str,
-                         layout: str = "packed", params: Optional[dict] = None, *, out=None,
-                         routing=None, workspace=None, stream=None) -> Prepared:
-    w13, w2 = (w13_q, w13_s, w13_z), (w2_q, w2_s, w2_z)
-    dev, n, hidden, e, inter, group, c13, c2 = _int4_args(x, w13, w2, act, layout)
-    _dev(x, logits)
+def _forward_int4(x, logits, w13, w2, topk, act, layout, params, out, routing, workspace,
+                  stream) -> _Call:
+    dev, n, hidden, e, inter, group, c13, c2 = _int4_layer(x, w13, w2, act, layout)
+    _index(x, logits)
     if logits.dtype != x.dtype or tuple(logits.shape) != (n, e):
         raise ValueError("logits must be [N, E] in the layer dtype")
     if routing is None:
         if stream is None:
-            routing = Routing.empty(n, e, topk, x.dtype, dev)
+            routing = Routing.empty(n, e, topk, x.dtype, x.device)
         else:
             with torch.cuda.stream(stream):
-                routing = Routing.empty(n, e, topk, x.dtype, dev)
+                routing = Routing.empty(n, e, topk, x.dtype, x.device)
     _check_routing(routing, n, e, topk)
-    out = _given(out, (n, hidden), x.dtype, dev, stream, "out")
-    need = moe_int4_workspace_bytes(n, e, topk, hidden, inter)
-    ws = _empty((need,), torch.uint8, dev, stream) if workspace is None \
-        else _workspace(workspace, need, dev)
+    _index(x, *(getattr(routing, f.name) for f in fields(routing)))
+    out = _output(out, x, (n, hidden), x.dtype, stream, "out")
+    ws = _scratch(workspace, x, moe_int4_workspace_bytes(n, e, topk, hidden, inter), stream)
     r = routing.as_c()
     p = _params(params)
     args = (x.data_ptr(), logits.data_ptr(), n, hidden, ctypes.byref(c13), ctypes.byref(c2), e,
             inter, topk, group, ACTS[act], LAYOUTS[layout], ctypes.byref(p) if p else None,
-            ctypes.byref(r), out.data_ptr(), ws.data_ptr(), _nbytes(ws), _stream(dev, stream))
-    return _DevicePrepared(dev, "moe_forward_int4", args,
-                           (r, p, c13, c2, x, logits, w13, w2, out, ws, routing), (out, routing))
+            ctypes.byref(r), out.data_ptr(), ws.data_ptr(), _nbytes(ws), _raw_stream(dev, stream))
+    return _Call(dev, "moe_forward_int4", args,
+                 (r, p, c13, c2, x, logits, w13, w2, out, ws, routing), (out, routing))
+
+
+def prepare_forward_int4(x: torch.Tensor, logits: torch.Tensor, w13_q: torch.Tensor,
+                         w13_s: torch.Tensor, w13_z: Optional[torch.Tensor], w2_q: torch.Tensor,
+                         w2_s: torch.Tensor, w2_z: Optional[torch.Tensor], topk: int, act: str,
+                         layout: str = "packed", params: Optional[dict] = None, *,
+                         out: Optional[torch.Tensor] = None, routing: Optional[Routing] = None,
+                         workspace: Optional[torch.Tensor] = None, stream=None) -> Prepared:
+    return _forward_int4(x, logits, (w13_q, w13_s, w13_z), (w2_q, w2_s, w2_z), topk, act, layout,
+                         params, out, routing, workspace, stream).prepared()
 
 
 def moe_forward_int4(x: torch.Tensor, logits: torch.Tensor, w13_q: torch.Tensor,
@@ -1234,6 +1358,5 @@ def moe_forward_int4(x: torch.Tensor, logits: torch.Tensor, w13_q: torch.Tensor,
                      out: Optional[torch.Tensor] = None, routing: Optional[Routing] = None,
                      workspace: Optional[torch.Tensor] = None, stream=None):
     """Routing then the 4-bit experts on one stream; returns ``(out, routing)``."""
-    return prepare_forward_int4(x, logits, w13_q, w13_s, w13_z, w2_q, w2_s, w2_z, topk, act,
-                                layout, params, out=out, routing=routing, workspace=workspace,
-                                stream=stream)()
+    return _forward_int4(x, logits, (w13_q, w13_s, w13_z), (w2_q, w2_s, w2_z), topk, act, layout,
+                         params, out, routing, workspace, stream).run()

@@ -332,9 +332,18 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(const float *__restric
   float *o = which == 0 ? out.d_w_pre : which == 1 ? out.d_w_post : out.d_gate;
   if (!o) return;  // the same for the whole workgroup
   float s = 0.f;
-  if (col < H)
-    for (int b = wave; b < blocks; b += 16)
-      s += partial[((int64_t)which * blocks + b) * H + col];
+  if (col < H) {
+    const float *p = partial + (int64_t)which * blocks * H + col;
+    int b = wave;
+    for (; b + 16 * 7 < blocks; b += 16 * 8) {  // eight loads in flight
+      float v[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] = p[(int64_t)(b + 16 * q) * H];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) s += v[q];
+    }
+    for (; b < blocks; b += 16) s += p[(int64_t)b * H];
+  }
   part[wave][lane] = s;
   __syncthreads();
   if (wave == 0 && col < H) {

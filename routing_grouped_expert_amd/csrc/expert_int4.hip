@@ -33,10 +33,29 @@
 #include "lds_dma.h"
 #include "rows.h"
 
+#include <type_traits>
+
 namespace moe {
 namespace {
 
-constexpr int kWaves = 4;
+#ifndef WPE
+#define WPE 4
+#endif
+#ifndef RULE4
+#define RULE4 2
+#endif
+#ifndef NWG
+#define NWG 2048
+#endif
+#ifndef KS4G
+#define KS4G 1024
+#endif
+#ifndef KS2G
+#define KS2G 4096
+#endif
+#ifndef LDSB
+#define LDSB 65536
+#endif
 
 struct Int4Args {
   const void *A;               // w13: x [N, K]; w2: activation rows [M, K]
@@ -53,34 +72,62 @@ struct Int4Args {
 };
 
 // Eight codes of a dword (element i in nibble i) as bf16 128 + q, in the order
-// (0, 4), (1, 5), (2, 6), (3, 7) that token_order gives the token rows.
-__device__ __forceinline__ bf16x8_t codes_plus_128(uint32_t w) {
+// (0, 4), (1, 5), (2, 6), (3, 7) that token_order gives the token rows: a shift
+// and one v_and_or_b32 for two codes.  mask and magic are 0x000f000f and
+// 0x43004300 in registers (known constants become an AND and an OR instead).
+__device__ __forceinline__ bf16x8_t codes_plus_128(uint32_t w, uint32_t mask, uint32_t magic) {
   u32x4_t v;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+  for (int i = 0; i < 4; ++i) v[i] = ((w >> (4 * i)) & mask) | magic;
   return __builtin_bit_cast(bf16x8_t, v);
 }
-__device__ __forceinline__ bf16x8_t token_order(u32x4_t a) {
+__device__ __forceinline__ u32x4_t token_order(u32x4_t a) {
   u32x4_t v;
   v[0] = __builtin_amdgcn_perm(a[2], a[0], 0x05040100u);  // low halves: elements 0, 4
   v[1] = __builtin_amdgcn_perm(a[2], a[0], 0x07060302u);  // high halves: 1, 5
   v[2] = __builtin_amdgcn_perm(a[3], a[1], 0x05040100u);
   v[3] = __builtin_amdgcn_perm(a[3], a[1], 0x07060302u);
-  return __builtin_bit_cast(bf16x8_t, v);
+  return v;
 }
 
-// Dword d of lane group c (of four groups of 16 lanes) becomes dword c of lane
-// group d.
-__device__ __forceinline__ void transpose_groups(u32x4_t &v) {
-  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-  const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(v[0], v[2], false, false));
-  const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(v[1], v[3], false, false));
-  const u32x2 c = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false));
-  const u32x2 d = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false));
-  v[0] = c[0];
-  v[1] = c[1];
-  v[2] = d[0];
-  v[3] = d[1];
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ u32x2_t swap32(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane32_swap(a, b, false, false));
+}
+__device__ __forceinline__ u32x2_t swap16(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane16_swap(a, b, false, false));
+}
+
+// Four dwords of lane group c (of four groups of 16 lanes) are 32 weights of
+// piece c.  For groups of 128 weights they stay: product j takes dword j of
+// all four pieces.  For 64 the halves are exchanged, so that products 0 and 1
+// take pieces 0 and 1 (lane group h: piece h % 2, dword 2 (h / 2) + j % 2) and
+// 2 and 3 the other two.  For 32, the full transpose: product j takes piece j
+// (lane group h: dword h).
+template <int GS> __device__ __forceinline__ void arrange(u32x4_t &v) {
+  if constexpr (GS < 4) {
+    const u32x2_t a = swap32(v[0], v[2]), b = swap32(v[1], v[3]);
+    if constexpr (GS == 2) {
+      v = u32x4_t{a[0], b[0], a[1], b[1]};
+    } else {
+      const u32x2_t c = swap16(a[0], b[0]), d = swap16(a[1], b[1]);
+      v = u32x4_t{c[0], c[1], d[0], d[1]};
+    }
+  }
+}
+// The 8-weight piece of a 128-weight block that lane group h gives product j.
+template <int GS> __device__ __forceinline__ int eighth(int j, int h) {
+  return GS == 4 ? 4 * h + j : GS == 2 ? 8 * (j >> 1) + 4 * (h & 1) + 2 * (h >> 1) + (j & 1)
+                                       : 4 * j + h;
+}
+
+// Sends lane group i's value to every lane, for i = 0 .. 3.
+__device__ __forceinline__ void spread_groups(uint32_t v, uint32_t (&out)[4]) {
+  const u32x2_t a = swap32(v, v), b = swap16(a[0], a[0]), c = swap16(a[1], a[1]);
+  out[0] = b[0];
+  out[1] = b[1];
+  out[2] = c[0];
+  out[3] = c[1];
 }
 
 // The blockIdx.y-th expert with rows and its range of sorted rows, found by
@@ -111,30 +158,48 @@ __device__ __forceinline__ void find_expert(const int32_t *offsets, int E, int w
   __syncthreads();
 }
 
-// GS = G / 32; NT: tiles of 16 token rows held at a time.
-template <int NSETS, int EPI, int GS, int NT>
-__global__ __launch_bounds__(64 * kWaves) void expert_int4_kernel(Int4Args g) {
+// The workgroup's place among all, so that neighbouring column tiles, which
+// share cache lines of the scales and zero points, run on one XCD (workgroups
+// go to the eight XCDs in turn).
+__device__ __forceinline__ void place(int &x, int &y) {
+  const uint32_t gx = gridDim.x, total = gx * gridDim.y, lin = blockIdx.y * gx + blockIdx.x;
+  const uint32_t per = total / 8, rest = total % 8, xcd = lin % 8;
+  const uint32_t at = xcd * per + min(xcd, rest) + lin / 8;
+  x = (int)(at % gx);
+  y = (int)(at / gx);
+}
+
+constexpr int kStepK = 256;  // weights of a row a step: one 128-byte line of codes
+
+// GS = G / 32; TR: token rows held at a time.  A wave streams 32 weight rows;
+// ks waves share them and split the steps; the workgroup's waves / ks column
+// groups share the token rows in LDS, kc values of each at a time.
+template <int EPI, int GS, int TR>
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(WPE))) void
+expert_int4_kernel(Int4Args g, int ks, int kc) {
+  constexpr int NM = GS == 1 ? 2 : 1;  // loads of four groups' scales a step and tile
+  constexpr bool kPlain = EPI == EPI_Y || EPI == EPI_OUT || EPI == EPI_RELU2;
+  constexpr int COLS = kPlain ? 32 : 16;  // output columns of a wave's 32 weight rows
   __shared__ int sel[3];
-  __shared__ float red[kWaves][NSETS][NT][16][17];
-  find_expert(g.offsets, g.E, (int)blockIdx.y, sel);
+  extern __shared__ __attribute__((aligned(16))) char lds[];  // [TR][kc] bf16; then the parts
+  int place_x, want;
+  place(place_x, want);
+  find_expert(g.offsets, g.E, want, sel);
   const int e = __builtin_amdgcn_readfirstlane(sel[0]);
   if (e < 0) return;  // the whole workgroup
   const int row0 = __builtin_amdgcn_readfirstlane(sel[1]);
   const int cnt = __builtin_amdgcn_readfirstlane(sel[2]);
 
-  const int lane = threadIdx.x & 63;
+  const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, h = lane >> 4;  // this lane's row in a tile, its lane group
-  const int K = g.K, Nout = g.Nout, nrows = NSETS * Nout;
-  const int n0 = (int)blockIdx.x * 16;
-  const int nblk = (K + 127) / 128, per = (nblk + kWaves - 1) / kWaves;
-  const int b0 = wave * per, b1 = min(b0 + per, nblk);
+  const int K = g.K, Nout = g.Nout, nrows = kPlain ? Nout : 2 * Nout;
+  const int cg = wave / ks, kw = wave % ks;  // column group, share of the steps
+  const int n0 = (place_x * (waves / ks) + cg) * COLS;
+  const bool live = n0 < Nout;  // (the last workgroup's last groups may be past the last column)
 
-  // this expert's weights (Nout is a multiple of 32); a group past K reads
-  // zeros: code 0 and zero point 0 are a weight of 128 - 128, and scale 0
   const uint32_t qbytes = (uint32_t)nrows * (uint32_t)(K / 2);
-  const uint32_t groups = (uint32_t)(K / (32 * GS));
-  const uint32_t sn = groups * (uint32_t)nrows;
+  const uint32_t sn = (uint32_t)(K / (32 * GS)) * (uint32_t)nrows;
   const __amdgpu_buffer_rsrc_t rq = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<uint8_t *>(g.q) + (size_t)e * qbytes, (short)0, (int)qbytes, kRsrcWord3);
   const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
@@ -142,113 +207,174 @@ __global__ __launch_bounds__(64 * kWaves) void expert_int4_kernel(Int4Args g) {
   const __amdgpu_buffer_rsrc_t rz = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<uint8_t *>(g.z) + (g.z ? (size_t)e * sn : 0), (short)0, g.z ? (int)sn : 0,
       kRsrcWord3);
-  const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<void *>(g.A), (short)0, (int)g.a_bytes, kRsrcWord3);
-  uint32_t wrow[NSETS];
-#pragma unroll
-  for (int s = 0; s < NSETS; ++s)
-    wrow[s] = NSETS == 1 ? n0 + r : g.interleaved ? 2 * (n0 + r) + s : s * Nout + n0 + r;
 
-  for (int a0 = 0; a0 < cnt; a0 += 16 * NT) {
-    uint32_t arow[NT];  // byte offset of this lane's token row in each tile
+  // Memory row of row x of tile t.  Gated: tile 0 the gate rows of 16 columns,
+  // tile 1 their up rows; plain: two runs of 16 columns.
+  auto memrow = [&](int t, int x) {
+    return kPlain ? n0 + 16 * t + x : g.interleaved ? 2 * (n0 + x) + t : t * Nout + n0 + x;
+  };
+  // Byte offsets, less the step's.  Codes: four lanes a row, 64 bytes; a lane
+  // swap puts them where the products want them.  Scales and zero points: lane
+  // group h loads the step's groups h (and h + 4).  Loads past K bring other
+  // rows' data, or zeros past the array's end; they are not used.
+  uint32_t qoff[2], moff[2];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int i = a0 + 16 * t + r;
-      uint32_t row = 0;
-      if (i < cnt) row = g.gather ? (uint32_t)g.col_sorted[row0 + i] / (uint32_t)g.topk : row0 + i;
-      arow[t] = i < cnt ? row * (uint32_t)(2 * K) : kOOB;
-    }
-    f32x4_t acc[NSETS][NT];
-#pragma unroll
-    for (int s = 0; s < NSETS; ++s)
-#pragma unroll
-      for (int t = 0; t < NT; ++t) acc[s][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int t = 0; t < 2; ++t) {
+    qoff[t] = (uint32_t)memrow(t, lane >> 2) * (uint32_t)(K / 2) + (uint32_t)((lane & 3) * 16);
+    moff[t] = (uint32_t)h * (uint32_t)nrows + (uint32_t)memrow(t, r);
+  }
+  const int from = (4 * r + h) * 4;  // lane (of four bytes each) that loaded what this one needs
+  uint32_t magic = 0x43004300u, mask = 0x000f000fu;
+  asm("" : "+v"(magic));  // (no instruction: hides the values, see codes_plus_128)
+  asm("" : "+s"(mask));
+  const bf16x8_t ones = __builtin_bit_cast(
+      bf16x8_t, u32x4_t{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u});
 
-    for (int b = b0; b < b1; ++b) {
-      u32x4_t cw[NSETS], tok[NT][4];
-      uint32_t sc[NSETS][4 / GS], zp[NSETS][4 / GS];
+  struct Codes {  // a step of this wave's rows
+    u32x4_t w[2][2];
+    uint32_t s[2][NM], z[2][NM];
+  };
+  auto load = [&](Codes &c, int step) {
+    const uint32_t k0 = (uint32_t)step * kStepK;
+    const uint32_t g0 = k0 / (32 * GS) * (uint32_t)nrows;
 #pragma unroll
-      for (int s = 0; s < NSETS; ++s) {
-        const int k = b * 128 + h * 32;
-        const uint32_t off =
-            k < K ? wrow[s] * (uint32_t)(K / 2) + (uint32_t)(k / 2) : kOOB;
-        cw[s] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rq, (int)off, 0, 0));
+    for (int t = 0; t < 2; ++t) {
 #pragma unroll
-        for (int i = 0; i < 4 / GS; ++i) {
-          const uint32_t gi = (uint32_t)(b * (4 / GS) + i);
-          const uint32_t at = gi < groups ? gi * (uint32_t)nrows + wrow[s] : kOOB / 2;
-          sc[s][i] = (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, (int)(2 * at), 0, 0);
-          zp[s][i] = g.z ? (uint32_t)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rz, (int)at, 0, 0)
-                     : gi < groups ? 8u : 0u;
-        }
+      for (int b = 0; b < 2; ++b)
+        c.w[t][b] = __builtin_bit_cast(
+            u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rq, (int)(qoff[t] + k0 / 2 + 64 * b), 0, 0));
+#pragma unroll
+      for (int m = 0; m < NM; ++m) {
+        const uint32_t at = moff[t] + g0 + 4 * m * (uint32_t)nrows;
+        c.s[t][m] = (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, (int)(2 * at), 0, 0);
+        c.z[t][m] =
+            g.z ? (uint32_t)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rz, (int)at, 0, 0) : 8u;
       }
+    }
+  };
+
+  const int rowb = 2 * kc;  // bytes of a token row in LDS (a multiple of 128)
+  for (int a0 = 0; a0 < cnt; a0 += TR) {
+    const int na = min(TR, cnt - a0);
+    f32x4_t acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    for (int kb = 0; kb < K; kb += kc) {
+      const int klen = min(kc, K - kb);
+      const int s0 = kb / kStepK, ns = (klen + kStepK - 1) / kStepK, per = (ns + ks - 1) / ks;
+      const int first = s0 + min(kw * per, ns), last = live ? s0 + min(kw * per + per, ns) : first;
+      Codes c0, c1;
+      if (first < last) load(c0, first);
+      // token rows: 16-byte piece c of row x at place c ^ (x % 8)
+      if (a0 > 0 || kb > 0) __syncthreads();
+      const int np = klen / 8;
+      for (int i = threadIdx.x; i < na * np; i += blockDim.x) {
+        const int x = i / np, c = i - x * np, p = row0 + a0 + x;
+        const int row = g.gather ? g.col_sorted[p] / g.topk : p;
+        const u32x4_t v = *reinterpret_cast<const u32x4_t *>(
+            reinterpret_cast<const bf16_t *>(g.A) + (size_t)row * K + kb + 8 * c);
+        *reinterpret_cast<u32x4_t *>(lds + x * rowb + ((c ^ (x & 7)) * 16)) = token_order(v);
+      }
+      __syncthreads();
+
+      // The products of one step; with kWhole = false only the groups ahead of K.
+      const int x = r % TR;  // rows past the expert's last hold anything: their sums are not used
+      auto work = [&](auto whole, const Codes &c, int step) {
+        constexpr bool kWhole = decltype(whole)::value;
+        const char *tok = lds + x * rowb + (step - s0) * (2 * kStepK);
+        const int ngroups = kWhole ? 8 / GS : (K - step * kStepK) / (32 * GS);
+        uint32_t mt[2][4 * NM];  // scale << 16 | zero point of each group
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int k = b * 128 + i * 32 + h * 8;
-          const uint32_t off = arow[t] != kOOB && k < K ? arow[t] + (uint32_t)(2 * k) : kOOB;
-          tok[t][i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(ra, (int)off, 0, 0));
-        }
+          for (int m = 0; m < NM; ++m) {
+            uint32_t v[4];
+            spread_groups(c.s[t][m] << 16 | c.z[t][m], v);
 #pragma unroll
-      for (int s = 0; s < NSETS; ++s) transpose_groups(cw[s]);
-      f32x4_t sum[NSETS][NT];
+            for (int q = 0; q < 4; ++q) mt[t][4 * m + q] = v[q];
+          }
+        f32x4_t sum[2], tot;
+        const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+        for (int b = 0; b < 2; ++b) {
+          u32x4_t cw[2];
 #pragma unroll
-        for (int s = 0; s < NSETS; ++s) {
-          const uint32_t zz = zp[s][i / GS] * 0x00010001u | 0xc300c300u;
-          const bf16x8_t wz = __builtin_bit_cast(bf16x8_t, u32x4_t{zz, zz, zz, zz});
-          const bf16x8_t wv = codes_plus_128(cw[s][i]);
+          for (int t = 0; t < 2; ++t) {
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            const bf16x8_t av = token_order(tok[t][i]);
-            if (i % GS == 0) sum[s][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-            sum[s][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, wv, sum[s][t], 0, 0, 0);
-            sum[s][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, wz, sum[s][t], 0, 0, 0);
-            if (i % GS == GS - 1) {
-              const float f = __uint_as_float(sc[s][i / GS] << 16);
+            for (int q = 0; q < 4; ++q)
+              cw[t][q] = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)c.w[t][b][q]);
+            arrange<GS>(cw[t]);
+          }
 #pragma unroll
-              for (int q = 0; q < 4; ++q) acc[s][t][q] = fmaf(f, sum[s][t][q], acc[s][t][q]);
+          for (int j = 0; j < 4; ++j) {
+            const int gr = (4 * b + j) / GS;
+            if (!kWhole && gr >= ngroups) break;
+            const bf16x8_t av = *reinterpret_cast<const bf16x8_t *>(
+                tok + 256 * b + ((eighth<GS>(j, h) ^ (x & 7)) * 16));
+            const bool begins = j % GS == 0;
+            tot = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, ones, begins ? zero : tot, 0, 0, 0);
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+              sum[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                  av, codes_plus_128(cw[t][j], mask, magic), begins ? zero : sum[t], 0, 0, 0);
+            if (j % GS == GS - 1) {
+#pragma unroll
+              for (int t = 0; t < 2; ++t) {
+                const float f = __uint_as_float(mt[t][gr] & 0xffff0000u);
+                const float z = 128.f + (float)(mt[t][gr] & 0xffu);
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                  acc[t][q] = fmaf(f, fmaf(-z, tot[q], sum[t][q]), acc[t][q]);
+              }
             }
           }
         }
+      };
+      auto run = [&](const Codes &c, int step) {
+        if ((step + 1) * kStepK <= K) work(std::true_type(), c, step);
+        else work(std::false_type(), c, step);
+      };
+      for (int step = first; step < last; step += 2) {
+        if (step + 1 < last) load(c1, step + 1);
+        run(c0, step);
+        if (step + 1 < last) {
+          if (step + 2 < last) load(c0, step + 2);
+          run(c1, step + 1);
+        }
       }
     }
 
-    // the waves' parts: lane (h, r) holds column r of token rows 4 h .. 4 h + 3
-    if (a0 > 0) __syncthreads();
-#pragma unroll
-    for (int s = 0; s < NSETS; ++s)
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) red[wave][s][t][4 * h + q][r] = acc[s][t][q];
+    // the waves' parts, through LDS that the token rows no longer need: lane
+    // (h, r) holds row r of a tile for token rows 4 h .. 4 h + 3
+    float *red = reinterpret_cast<float *>(lds);  // [wave][tile][TR token rows][17]
     __syncthreads();
-    const int col = threadIdx.x & 15, trow = threadIdx.x >> 4;
+    if (4 * h < TR) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int i = a0 + 16 * t + trow;
-      if (i >= cnt) continue;
-      float v[NSETS];
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int s = 0; s < NSETS; ++s) {
-        v[s] = red[0][s][t][trow][col];
-#pragma unroll
-        for (int w = 1; w < kWaves; ++w) v[s] += red[w][s][t][trow][col];
-      }
-      const size_t p = (size_t)(row0 + i);
+        for (int q = 0; q < 4; ++q) red[((wave * 2 + t) * TR + 4 * h + q) * 17 + r] = acc[t][q];
+    }
+    __syncthreads();
+    for (int i = kw * 64 + lane; i < na * COLS && live; i += ks * 64) {
+      const int col = i % COLS, trow = i / COLS;
+      auto part = [&](int t, int c) {
+        float v = 0.f;
+        for (int w = cg * ks; w < cg * ks + ks; ++w) v += red[((w * 2 + t) * TR + trow) * 17 + c];
+        return v;
+      };
+      const size_t p = (size_t)(row0 + a0 + trow);
       if constexpr (EPI == EPI_Y || EPI == EPI_OUT) {
-        const float y = v[0] * weight_at(g.gate_scal, g.gate_bf16, (int64_t)p);
+        const float y =
+            part(col >> 4, col & 15) * weight_at(g.gate_scal, g.gate_bf16, (int64_t)p);
         if (EPI == EPI_Y)  // summed over the slots by sum_slots_kernel, in fp32
           reinterpret_cast<float *>(g.C)[p * Nout + n0 + col] = y;
         else               // one slot a token: entry == token
           reinterpret_cast<bf16_t *>(g.C)[(size_t)g.col_sorted[p] * Nout + n0 + col] = bf16_rne(y);
       } else {
+        const float v0 = part(kPlain ? col >> 4 : 0, col & 15);
+        const float v1 = kPlain ? v0 : part(1, col & 15);
         const float nal = -g.prm.alpha * 1.44269504088896341f;
-        float a = act_val<EPI>(v[0], v[NSETS - 1], nal, g.prm);
+        float a = act_val<EPI>(v0, v1, nal, g.prm);
         // the clamps and the rectifier drop a NaN; the token's row shall show it
-        if (__builtin_isnan(v[0]) || __builtin_isnan(v[NSETS - 1])) a = __builtin_nanf("");
+        if (__builtin_isnan(v0) || __builtin_isnan(v1)) a = __builtin_nanf("");
         reinterpret_cast<bf16_t *>(g.C)[p * Nout + n0 + col] = bf16_rne(a);
       }
     }
@@ -282,22 +408,36 @@ __global__ __launch_bounds__(256) void sum_slots_kernel(const float *__restrict_
   *reinterpret_cast<u32x4_t *>(out + t * H + c) = pack(acc);
 }
 
-template <int NSETS, int EPI, int GS>
-void launch_tiles(const Int4Args &a, int64_t n_tokens, int64_t M, hipStream_t s) {
-  const dim3 grid((unsigned)(a.Nout / 16), (unsigned)(M < a.E ? M : a.E));
-  // an expert holds at most one row a token
-  if (n_tokens <= 16)
-    hipLaunchKernelGGL((expert_int4_kernel<NSETS, EPI, GS, 1>), grid, dim3(64 * kWaves), 0, s, a);
-  else
-    hipLaunchKernelGGL((expert_int4_kernel<NSETS, EPI, GS, 2>), grid, dim3(64 * kWaves), 0, s, a);
+template <int EPI, int GS, int TR>
+void launch_rows(const Int4Args &a, int64_t M, hipStream_t s) {
+  const int nstep = (a.K + kStepK - 1) / kStepK;
+  const int cols = EPI == EPI_Y || EPI == EPI_OUT || EPI == EPI_RELU2 ? 32 : 16;
+  const int64_t experts = M < a.E ? M : a.E, groups = (a.Nout / cols) * experts;
+  const int waves = groups < NWG ? 4 : 8;
+  const int ks = groups < KS4G ? 4 : groups < KS2G ? 2 : 1;
+  const int wide = cols * (waves / ks);
+  // token rows in LDS: all of K, or equal parts of it in whole steps
+  const int most = LDSB / (2 * TR), parts = (a.K + most - 1) / most;
+  const int kc = ((nstep + parts - 1) / parts) * kStepK;
+  const size_t rows = (size_t)TR * kc * 2, red = sizeof(float) * waves * 2 * TR * 17;
+  hipLaunchKernelGGL((expert_int4_kernel<EPI, GS, TR>),
+                     dim3((unsigned)((a.Nout + wide - 1) / wide), (unsigned)experts),
+                     dim3(64 * waves), rows > red ? rows : red, s, a, ks, kc);
 }
 
-template <int NSETS, int EPI>
+template <int EPI, int GS>
+void launch_tiles(const Int4Args &a, int64_t n_tokens, int64_t M, hipStream_t s) {
+  // an expert holds at most one row a token
+  if (n_tokens <= 4 || M <= RULE4 * a.E) launch_rows<EPI, GS, 4>(a, M, s);
+  else launch_rows<EPI, GS, 16>(a, M, s);
+}
+
+template <int EPI>
 hipError_t launch_groups(const Int4Args &a, int group, int64_t n_tokens, int64_t M,
                          hipStream_t s) {
-  if (group == 32) launch_tiles<NSETS, EPI, 1>(a, n_tokens, M, s);
-  else if (group == 64) launch_tiles<NSETS, EPI, 2>(a, n_tokens, M, s);
-  else launch_tiles<NSETS, EPI, 4>(a, n_tokens, M, s);
+  if (group == 32) launch_tiles<EPI, 1>(a, n_tokens, M, s);
+  else if (group == 64) launch_tiles<EPI, 2>(a, n_tokens, M, s);
+  else launch_tiles<EPI, 4>(a, n_tokens, M, s);
   return hipGetLastError();
 }
 
@@ -373,17 +513,17 @@ hipError_t launch_experts_int4(const Int4Weights &w13, const Int4Weights &w2, co
              (uint32_t)(n_tokens * hidden * 2), 0, n_experts, hidden, inter, topk, 1,
              layout == MOE_W13_INTERLEAVED, prm};
   const bool clamp = __builtin_isfinite(prm.limit);
-  hipError_t err = kind == MOE_ACT_RELU2 ? launch_groups<1, EPI_RELU2>(a, group, n_tokens, M, s)
-                   : clamp ? launch_groups<2, EPI_GATED_CLAMP>(a, group, n_tokens, M, s)
-                           : launch_groups<2, EPI_GATED>(a, group, n_tokens, M, s);
+  hipError_t err = kind == MOE_ACT_RELU2 ? launch_groups<EPI_RELU2>(a, group, n_tokens, M, s)
+                   : clamp ? launch_groups<EPI_GATED_CLAMP>(a, group, n_tokens, M, s)
+                           : launch_groups<EPI_GATED>(a, group, n_tokens, M, s);
   if (err != hipSuccess) return err;
   const bool direct = topk == 1;
   Int4Args b{act, reinterpret_cast<const uint8_t *>(w2.q), reinterpret_cast<const bf16_t *>(w2.s),
              reinterpret_cast<const uint8_t *>(w2.z), direct ? out : y, r->offsets, r->col_sorted,
              r->gate_scal, (uint32_t)(M * inter * 2), r->w_dtype == MOE_BF16, n_experts, inter,
              hidden, topk, 0, 0, prm};
-  if (direct) return launch_groups<1, EPI_OUT>(b, group, n_tokens, M, s);
-  if ((err = launch_groups<1, EPI_Y>(b, group, n_tokens, M, s)) != hipSuccess) return err;
+  if (direct) return launch_groups<EPI_OUT>(b, group, n_tokens, M, s);
+  if ((err = launch_groups<EPI_Y>(b, group, n_tokens, M, s)) != hipSuccess) return err;
   const int64_t total = n_tokens * (hidden / 8);
   hipLaunchKernelGGL(sum_slots_kernel, dim3((unsigned)((total + 255) / 256)), dim3(256), 0, s,
                      reinterpret_cast<const float *>(y), r->row_sorted,

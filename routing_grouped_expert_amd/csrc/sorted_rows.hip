@@ -37,7 +37,41 @@ __device__ __forceinline__ bool own_chunk(int64_t n, int nch, int64_t &t, int &c
   return t < n;
 }
 
-template <typename T>
+#ifndef NTL
+#define NTL 1
+#endif
+#ifndef NTS
+#define NTS 1
+#endif
+template <typename T> __device__ __forceinline__ u32x4_t load16(const T *p) {
+#if NTL
+  return __builtin_nontemporal_load(reinterpret_cast<const u32x4_t *>(p));
+#else
+  return *reinterpret_cast<const u32x4_t *>(p);
+#endif
+}
+template <typename T> __device__ __forceinline__ void store16(T *p, u32x4_t v) {
+#if NTS
+  __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t *>(p));
+#else
+  *reinterpret_cast<u32x4_t *>(p) = v;
+#endif
+}
+
+// Positions of the slots j0 .. j0 + JB - 1 of token t; kNone past the last
+// slot and for slots that point nowhere.
+constexpr uint32_t kNone = 0xffffffffu;
+template <int JB>
+__device__ __forceinline__ void slot_rows(const int32_t *__restrict__ row_sorted, int64_t t, int K,
+                                          int j0, uint32_t M, uint32_t (&p)[JB]) {
+#pragma unroll
+  for (int j = 0; j < JB; ++j) {
+    p[j] = j0 + j < K ? (uint32_t)row_sorted[t * K + j0 + j] : kNone;
+    if (p[j] >= M) p[j] = kNone;
+  }
+}
+
+template <typename T, int JB>
 __global__ __launch_bounds__(kThreads) void dispatch_kernel(const T *__restrict__ x,
                                                             const int32_t *__restrict__ row_sorted,
                                                             T *__restrict__ xs, int64_t N, int K,
@@ -46,15 +80,17 @@ __global__ __launch_bounds__(kThreads) void dispatch_kernel(const T *__restrict_
   int64_t t;
   int c;
   if (!own_chunk(N, H / CH, t, c)) return;
-  const uint32_t M = (uint32_t)(N * K);
-  const u32x4_t v = *reinterpret_cast<const u32x4_t *>(x + t * H + (int64_t)c * CH);
-  for (int j = 0; j < K; ++j) {
-    const uint32_t p = (uint32_t)row_sorted[t * K + j];
-    if (p < M) *reinterpret_cast<u32x4_t *>(xs + (int64_t)p * H + (int64_t)c * CH) = v;
+  const u32x4_t v = load16(x + t * H + (int64_t)c * CH);
+  for (int j0 = 0; j0 < K; j0 += JB) {
+    uint32_t p[JB];
+    slot_rows<JB>(row_sorted, t, K, j0, (uint32_t)(N * K), p);
+#pragma unroll
+    for (int j = 0; j < JB; ++j)
+      if (p[j] != kNone) store16(xs + (int64_t)p[j] * H + (int64_t)c * CH, v);
   }
 }
 
-template <typename T>
+template <typename T, int JB>
 __global__ __launch_bounds__(kThreads) void combine_weighted_kernel(
     const T *__restrict__ y, const int32_t *__restrict__ row_sorted, const void *__restrict__ w,
     bool w_bf16, T *__restrict__ out, int64_t N, int K, int H) {
@@ -62,55 +98,94 @@ __global__ __launch_bounds__(kThreads) void combine_weighted_kernel(
   int64_t t;
   int c;
   if (!own_chunk(N, H / CH, t, c)) return;
-  const uint32_t M = (uint32_t)(N * K);
   float acc[CH];
 #pragma unroll
   for (int i = 0; i < CH; ++i) acc[i] = 0.f;
-  for (int j = 0; j < K; ++j) {
-    const uint32_t p = (uint32_t)row_sorted[t * K + j];
-    if (p < M) {
-      const float wj = weight_at(w, w_bf16, t * K + j);
-      float f[CH];
-      unpack(*reinterpret_cast<const u32x4_t *>(y + (int64_t)p * H + (int64_t)c * CH), f);
+  for (int j0 = 0; j0 < K; j0 += JB) {
+    uint32_t p[JB];
+    slot_rows<JB>(row_sorted, t, K, j0, (uint32_t)(N * K), p);
+    u32x4_t v[JB];
+    float wj[JB];
 #pragma unroll
-      for (int i = 0; i < CH; ++i) acc[i] = fmaf(wj, f[i], acc[i]);
+    for (int j = 0; j < JB; ++j) {
+      wj[j] = p[j] != kNone ? weight_at(w, w_bf16, t * K + j0 + j) : 0.f;
+      v[j] = p[j] != kNone ? load16(y + (int64_t)p[j] * H + (int64_t)c * CH)
+                           : u32x4_t{0u, 0u, 0u, 0u};
+    }
+#pragma unroll
+    for (int j = 0; j < JB; ++j) {
+      float f[CH];
+      unpack(v[j], f);
+#pragma unroll
+      for (int i = 0; i < CH; ++i) acc[i] = fmaf(wj[j], f[i], acc[i]);
     }
   }
-  *reinterpret_cast<u32x4_t *>(out + t * H + (int64_t)c * CH) = pack(acc);
+  store16(out + t * H + (int64_t)c * CH, pack(acc));
 }
 
-// One wave a token: it keeps a piece of d_out in registers while it passes
-// over the same piece of the token's k expert rows.
-template <typename T>
+// WPT waves a token: each keeps a piece of d_out in registers while it passes
+// over the same piece of the token's expert rows, JB at a time.
+template <typename T, int JB, int WPT>
 __global__ __launch_bounds__(kThreads) void combine_weighted_backward_kernel(
     const T *__restrict__ d_out, const T *__restrict__ y, const int32_t *__restrict__ row_sorted,
     const void *__restrict__ w, bool w_bf16, T *__restrict__ dy, float *__restrict__ dw, int64_t N,
     int K, int H) {
-  constexpr int CH = chunk_elems<T>();
-  const int lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
-  if (t >= N) return;  // a whole wave
-  const uint32_t M = (uint32_t)(N * K);
-  const int nch = H / CH;
-  for (int j = 0; j < K; ++j) {
-    const uint32_t p = (uint32_t)row_sorted[t * K + j];
-    float dot = 0.f;
-    if (p < M) {  // the same for the whole wave
-      const float wj = weight_at(w, w_bf16, t * K + j);
-      for (int c = lane; c < nch; c += 64) {
-        float d[CH], f[CH];
-        unpack(*reinterpret_cast<const u32x4_t *>(d_out + t * H + (int64_t)c * CH), d);
-        unpack(*reinterpret_cast<const u32x4_t *>(y + (int64_t)p * H + (int64_t)c * CH), f);
+  constexpr int CH = chunk_elems<T>(), TPB = kThreads / 64 / WPT;  // tokens a workgroup
+  __shared__ float part[WPT > 1 ? WPT : 1][JB];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t t = (int64_t)blockIdx.x * TPB + (WPT == 1 ? wave : 0);
+  if (t >= N) return;  // a whole wave, or (WPT > 1) never
+  const int nch = H / CH, first = WPT == 1 ? lane : (int)threadIdx.x;
+  for (int j0 = 0; j0 < K; j0 += JB) {
+    uint32_t p[JB];
+    slot_rows<JB>(row_sorted, t, K, j0, (uint32_t)(N * K), p);
+    float wj[JB], dot[JB];
+#pragma unroll
+    for (int j = 0; j < JB; ++j) {
+      wj[j] = p[j] != kNone ? weight_at(w, w_bf16, t * K + j0 + j) : 0.f;
+      dot[j] = 0.f;
+    }
+    for (int c = first; c < nch; c += 64 * WPT) {
+      const int64_t at = (int64_t)c * CH;
+      const u32x4_t dv = *reinterpret_cast<const u32x4_t *>(d_out + t * H + at);
+      u32x4_t v[JB];
+#pragma unroll
+      for (int j = 0; j < JB; ++j)
+        v[j] = p[j] != kNone ? load16(y + (int64_t)p[j] * H + at) : u32x4_t{0u, 0u, 0u, 0u};
+      float d[CH];
+      unpack(dv, d);
+#pragma unroll
+      for (int j = 0; j < JB; ++j) {
+        if (p[j] == kNone) continue;  // the same for the whole wave
+        float f[CH];
+        unpack(v[j], f);
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-          dot = fmaf(d[i], f[i], dot);
-          d[i] *= wj;
+          dot[j] = fmaf(d[i], f[i], dot[j]);
+          f[i] = wj[j] * d[i];
         }
-        *reinterpret_cast<u32x4_t *>(dy + (int64_t)p * H + (int64_t)c * CH) = pack(d);
+        store16(dy + (int64_t)p[j] * H + at, pack(f));
       }
     }
-    dot = wave_sum_f32(dot);
-    if (lane == 0) dw[t * K + j] = dot;
+#pragma unroll
+    for (int j = 0; j < JB; ++j) dot[j] = wave_sum_f32(dot[j]);
+    if constexpr (WPT == 1) {
+#pragma unroll
+      for (int j = 0; j < JB; ++j)
+        if (lane == 0 && j0 + j < K) dw[t * K + j0 + j] = dot[j];
+    } else {
+      if (j0 > 0) __syncthreads();
+#pragma unroll
+      for (int j = 0; j < JB; ++j)
+        if (lane == 0) part[wave][j] = dot[j];
+      __syncthreads();
+      if (threadIdx.x < JB && j0 + (int)threadIdx.x < K) {
+        float s = part[0][threadIdx.x];
+#pragma unroll
+        for (int q = 1; q < WPT; ++q) s += part[q][threadIdx.x];
+        dw[t * K + j0 + threadIdx.x] = s;
+      }
+    }
   }
 }
 
@@ -139,31 +214,46 @@ template <typename T> int64_t chunk_blocks(int64_t n, int hidden) {
   return (n * (hidden / (16 / (int)sizeof(T))) + kThreads - 1) / kThreads;
 }
 
+// Calls go(T(), JB) for the row type and the number of slots taken at a time.
+template <typename F> void by_slots(moe_dtype_t dt, int topk, F go) {
+  auto jb = [&](auto tag) {
+    if (topk == 1) go(tag, std::integral_constant<int, 1>());
+    else if (topk == 2) go(tag, std::integral_constant<int, 2>());
+    else if (topk <= 4) go(tag, std::integral_constant<int, 4>());
+    else go(tag, std::integral_constant<int, 8>());
+  };
+  if (dt == MOE_BF16) jb(bf16_t()); else jb(float());
+}
+#ifndef WPT_TOK
+#define WPT_TOK 4096
+#endif
+// Below this many tokens a token gets the four waves of a workgroup.
+constexpr int64_t kWaveTokens = WPT_TOK;
+
 }  // namespace
 
 hipError_t launch_dispatch(const void *x, const int32_t *row_sorted, void *x_sorted,
                            moe_dtype_t dt, int64_t n_tokens, int topk, int hidden, hipStream_t s) {
-  auto go = [&](auto tag) {
+  by_slots(dt, topk, [&](auto tag, auto jb) {
     using T = decltype(tag);
-    hipLaunchKernelGGL(dispatch_kernel<T>, dim3((unsigned)chunk_blocks<T>(n_tokens, hidden)),
-                       dim3(kThreads), 0, s, reinterpret_cast<const T *>(x), row_sorted,
+    hipLaunchKernelGGL((dispatch_kernel<T, decltype(jb)::value>),
+                       dim3((unsigned)chunk_blocks<T>(n_tokens, hidden)), dim3(kThreads), 0, s,
+                       reinterpret_cast<const T *>(x), row_sorted,
                        reinterpret_cast<T *>(x_sorted), n_tokens, topk, hidden);
-  };
-  if (dt == MOE_BF16) go(bf16_t()); else go(float());
+  });
   return hipGetLastError();
 }
 
 hipError_t launch_combine_weighted(const void *y_sorted, const int32_t *row_sorted,
                                    const void *topk_w, moe_dtype_t w_dt, void *out, moe_dtype_t dt,
                                    int64_t n_tokens, int topk, int hidden, hipStream_t s) {
-  auto go = [&](auto tag) {
+  by_slots(dt, topk, [&](auto tag, auto jb) {
     using T = decltype(tag);
-    hipLaunchKernelGGL(combine_weighted_kernel<T>,
+    hipLaunchKernelGGL((combine_weighted_kernel<T, decltype(jb)::value>),
                        dim3((unsigned)chunk_blocks<T>(n_tokens, hidden)), dim3(kThreads), 0, s,
                        reinterpret_cast<const T *>(y_sorted), row_sorted, topk_w,
                        w_dt == MOE_BF16, reinterpret_cast<T *>(out), n_tokens, topk, hidden);
-  };
-  if (dt == MOE_BF16) go(bf16_t()); else go(float());
+  });
   return hipGetLastError();
 }
 
@@ -172,15 +262,20 @@ hipError_t launch_combine_weighted_backward(const void *d_out, const void *y_sor
                                             moe_dtype_t w_dt, void *d_y_sorted, float *d_topk_w,
                                             moe_dtype_t dt, int64_t n_tokens, int topk, int hidden,
                                             hipStream_t s) {
-  const unsigned blocks = (unsigned)((n_tokens + kThreads / 64 - 1) / (kThreads / 64));
-  auto go = [&](auto tag) {
+  by_slots(dt, topk, [&](auto tag, auto jb) {
     using T = decltype(tag);
-    hipLaunchKernelGGL(combine_weighted_backward_kernel<T>, dim3(blocks), dim3(kThreads), 0, s,
-                       reinterpret_cast<const T *>(d_out), reinterpret_cast<const T *>(y_sorted),
-                       row_sorted, topk_w, w_dt == MOE_BF16, reinterpret_cast<T *>(d_y_sorted),
-                       d_topk_w, n_tokens, topk, hidden);
-  };
-  if (dt == MOE_BF16) go(bf16_t()); else go(float());
+    constexpr int JB = decltype(jb)::value;
+    auto run = [&](auto wpt) {
+      constexpr int WPT = decltype(wpt)::value, TPB = kThreads / 64 / WPT;
+      hipLaunchKernelGGL((combine_weighted_backward_kernel<T, JB, WPT>),
+                         dim3((unsigned)((n_tokens + TPB - 1) / TPB)), dim3(kThreads), 0, s,
+                         reinterpret_cast<const T *>(d_out), reinterpret_cast<const T *>(y_sorted),
+                         row_sorted, topk_w, w_dt == MOE_BF16, reinterpret_cast<T *>(d_y_sorted),
+                         d_topk_w, n_tokens, topk, hidden);
+    };
+    if (n_tokens < kWaveTokens) run(std::integral_constant<int, 4>());
+    else run(std::integral_constant<int, 1>());
+  });
   return hipGetLastError();
 }
 
