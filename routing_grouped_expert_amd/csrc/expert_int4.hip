@@ -20,15 +20,26 @@
 // scale enters in fp32 once a group.  Nothing is rounded to bf16 but the
 // activation rows between the two products (the bf16 layer's own type).
 //
-// One workgroup of four waves computes 16 output columns (16 weight rows, or
-// 16 gate and 16 up rows) of one expert that has rows; the waves split K and
-// add up through LDS.  A 16x16x32 product takes the expert's token rows as its
-// 16 rows (missing ones are zeros and cost no traffic) and the weight rows as
-// its 16 columns, so a lane holds codes, scale and zero point of one weight
-// row.  A lane loads 16 bytes of codes, 32 weights of its row; the four lanes
-// of a row hold 128 weights, and a 4 x 4 transpose of dwords between the lane
-// groups (four lane swaps) gives each of the four products 32 consecutive
-// weights, so that no product mixes two groups.
+// A wave streams 32 weight rows of one expert (16 gate and 16 up rows, or 32
+// plain ones) and no other wave reads them, so they go straight to registers,
+// two steps of 256 weights a row ahead of the products.  The expert's token
+// rows stand in LDS, read by all waves of the workgroup.  A 16x16x32 product
+// takes token rows as its 16 rows (missing ones may be anything: their sums are
+// not used) and weight rows as its 16 columns, so a lane holds codes, scale and
+// zero point of one weight row and no sum leaves its lane until the end.
+//
+// Four neighbouring lanes load 64 bytes of a row (lanes that are rows apart
+// measured 3.1 TB/s instead of 4.4 on the 64-expert layer); a lane permutation
+// and, for groups of 32 and 64, lane swaps bring the dwords to the lanes whose
+// product they belong to, so that no product mixes two groups.
+//
+// What bounds it: vector instructions and products (one after the other, about
+// 230 and 24 a step of 8192 weights) at one token, the loads' rate from eight
+// tokens on.  Measured against the bytes of the touched experts: 64 experts
+// (H 4096, I 1536, k 8), 32 tokens, groups of 128: 145 us, 4.2 TB/s; 128 experts
+// (H = I = 2880, k 4), groups of 64 with zero points: 128 tokens 413 us, 4.1
+// TB/s, 33 tokens 350 us, 3.2 TB/s (rows of 1440 bytes straddle cache lines;
+// 2816 wide 3.8 TB/s), one token 26 us.
 #include "gemm_common.h"
 #include "lds_dma.h"
 #include "rows.h"
@@ -37,25 +48,6 @@
 
 namespace moe {
 namespace {
-
-#ifndef WPE
-#define WPE 4
-#endif
-#ifndef RULE4
-#define RULE4 2
-#endif
-#ifndef NWG
-#define NWG 2048
-#endif
-#ifndef KS4G
-#define KS4G 1024
-#endif
-#ifndef KS2G
-#define KS2G 4096
-#endif
-#ifndef LDSB
-#define LDSB 65536
-#endif
 
 struct Int4Args {
   const void *A;               // w13: x [N, K]; w2: activation rows [M, K]
@@ -66,7 +58,6 @@ struct Int4Args {
   const int32_t *offsets;      // [E + 1]
   const int32_t *col_sorted;   // [M]
   const void *gate_scal;       // [M] (w2)
-  uint32_t a_bytes;
   int gate_bf16, E, K, Nout, topk, gather, interleaved;
   ActParams prm;
 };
@@ -171,13 +162,167 @@ __device__ __forceinline__ void place(int &x, int &y) {
 
 constexpr int kStepK = 256;  // weights of a row a step: one 128-byte line of codes
 
+// One wave's 32 weight rows (two tiles of 16) of one expert: where they are,
+// and the products of a step of them with the token rows in LDS.  With NQ = 1
+// all 16 rows of a product are one token row, and one of a lane's four results
+// is taken.
+template <int GS, int NQ> struct WaveRows {
+  static constexpr int NM = GS == 1 ? 2 : 1;  // loads of four groups' scales a step and tile
+
+  struct Codes {  // a step of the rows
+    u32x4_t w[2][2];
+    uint32_t s[2][NM], z[2][NM];
+  };
+
+  __amdgpu_buffer_rsrc_t rq, rs, rz;
+  bool has_z;
+  uint32_t nrows, qoff[2], moff[2], magic, mask;
+  int lane, K;
+
+  // memrow(t, x): memory row of row x of tile t.  Codes: four lanes a row, 64
+  // bytes; a lane permutation puts them where the products want them.  Scales
+  // and zero points: lane group h loads the step's groups h (and h + 4).  Loads
+  // past K bring other rows' data, or zeros past the array's end; they are not
+  // used.
+  template <typename F> __device__ __forceinline__ void init(const Int4Args &g, int e, int rows,
+                                                             F memrow) {
+    lane = threadIdx.x & 63;
+    K = g.K;
+    nrows = (uint32_t)rows;
+    has_z = g.z != nullptr;
+    const uint32_t qbytes = nrows * (uint32_t)(K / 2), sn = (uint32_t)(K / (32 * GS)) * nrows;
+    rq = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(g.q) + (size_t)e * qbytes,
+                                           (short)0, (int)qbytes, kRsrcWord3);
+    rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<bf16_t *>(g.s) + (size_t)e * sn, (short)0,
+                                           (int)(2 * sn), kRsrcWord3);
+    rz = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(g.z) + (has_z ? (size_t)e * sn : 0),
+                                           (short)0, has_z ? (int)sn : 0, kRsrcWord3);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      qoff[t] = (uint32_t)memrow(t, lane >> 2) * (uint32_t)(K / 2) + (uint32_t)((lane & 3) * 16);
+      moff[t] = (uint32_t)(lane >> 4) * nrows + (uint32_t)memrow(t, lane & 15);
+    }
+    magic = 0x43004300u;
+    mask = 0x000f000fu;
+    asm("" : "+v"(magic));  // (no instruction: hides the values, see codes_plus_128)
+    asm("" : "+s"(mask));
+  }
+
+  __device__ __forceinline__ void load(Codes &c, int step) const {
+    const uint32_t k0 = (uint32_t)step * kStepK, g0 = k0 / (32 * GS) * nrows;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+        c.w[t][b] = __builtin_bit_cast(
+            u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rq, (int)(qoff[t] + k0 / 2 + 64 * b), 0, 0));
+#pragma unroll
+      for (int m = 0; m < NM; ++m) {
+        const uint32_t at = moff[t] + g0 + 4 * m * nrows;
+        c.s[t][m] = (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, (int)(2 * at), 0, 0);
+        c.z[t][m] =
+            has_z ? (uint32_t)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rz, (int)at, 0, 0) : 8u;
+      }
+    }
+  }
+
+  // acc[t] += this step's products with the lane's token row x, whose part of
+  // the step is at `tok` (16-byte piece c at place c ^ (x % 8)); with kWhole =
+  // false only the groups ahead of K.
+  template <bool kWhole>
+  __device__ __forceinline__ void work(const Codes &c, int step, const char *tok, int x,
+                                       f32x4_t (&acc)[2]) const {
+    const int h = lane >> 4, from = (4 * (lane & 15) + h) * 4;
+    const int ngroups = kWhole ? 8 / GS : (K - step * kStepK) / (32 * GS);
+    const bf16x8_t ones = __builtin_bit_cast(
+        bf16x8_t, u32x4_t{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u});
+    uint32_t mt[2][4 * NM];  // scale << 16 | zero point of each group
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int m = 0; m < NM; ++m) {
+        uint32_t v[4];
+        spread_groups(c.s[t][m] << 16 | c.z[t][m], v);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) mt[t][4 * m + q] = v[q];
+      }
+    f32x4_t sum[2], tot;
+    const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      u32x4_t cw[2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          cw[t][q] = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)c.w[t][b][q]);
+        arrange<GS>(cw[t]);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int gr = (4 * b + j) / GS;
+        if (!kWhole && gr >= ngroups) break;
+        const bf16x8_t av = *reinterpret_cast<const bf16x8_t *>(
+            tok + 256 * b + ((eighth<GS>(j, h) ^ (x & 7)) * 16));
+        const bool begins = j % GS == 0;
+        tot = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, ones, begins ? zero : tot, 0, 0, 0);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          sum[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              av, codes_plus_128(cw[t][j], mask, magic), begins ? zero : sum[t], 0, 0, 0);
+        if (j % GS == GS - 1) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const float f = __uint_as_float(mt[t][gr] & 0xffff0000u);
+            const float z = 128.f + (float)(mt[t][gr] & 0xffu);
+#pragma unroll
+            for (int q = 0; q < NQ; ++q)
+              acc[t][q] = fmaf(f, fmaf(-z, tot[q], sum[t][q]), acc[t][q]);
+          }
+        }
+      }
+    }
+  }
+
+  // Steps first .. last - 1, the first two already in c0 and c1, two ahead;
+  // tok0: the lane's token row at step s0.
+  __device__ __forceinline__ void stream(Codes &c0, Codes &c1, int first, int last, int s0,
+                                         const char *tok0, int x, f32x4_t (&acc)[2]) const {
+    auto run = [&](const Codes &c, int step) {
+      const char *tok = tok0 + (step - s0) * (2 * kStepK);
+      if ((step + 1) * kStepK <= K) work<true>(c, step, tok, x, acc);
+      else work<false>(c, step, tok, x, acc);
+    };
+    for (int step = first; step < last; step += 2) {
+      run(c0, step);
+      if (step + 1 >= last) break;
+      if (step + 2 < last) load(c0, step + 2);
+      run(c1, step + 1);
+      if (step + 3 < last) load(c1, step + 3);
+    }
+  }
+};
+
+// Token rows into LDS by the whole workgroup: values kb .. kb + klen - 1 of the
+// rows row(0) .. row(n - 1), rowb bytes apart.
+template <typename F>
+__device__ __forceinline__ void stage_rows(const Int4Args &g, char *lds, int rowb, int n, int kb,
+                                           int klen, F row) {
+  const int np = klen / 8;
+  for (int i = threadIdx.x; i < n * np; i += blockDim.x) {
+    const int x = i / np, c = i - x * np, at = row(x);
+    const u32x4_t v = *reinterpret_cast<const u32x4_t *>(
+        reinterpret_cast<const bf16_t *>(g.A) + (size_t)at * g.K + kb + 8 * c);
+    *reinterpret_cast<u32x4_t *>(lds + x * rowb + ((c ^ (x & 7)) * 16)) = token_order(v);
+  }
+}
+
 // GS = G / 32; TR: token rows held at a time.  A wave streams 32 weight rows;
 // ks waves share them and split the steps; the workgroup's waves / ks column
 // groups share the token rows in LDS, kc values of each at a time.
 template <int EPI, int GS, int TR>
-__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(WPE))) void
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void
 expert_int4_kernel(Int4Args g, int ks, int kc) {
-  constexpr int NM = GS == 1 ? 2 : 1;  // loads of four groups' scales a step and tile
   constexpr bool kPlain = EPI == EPI_Y || EPI == EPI_OUT || EPI == EPI_RELU2;
   constexpr int COLS = kPlain ? 32 : 16;  // output columns of a wave's 32 weight rows
   __shared__ int sel[3];
@@ -193,67 +338,21 @@ expert_int4_kernel(Int4Args g, int ks, int kc) {
   const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, h = lane >> 4;  // this lane's row in a tile, its lane group
-  const int K = g.K, Nout = g.Nout, nrows = kPlain ? Nout : 2 * Nout;
+  const int K = g.K, Nout = g.Nout;
   const int cg = wave / ks, kw = wave % ks;  // column group, share of the steps
   const int n0 = (place_x * (waves / ks) + cg) * COLS;
   const bool live = n0 < Nout;  // (the last workgroup's last groups may be past the last column)
 
-  const uint32_t qbytes = (uint32_t)nrows * (uint32_t)(K / 2);
-  const uint32_t sn = (uint32_t)(K / (32 * GS)) * (uint32_t)nrows;
-  const __amdgpu_buffer_rsrc_t rq = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<uint8_t *>(g.q) + (size_t)e * qbytes, (short)0, (int)qbytes, kRsrcWord3);
-  const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<bf16_t *>(g.s) + (size_t)e * sn, (short)0, (int)(2 * sn), kRsrcWord3);
-  const __amdgpu_buffer_rsrc_t rz = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<uint8_t *>(g.z) + (g.z ? (size_t)e * sn : 0), (short)0, g.z ? (int)sn : 0,
-      kRsrcWord3);
-
-  // Memory row of row x of tile t.  Gated: tile 0 the gate rows of 16 columns,
-  // tile 1 their up rows; plain: two runs of 16 columns.
-  auto memrow = [&](int t, int x) {
+  // Gated: tile 0 the gate rows of 16 columns, tile 1 their up rows; plain: two
+  // runs of 16 columns.
+  constexpr int NQ = TR < 4 ? TR : 4;
+  WaveRows<GS, NQ> rows;
+  rows.init(g, e, kPlain ? Nout : 2 * Nout, [&](int t, int x) {
     return kPlain ? n0 + 16 * t + x : g.interleaved ? 2 * (n0 + x) + t : t * Nout + n0 + x;
-  };
-  // Byte offsets, less the step's.  Codes: four lanes a row, 64 bytes; a lane
-  // swap puts them where the products want them.  Scales and zero points: lane
-  // group h loads the step's groups h (and h + 4).  Loads past K bring other
-  // rows' data, or zeros past the array's end; they are not used.
-  uint32_t qoff[2], moff[2];
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    qoff[t] = (uint32_t)memrow(t, lane >> 2) * (uint32_t)(K / 2) + (uint32_t)((lane & 3) * 16);
-    moff[t] = (uint32_t)h * (uint32_t)nrows + (uint32_t)memrow(t, r);
-  }
-  const int from = (4 * r + h) * 4;  // lane (of four bytes each) that loaded what this one needs
-  uint32_t magic = 0x43004300u, mask = 0x000f000fu;
-  asm("" : "+v"(magic));  // (no instruction: hides the values, see codes_plus_128)
-  asm("" : "+s"(mask));
-  const bf16x8_t ones = __builtin_bit_cast(
-      bf16x8_t, u32x4_t{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u});
+  });
 
-  struct Codes {  // a step of this wave's rows
-    u32x4_t w[2][2];
-    uint32_t s[2][NM], z[2][NM];
-  };
-  auto load = [&](Codes &c, int step) {
-    const uint32_t k0 = (uint32_t)step * kStepK;
-    const uint32_t g0 = k0 / (32 * GS) * (uint32_t)nrows;
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
-        c.w[t][b] = __builtin_bit_cast(
-            u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rq, (int)(qoff[t] + k0 / 2 + 64 * b), 0, 0));
-#pragma unroll
-      for (int m = 0; m < NM; ++m) {
-        const uint32_t at = moff[t] + g0 + 4 * m * (uint32_t)nrows;
-        c.s[t][m] = (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, (int)(2 * at), 0, 0);
-        c.z[t][m] =
-            g.z ? (uint32_t)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rz, (int)at, 0, 0) : 8u;
-      }
-    }
-  };
-
-  const int rowb = 2 * kc;  // bytes of a token row in LDS (a multiple of 128)
+  const int rowb = 2 * kc;  // bytes of a token row in LDS (a multiple of 512)
+  const int x = r % TR;     // rows past the expert's last hold anything: their sums are not used
   for (int a0 = 0; a0 < cnt; a0 += TR) {
     const int na = min(TR, cnt - a0);
     f32x4_t acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
@@ -261,85 +360,16 @@ expert_int4_kernel(Int4Args g, int ks, int kc) {
       const int klen = min(kc, K - kb);
       const int s0 = kb / kStepK, ns = (klen + kStepK - 1) / kStepK, per = (ns + ks - 1) / ks;
       const int first = s0 + min(kw * per, ns), last = live ? s0 + min(kw * per + per, ns) : first;
-      Codes c0, c1;
-      if (first < last) load(c0, first);
-      // token rows: 16-byte piece c of row x at place c ^ (x % 8)
+      typename WaveRows<GS, NQ>::Codes c0, c1;
+      if (first < last) rows.load(c0, first);
+      if (first + 1 < last) rows.load(c1, first + 1);
       if (a0 > 0 || kb > 0) __syncthreads();
-      const int np = klen / 8;
-      for (int i = threadIdx.x; i < na * np; i += blockDim.x) {
-        const int x = i / np, c = i - x * np, p = row0 + a0 + x;
-        const int row = g.gather ? g.col_sorted[p] / g.topk : p;
-        const u32x4_t v = *reinterpret_cast<const u32x4_t *>(
-            reinterpret_cast<const bf16_t *>(g.A) + (size_t)row * K + kb + 8 * c);
-        *reinterpret_cast<u32x4_t *>(lds + x * rowb + ((c ^ (x & 7)) * 16)) = token_order(v);
-      }
+      stage_rows(g, lds, rowb, na, kb, klen, [&](int i) {
+        const int p = row0 + a0 + i;
+        return g.gather ? g.col_sorted[p] / g.topk : p;
+      });
       __syncthreads();
-
-      // The products of one step; with kWhole = false only the groups ahead of K.
-      const int x = r % TR;  // rows past the expert's last hold anything: their sums are not used
-      auto work = [&](auto whole, const Codes &c, int step) {
-        constexpr bool kWhole = decltype(whole)::value;
-        const char *tok = lds + x * rowb + (step - s0) * (2 * kStepK);
-        const int ngroups = kWhole ? 8 / GS : (K - step * kStepK) / (32 * GS);
-        uint32_t mt[2][4 * NM];  // scale << 16 | zero point of each group
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int m = 0; m < NM; ++m) {
-            uint32_t v[4];
-            spread_groups(c.s[t][m] << 16 | c.z[t][m], v);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) mt[t][4 * m + q] = v[q];
-          }
-        f32x4_t sum[2], tot;
-        const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          u32x4_t cw[2];
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              cw[t][q] = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)c.w[t][b][q]);
-            arrange<GS>(cw[t]);
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int gr = (4 * b + j) / GS;
-            if (!kWhole && gr >= ngroups) break;
-            const bf16x8_t av = *reinterpret_cast<const bf16x8_t *>(
-                tok + 256 * b + ((eighth<GS>(j, h) ^ (x & 7)) * 16));
-            const bool begins = j % GS == 0;
-            tot = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, ones, begins ? zero : tot, 0, 0, 0);
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-              sum[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                  av, codes_plus_128(cw[t][j], mask, magic), begins ? zero : sum[t], 0, 0, 0);
-            if (j % GS == GS - 1) {
-#pragma unroll
-              for (int t = 0; t < 2; ++t) {
-                const float f = __uint_as_float(mt[t][gr] & 0xffff0000u);
-                const float z = 128.f + (float)(mt[t][gr] & 0xffu);
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                  acc[t][q] = fmaf(f, fmaf(-z, tot[q], sum[t][q]), acc[t][q]);
-              }
-            }
-          }
-        }
-      };
-      auto run = [&](const Codes &c, int step) {
-        if ((step + 1) * kStepK <= K) work(std::true_type(), c, step);
-        else work(std::false_type(), c, step);
-      };
-      for (int step = first; step < last; step += 2) {
-        if (step + 1 < last) load(c1, step + 1);
-        run(c0, step);
-        if (step + 1 < last) {
-          if (step + 2 < last) load(c0, step + 2);
-          run(c1, step + 1);
-        }
-      }
+      rows.stream(c0, c1, first, last, s0, lds + x * rowb, x, acc);
     }
 
     // the waves' parts, through LDS that the token rows no longer need: lane
@@ -350,7 +380,7 @@ expert_int4_kernel(Int4Args g, int ks, int kc) {
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) red[((wave * 2 + t) * TR + 4 * h + q) * 17 + r] = acc[t][q];
+        for (int q = 0; q < NQ; ++q) red[((wave * 2 + t) * TR + 4 * h + q) * 17 + r] = acc[t][q];
     }
     __syncthreads();
     for (int i = kw * 64 + lane; i < na * COLS && live; i += ks * 64) {
@@ -408,17 +438,34 @@ __global__ __launch_bounds__(256) void sum_slots_kernel(const float *__restrict_
   *reinterpret_cast<u32x4_t *>(out + t * H + c) = pack(acc);
 }
 
+// LDS for token rows: 128 KB for whole rows of 4096 values leaves one workgroup
+// a compute unit (8 experts, 64 tokens: 114 us -> 161; 32 KB: 124).
+constexpr int kTokenLds = 64 * 1024;
+
+// Values of a token row that LDS holds at a time: all of K, or equal parts of
+// it in whole steps, `most` at most.
+int staged_values(int K, int most) {
+  const int nstep = (K + kStepK - 1) / kStepK, parts = (K + most - 1) / most;
+  return (nstep + parts - 1) / parts * kStepK;
+}
+
+// Waves a workgroup and waves that split K, by the number of column groups of
+// all experts (G): fewer waves are left to wait for memory when G is small, and
+// each further wave on the same rows costs its start and a share of the sum at
+// the end.  Measured (us, split in 4 / 2 / 1): G = 720, one token of 128
+// experts, 27.2 / 31.5 / 42.6; G = 2880, four tokens, 75.0 / 67.8 / 77.3; G =
+// 2048, 8 experts, 149 / 114 / 133; G = 23040, 33 tokens, 421 / 364 / 349.
+// Eight waves share the token rows of one workgroup from 2048 groups on (8
+// experts, 64 tokens: 109 us against 151 with four); with fewer groups four
+// spread over more compute units (one token: 27.6 against 29.6).
 template <int EPI, int GS, int TR>
 void launch_rows(const Int4Args &a, int64_t M, hipStream_t s) {
-  const int nstep = (a.K + kStepK - 1) / kStepK;
   const int cols = EPI == EPI_Y || EPI == EPI_OUT || EPI == EPI_RELU2 ? 32 : 16;
   const int64_t experts = M < a.E ? M : a.E, groups = (a.Nout / cols) * experts;
-  const int waves = groups < NWG ? 4 : 8;
-  const int ks = groups < KS4G ? 4 : groups < KS2G ? 2 : 1;
+  const int waves = groups < 2048 ? 4 : 8;
+  const int ks = groups < 1024 ? 4 : groups < 4096 ? 2 : 1;
   const int wide = cols * (waves / ks);
-  // token rows in LDS: all of K, or equal parts of it in whole steps
-  const int most = LDSB / (2 * TR), parts = (a.K + most - 1) / most;
-  const int kc = ((nstep + parts - 1) / parts) * kStepK;
+  const int kc = staged_values(a.K, kTokenLds / (2 * TR));
   const size_t rows = (size_t)TR * kc * 2, red = sizeof(float) * waves * 2 * TR * 17;
   hipLaunchKernelGGL((expert_int4_kernel<EPI, GS, TR>),
                      dim3((unsigned)((a.Nout + wide - 1) / wide), (unsigned)experts),
@@ -427,8 +474,12 @@ void launch_rows(const Int4Args &a, int64_t M, hipStream_t s) {
 
 template <int EPI, int GS>
 void launch_tiles(const Int4Args &a, int64_t n_tokens, int64_t M, hipStream_t s) {
-  // an expert holds at most one row a token
-  if (n_tokens <= 4 || M <= RULE4 * a.E) launch_rows<EPI, GS, 4>(a, M, s);
+  // Token rows held at a time: an expert has at most one a token, and past
+  // those held its weights are read again.  Up to two rows an expert on average
+  // four are enough (33 tokens, 128 experts: 350 us against 366 with 16); at
+  // four an expert they are not (64 experts, 32 tokens: 198 against 145).
+  if (n_tokens == 1) launch_rows<EPI, GS, 1>(a, M, s);
+  else if (n_tokens <= 4 || M <= 2 * (int64_t)a.E) launch_rows<EPI, GS, 4>(a, M, s);
   else launch_rows<EPI, GS, 16>(a, M, s);
 }
 
@@ -510,8 +561,7 @@ hipError_t launch_experts_int4(const Int4Weights &w13, const Int4Weights &w2, co
   const int64_t M = n_tokens * topk;
   Int4Args a{x, reinterpret_cast<const uint8_t *>(w13.q), reinterpret_cast<const bf16_t *>(w13.s),
              reinterpret_cast<const uint8_t *>(w13.z), act, r->offsets, r->col_sorted, nullptr,
-             (uint32_t)(n_tokens * hidden * 2), 0, n_experts, hidden, inter, topk, 1,
-             layout == MOE_W13_INTERLEAVED, prm};
+             0, n_experts, hidden, inter, topk, 1, layout == MOE_W13_INTERLEAVED, prm};
   const bool clamp = __builtin_isfinite(prm.limit);
   hipError_t err = kind == MOE_ACT_RELU2 ? launch_groups<EPI_RELU2>(a, group, n_tokens, M, s)
                    : clamp ? launch_groups<EPI_GATED_CLAMP>(a, group, n_tokens, M, s)
@@ -520,8 +570,7 @@ hipError_t launch_experts_int4(const Int4Weights &w13, const Int4Weights &w2, co
   const bool direct = topk == 1;
   Int4Args b{act, reinterpret_cast<const uint8_t *>(w2.q), reinterpret_cast<const bf16_t *>(w2.s),
              reinterpret_cast<const uint8_t *>(w2.z), direct ? out : y, r->offsets, r->col_sorted,
-             r->gate_scal, (uint32_t)(M * inter * 2), r->w_dtype == MOE_BF16, n_experts, inter,
-             hidden, topk, 0, 0, prm};
+             r->gate_scal, r->w_dtype == MOE_BF16, n_experts, inter, hidden, topk, 0, 0, prm};
   if (direct) return launch_groups<EPI_OUT>(b, group, n_tokens, M, s);
   if ((err = launch_groups<EPI_Y>(b, group, n_tokens, M, s)) != hipSuccess) return err;
   const int64_t total = n_tokens * (hidden / 8);

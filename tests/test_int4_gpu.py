@@ -129,6 +129,12 @@ CASES = [
     ("e256", 64, 128, 128, 256, 8, 64, True, "silu", "packed", {}, None),
     ("many-rows", 300, 128, 128, 4, 2, 32, True, "silu", "interleaved", {}, None),
     ("long", 3, 4096, 1536, 8, 2, 32, True, "silu", "packed", {}, None),
+    # about one row an expert: w2 and the sum over the slots in one kernel
+    ("seven-slots", 9, 128, 352, 64, 7, 32, True, "silu", "packed", {}, None),
+    ("sixteen-slots", 1, 160, 224, 16, 16, 32, False, "silu", "interleaved", {}, None),
+    ("three-slots", 20, 128, 1024, 64, 3, 128, True, "relu2", "packed", {}, None),
+    ("two-slots-long", 2, 64, 8448, 8, 2, 64, True, "silu", "packed", {}, None),
+    ("long-rows", 20, 64, 4416, 2, 2, 64, False, "silu", "packed", {}, None),
 ]
 
 
