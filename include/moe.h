@@ -299,6 +299,22 @@ moe_status_t moe_block_norm_backward(const void *d_x_out, const void *d_n_out, c
                                      void *d_y, float *d_w_post, float *d_w_pre, float *d_gate,
                                      void *workspace, size_t ws_bytes, void *stream);
 
+/* moe_block_forward: the whole block around the layer,
+ *   n = x * rstd(x) * w_pre;  y = moe_gate_forward of n;
+ *   x_out = x + residual_scale * gate * z(y),   z as above with w_post
+ * (norm->w_pre, required here, is this block's own norm; n and y are rounded to
+ * `dtype`).  Arguments as moe_gate_forward, x_out [N, hidden] (may be x).
+ * workspace: moe_workspace_bytes(n_tokens, n_experts, topk, hidden, inter,
+ * dtype) and n_tokens * hidden elements of `dtype`, each rounded up to 256
+ * bytes. */
+moe_status_t moe_block_forward(const void *x, const void *w_gate, moe_dtype_t dtype,
+                               int64_t n_tokens, int32_t hidden, const void *w13, const void *w2,
+                               int32_t n_experts, int32_t inter, int32_t topk, moe_act_t act,
+                               moe_w13_layout_t layout, const moe_act_params_t *params,
+                               const moe_block_norm_t *norm, void *logits_out,
+                               const moe_routing_t *routing_out, void *x_out, void *workspace,
+                               size_t ws_bytes, void *stream);
+
 /* moe_route on `logits` (dtype `dtype`) into *routing_out, then moe_experts. */
 moe_status_t moe_forward(const void *x, const void *logits, moe_dtype_t dtype,
                          int64_t n_tokens, int32_t hidden, const void *w13, const void *w2,

@@ -66,7 +66,8 @@ __all__ = ["Routing", "MoeError", "Prepared", "moe_route", "moe_experts", "moe_e
            "moe_route_backward", "prepare_dispatch", "prepare_combine_weighted",
            "prepare_combine_weighted_backward", "prepare_route_backward", "BlockNorm",
            "BlockNormGrads", "moe_block_norm", "moe_block_norm_backward", "prepare_block_norm",
-           "prepare_block_norm_backward", "moe_block_norm_workspace_bytes", "moe_quantize_int4",
+           "prepare_block_norm_backward", "moe_block_norm_workspace_bytes", "moe_block_forward",
+           "prepare_block_forward", "moe_quantize_int4",
            "moe_dequantize_int4", "moe_experts_int4", "moe_forward_int4", "prepare_experts_int4",
            "prepare_forward_int4", "moe_int4_workspace_bytes",
            "moe_workspace_bytes", "moe_status_str", "ACTS", "LAYOUTS"]
@@ -842,6 +843,8 @@ def _output(t, like: torch.Tensor, shape, dtype, stream, name: str) -> torch.Ten
     stream the call runs on."""
     if t is None:
         if stream is None:
+            if dtype == like.dtype:  # (the quicker calls)
+                return torch.empty_like(like) if shape == like.shape else like.new_empty(shape)
             return like.new_empty(shape, dtype=dtype)
         with torch.cuda.stream(stream):
             return like.new_empty(shape, dtype=dtype)
@@ -860,6 +863,13 @@ def _scratch(ws, like: torch.Tensor, nbytes: int, stream) -> torch.Tensor:
         return _output(None, like, (nbytes,), torch.uint8, stream, "workspace")
     _index(like, ws)
     return _workspace(ws, nbytes, None)
+
+
+def _new_routing(n: int, e: int, topk: int, like: torch.Tensor, stream) -> Routing:
+    if stream is None:
+        return Routing.empty(n, e, topk, like.dtype, like.device)
+    with torch.cuda.stream(stream):
+        return Routing.empty(n, e, topk, like.dtype, like.device)
 
 
 def _row_routing(routing: Routing, dev: int, order: str, weights: bool):
@@ -1192,6 +1202,68 @@ def moe_block_norm_backward(d_x_out: Optional[torch.Tensor], d_n_out: Optional[t
                                 workspace, stream).run()
 
 
+def _block_forward(x, w_gate, w13, w2, topk, act, layout, params, w_pre, w_post, gate,
+                   residual_scale, eps, x_out, logits, routing, workspace, stream) -> _Call:
+    if w_pre is None:
+        raise ValueError("w_pre, the weight of the norm ahead of the block, is needed")
+    # (x stands for the block's output, which has its shape)
+    dev, n, hidden, c = _block_norm_args(x, x, w_post, w_pre, gate, residual_scale, eps)
+    _index(x, w_gate, w13, w2)
+    if w_gate.dim() != 2 or w_gate.shape[1] != hidden or w_gate.dtype != x.dtype:
+        raise ValueError("w_gate must be [E, hidden] in the dtype of x")
+    _shapes(x, w13, w2, act)
+    e, inter = w2.shape[0], w2.shape[2]
+    if w_gate.shape[0] != e:
+        raise ValueError("w_gate and the experts differ in their number")
+    if layout not in LAYOUTS:
+        raise ValueError(f"unknown w13 layout {layout!r}")
+    x_out = _output(x_out, x, (n, hidden), x.dtype, stream, "x_out")
+    logits = _output(logits, x, (n, e), x.dtype, stream, "logits")
+    if routing is None:
+        routing = _new_routing(n, e, topk, x, stream)
+    _check_routing(routing, n, e, topk)
+    _index(x, *(getattr(routing, f.name) for f in fields(routing)))
+    need = (moe_workspace_bytes(n, e, topk, hidden, inter, x.dtype) + 255) // 256 * 256 \
+        + (n * hidden * x.element_size() + 255) // 256 * 256
+    ws = _scratch(workspace, x, need, stream)
+    r = routing.as_c()
+    p = _params(params)
+    args = (x.data_ptr(), w_gate.data_ptr(), _dt(x), n, hidden, w13.data_ptr(), w2.data_ptr(), e,
+            inter, topk, ACTS[act], LAYOUTS[layout], ctypes.byref(p) if p else None,
+            ctypes.byref(c), logits.data_ptr(), ctypes.byref(r), x_out.data_ptr(), ws.data_ptr(),
+            _nbytes(ws), _raw_stream(dev, stream))
+    return _Call(dev, "moe_block_forward", args,
+                 (r, p, c, x, w_gate, w13, w2, w_pre, w_post, gate, x_out, logits, ws, routing),
+                 (x_out, logits, routing))
+
+
+def prepare_block_forward(x: torch.Tensor, w_gate: torch.Tensor, w13: torch.Tensor,
+                          w2: torch.Tensor, topk: int, act: str, layout: str = "packed",
+                          params: Optional[dict] = None, *, w_pre: torch.Tensor,
+                          w_post: Optional[torch.Tensor] = None,
+                          gate: Optional[torch.Tensor] = None, residual_scale: float = 1.0,
+                          eps: float = 1e-6, x_out: Optional[torch.Tensor] = None,
+                          logits: Optional[torch.Tensor] = None,
+                          routing: Optional[Routing] = None,
+                          workspace: Optional[torch.Tensor] = None, stream=None) -> Prepared:
+    return _block_forward(x, w_gate, w13, w2, topk, act, layout, params, w_pre, w_post, gate,
+                          residual_scale, eps, x_out, logits, routing, workspace,
+                          stream).prepared()
+
+
+def moe_block_forward(x: torch.Tensor, w_gate: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor,
+                      topk: int, act: str, layout: str = "packed", params: Optional[dict] = None,
+                      *, w_pre: torch.Tensor, w_post: Optional[torch.Tensor] = None,
+                      gate: Optional[torch.Tensor] = None, residual_scale: float = 1.0,
+                      eps: float = 1e-6, x_out: Optional[torch.Tensor] = None,
+                      logits: Optional[torch.Tensor] = None, routing: Optional[Routing] = None,
+                      workspace: Optional[torch.Tensor] = None, stream=None):
+    """The block around the layer: norm, moe_gate_forward, norm, gate and residual
+    sum (see moe.h); returns ``(x_out, logits, routing)``.  ``x_out`` may be ``x``."""
+    return _block_forward(x, w_gate, w13, w2, topk, act, layout, params, w_pre, w_post, gate,
+                          residual_scale, eps, x_out, logits, routing, workspace, stream).run()
+
+
 # ------------------------------------------------- 4-bit expert weights with group scales
 
 _INT4_GROUPS = (32, 64, 128)
@@ -1323,11 +1395,7 @@ def _forward_int4(x, logits, w13, w2, topk, act, layout, params, out, routing, w
     if logits.dtype != x.dtype or tuple(logits.shape) != (n, e):
         raise ValueError("logits must be [N, E] in the layer dtype")
     if routing is None:
-        if stream is None:
-            routing = Routing.empty(n, e, topk, x.dtype, x.device)
-        else:
-            with torch.cuda.stream(stream):
-                routing = Routing.empty(n, e, topk, x.dtype, x.device)
+        routing = _new_routing(n, e, topk, x, stream)
     _check_routing(routing, n, e, topk)
     _index(x, *(getattr(routing, f.name) for f in fields(routing)))
     out = _output(out, x, (n, hidden), x.dtype, stream, "out")

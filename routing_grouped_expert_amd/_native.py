@@ -97,6 +97,9 @@ SIGNATURES = {
     "moe_block_norm_backward": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_i32, c_i64, c_i32, _P_NORM,
                                         c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_sz,
                                         c_vp]),
+    "moe_block_forward": (c_i32, [c_vp, c_vp, c_i32, c_i64, c_i32, c_vp, c_vp, c_i32, c_i32, c_i32,
+                                  c_i32, c_i32, _P_PARAMS, _P_NORM, c_vp, _P_ROUTING, c_vp, c_vp,
+                                  c_sz, c_vp]),
     "moe_int4_workspace_bytes": (c_sz, [c_i64, c_i32, c_i32, c_i32, c_i32]),
     "moe_quantize_int4": (c_i32, [c_vp, c_i32, c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp,
                                   c_vp]),

@@ -935,6 +935,58 @@ moe_status_t moe_block_norm_backward(const void *d_x_out, const void *d_n_out, c
              : MOE_ERR_HIP;
 }
 
+moe_status_t moe_block_forward(const void *x, const void *w_gate, moe_dtype_t dtype,
+                               int64_t n_tokens, int32_t hidden, const void *w13, const void *w2,
+                               int32_t n_experts, int32_t inter, int32_t topk, moe_act_t act,
+                               moe_w13_layout_t layout, const moe_act_params_t *params,
+                               const moe_block_norm_t *norm, void *logits_out,
+                               const moe_routing_t *routing_out, void *x_out, void *workspace,
+                               size_t ws_bytes, void *stream) {
+  // workspace: what moe_gate_forward takes, then the block's normed rows, which
+  // the block's output replaces (the rows are dead once GEMM1 has run)
+  const size_t inner = align256(
+      moe_workspace_bytes(n_tokens, n_experts, topk, hidden, inter, dtype));
+  if (inner == 0) return !dtype_ok(dtype) ? MOE_ERR_DTYPE : MOE_ERR_SHAPE;
+  moe_status_t st = check_block_norm(x, x, dtype, n_tokens, hidden, norm);
+  if (st != MOE_OK) return st;
+  ActParams prm;
+  if (n_tokens > 0) {
+    if (!norm->w_pre || !x_out) return MOE_ERR_NULL;
+    if (!aligned16(x_out)) return MOE_ERR_ALIGN;
+    if ((st = check_ws(workspace, ws_bytes,
+                       inner + align256((size_t)n_tokens * hidden * dsize(dtype)))) != MOE_OK)
+      return st;
+  }
+  char *rows = reinterpret_cast<char *>(workspace) + inner;
+  if ((st = check_gate(rows, w_gate, dtype, n_tokens, hidden, n_experts, logits_out)) != MOE_OK)
+    return st;
+  st = check_route(logits_out, dtype, n_tokens, n_experts, topk, routing_out, workspace, inner);
+  if (st != MOE_OK) return st;
+  st = check_experts(rows, dtype, n_tokens, hidden, w13, w2, n_experts, inter, topk, act, layout,
+                     params, routing_out, rows, workspace, inner, &prm);
+  if (st != MOE_OK || n_tokens == 0) return st;
+  hipStream_t s = (hipStream_t)stream;
+  moe::BlockNormArgs pre{};
+  pre.x = x;
+  pre.w_pre = norm->w_pre;
+  pre.n_out = rows;
+  pre.n_tokens = n_tokens;
+  pre.hidden = hidden;
+  pre.residual_scale = 1.f;
+  pre.eps = norm->eps;
+  if (moe::launch_block_norm(pre, dtype, s) != hipSuccess ||
+      moe::launch_route(logits_out, dtype, n_tokens, n_experts, topk, 0, n_experts, routing_out,
+                        workspace, s, rows, w_gate, hidden) != hipSuccess)
+    return MOE_ERR_HIP;
+  st = run_experts(rows, dtype, n_tokens, hidden, w13, w2, n_experts, inter, topk, act, layout, prm,
+                   routing_out, rows, workspace, s);
+  if (st != MOE_OK) return st;
+  moe::BlockNormArgs post = block_norm_args(x, rows, n_tokens, hidden, norm);
+  post.w_pre = nullptr;
+  post.x_out = x_out;
+  return moe::launch_block_norm(post, dtype, s) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
 const char *moe_status_str(moe_status_t status) {
   switch (status) {
     case MOE_OK: return "ok";

@@ -184,25 +184,30 @@ __global__ __launch_bounds__(kThreads) void combine_weighted_backward_kernel(
   }
 }
 
-// One thread per element of d_logits.
-template <typename W>
+// C consecutive elements of one token's d_logits a thread: 16 bytes where rows
+// are whole 16-byte chunks, else one element (16384 tokens x 64 experts bf16, 8
+// slots: 4.0 us against 7.0).
+template <typename W, int C>
 __global__ __launch_bounds__(kThreads) void route_backward_kernel(
     const float *__restrict__ dw, const int32_t *__restrict__ topk_idx, const W *__restrict__ w,
     W *__restrict__ d_logits, int64_t N, int E, int K) {
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (i >= N * E) return;
-  const int64_t t = i / E;
-  const int e = (int)(i - t * E);
-  float s = 0.f, wm = 0.f, dm = 0.f;
+  int64_t t;
+  int c;
+  if (!own_chunk(N, E / C, t, c)) return;
+  float s = 0.f;
+  for (int j = 0; j < K; ++j) s = fmaf(to_f32(w[t * K + j]), dw[t * K + j], s);
+  float v[C];
+#pragma unroll
+  for (int i = 0; i < C; ++i) v[i] = 0.f;
   for (int j = 0; j < K; ++j) {
-    const float wj = to_f32(w[t * K + j]), dj = dw[t * K + j];
-    s = fmaf(wj, dj, s);
-    if (topk_idx[t * K + j] == e) {
-      wm = wj;
-      dm = dj;
-    }
+    const int e = topk_idx[t * K + j] - c * C;
+    const float d = to_f32(w[t * K + j]) * (dw[t * K + j] - s);
+#pragma unroll
+    for (int i = 0; i < C; ++i) v[i] = e == i ? d : v[i];
   }
-  d_logits[i] = from_f32<W>(wm * (dm - s));
+  W *out = d_logits + t * E + (int64_t)c * C;
+  if constexpr (C == 1) *out = from_f32<W>(v[0]);
+  else store16(out, pack(v));
 }
 
 template <typename T> int64_t chunk_blocks(int64_t n, int hidden) {
@@ -276,14 +281,21 @@ hipError_t launch_combine_weighted_backward(const void *d_out, const void *y_sor
 hipError_t launch_route_backward(const float *d_topk_w, const int32_t *topk_idx,
                                  const void *topk_w, void *d_logits, moe_dtype_t w_dt,
                                  int64_t n_tokens, int n_experts, int topk, hipStream_t s) {
-  const unsigned blocks = (unsigned)((n_tokens * n_experts + kThreads - 1) / kThreads);
-  auto go = [&](auto tag) {
+  auto go = [&](auto tag, auto chunk) {
     using W = decltype(tag);
-    hipLaunchKernelGGL(route_backward_kernel<W>, dim3(blocks), dim3(kThreads), 0, s, d_topk_w,
-                       topk_idx, reinterpret_cast<const W *>(topk_w),
+    constexpr int C = decltype(chunk)::value;
+    const int64_t total = n_tokens * (n_experts / C);
+    hipLaunchKernelGGL((route_backward_kernel<W, C>),
+                       dim3((unsigned)((total + kThreads - 1) / kThreads)), dim3(kThreads), 0, s,
+                       d_topk_w, topk_idx, reinterpret_cast<const W *>(topk_w),
                        reinterpret_cast<W *>(d_logits), n_tokens, n_experts, topk);
   };
-  if (w_dt == MOE_BF16) go(bf16_t()); else go(float());
+  auto by_chunk = [&](auto tag) {
+    constexpr int C = chunk_elems<decltype(tag)>();
+    if (n_experts % C == 0) go(tag, std::integral_constant<int, C>());
+    else go(tag, std::integral_constant<int, 1>());
+  };
+  if (w_dt == MOE_BF16) by_chunk(bf16_t()); else by_chunk(float());
   return hipGetLastError();
 }
 

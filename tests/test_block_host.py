@@ -194,3 +194,29 @@ def test_int4_calls(lib):
     assert dequantize(int4(z=MISALIGNED)) == N.MOE_ERR_ALIGN
     assert dequantize(o=None) == N.MOE_ERR_NULL
     assert dequantize(k=100) == N.MOE_ERR_SHAPE
+
+
+def test_block_forward_call(lib):
+    def block(x=FAKE, wg=FAKE, n=33, h=128, e=8, i=256, k=2, dt=N.MOE_BF16, act=N.MOE_ACT_SILU,
+              layout=N.MOE_W13_PACKED, s=None, lg=FAKE, r=None, xo=FAKE, ws=FAKE, wsb=1 << 30):
+        return lib.moe_block_forward(x, wg, dt, n, h, FAKE, FAKE, e, i, k, act, layout, None,
+                                     s or norm_struct(), lg, r or routing(w_dtype=dt), xo, ws,
+                                     wsb, None)
+    assert block(None, n=0, xo=None, ws=None) == N.MOE_OK
+    assert block(None) == N.MOE_ERR_NULL
+    assert block(wg=None) == N.MOE_ERR_NULL
+    assert block(lg=None) == N.MOE_ERR_NULL
+    assert block(xo=None) == N.MOE_ERR_NULL
+    assert block(xo=MISALIGNED) == N.MOE_ERR_ALIGN
+    assert block(s=norm_struct(w_pre=None)) == N.MOE_ERR_NULL
+    assert block(s=norm_struct(eps=0.0)) == N.MOE_ERR_SHAPE
+    assert block(s=norm_struct(kind=N.MOE_GATE_CHANNEL)) == N.MOE_ERR_NULL
+    assert block(r=routing({"col_sum": None})) == N.MOE_ERR_NULL
+    for bad in ({"h": 100}, {"h": 16392}, {"k": 9}, {"e": 257}, {"i": 12}, {"n": -1}):
+        assert block(**bad) == N.MOE_ERR_SHAPE, bad
+    assert block(dt=5) == N.MOE_ERR_DTYPE
+    assert block(act=N.MOE_ACT_RELU2, layout=N.MOE_W13_INTERLEAVED) == N.MOE_ERR_UNSUPPORTED
+    inner = lib.moe_workspace_bytes(33, 8, 2, 128, 256, N.MOE_BF16)
+    assert block(ws=None) == N.MOE_ERR_WORKSPACE
+    assert block(wsb=inner) == N.MOE_ERR_WORKSPACE
+    assert block(ws=MISALIGNED) == N.MOE_ERR_ALIGN

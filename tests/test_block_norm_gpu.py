@@ -14,7 +14,7 @@ import pytest
 import torch
 
 import oracle
-from routing_grouped_expert_amd import (moe_block_norm, moe_block_norm_backward,
+from routing_grouped_expert_amd import (MoeError, moe_block_norm, moe_block_norm_backward,
                                         prepare_block_norm, prepare_block_norm_backward)
 
 pytestmark = pytest.mark.gpu
@@ -309,3 +309,51 @@ def test_gradient_against_differences():
             diff = (up - loss()) / (2 * step)
             t[i] = old
             assert abs(diff - grad[i]) <= 512 * U32 / step + step ** 2, (name, i)
+
+
+def test_refusals():
+    a, d = _inputs(8, 64, "bf16", "token")
+    da, dd = _dev(a), _dev(d)
+
+    def fwd(**kw):
+        return moe_block_norm(**{**da, **kw})
+
+    def bwd(d_x_out=dd["d_x_out"], d_n_out=dd["d_n_out"], **kw):
+        ok = torch.ones(8, device=DEV)
+        return moe_block_norm_backward(d_x_out, d_n_out,
+                                       **{**da, "rstd_post": ok, "rstd_pre": ok, **kw})
+
+    bf = dict(dtype=torch.bfloat16, device=DEV)
+    for call in (fwd, bwd):
+        for bad in ({"y": torch.zeros(8, 72, **bf)}, {"w_post": torch.zeros(72, **bf)},
+                    {"w_pre": torch.zeros(8, 64, **bf)}, {"gate": torch.zeros(8, 64, **bf)},
+                    {"gate": torch.zeros(8, **bf)}, {"y": None}, {"x": a["x"]},
+                    {"x": torch.zeros(64, 8, **bf).t()}):
+            with pytest.raises(ValueError):
+                call(**bad)
+        for bad in ({"w_post": torch.zeros(64, device=DEV)}, {"y": da["y"].float()}):
+            with pytest.raises(TypeError):
+                call(**bad)
+    with pytest.raises(ValueError):
+        fwd(y=None, w_post=None, gate=None, w_pre=None)
+    with pytest.raises(ValueError):
+        fwd(w_pre=None, n_out=torch.zeros(8, 64, **bf))
+    with pytest.raises(ValueError):
+        fwd(x_out=torch.zeros(8, 64, device=DEV))
+    for eps in (0.0, -1.0, float("nan")):
+        with pytest.raises(MoeError):
+            fwd(eps=eps)
+    with pytest.raises(MoeError):
+        fwd(residual_scale=float("inf"))
+    with pytest.raises(MoeError):  # wider than a row may be
+        moe_block_norm(torch.zeros(1, 16392, **bf), w_pre=torch.zeros(16392, **bf))
+    with pytest.raises(ValueError):
+        bwd(d_n_out=None)
+    with pytest.raises(ValueError):
+        bwd(rstd_post=None)
+    with pytest.raises(ValueError):
+        bwd(d_gate=torch.zeros(8, device=DEV))
+    with pytest.raises(ValueError):
+        bwd(d_x_out=None, d_n_out=None, w_pre=None)
+    with pytest.raises(MoeError):
+        bwd(workspace=torch.zeros(16, dtype=torch.uint8, device=DEV))

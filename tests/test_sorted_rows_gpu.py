@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import oracle
-from routing_grouped_expert_amd import (Routing, moe_combine, moe_combine_weighted,
+from routing_grouped_expert_amd import (MoeError, Routing, moe_combine, moe_combine_weighted,
                                         moe_combine_weighted_backward, moe_dispatch, moe_route,
                                         moe_route_backward, moe_route_ep, prepare_combine_weighted,
                                         prepare_combine_weighted_backward, prepare_dispatch,
@@ -238,3 +238,59 @@ def test_row_offsets_past_32_bits():
         assert torch.equal(dy[row[:, j]], want)
     norm2 = x.double().square().sum(1)
     assert ((dw.double() - norm2[:, None]).abs() <= (h + 1) * U32 * norm2[:, None]).all()
+
+
+def test_refusals():
+    r, x, y, d = _inputs(20, 64, 8, 2, "bf16", "bf16")
+    x, y, d = x.to(DEV), y.to(DEV), d.to(DEV)
+    dw = torch.zeros(20, 2, device=DEV)
+    with pytest.raises(ValueError):
+        moe_dispatch(x[:19].contiguous(), r)
+    with pytest.raises(ValueError):
+        moe_dispatch(x.cpu(), r)
+    with pytest.raises(ValueError):  # not contiguous
+        moe_dispatch(x.t().contiguous().t(), r)
+    with pytest.raises(TypeError):
+        moe_dispatch(x.half(), r)
+    with pytest.raises(ValueError):
+        moe_dispatch(x, r, x_sorted=y[:39].contiguous())
+    with pytest.raises(ValueError):
+        moe_combine_weighted(y[:39].contiguous(), r)
+    with pytest.raises(ValueError):
+        moe_combine_weighted(y, r, out=torch.empty(20, 64, device=DEV))
+    with pytest.raises(ValueError):
+        moe_combine_weighted_backward(d[:, :56].contiguous(), y, r)
+    with pytest.raises(ValueError):
+        moe_combine_weighted_backward(d.float(), y, r)
+    with pytest.raises(ValueError):
+        moe_route_backward(dw.double(), r)
+    with pytest.raises(MoeError):  # a width that is no multiple of 8
+        moe_dispatch(x[:, :60].contiguous(), r)
+    with pytest.raises(MoeError):  # fewer experts than slots
+        moe_route_backward(dw, r, 1)
+    bad = Routing(**{**vars(r), "row_sorted": r.row_sorted.long()})
+    with pytest.raises(TypeError):
+        moe_combine_weighted(y, bad)
+    bad = Routing(**{**vars(r), "row_sorted": r.row_sorted[:39]})
+    with pytest.raises(ValueError):
+        moe_dispatch(x, bad)
+    bad = Routing(**{**vars(r), "topk_w": r.topk_w[:, :1]})
+    with pytest.raises(ValueError):
+        moe_combine_weighted(y, bad)
+
+
+def test_positions_out_of_range_are_skipped():
+    # the documented contract: a slot outside [0, N*k) moves and adds nothing
+    r, x, y, d = _inputs(12, 64, 8, 2, "f32", "f32")
+    row = r.row_sorted.clone()
+    row[5], row[9] = 24, 2 ** 31 - 1
+    r2 = Routing(**{**vars(r), "row_sorted": row})
+    want = Routing(**{**vars(r), "row_sorted": torch.where(row >= 24, -1, row).int()})
+    x, y, d = x.to(DEV), y.to(DEV), d.to(DEV)
+    z = torch.zeros(24, 64, device=DEV)
+    assert torch.equal(moe_dispatch(x, r2, x_sorted=z.clone()),
+                       moe_dispatch(x, want, x_sorted=z.clone()))
+    assert torch.equal(moe_combine_weighted(y, r2), moe_combine_weighted(y, want))
+    for a, b in zip(moe_combine_weighted_backward(d, y, r2, d_y_sorted=z.clone()),
+                    moe_combine_weighted_backward(d, y, want, d_y_sorted=z.clone())):
+        assert torch.equal(a, b)
