@@ -214,8 +214,10 @@ moe_status_t moe_combine(const void *y_sorted, moe_dtype_t dtype, int64_t n_toke
  * is outside [0, n_tokens * topk) (-1: outside an expert share) move nothing,
  * add nothing and get a zero weight gradient, and sorted rows that no slot
  * points to are left as they were.  dtype and routing->w_dtype are independent.
- * Deterministic, no atomics, no workspace; limits as moe_combine.  Outputs must
- * not overlap inputs.
+ * Deterministic, no atomics, no workspace; limits as moe_combine, and n_tokens *
+ * hidden below 2^32 16-byte chunks (moe_combine_weighted_backward: n_tokens
+ * below 2^24; moe_route_backward: n_tokens * n_experts below 2^32 - 2^10).
+ * Outputs must not overlap inputs.
  *
  * moe_dispatch: x_sorted [N*topk, hidden]; x_sorted[row_sorted[t*topk + j]] =
  *   x[t].  Reads routing->row_sorted only.  Its gradient with respect to x is
@@ -532,8 +534,8 @@ moe_status_t moe_dequantize_int4(const moe_int4_weights_t *w, int32_t n_experts,
  *   moe_experts, the weighted expert rows stay fp32 and the output is rounded
  *   once.  x must be finite (an infinity becomes NaN in its token's row).
  *   Deterministic.
- *   Any batch is right; the kernel is shaped for decode-sized ones, a few rows
- *   an expert.  For prompts, moe_dequantize_int4 once and moe_experts are
+ *   The routing is the whole layer's, not an expert share's.  Any batch is
+ *   right; the kernel is shaped for decode-sized ones, a few rows an expert.  For prompts, moe_dequantize_int4 once and moe_experts are
  *   faster.  workspace: moe_int4_workspace_bytes(...). */
 size_t moe_int4_workspace_bytes(int64_t n_tokens, int32_t n_experts, int32_t topk, int32_t hidden,
                                 int32_t inter);

@@ -827,30 +827,46 @@ def _index(*ts: torch.Tensor) -> int:
     """Device index of tensors that must be contiguous on one GPU."""
     dev = ts[0].get_device()
     for t in ts:
-        if dev < 0 or t.get_device() != dev:
-            raise ValueError("all tensors must be on the same GPU")
-        if not t.is_contiguous():
-            raise ValueError("tensors must be contiguous")
-    return dev
+        if t.get_device() != dev or not t.is_contiguous():
+            break
+    else:
+        if dev >= 0:
+            return dev
+    if any(t.get_device() != dev for t in ts) or dev < 0:
+        raise ValueError("all tensors must be on the same GPU")
+    raise ValueError("tensors must be contiguous")
 
 
 def _raw_stream(dev: int, stream) -> int:
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
+def _like(t: torch.Tensor, stream) -> torch.Tensor:
+    """New memory like ``t`` that belongs to the stream the call runs on."""
+    if stream is None:
+        return torch.empty_like(t)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(t)
+
+
+def _new(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
+def _is(t: torch.Tensor, shape, dtype, dev: int, name: str):
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {tuple(shape)} {dtype} on GPU {dev}, got "
+                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
+
+
 def _output(t, like: torch.Tensor, shape, dtype, stream, name: str) -> torch.Tensor:
-    """The caller's output tensor, checked, or new memory that belongs to the
-    stream the call runs on."""
+    """The caller's output tensor, checked, or new memory."""
     if t is None:
-        if stream is None:
-            if dtype == like.dtype:  # (the quicker calls)
-                return torch.empty_like(like) if shape == like.shape else like.new_empty(shape)
-            return like.new_empty(shape, dtype=dtype)
-        with torch.cuda.stream(stream):
-            return like.new_empty(shape, dtype=dtype)
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous() \
-            or t.device != like.device:
-        raise ValueError(f"{name} must be contiguous {tuple(shape)} {dtype} on {like.device}")
+        return _new(like, shape, dtype, stream)
+    _is(t, shape, dtype, like.get_device(), name)
     return t
 
 
@@ -860,7 +876,7 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def _scratch(ws, like: torch.Tensor, nbytes: int, stream) -> torch.Tensor:
     if ws is None:
-        return _output(None, like, (nbytes,), torch.uint8, stream, "workspace")
+        return _new(like, nbytes, torch.uint8, stream)
     _index(like, ws)
     return _workspace(ws, nbytes, None)
 
@@ -872,34 +888,31 @@ def _new_routing(n: int, e: int, topk: int, like: torch.Tensor, stream) -> Routi
         return Routing.empty(n, e, topk, like.dtype, like.device)
 
 
-def _row_routing(routing: Routing, dev: int, order: str, weights: bool):
-    """The routing fields a row call reads (`order`: row_sorted or topk_idx);
-    returns (N, k, the C struct with just these)."""
-    idx = getattr(routing, order)
+def _row_routing(routing: Routing, dev: int, order: torch.Tensor, name: str, weights: bool):
+    """Checks the routing fields a row call reads (`order`: row_sorted or
+    topk_idx); returns (N, k, topk_w's pointer or None, its dtype)."""
     n, k = routing.topk_idx.shape
-    if idx.numel() != n * k or idx.get_device() != dev or not idx.is_contiguous():
-        raise ValueError(f"routing.{order} must be contiguous with N*k = {n * k} entries on the "
+    if order.numel() != n * k or order.get_device() != dev or not order.is_contiguous():
+        raise ValueError(f"routing.{name} must be contiguous with N*k = {n * k} entries on the "
                          f"GPU of the rows")
-    if idx.dtype != torch.int32:
-        raise TypeError(f"routing.{order} must be int32")
+    if order.dtype is not torch.int32:
+        raise TypeError(f"routing.{name} must be int32")
+    if not weights:
+        return n, k, None, 0
     w = routing.topk_w
-    r = N.MoeRouting()
-    setattr(r, order, idx.data_ptr())
-    if weights:
-        if w.shape != (n, k) or w.get_device() != dev or not w.is_contiguous():
-            raise ValueError("routing.topk_w must be contiguous [N, k] on the GPU of the rows")
-        r.topk_w = w.data_ptr()
-        r.w_dtype = _dt(w)
-    return n, k, r
+    if w.shape != (n, k) or w.get_device() != dev or not w.is_contiguous():
+        raise ValueError("routing.topk_w must be contiguous [N, k] on the GPU of the rows")
+    return n, k, w.data_ptr(), _dt(w)
 
 
 def _dispatch(x, routing, x_sorted, stream) -> _Call:
-    dev = _index(x)
-    n, k, r = _row_routing(routing, dev, "row_sorted", False)
+    dev, order = _index(x), routing.row_sorted
+    n, k, _, _ = _row_routing(routing, dev, order, "row_sorted", False)
     if x.dim() != 2 or x.shape[0] != n:
         raise ValueError("x must be [N, hidden] with the routing's N")
     hidden = x.shape[1]
     x_sorted = _output(x_sorted, x, (n * k, hidden), x.dtype, stream, "x_sorted")
+    r = N.MoeRouting(row_sorted=order.data_ptr())
     args = (x.data_ptr(), _dt(x), n, hidden, k, ctypes.byref(r), x_sorted.data_ptr(),
             _raw_stream(dev, stream))
     return _Call(dev, "moe_dispatch", args, (r, x, x_sorted, routing), x_sorted)
@@ -919,12 +932,13 @@ def moe_dispatch(x: torch.Tensor, routing: Routing, *, x_sorted: Optional[torch.
 
 
 def _combine_weighted(y_sorted, routing, out, stream) -> _Call:
-    dev = _index(y_sorted)
-    n, k, r = _row_routing(routing, dev, "row_sorted", True)
+    dev, order = _index(y_sorted), routing.row_sorted
+    n, k, w, wdt = _row_routing(routing, dev, order, "row_sorted", True)
     if y_sorted.dim() != 2 or y_sorted.shape[0] != n * k:
         raise ValueError("y_sorted must be [N*k, hidden]")
     hidden = y_sorted.shape[1]
     out = _output(out, y_sorted, (n, hidden), y_sorted.dtype, stream, "out")
+    r = N.MoeRouting(topk_w=w, row_sorted=order.data_ptr(), w_dtype=wdt)
     args = (y_sorted.data_ptr(), _dt(y_sorted), n, hidden, k, ctypes.byref(r), out.data_ptr(),
             _raw_stream(dev, stream))
     return _Call(dev, "moe_combine_weighted", args, (r, y_sorted, out, routing), out)
@@ -944,16 +958,19 @@ def moe_combine_weighted(y_sorted: torch.Tensor, routing: Routing, *,
 
 
 def _combine_weighted_backward(d_out, y_sorted, routing, d_y_sorted, d_topk_w, stream) -> _Call:
-    dev = _index(d_out, y_sorted)
-    n, k, r = _row_routing(routing, dev, "row_sorted", True)
+    dev, order = _index(d_out, y_sorted), routing.row_sorted
+    n, k, w, wdt = _row_routing(routing, dev, order, "row_sorted", True)
     if y_sorted.dim() != 2 or y_sorted.shape[0] != n * k:
         raise ValueError("y_sorted must be [N*k, hidden]")
     hidden = y_sorted.shape[1]
     if tuple(d_out.shape) != (n, hidden) or d_out.dtype != y_sorted.dtype:
         raise ValueError("d_out must be [N, hidden] in the dtype of y_sorted")
-    d_y_sorted = _output(d_y_sorted, y_sorted, (n * k, hidden), y_sorted.dtype, stream,
-                         "d_y_sorted")
+    if d_y_sorted is None:
+        d_y_sorted = _like(y_sorted, stream)
+    else:
+        _is(d_y_sorted, (n * k, hidden), y_sorted.dtype, dev, "d_y_sorted")
     d_topk_w = _output(d_topk_w, y_sorted, (n, k), torch.float32, stream, "d_topk_w")
+    r = N.MoeRouting(topk_w=w, row_sorted=order.data_ptr(), w_dtype=wdt)
     args = (d_out.data_ptr(), y_sorted.data_ptr(), _dt(y_sorted), n, hidden, k, ctypes.byref(r),
             d_y_sorted.data_ptr(), d_topk_w.data_ptr(), _raw_stream(dev, stream))
     return _Call(dev, "moe_combine_weighted_backward", args,
@@ -980,12 +997,13 @@ def moe_combine_weighted_backward(d_out: torch.Tensor, y_sorted: torch.Tensor, r
 
 
 def _route_backward(d_topk_w, routing, n_experts, d_logits, stream) -> _Call:
-    dev = _index(d_topk_w)
-    n, k, r = _row_routing(routing, dev, "topk_idx", True)
+    dev, order = _index(d_topk_w), routing.topk_idx
+    n, k, w, wdt = _row_routing(routing, dev, order, "topk_idx", True)
     if tuple(d_topk_w.shape) != (n, k) or d_topk_w.dtype != torch.float32:
         raise ValueError("d_topk_w must be fp32 [N, k]")
     e = routing.n_experts if n_experts is None else n_experts
     d_logits = _output(d_logits, d_topk_w, (n, e), routing.topk_w.dtype, stream, "d_logits")
+    r = N.MoeRouting(topk_idx=order.data_ptr(), topk_w=w, w_dtype=wdt)
     args = (d_topk_w.data_ptr(), n, e, k, ctypes.byref(r), d_logits.data_ptr(),
             _raw_stream(dev, stream))
     return _Call(dev, "moe_route_backward", args, (r, d_topk_w, d_logits, routing), d_logits)
@@ -1041,50 +1059,70 @@ def moe_block_norm_workspace_bytes(n_tokens: int, hidden: int,
 def _block_norm_args(x, y, w_post, w_pre, gate, residual_scale, eps):
     """Checks what both directions take; returns (device, n, hidden, C struct)."""
     here = [t for t in (x, y, w_post, w_pre, gate) if t is not None]
-    dev = _index(*here)
+    dev, dtype = _index(*here), x.dtype
     if x.dim() != 2:
         raise ValueError("x must be [N, hidden]")
-    dtype = x.dtype
     for t in here:
-        if t.dtype != dtype:
+        if t.dtype is not dtype:
             raise TypeError("x, y, the weights and the gate must share a dtype")
-    n, hidden = x.shape
-    if y is not None and y.shape != x.shape:
-        raise ValueError("y must have the shape of x")
-    if w_post is not None and w_post.shape != (hidden,):
-        raise ValueError("w_post must be [hidden]")
-    if w_pre is not None and w_pre.shape != (hidden,):
-        raise ValueError("w_pre must be [hidden]")
-    kind = N.MOE_GATE_NONE
-    if gate is not None:
-        if gate.shape != (n, 1) and gate.shape != (hidden,):
-            raise ValueError("gate must be [N, 1] (a value per token) or [hidden] (per channel)")
-        kind = N.MOE_GATE_CHANNEL if gate.dim() == 1 else N.MOE_GATE_TOKEN
-    if y is None and (w_post is not None or gate is not None):
+    n, hidden = shape = x.shape
+    if y is not None:
+        if y.shape != shape:
+            raise ValueError("y must have the shape of x")
+    elif w_post is not None or gate is not None:
         raise ValueError("w_post and gate need the block's output y")
-    if y is None and w_pre is None:
+    elif w_pre is None:
         raise ValueError("nothing to do without y and w_pre")
-    c = N.MoeBlockNorm(_ptr(w_post), _ptr(w_pre), _ptr(gate), kind, residual_scale, eps)
-    return dev, n, hidden, c
+    post = pre = gp = None
+    kind = N.MOE_GATE_NONE
+    if w_post is not None:
+        if w_post.shape != (hidden,):
+            raise ValueError("w_post must be [hidden]")
+        post = w_post.data_ptr()
+    if w_pre is not None:
+        if w_pre.shape != (hidden,):
+            raise ValueError("w_pre must be [hidden]")
+        pre = w_pre.data_ptr()
+    if gate is not None:
+        if gate.shape == (n, 1):
+            kind = N.MOE_GATE_TOKEN
+        elif gate.shape == (hidden,):
+            kind = N.MOE_GATE_CHANNEL
+        else:
+            raise ValueError("gate must be [N, 1] (a value per token) or [hidden] (per channel)")
+        gp = gate.data_ptr()
+    return dev, n, hidden, N.MoeBlockNorm(post, pre, gp, kind, residual_scale, eps)
 
 
 def _block_norm(x, y, w_post, w_pre, gate, residual_scale, eps, x_out, n_out, rstd_post, rstd_pre,
                 stream) -> _Call:
     dev, n, hidden, c = _block_norm_args(x, y, w_post, w_pre, gate, residual_scale, eps)
-    for name, t, have in (("x_out", x_out, y), ("n_out", n_out, w_pre),
-                          ("rstd_post", rstd_post, w_post), ("rstd_pre", rstd_pre, w_pre)):
-        if t is not None and have is None:
-            raise ValueError(f"the call has no {name}")
-    dtype, f32 = x.dtype, torch.float32
+    f32, xo, no, rpost, rpre = torch.float32, None, None, None, None
     if y is not None:
-        x_out = _output(x_out, x, (n, hidden), dtype, stream, "x_out")
+        if x_out is None:
+            x_out = _like(x, stream)
+        else:
+            _is(x_out, x.shape, x.dtype, dev, "x_out")
+        xo = x_out.data_ptr()
+    elif x_out is not None:
+        raise ValueError("the call has no x_out")
     if w_pre is not None:
-        n_out = _output(n_out, x, (n, hidden), dtype, stream, "n_out")
+        if n_out is None:
+            n_out = _like(x, stream)
+        else:
+            _is(n_out, x.shape, x.dtype, dev, "n_out")
+        no = n_out.data_ptr()
         rstd_pre = _output(rstd_pre, x, (n,), f32, stream, "rstd_pre")
+        rpre = rstd_pre.data_ptr()
+    elif n_out is not None or rstd_pre is not None:
+        raise ValueError("the call has no n_out and rstd_pre")
     if w_post is not None:
         rstd_post = _output(rstd_post, x, (n,), f32, stream, "rstd_post")
-    args = (x.data_ptr(), _ptr(y), _dt(x), n, hidden, ctypes.byref(c), _ptr(x_out), _ptr(n_out),
-            _ptr(rstd_post), _ptr(rstd_pre), _raw_stream(dev, stream))
+        rpost = rstd_post.data_ptr()
+    elif rstd_post is not None:
+        raise ValueError("the call has no rstd_post")
+    args = (x.data_ptr(), _ptr(y), _dt(x), n, hidden, ctypes.byref(c), xo, no, rpost, rpre,
+            _raw_stream(dev, stream))
     res = BlockNorm(x_out, n_out, rstd_post, rstd_pre)
     return _Call(dev, "moe_block_norm", args, (c, x, y, w_post, w_pre, gate, res), res)
 
@@ -1123,37 +1161,57 @@ def _block_norm_backward(d_x_out, d_n_out, x, y, w_post, w_pre, gate, residual_s
                          stream) -> _Call:
     # the gradient takes the saved rstds, so eps no longer matters
     dev, n, hidden, c = _block_norm_args(x, y, w_post, w_pre, gate, residual_scale, 1.0)
-    if d_x_out is None and w_pre is None:
+    dtype, f32, rows, token, width = x.dtype, torch.float32, x.shape, (n,), (hidden,)
+    ins = [None] * 4   # d_x_out, d_n_out, rstd_post, rstd_pre
+    outs = [None] * 4  # d_y, d_w_post, d_w_pre, d_gate
+    if d_x_out is not None:
+        _is(d_x_out, rows, dtype, dev, "d_x_out")
+        ins[0] = d_x_out.data_ptr()
+    elif w_pre is None:
         raise ValueError("no gradient flows in: d_x_out or w_pre with d_n_out is needed")
-    if (d_n_out is None) != (w_pre is None):
-        raise ValueError("d_n_out goes with w_pre")
-    dtype, f32 = x.dtype, torch.float32
-    for name, t, shape, dt, need in (("d_x_out", d_x_out, (n, hidden), dtype, None),
-                                     ("d_n_out", d_n_out, (n, hidden), dtype, w_pre),
-                                     ("rstd_post", rstd_post, (n,), f32, w_post),
-                                     ("rstd_pre", rstd_pre, (n,), f32, w_pre)):
-        if t is not None:
-            _output(t, x, shape, dt, stream, name)
-        elif need is not None:
-            raise ValueError(f"{name} of the forward call is needed")
-    for name, t, have in (("d_y", d_y, y), ("d_w_post", d_w_post, w_post),
-                          ("d_w_pre", d_w_pre, w_pre), ("d_gate", d_gate, gate)):
-        if t is not None and have is None:
-            raise ValueError(f"the call has no {name}")
-    d_x = _output(d_x, x, (n, hidden), dtype, stream, "d_x")
-    if y is not None:
-        d_y = _output(d_y, x, (n, hidden), dtype, stream, "d_y")
-    if w_post is not None:
-        d_w_post = _output(d_w_post, x, (hidden,), f32, stream, "d_w_post")
     if w_pre is not None:
-        d_w_pre = _output(d_w_pre, x, (hidden,), f32, stream, "d_w_pre")
+        if d_n_out is None or rstd_pre is None:
+            raise ValueError("d_n_out and the forward call's rstd_pre go with w_pre")
+        _is(d_n_out, rows, dtype, dev, "d_n_out")
+        _is(rstd_pre, token, f32, dev, "rstd_pre")
+        ins[1], ins[3] = d_n_out.data_ptr(), rstd_pre.data_ptr()
+        d_w_pre = _output(d_w_pre, x, width, f32, stream, "d_w_pre")
+        outs[2] = d_w_pre.data_ptr()
+    elif d_n_out is not None or d_w_pre is not None:
+        raise ValueError("d_n_out and d_w_pre go with w_pre")
+    if w_post is not None:
+        if rstd_post is None:
+            raise ValueError("the forward call's rstd_post goes with w_post")
+        _is(rstd_post, token, f32, dev, "rstd_post")
+        ins[2] = rstd_post.data_ptr()
+        d_w_post = _output(d_w_post, x, width, f32, stream, "d_w_post")
+        outs[1] = d_w_post.data_ptr()
+    elif d_w_post is not None:
+        raise ValueError("d_w_post goes with w_post")
     if gate is not None:
         d_gate = _output(d_gate, x, gate.shape, f32, stream, "d_gate")
-    ws = _scratch(workspace, x, moe_block_norm_workspace_bytes(n, hidden, dtype), stream)
-    args = (_ptr(d_x_out), _ptr(d_n_out), x.data_ptr(), _ptr(y), _dt(x), n, hidden,
-            ctypes.byref(c), _ptr(rstd_post), _ptr(rstd_pre), d_x.data_ptr(), _ptr(d_y),
-            _ptr(d_w_post), _ptr(d_w_pre), _ptr(d_gate), ws.data_ptr(), _nbytes(ws),
-            _raw_stream(dev, stream))
+        outs[3] = d_gate.data_ptr()
+    elif d_gate is not None:
+        raise ValueError("d_gate goes with gate")
+    if d_x is None:
+        d_x = _like(x, stream)
+    else:
+        _is(d_x, rows, dtype, dev, "d_x")
+    if y is not None:
+        if d_y is None:
+            d_y = _like(x, stream)
+        else:
+            _is(d_y, rows, dtype, dev, "d_y")
+        outs[0] = d_y.data_ptr()
+    elif d_y is not None:
+        raise ValueError("d_y goes with y")
+    dt = _dt(x)
+    need = N.load().moe_block_norm_workspace_bytes(n, hidden, dt)
+    if need == 0:
+        raise MoeError(N.MOE_ERR_SHAPE, "moe_block_norm_backward")
+    ws = _scratch(workspace, x, need, stream)
+    args = (ins[0], ins[1], x.data_ptr(), _ptr(y), dt, n, hidden, ctypes.byref(c), ins[2], ins[3],
+            d_x.data_ptr(), *outs, ws.data_ptr(), _nbytes(ws), _raw_stream(dev, stream))
     res = BlockNormGrads(d_x, d_y, d_w_post, d_w_pre, d_gate)
     return _Call(dev, "moe_block_norm_backward", args,
                  (c, d_x_out, d_n_out, x, y, w_post, w_pre, gate, rstd_post, rstd_pre, res, ws),
@@ -1290,18 +1348,21 @@ def moe_quantize_int4(w: torch.Tensor, group: int = 128, *, zeros: bool = True, 
 
 def _int4_weights(q, s, z, name: str):
     """Checks one weight array; returns (E, rows, K, group, the C struct)."""
-    if q.dtype != torch.uint8 or s.dtype != torch.bfloat16 or q.dim() != 3 or s.dim() != 3:
+    if q.dtype is not torch.uint8 or s.dtype is not torch.bfloat16 or q.dim() != 3 or s.dim() != 3:
         raise TypeError(f"{name}: expected uint8 codes [E, rows, K/2] and bf16 scales "
                         f"[E, K/group, rows]")
     e, rows, half = q.shape
-    ng, k = s.shape[1], 2 * half
+    es, ng, rs = s.shape
+    k = 2 * half
     group = k // ng if ng else 0
-    if group not in _INT4_GROUPS or k != ng * group or s.shape != (e, ng, rows):
+    if group not in _INT4_GROUPS or k != ng * group or es != e or rs != rows:
         raise ValueError(f"{name}: scales {tuple(s.shape)} do not give groups of 32, 64 or 128 "
                          f"of codes {tuple(q.shape)}")
-    if z is not None and (z.dtype != torch.uint8 or z.shape != s.shape):
+    if z is None:
+        return e, rows, k, group, N.MoeInt4Weights(q.data_ptr(), s.data_ptr(), None)
+    if z.dtype is not torch.uint8 or z.shape != s.shape:
         raise ValueError(f"{name}: zeros must be uint8 in the shape of the scales")
-    return e, rows, k, group, N.MoeInt4Weights(q.data_ptr(), s.data_ptr(), _ptr(z))
+    return e, rows, k, group, N.MoeInt4Weights(q.data_ptr(), s.data_ptr(), z.data_ptr())
 
 
 def moe_dequantize_int4(q: torch.Tensor, scales: torch.Tensor,
@@ -1325,7 +1386,7 @@ def moe_int4_workspace_bytes(n_tokens: int, n_experts: int, topk: int, hidden: i
 
 def _int4_layer(x, w13, w2, act, layout):
     """Checks the layer; returns (device, n, hidden, E, inter, group, structs)."""
-    dev = _index(x, *(t for t in (*w13, *w2) if t is not None))
+    dev = _index(x, *[t for t in (*w13, *w2) if t is not None])
     if act not in ACTS:
         raise ValueError(f"unknown activation {act!r}")
     if layout not in LAYOUTS:
@@ -1346,18 +1407,21 @@ def _int4_layer(x, w13, w2, act, layout):
 def _experts_int4(x, w13, w2, routing, act, layout, params, out, workspace, stream) -> _Call:
     dev, n, hidden, e, inter, group, c13, c2 = _int4_layer(x, w13, w2, act, layout)
     k = routing.topk
-    m = n * k
-    for f, size in (("offsets", e + 1), ("col_sorted", m), ("row_sorted", m), ("gate_scal", m)):
-        t = getattr(routing, f)
-        if t.shape != (size,) or t.get_device() != dev or not t.is_contiguous():
-            raise ValueError(f"routing.{f} must be contiguous [{size}] on the GPU of x")
-        if f != "gate_scal" and t.dtype != torch.int32:
-            raise TypeError(f"routing.{f} must be int32")
-    out = _output(out, x, (n, hidden), x.dtype, stream, "out")
+    off, col, row, scal = (routing.offsets, routing.col_sorted, routing.row_sorted,
+                           routing.gate_scal)
+    if _index(off, col, row, scal) != dev:
+        raise ValueError("the routing must be on the GPU of x")
+    if off.numel() != e + 1 or not col.numel() == row.numel() == scal.numel() == n * k:
+        raise ValueError(f"the routing is not one of {n} tokens and {e} experts")
+    if not off.dtype is col.dtype is row.dtype is torch.int32:
+        raise TypeError("the routing's offsets, col_sorted and row_sorted must be int32")
+    if out is None:
+        out = _like(x, stream)
+    else:
+        _is(out, x.shape, x.dtype, dev, "out")
     ws = _scratch(workspace, x, moe_int4_workspace_bytes(n, e, k, hidden, inter), stream)
-    r = N.MoeRouting(None, None, None, None, routing.offsets.data_ptr(),
-                     routing.col_sorted.data_ptr(), routing.row_sorted.data_ptr(),
-                     routing.gate_scal.data_ptr(), _dt(routing.gate_scal))
+    r = N.MoeRouting(None, None, None, None, off.data_ptr(), col.data_ptr(), row.data_ptr(),
+                     scal.data_ptr(), _dt(scal))
     p = _params(params)
     args = (x.data_ptr(), n, hidden, ctypes.byref(c13), ctypes.byref(c2), e, inter, k, group,
             ACTS[act], LAYOUTS[layout], ctypes.byref(p) if p else None, ctypes.byref(r),

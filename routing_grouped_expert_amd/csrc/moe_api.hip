@@ -112,6 +112,9 @@ moe_status_t check_ptrs(std::initializer_list<const void *> ptrs) {
   return MOE_OK;
 }
 
+// Threads of a launch, in whole workgroups of up to 1024.
+constexpr int64_t kMostThreads = 0xffffffffLL - 1023;
+
 // Sizes and types of the calls that move rows between token and sorted order.
 moe_status_t check_rows(moe_dtype_t dtype, int64_t n, int32_t hidden, int32_t k,
                         const moe_routing_t *routing, bool weights) {
@@ -119,8 +122,8 @@ moe_status_t check_rows(moe_dtype_t dtype, int64_t n, int32_t hidden, int32_t k,
   if (st != MOE_OK) return st;
   if (check_ffn_sizes(hidden, 8) != MOE_OK) return MOE_ERR_SHAPE;
   if (!dtype_ok(dtype)) return MOE_ERR_DTYPE;
-  // one thread per 16-byte chunk of a token row: below 2^31 workgroups of 256
-  if (n * hidden * (int64_t)dsize(dtype) / 16 > 0x7fffffffLL * 256) return MOE_ERR_SHAPE;
+  // one thread per 16-byte chunk of a token row, and a grid's threads are counted in 32 bits
+  if (n * hidden * (int64_t)dsize(dtype) / 16 > kMostThreads) return MOE_ERR_SHAPE;
   if (!routing) return MOE_ERR_NULL;
   return weights && !dtype_ok(routing->w_dtype) ? MOE_ERR_DTYPE : MOE_OK;
 }
@@ -464,6 +467,7 @@ moe_status_t moe_combine_weighted_backward(const void *d_out, const void *y_sort
                                            void *d_y_sorted, float *d_topk_w, void *stream) {
   moe_status_t st = check_rows(dtype, n_tokens, hidden, topk, routing, true);
   if (st != MOE_OK || n_tokens == 0) return st;
+  if (n_tokens * 256 > kMostThreads) return MOE_ERR_SHAPE;  // up to four waves a token
   if ((st = check_ptrs({d_out, y_sorted, routing->row_sorted, routing->topk_w, d_y_sorted,
                         d_topk_w})) != MOE_OK)
     return st;
@@ -480,6 +484,7 @@ moe_status_t moe_route_backward(const float *d_topk_w, int64_t n_tokens, int32_t
                                 void *stream) {
   moe_status_t st = check_sizes(n_tokens, n_experts, topk);
   if (st != MOE_OK) return st;
+  if (n_tokens * n_experts > kMostThreads) return MOE_ERR_SHAPE;
   if (!routing) return MOE_ERR_NULL;
   if (!dtype_ok(routing->w_dtype)) return MOE_ERR_DTYPE;
   if (n_tokens == 0) return MOE_OK;
@@ -788,8 +793,8 @@ moe_status_t run_int4(const void *x, int64_t n, int32_t hidden, const moe_int4_w
 moe_status_t check_int4_array(int32_t e, int32_t rows, int32_t k, int32_t group) {
   if (e < 1 || rows < 1 || k < 1 || k > (1 << 24) || !group_ok(group) || k % group)
     return MOE_ERR_SHAPE;
-  // one thread per eight weights at most: below 2^31 workgroups of 256
-  if ((int64_t)e * rows > 0x7fffffffLL * 256 / (k / 8)) return MOE_ERR_SHAPE;
+  // one thread per eight weights at most
+  if ((int64_t)e * rows > kMostThreads / (k / 8)) return MOE_ERR_SHAPE;
   return MOE_OK;
 }
 }  // namespace

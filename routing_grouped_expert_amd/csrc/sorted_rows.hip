@@ -126,19 +126,19 @@ __global__ __launch_bounds__(kThreads) void combine_weighted_backward_kernel(
   constexpr int CH = chunk_elems<T>(), TPB = kThreads / 64 / WPT;  // tokens a workgroup
   __shared__ float part[kThreads / 64][JB];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  // (tokens past the last repeat it, so that every wave reaches the barriers)
-  const int64_t mine = (int64_t)blockIdx.x * TPB + wave / WPT, t = mine < N ? mine : N - 1;
+  const int64_t t = (int64_t)blockIdx.x * TPB + wave / WPT;
+  const bool live = t < N;  // (waves past the last token still reach the barriers)
   const int nch = H / CH, first = wave % WPT * 64 + lane;
   for (int j0 = 0; j0 < K; j0 += JB) {
     uint32_t p[JB];
-    slot_rows<JB>(row_sorted, t, K, j0, (uint32_t)(N * K), p);
+    slot_rows<JB>(row_sorted, t, live ? K : 0, j0, (uint32_t)(N * K), p);
     float wj[JB], dot[JB];
 #pragma unroll
     for (int j = 0; j < JB; ++j) {
       wj[j] = p[j] != kNone ? weight_at(w, w_bf16, t * K + j0 + j) : 0.f;
       dot[j] = 0.f;
     }
-    for (int c = first; c < nch; c += 64 * WPT) {
+    for (int c = first; live && c < nch; c += 64 * WPT) {
       const int64_t at = (int64_t)c * CH;
       const u32x4_t dv = *reinterpret_cast<const u32x4_t *>(d_out + t * H + at);
       u32x4_t v[JB];
@@ -167,14 +167,14 @@ __global__ __launch_bounds__(kThreads) void combine_weighted_backward_kernel(
     if constexpr (WPT == 1) {
 #pragma unroll
       for (int j = 0; j < JB; ++j)
-        if (lane == 0 && j0 + j < K) dw[t * K + j0 + j] = dot[j];
+        if (live && lane == 0 && j0 + j < K) dw[t * K + j0 + j] = dot[j];
     } else {
       if (j0 > 0) __syncthreads();
 #pragma unroll
       for (int j = 0; j < JB; ++j)
         if (lane == 0) part[wave][j] = dot[j];
       __syncthreads();
-      if (wave % WPT == 0 && lane < JB && j0 + lane < K) {
+      if (live && wave % WPT == 0 && lane < JB && j0 + lane < K) {
         float s = part[wave][lane];
 #pragma unroll
         for (int q = 1; q < WPT; ++q) s += part[wave + q][lane];

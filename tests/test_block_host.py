@@ -50,6 +50,9 @@ def test_row_calls(lib):
         for bad in ({"h": 0}, {"h": 12}, {"h": -8}, {"k": 0}, {"k": 17}, {"n": -1},
                     {"n": 1 << 30, "k": 2}, {"h": (1 << 24) + 8}):
             assert call(**bad) == N.MOE_ERR_SHAPE, bad
+        # more 16-byte chunks than a grid has threads
+        assert call(n=1 << 23, h=1 << 14, k=1) == N.MOE_ERR_SHAPE
+    assert backward(n=1 << 24, h=8, k=1) == N.MOE_ERR_SHAPE
     for call in (combine, backward):
         assert call(r=routing({"topk_w": None})) == N.MOE_ERR_NULL
         assert call(r=routing(w_dtype=5)) == N.MOE_ERR_DTYPE
@@ -64,7 +67,7 @@ def test_row_calls(lib):
     assert softmax(o=MISALIGNED) == N.MOE_ERR_ALIGN
     assert softmax(r=routing({"topk_idx": None})) == N.MOE_ERR_NULL
     assert softmax(r=routing(w_dtype=9)) == N.MOE_ERR_DTYPE
-    for bad in ({"e": 0}, {"e": 257}, {"k": 9}, {"n": -1}):
+    for bad in ({"e": 0}, {"e": 257}, {"k": 9}, {"n": -1}, {"n": 1 << 25, "e": 128}):
         assert softmax(**bad) == N.MOE_ERR_SHAPE, bad
 
 
