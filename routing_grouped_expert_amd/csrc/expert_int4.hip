@@ -33,13 +33,14 @@
 // and, for groups of 32 and 64, lane swaps bring the dwords to the lanes whose
 // product they belong to, so that no product mixes two groups.
 //
-// What bounds it: vector instructions and products (one after the other, about
-// 230 and 24 a step of 8192 weights) at one token, the loads' rate from eight
-// tokens on.  Measured against the bytes of the touched experts: 64 experts
-// (H 4096, I 1536, k 8), 32 tokens, groups of 128: 145 us, 4.2 TB/s; 128 experts
-// (H = I = 2880, k 4), groups of 64 with zero points: 128 tokens 413 us, 4.1
-// TB/s, 33 tokens 350 us, 3.2 TB/s (rows of 1440 bytes straddle cache lines;
-// 2816 wide 3.8 TB/s), one token 26 us.
+// What bounds it: the rate of the loads, and about 230 vector instructions and
+// 24 products, one after the other, a step of 8192 weights; at one token the
+// start of three kernels and of their loads.  Measured against the bytes of the
+// touched experts: 64 experts (H 4096, I 1536, k 8), 32 tokens, groups of 128:
+// 147 us, 4.2 TB/s; 128 experts (H = I = 2880, k 4), groups of 64 with zero
+// points: 128 tokens 420 us, 4.1 TB/s, 33 tokens 354 us, 3.2 TB/s (rows of 1440
+// bytes straddle cache lines: 2816 wide 3.8 TB/s; the loads alone 319 us), one
+// token 25 us (the loads alone 21, three empty kernels 10).
 #include "gemm_common.h"
 #include "lds_dma.h"
 #include "rows.h"
@@ -162,30 +163,14 @@ __device__ __forceinline__ void place(int &x, int &y) {
 
 constexpr int kStepK = 256;  // weights of a row a step: one 128-byte line of codes
 
-// One wave's 32 weight rows (two tiles of 16) of one expert: where they are,
-// and the products of a step of them with the token rows in LDS.  With NQ = 1
-// all 16 rows of a product are one token row, and one of a lane's four results
-// is taken.
-template <int GS, int NQ> struct WaveRows {
-  static constexpr int NM = GS == 1 ? 2 : 1;  // loads of four groups' scales a step and tile
-
-  struct Codes {  // a step of the rows
-    u32x4_t w[2][2];
-    uint32_t s[2][NM], z[2][NM];
-  };
-
-  __amdgpu_buffer_rsrc_t rq, rs, rz;
+// One expert's weight arrays as a wave reads them.
+template <int GS> struct ExpertArrays {
+  __amdgpu_buffer_rsrc_t rq, rs, rz;  // (without zero points rz is empty: loads give 0)
   bool has_z;
-  uint32_t nrows, qoff[2], moff[2], magic, mask;
+  uint32_t nrows, magic, mask;
   int lane, K;
 
-  // memrow(t, x): memory row of row x of tile t.  Codes: four lanes a row, 64
-  // bytes; a lane permutation puts them where the products want them.  Scales
-  // and zero points: lane group h loads the step's groups h (and h + 4).  Loads
-  // past K bring other rows' data, or zeros past the array's end; they are not
-  // used.
-  template <typename F> __device__ __forceinline__ void init(const Int4Args &g, int e, int rows,
-                                                             F memrow) {
+  __device__ __forceinline__ void open(const Int4Args &g, int e, int rows) {
     lane = threadIdx.x & 63;
     K = g.K;
     nrows = (uint32_t)rows;
@@ -197,31 +182,62 @@ template <int GS, int NQ> struct WaveRows {
                                            (int)(2 * sn), kRsrcWord3);
     rz = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(g.z) + (has_z ? (size_t)e * sn : 0),
                                            (short)0, has_z ? (int)sn : 0, kRsrcWord3);
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      qoff[t] = (uint32_t)memrow(t, lane >> 2) * (uint32_t)(K / 2) + (uint32_t)((lane & 3) * 16);
-      moff[t] = (uint32_t)(lane >> 4) * nrows + (uint32_t)memrow(t, lane & 15);
-    }
     magic = 0x43004300u;
     mask = 0x000f000fu;
     asm("" : "+v"(magic));  // (no instruction: hides the values, see codes_plus_128)
     asm("" : "+s"(mask));
   }
+  __device__ __forceinline__ u32x4_t codes(uint32_t at) const {
+    return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rq, (int)at, 0, 0));
+  }
+  __device__ __forceinline__ uint32_t scale(uint32_t at) const {  // bf16 bits
+    return (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, (int)(2 * at), 0, 0);
+  }
+  __device__ __forceinline__ uint32_t zero(uint32_t at) const {
+    return (uint32_t)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rz, (int)at, 0, 0);
+  }
+};
+
+// One wave's 32 weight rows (two tiles of 16) of one expert: where they are,
+// and the products of a step of them with the token rows in LDS.
+template <int GS> struct WaveRows : ExpertArrays<GS> {
+  using A = ExpertArrays<GS>;
+  static constexpr int NM = GS == 1 ? 2 : 1;  // loads of four groups' scales a step and tile
+
+  struct Codes {  // a step of the rows
+    u32x4_t w[2][2];
+    uint32_t s[2][NM], z[2][NM];
+  };
+
+  uint32_t qoff[2], moff[2];
+
+  // memrow(t, x): memory row of row x of tile t.  Codes: four lanes a row, 64
+  // bytes; a lane permutation puts them where the products want them.  Scales
+  // and zero points: lane group h loads the step's groups h (and h + 4).  Loads
+  // past K bring other rows' data, or zeros past the array's end; they are not
+  // used.
+  template <typename F> __device__ __forceinline__ void init(const Int4Args &g, int e, int rows,
+                                                             F memrow) {
+    A::open(g, e, rows);
+    const int lane = A::lane;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      qoff[t] = (uint32_t)memrow(t, lane >> 2) * (uint32_t)(A::K / 2) + (uint32_t)((lane & 3) * 16);
+      moff[t] = (uint32_t)(lane >> 4) * A::nrows + (uint32_t)memrow(t, lane & 15);
+    }
+  }
 
   __device__ __forceinline__ void load(Codes &c, int step) const {
-    const uint32_t k0 = (uint32_t)step * kStepK, g0 = k0 / (32 * GS) * nrows;
+    const uint32_t k0 = (uint32_t)step * kStepK, g0 = k0 / (32 * GS) * A::nrows;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
-        c.w[t][b] = __builtin_bit_cast(
-            u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rq, (int)(qoff[t] + k0 / 2 + 64 * b), 0, 0));
+      for (int b = 0; b < 2; ++b) c.w[t][b] = A::codes(qoff[t] + k0 / 2 + 64 * b);
 #pragma unroll
       for (int m = 0; m < NM; ++m) {
-        const uint32_t at = moff[t] + g0 + 4 * m * nrows;
-        c.s[t][m] = (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, (int)(2 * at), 0, 0);
-        c.z[t][m] =
-            has_z ? (uint32_t)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rz, (int)at, 0, 0) : 8u;
+        const uint32_t at = moff[t] + g0 + 4 * m * A::nrows;
+        c.s[t][m] = A::scale(at);
+        c.z[t][m] = A::has_z ? A::zero(at) : 8u;
       }
     }
   }
@@ -232,8 +248,8 @@ template <int GS, int NQ> struct WaveRows {
   template <bool kWhole>
   __device__ __forceinline__ void work(const Codes &c, int step, const char *tok, int x,
                                        f32x4_t (&acc)[2]) const {
-    const int h = lane >> 4, from = (4 * (lane & 15) + h) * 4;
-    const int ngroups = kWhole ? 8 / GS : (K - step * kStepK) / (32 * GS);
+    const int h = A::lane >> 4, from = (4 * (A::lane & 15) + h) * 4;
+    const int ngroups = kWhole ? 8 / GS : (A::K - step * kStepK) / (32 * GS);
     const bf16x8_t ones = __builtin_bit_cast(
         bf16x8_t, u32x4_t{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u});
     uint32_t mt[2][4 * NM];  // scale << 16 | zero point of each group
@@ -269,15 +285,14 @@ template <int GS, int NQ> struct WaveRows {
 #pragma unroll
         for (int t = 0; t < 2; ++t)
           sum[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              av, codes_plus_128(cw[t][j], mask, magic), begins ? zero : sum[t], 0, 0, 0);
+              av, codes_plus_128(cw[t][j], A::mask, A::magic), begins ? zero : sum[t], 0, 0, 0);
         if (j % GS == GS - 1) {
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             const float f = __uint_as_float(mt[t][gr] & 0xffff0000u);
             const float z = 128.f + (float)(mt[t][gr] & 0xffu);
 #pragma unroll
-            for (int q = 0; q < NQ; ++q)
-              acc[t][q] = fmaf(f, fmaf(-z, tot[q], sum[t][q]), acc[t][q]);
+            for (int q = 0; q < 4; ++q) acc[t][q] = fmaf(f, fmaf(-z, tot[q], sum[t][q]), acc[t][q]);
           }
         }
       }
@@ -290,8 +305,101 @@ template <int GS, int NQ> struct WaveRows {
                                          const char *tok0, int x, f32x4_t (&acc)[2]) const {
     auto run = [&](const Codes &c, int step) {
       const char *tok = tok0 + (step - s0) * (2 * kStepK);
-      if ((step + 1) * kStepK <= K) work<true>(c, step, tok, x, acc);
+      if ((step + 1) * kStepK <= A::K) work<true>(c, step, tok, x, acc);
       else work<false>(c, step, tok, x, acc);
+    };
+    for (int step = first; step < last; step += 2) {
+      run(c0, step);
+      if (step + 1 >= last) break;
+      if (step + 2 < last) load(c0, step + 2);
+      run(c1, step + 1);
+      if (step + 3 < last) load(c1, step + 3);
+    }
+  }
+};
+
+// acc + a.lo * b.lo + a.hi * b.hi on packed bf16 pairs (v_dot2_f32_bf16).
+__device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float acc) {
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, a),
+                                         __builtin_bit_cast(bf16x2_t, b), acc, false);
+}
+
+// The same rows for a single token row, where a product of 16 token rows would
+// compute one: dot products, every lane its own 32 weights of a row (lane l:
+// row l / 4 of a tile, piece l % 4 of 128 weights) with the token's values at
+// those places, the scale and zero point of the lane's own group, and one sum
+// over the four lanes of a row at the end.  The lanes keep what they load: no
+// permutation, no swaps (one token of 128 experts, groups of 64: 25.9 -> 24.8
+// us; of 32 experts, groups of 32: 29.0 -> 25.1).
+template <int GS> struct DotRows : ExpertArrays<GS> {
+  using A = ExpertArrays<GS>;
+  struct Codes {  // a step of the rows
+    u32x4_t w[2][2];
+    uint32_t s[2][2], z[2][2];
+  };
+
+  uint32_t qoff[2], mrow[2];
+
+  template <typename F> __device__ __forceinline__ void init(const Int4Args &g, int e, int rows,
+                                                             F memrow) {
+    A::open(g, e, rows);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      mrow[t] = (uint32_t)memrow(t, A::lane >> 2);
+      qoff[t] = mrow[t] * (uint32_t)(A::K / 2) + (uint32_t)((A::lane & 3) * 16);
+    }
+  }
+
+  __device__ __forceinline__ void load(Codes &c, int step) const {
+    const uint32_t k0 = (uint32_t)step * kStepK;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const uint32_t piece = k0 + 128 * b + 32 * (uint32_t)(A::lane & 3);
+        c.w[t][b] = A::codes(qoff[t] + k0 / 2 + 64 * b);
+        c.s[t][b] = A::scale(piece / (32 * GS) * A::nrows + mrow[t]);
+        c.z[t][b] = A::zero(piece / (32 * GS) * A::nrows + mrow[t]);
+      }
+  }
+
+  // acc[t] += the lane's part of row lane / 4 of tile t; tok: the token row at
+  // this step, sums: the sums of its pieces of 32.
+  __device__ __forceinline__ void work(const Codes &c, int step, const char *tok,
+                                       const float *sums, float (&acc)[2]) const {
+    const float zero0 = A::has_z ? 128.f : 136.f;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      // (a piece past K: the loads brought anything, nothing is added)
+      const bool in = step * kStepK + 128 * b + 32 * (A::lane & 3) < A::K;
+      const float total = sums[4 * b + (A::lane & 3)];
+      float dot[2] = {0.f, 0.f};
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        const u32x4_t av = *reinterpret_cast<const u32x4_t *>(tok + 256 * b + (A::lane & 3) * 64 + 16 * d);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const u32x4_t wv =
+              __builtin_bit_cast(u32x4_t, codes_plus_128(c.w[t][b][d], A::mask, A::magic));
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            dot[t] = dot2(wv[i], av[i], dot[t]);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const float f = __uint_as_float(c.s[t][b] << 16), z = zero0 + (float)c.z[t][b];
+        const float v = fmaf(f, fmaf(-z, total, dot[t]), acc[t]);
+        acc[t] = in ? v : acc[t];
+      }
+    }
+  }
+
+  __device__ __forceinline__ void stream(Codes &c0, Codes &c1, int first, int last, int s0,
+                                         const char *tok0, const float *sums0,
+                                         float (&acc)[2]) const {
+    auto run = [&](const Codes &c, int step) {
+      work(c, step, tok0 + (step - s0) * (2 * kStepK), sums0 + (step - s0) * (kStepK / 32), acc);
     };
     for (int step = first; step < last; step += 2) {
       run(c0, step);
@@ -329,6 +437,25 @@ __device__ __forceinline__ void stage_rows(const Int4Args &g, char *lds, int row
   }
 }
 
+// The epilogue of sorted row p's column: v0 (gated: and v1, the up value) are
+// the products.
+template <int EPI>
+__device__ __forceinline__ void finish(const Int4Args &g, int p, int col, float v0, float v1) {
+  if constexpr (EPI == EPI_Y || EPI == EPI_OUT) {
+    const float y = v0 * weight_at(g.gate_scal, g.gate_bf16, p);
+    if (EPI == EPI_Y)  // summed over the slots by sum_slots_kernel, in fp32
+      reinterpret_cast<float *>(g.C)[(size_t)p * g.Nout + col] = y;
+    else               // one slot a token: entry == token
+      reinterpret_cast<bf16_t *>(g.C)[(size_t)g.col_sorted[p] * g.Nout + col] = bf16_rne(y);
+  } else {
+    const float nal = -g.prm.alpha * 1.44269504088896341f;
+    float a = act_val<EPI>(v0, v1, nal, g.prm);
+    // the clamps and the rectifier drop a NaN; the token's row shall show it
+    if (__builtin_isnan(v0) || __builtin_isnan(v1)) a = __builtin_nanf("");
+    reinterpret_cast<bf16_t *>(g.C)[(size_t)p * g.Nout + col] = bf16_rne(a);
+  }
+}
+
 // GS = G / 32; TR: token rows held at a time.  A wave streams 32 weight rows;
 // ks waves share them and split the steps; the workgroup's waves / ks column
 // groups share the token rows in LDS, kc values of each at a time.
@@ -357,8 +484,7 @@ expert_int4_kernel(Int4Args g, int ks, int kc) {
 
   // Gated: tile 0 the gate rows of 16 columns, tile 1 their up rows; plain: two
   // runs of 16 columns.
-  constexpr int NQ = TR < 4 ? TR : 4;
-  WaveRows<GS, NQ> rows;
+  WaveRows<GS> rows;
   rows.init(g, e, kPlain ? Nout : 2 * Nout, [&](int t, int x) {
     return kPlain ? n0 + 16 * t + x : g.interleaved ? 2 * (n0 + x) + t : t * Nout + n0 + x;
   });
@@ -372,7 +498,7 @@ expert_int4_kernel(Int4Args g, int ks, int kc) {
       const int klen = min(kc, K - kb);
       const int s0 = kb / kStepK, ns = (klen + kStepK - 1) / kStepK, per = (ns + ks - 1) / ks;
       const int first = s0 + min(kw * per, ns), last = live ? s0 + min(kw * per + per, ns) : first;
-      typename WaveRows<GS, NQ>::Codes c0, c1;
+      typename WaveRows<GS>::Codes c0, c1;
       if (first < last) rows.load(c0, first);
       if (first + 1 < last) rows.load(c1, first + 1);
       if (a0 > 0 || kb > 0) __syncthreads();
@@ -394,7 +520,7 @@ expert_int4_kernel(Int4Args g, int ks, int kc) {
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int q = 0; q < NQ; ++q) red[((wave * 2 + t) * TR + 4 * h + q) * 17 + r] = acc[t][q];
+        for (int q = 0; q < 4; ++q) red[((wave * 2 + t) * TR + 4 * h + q) * 17 + r] = acc[t][q];
     }
     __syncthreads();
     for (int i = kw * 64 + lane; i < na * COLS && live; i += ks * 64) {
@@ -404,25 +530,81 @@ expert_int4_kernel(Int4Args g, int ks, int kc) {
         for (int w = cg * ks; w < cg * ks + ks; ++w) v += red[((w * 2 + t) * TR + trow) * 17 + c];
         return v;
       };
-      const size_t p = (size_t)(row0 + a0 + trow);
-      if constexpr (EPI == EPI_Y || EPI == EPI_OUT) {
-        const float y =
-            part(col >> 4, col & 15) * weight_at(g.gate_scal, g.gate_bf16, (int64_t)p);
-        if (EPI == EPI_Y)  // summed over the slots by sum_slots_kernel, in fp32
-          reinterpret_cast<float *>(g.C)[p * Nout + n0 + col] = y;
-        else               // one slot a token: entry == token
-          reinterpret_cast<bf16_t *>(g.C)[(size_t)g.col_sorted[p] * Nout + n0 + col] = bf16_rne(y);
-      } else {
-        const float v0 = part(kPlain ? col >> 4 : 0, col & 15);
-        const float v1 = kPlain ? v0 : part(1, col & 15);
-        const float nal = -g.prm.alpha * 1.44269504088896341f;
-        float a = act_val<EPI>(v0, v1, nal, g.prm);
-        // the clamps and the rectifier drop a NaN; the token's row shall show it
-        if (__builtin_isnan(v0) || __builtin_isnan(v1)) a = __builtin_nanf("");
-        reinterpret_cast<bf16_t *>(g.C)[p * Nout + n0 + col] = bf16_rne(a);
-      }
+      finish<EPI>(g, row0 + a0 + trow, n0 + col, part(kPlain ? col >> 4 : 0, col & 15),
+                  kPlain ? 0.f : part(1, col & 15));
     }
   }
+}
+
+// One token (its expert's only row): as expert_int4_kernel, on DotRows.
+template <int EPI, int GS>
+__global__ __launch_bounds__(512) void expert_int4_one_kernel(Int4Args g, int ks, int kc) {
+  constexpr bool kPlain = EPI == EPI_Y || EPI == EPI_OUT || EPI == EPI_RELU2;
+  constexpr int COLS = kPlain ? 32 : 16;
+  __shared__ int sel[3];
+  __shared__ float red[8][2][16];
+  extern __shared__ __attribute__((aligned(16))) char lds[];  // [kc] bf16, [kc / 32] fp32
+  int place_x, want;
+  place(place_x, want);
+  find_expert(g.offsets, g.E, want, sel);
+  const int e = __builtin_amdgcn_readfirstlane(sel[0]);
+  if (e < 0) return;  // the whole workgroup
+  const int p = __builtin_amdgcn_readfirstlane(sel[1]);
+
+  const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int K = g.K, Nout = g.Nout;
+  const int cg = wave / ks, kw = wave % ks;
+  const int n0 = (place_x * (waves / ks) + cg) * COLS;
+  const bool live = n0 < Nout;
+  DotRows<GS> rows;
+  rows.init(g, e, kPlain ? Nout : 2 * Nout, [&](int t, int x) {
+    return kPlain ? n0 + 16 * t + x : g.interleaved ? 2 * (n0 + x) + t : t * Nout + n0 + x;
+  });
+  float *sums = reinterpret_cast<float *>(lds + 2 * kc);
+  float acc[2] = {0.f, 0.f};
+  for (int kb = 0; kb < K; kb += kc) {
+    const int klen = min(kc, K - kb);
+    const int s0 = kb / kStepK, ns = (klen + kStepK - 1) / kStepK, per = (ns + ks - 1) / ks;
+    const int first = s0 + min(kw * per, ns), last = live ? s0 + min(kw * per + per, ns) : first;
+    typename DotRows<GS>::Codes c0, c1;
+    if (first < last) rows.load(c0, first);
+    if (first + 1 < last) rows.load(c1, first + 1);
+    if (kb > 0) __syncthreads();
+    const int row = g.gather ? g.col_sorted[p] / g.topk : p;
+    for (int c = threadIdx.x; c < klen / 8; c += blockDim.x) {
+      const u32x4_t v = *reinterpret_cast<const u32x4_t *>(
+          reinterpret_cast<const bf16_t *>(g.A) + (size_t)row * K + kb + 8 * c);
+      *reinterpret_cast<u32x4_t *>(lds + 16 * c) = token_order(v);
+      float f[8], s = 0.f;  // sums of 32: four neighbouring lanes
+      unpack(v, f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += f[i];
+      s += __shfl_xor(s, 1);
+      s += __shfl_xor(s, 2);
+      if ((c & 3) == 0) sums[c >> 2] = s;
+    }
+    __syncthreads();
+    rows.stream(c0, c1, first, last, s0, lds, sums, acc);
+  }
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    acc[t] += __shfl_xor(acc[t], 1);
+    acc[t] += __shfl_xor(acc[t], 2);
+  }
+  if ((lane & 3) == 0) {
+    red[wave][0][lane >> 2] = acc[0];
+    red[wave][1][lane >> 2] = acc[1];
+  }
+  __syncthreads();
+  if (kw != 0 || lane >= COLS || !live) return;
+  auto part = [&](int t, int c) {
+    float v = 0.f;
+    for (int w = wave; w < wave + ks; ++w) v += red[w][t][c];
+    return v;
+  };
+  finish<EPI>(g, p, n0 + lane, part(kPlain ? lane >> 4 : 0, lane & 15),
+              kPlain ? 0.f : part(1, lane & 15));
 }
 
 // out[t] = sum over the token's slots of its fp32 rows, rounded once.
@@ -481,14 +663,18 @@ void launch_rows(const Int4Args &a, int64_t M, hipStream_t s) {
   const int wide = cols * (waves / ks);
   const int kc = staged_values(a.K, kTokenLds / (2 * TR));
   const size_t rows = (size_t)TR * kc * 2, red = sizeof(float) * waves * 2 * TR * 17;
-  hipLaunchKernelGGL((expert_int4_kernel<EPI, GS, TR>),
-                     dim3((unsigned)((a.Nout + wide - 1) / wide), (unsigned)experts),
-                     dim3(64 * waves), rows > red ? rows : red, s, a, ks, kc);
+  const dim3 grid((unsigned)((a.Nout + wide - 1) / wide), (unsigned)experts), block(64 * waves);
+  if constexpr (TR == 1)
+    hipLaunchKernelGGL((expert_int4_one_kernel<EPI, GS>), grid, block,
+                       rows + (size_t)kc / 32 * sizeof(float), s, a, ks, kc);
+  else
+    hipLaunchKernelGGL((expert_int4_kernel<EPI, GS, TR>), grid, block, rows > red ? rows : red, s,
+                       a, ks, kc);
 }
 
 template <int EPI, int GS>
 void launch_tiles(const Int4Args &a, int64_t n_tokens, int64_t M, hipStream_t s) {
-  // Token rows held at a time: an expert has at most one a token, and past
+  // One token has a kernel of its own.  Token rows held at a time: an expert has at most one a token, and past
   // those held its weights are read again.  Up to two rows an expert on average
   // four are enough (33 tokens, 128 experts: 350 us against 366 with 16); at
   // four an expert they are not (64 experts, 32 tokens: 198 against 145).

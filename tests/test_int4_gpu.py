@@ -134,6 +134,9 @@ CASES = [
     ("sixteen-slots", 1, 160, 224, 16, 16, 32, False, "silu", "interleaved", {}, None),
     ("three-slots", 20, 128, 1024, 64, 3, 128, True, "relu2", "packed", {}, None),
     ("two-slots-long", 2, 64, 8448, 8, 2, 64, True, "silu", "packed", {}, None),
+    # one token, rows longer than LDS holds at a time
+    ("one-token-long", 1, 64, 33280, 4, 2, 64, True, "silu", "packed", {}, None),
+    ("one-token-tail", 1, 416, 96, 8, 3, 32, False, "relu2", "packed", {}, None),
     ("long-rows", 20, 64, 4416, 2, 2, 64, False, "silu", "packed", {}, None),
 ]
 
