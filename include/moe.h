@@ -18,6 +18,13 @@
  * routing weight + combine), and the latter as moe_experts_w2_rows (GEMM2 +
  * routing weight into sorted rows) and moe_combine (the scatter-combine).
  *
+ * Around the layer: moe_block_norm (norms, gate and residual sum of a block, with
+ * moe_block_norm_backward) and moe_block_forward (the block from its residual
+ * stream).  Around expert products that run elsewhere: moe_dispatch and
+ * moe_combine_weighted with moe_combine_weighted_backward, and
+ * moe_route_backward.  With 4-bit expert weights: moe_quantize_int4,
+ * moe_dequantize_int4, moe_experts_int4 and moe_forward_int4.
+ *
  * Sources of the operations (the pages are cited by title and section):
  *  - top-k over the router logits with softmax over the selected values, and the
  *    metadata it yields -- expert bitmatrix, per-expert column sums (col_sum),
@@ -535,8 +542,10 @@ moe_status_t moe_dequantize_int4(const moe_int4_weights_t *w, int32_t n_experts,
  *   once.  x must be finite (an infinity becomes NaN in its token's row).
  *   Deterministic.
  *   The routing is the whole layer's, not an expert share's.  Any batch is
- *   right; the kernel is shaped for decode-sized ones, a few rows an expert.  For prompts, moe_dequantize_int4 once and moe_experts are
- *   faster.  workspace: moe_int4_workspace_bytes(...). */
+ *   right; the kernel is shaped for decode-sized ones, a few rows an expert.
+ *   From 48 rows an expert on, moe_dequantize_int4 once and moe_experts measured
+ *   faster (8 experts, 4096 x 2048, groups of 64: 148 against 124 us at 48 rows,
+ *   111 against 153 at 32).  workspace: moe_int4_workspace_bytes(...). */
 size_t moe_int4_workspace_bytes(int64_t n_tokens, int32_t n_experts, int32_t topk, int32_t hidden,
                                 int32_t inter);
 moe_status_t moe_experts_int4(const void *x, int64_t n_tokens, int32_t hidden,

@@ -41,6 +41,13 @@ The norms around the layer, with the gate and the residual sum, are one call:
     g = moe_block_norm_backward(d_x_out, d_n_out, x, y, w_post=w_post, gate=gate, w_pre=w_next,
                                 residual_scale=0.22, rstd_post=s.rstd_post,
                                 rstd_pre=s.rstd_pre)
+
+``moe_block_forward`` runs the whole block from its residual stream.  Expert
+weights of 4-bit codes with a scale and a zero point a group, for decoding:
+
+    w13_q, w13_s, w13_z = moe_quantize_int4(w13, group=128)
+    w2_q, w2_s, w2_z = moe_quantize_int4(w2, group=128)
+    out = moe_experts_int4(x, w13_q, w13_s, w13_z, w2_q, w2_s, w2_z, routing, act="silu")
 """
 from __future__ import annotations
 

@@ -21,11 +21,11 @@
 // A row is read once into registers (TPR threads a row, V 16-byte chunks a
 // thread), summed across its threads in fp32 and written once; the step is
 // bound by HBM: forward 16384 x 4096 bf16 (537 MB) 102 us, 5.2 TB/s, a copy's
-// rate; backward (805 MB) 162 us, 5.0 TB/s; one token 3.4 us.  Loading the next
-// row ahead of the sums measured no faster (backward 164 -> 167 us).  A workgroup takes rows in turn, so that the weights are loaded
-// once and the column sums of the gradient are added up in registers; the
-// workgroups' sums are then added in a fixed order by a second kernel, with no
-// atomics.
+// rate; backward (805 MB) 158 us, 5.1 TB/s; one token 3.2 us.  Loading the next
+// row ahead of the sums measured no faster (backward 164 -> 167 us).  A workgroup
+// takes rows in turn, so that the weights are loaded once and the column sums of
+// the gradient are added up in registers; the workgroups' sums are then added in
+// a fixed order by a second kernel, with no atomics.
 #include "rows.h"
 
 #include <type_traits>

@@ -329,8 +329,8 @@ __device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float acc) {
 // row l / 4 of a tile, piece l % 4 of 128 weights) with the token's values at
 // those places, the scale and zero point of the lane's own group, and one sum
 // over the four lanes of a row at the end.  The lanes keep what they load: no
-// permutation, no swaps (one token of 128 experts, groups of 64: 25.9 -> 24.8
-// us; of 32 experts, groups of 32: 29.0 -> 25.1).
+// permutation, no swaps (one token of 128 experts, groups of 64: 25.9 -> 25.2
+// us; of 32 experts, groups of 32: 29.0 -> 25.0).
 template <int GS> struct DotRows : ExpertArrays<GS> {
   using A = ExpertArrays<GS>;
   struct Codes {  // a step of the rows
@@ -674,9 +674,9 @@ void launch_rows(const Int4Args &a, int64_t M, hipStream_t s) {
 
 template <int EPI, int GS>
 void launch_tiles(const Int4Args &a, int64_t n_tokens, int64_t M, hipStream_t s) {
-  // One token has a kernel of its own.  Token rows held at a time: an expert has at most one a token, and past
-  // those held its weights are read again.  Up to two rows an expert on average
-  // four are enough (33 tokens, 128 experts: 350 us against 366 with 16); at
+  // One token has a kernel of its own.  Token rows held at a time: an expert has
+  // at most one a token, and past those held its weights are read again.  Up to
+  // two rows an expert on average four are enough (33 tokens, 128 experts: 350 us against 366 with 16); at
   // four an expert they are not (64 experts, 32 tokens: 198 against 145).
   if (n_tokens == 1) launch_rows<EPI, GS, 1>(a, M, s);
   else if (n_tokens <= 4 || M <= 2 * (int64_t)a.E) launch_rows<EPI, GS, 4>(a, M, s);

@@ -17,9 +17,9 @@
 // add nothing.  A token's slots are taken up to eight at a time, their
 // positions and then their rows all in flight.  All of it is bound by HBM, at
 // the rate of a large copy (5.1 - 5.4 TB/s): 16384 tokens x 4096 bf16, 8 slots:
-// dispatch (1.2 GB) 229 us, 5.3 TB/s; gradient (2.3 GB) 456 us, 5.0 TB/s; 4096
-// x 2880, 4 slots: weighted combine (118 MB, partly from the last-level cache)
-// 19.8 us.  Small batches cost 2.3 - 5.8 us a kernel.
+// dispatch (1.2 GB) 230 us, 5.3 TB/s; gradient (2.3 GB) 452 us, 5.1 TB/s; 4096
+// x 2880, 4 slots: weighted combine (118 MB, above a copy's rate, so partly from
+// a cache) 21 us.  Small batches cost 2.2 - 5.8 us a kernel.
 #include "rows.h"
 
 #include <type_traits>
@@ -116,8 +116,9 @@ __global__ __launch_bounds__(kThreads) void combine_weighted_kernel(
 
 // The expert rows are read once and past the caches (fp32, 4095 tokens x 1416, 6
 // slots: 66 -> 60 us); non-temporal stores made it 68, and changed nothing or
-// lost up to 6 % elsewhere.  WPT waves a token: each keeps a piece of d_out in registers while it passes
-// over the same piece of the token's expert rows, JB at a time.
+// lost up to 6 % elsewhere.  WPT waves a token: each keeps a piece of d_out in
+// registers while it passes over the same piece of the token's expert rows, JB
+// at a time.
 template <typename T, int JB, int WPT>
 __global__ __launch_bounds__(kThreads) void combine_weighted_backward_kernel(
     const T *__restrict__ d_out, const T *__restrict__ y, const int32_t *__restrict__ row_sorted,
