@@ -14,10 +14,10 @@
 //   sum_k a_k w_k = sum over groups of s * (sum_k a_k (q_k - z)),
 // and the inner sum is taken exactly as products of small integers with bf16
 // activations, on the matrix cores: a code q put into the low mantissa bits of
-// bf16 128.0 (0x4300 | q) is the number 128 + q, one AND and one OR for two
-// weights, and a second product with the constant -(128 + z), also exact in
-// bf16, takes the offset and the zero point off again.  Sums are fp32; the
-// scale enters in fp32 once a group.  Nothing is rounded to bf16 but the
+// bf16 128.0 (0x4300 | q) is the number 128 + q, a shift and one AND-OR for two
+// weights.  A product with ones gives the group's sum of a, once for all the
+// weight rows of the wave, and s * (sum_k a_k (128 + q_k) - (128 + z) sum_k a_k)
+// enters the result in fp32 once a group.  Nothing is rounded to bf16 but the
 // activation rows between the two products (the bf16 layer's own type).
 //
 // A wave streams 32 weight rows of one expert (16 gate and 16 up rows, or 32
@@ -33,8 +33,8 @@
 // and, for groups of 32 and 64, lane swaps bring the dwords to the lanes whose
 // product they belong to, so that no product mixes two groups.
 //
-// What bounds it: the rate of the loads, and about 230 vector instructions and
-// 24 products, one after the other, a step of 8192 weights; at one token the
+// What bounds it: the rate of the loads, and about 240 vector instructions (of
+// the whole kernel, counted) and 24 products a step of 8192 weights; at one token the
 // start of three kernels and of their loads.  Measured against the bytes of the
 // touched experts: 64 experts (H 4096, I 1536, k 8), 32 tokens, groups of 128:
 // 147 us, 4.2 TB/s; 128 experts (H = I = 2880, k 4), groups of 64 with zero
