@@ -537,9 +537,10 @@ moe_status_t moe_dequantize_int4(const moe_int4_weights_t *w, int32_t n_experts,
  *   with 4-bit weights: w13 [E, w13 rows, hidden] and w2 [E, hidden, inter] as
  *   above, with one group size for both (hidden and inter multiples of it).
  *   The products of codes and activations are exact and summed in fp32, the
- *   scales enter in fp32; the activation rows are rounded to bf16 as in
- *   moe_experts, the weighted expert rows stay fp32 and the output is rounded
- *   once.  x must be finite (an infinity becomes NaN in its token's row).
+ *   scales enter in fp32; the activation rows are kept to 16 bits of mantissa
+ *   (moe_experts rounds them to bf16), the weighted expert rows stay fp32 and
+ *   the output is rounded once.  x must be finite (an infinity becomes NaN in
+ *   its token's row).
  *   Deterministic.
  *   The routing is the whole layer's, not an expert share's.  Any batch is
  *   right; the kernel is shaped for decode-sized ones, a few rows an expert.

@@ -17,8 +17,12 @@
 // bf16 128.0 (0x4300 | q) is the number 128 + q, a shift and one AND-OR for two
 // weights.  A product with ones gives the group's sum of a, once for all the
 // weight rows of the wave, and s * (sum_k a_k (128 + q_k) - (128 + z) sum_k a_k)
-// enters the result in fp32 once a group.  Nothing is rounded to bf16 but the
-// activation rows between the two products (the bf16 layer's own type).
+// enters the result in fp32 once a group.  The activation rows between the two
+// products are kept as two bf16 parts, a = hi + lo with hi = bf16(a) and lo =
+// bf16(a - hi), off by 2^-16 of a value at most; the second product takes both
+// parts into the same sums.  So the only rounding to bf16 of a whole call is
+// that of its output (one part would add as much error as that rounding again:
+// 0.0022 instead of 0.0017 in the 2-norm).
 //
 // A wave streams 32 weight rows of one expert (16 gate and 16 up rows, or 32
 // plain ones) and no other wave reads them, so they go straight to registers,
@@ -51,11 +55,11 @@ namespace moe {
 namespace {
 
 struct Int4Args {
-  const void *A;               // w13: x [N, K]; w2: activation rows [M, K]
+  const void *A;               // w13: x [N, K]; w2: activation rows [M, 2, K] (hi, lo)
   const uint8_t *q;            // [E, NSETS * Nout, K / 2]
   const bf16_t *s;             // [E, K / G, NSETS * Nout]
   const uint8_t *z;            // [E, K / G, NSETS * Nout] or NULL (8)
-  void *C;                     // w13: [M, Nout] bf16; w2: [M, Nout] fp32 or [N, Nout] bf16
+  void *C;                     // w13: [M, 2, Nout] bf16; w2: [M, Nout] fp32 or [N, Nout] bf16
   const int32_t *offsets;      // [E + 1]
   const int32_t *col_sorted;   // [M]
   const void *gate_scal;       // [M] (w2)
@@ -242,12 +246,13 @@ template <int GS> struct WaveRows : ExpertArrays<GS> {
     }
   }
 
-  // acc[t] += this step's products with the lane's token row x, whose part of
-  // the step is at `tok` (16-byte piece c at place c ^ (x % 8)); with kWhole =
-  // false only the groups ahead of K.
-  template <bool kWhole>
-  __device__ __forceinline__ void work(const Codes &c, int step, const char *tok, int x,
-                                       f32x4_t (&acc)[2]) const {
+  // acc[t] += this step's products with the lane's token row, whose part of the
+  // step is at `tok` (16-byte piece c at place c ^ swz); with PARTS = 2 its
+  // second part is `part` bytes further on; with kWhole = false only the groups
+  // ahead of K.
+  template <int PARTS, bool kWhole>
+  __device__ __forceinline__ void work(const Codes &c, int step, const char *tok, int part,
+                                       int swz, f32x4_t (&acc)[2]) const {
     const int h = A::lane >> 4, from = (4 * (A::lane & 15) + h) * 4;
     const int ngroups = kWhole ? 8 / GS : (A::K - step * kStepK) / (32 * GS);
     const bf16x8_t ones = __builtin_bit_cast(
@@ -278,14 +283,20 @@ template <int GS> struct WaveRows : ExpertArrays<GS> {
       for (int j = 0; j < 4; ++j) {
         const int gr = (4 * b + j) / GS;
         if (!kWhole && gr >= ngroups) break;
-        const bf16x8_t av = *reinterpret_cast<const bf16x8_t *>(
-            tok + 256 * b + ((eighth<GS>(j, h) ^ (x & 7)) * 16));
-        const bool begins = j % GS == 0;
-        tot = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, ones, begins ? zero : tot, 0, 0, 0);
+        bf16x8_t wv[2];
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-          sum[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              av, codes_plus_128(cw[t][j], A::mask, A::magic), begins ? zero : sum[t], 0, 0, 0);
+        for (int t = 0; t < 2; ++t) wv[t] = codes_plus_128(cw[t][j], A::mask, A::magic);
+#pragma unroll
+        for (int u = 0; u < PARTS; ++u) {
+          const bf16x8_t av = *reinterpret_cast<const bf16x8_t *>(
+              tok + u * part + 256 * b + ((eighth<GS>(j, h) ^ swz) * 16));
+          const bool begins = j % GS == 0 && u == 0;
+          tot = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, ones, begins ? zero : tot, 0, 0, 0);
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+            sum[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, wv[t], begins ? zero : sum[t], 0,
+                                                             0, 0);
+        }
         if (j % GS == GS - 1) {
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
@@ -301,12 +312,14 @@ template <int GS> struct WaveRows : ExpertArrays<GS> {
 
   // Steps first .. last - 1, the first two already in c0 and c1, two ahead;
   // tok0: the lane's token row at step s0.
+  template <int PARTS>
   __device__ __forceinline__ void stream(Codes &c0, Codes &c1, int first, int last, int s0,
-                                         const char *tok0, int x, f32x4_t (&acc)[2]) const {
+                                         const char *tok0, int part, int swz,
+                                         f32x4_t (&acc)[2]) const {
     auto run = [&](const Codes &c, int step) {
       const char *tok = tok0 + (step - s0) * (2 * kStepK);
-      if ((step + 1) * kStepK <= A::K) work<true>(c, step, tok, x, acc);
-      else work<false>(c, step, tok, x, acc);
+      if ((step + 1) * kStepK <= A::K) work<PARTS, true>(c, step, tok, part, swz, acc);
+      else work<PARTS, false>(c, step, tok, part, swz, acc);
     };
     for (int step = first; step < last; step += 2) {
       run(c0, step);
@@ -364,8 +377,10 @@ template <int GS> struct DotRows : ExpertArrays<GS> {
   }
 
   // acc[t] += the lane's part of row lane / 4 of tile t; tok: the token row at
-  // this step, sums: the sums of its pieces of 32.
-  __device__ __forceinline__ void work(const Codes &c, int step, const char *tok,
+  // this step (with PARTS = 2 its second part `part` bytes further on), sums: the
+  // sums of its pieces of 32.
+  template <int PARTS>
+  __device__ __forceinline__ void work(const Codes &c, int step, const char *tok, int part,
                                        const float *sums, float (&acc)[2]) const {
     const float zero0 = A::has_z ? 128.f : 136.f;
 #pragma unroll
@@ -376,14 +391,19 @@ template <int GS> struct DotRows : ExpertArrays<GS> {
       float dot[2] = {0.f, 0.f};
 #pragma unroll
       for (int d = 0; d < 4; ++d) {
-        const u32x4_t av = *reinterpret_cast<const u32x4_t *>(tok + 256 * b + (A::lane & 3) * 64 + 16 * d);
+        u32x4_t av[PARTS];
+#pragma unroll
+        for (int u = 0; u < PARTS; ++u)
+          av[u] = *reinterpret_cast<const u32x4_t *>(tok + u * part + 256 * b +
+                                                     (A::lane & 3) * 64 + 16 * d);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           const u32x4_t wv =
               __builtin_bit_cast(u32x4_t, codes_plus_128(c.w[t][b][d], A::mask, A::magic));
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            dot[t] = dot2(wv[i], av[i], dot[t]);
+          for (int u = 0; u < PARTS; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dot[t] = dot2(wv[i], av[u][i], dot[t]);
         }
       }
 #pragma unroll
@@ -395,11 +415,13 @@ template <int GS> struct DotRows : ExpertArrays<GS> {
     }
   }
 
+  template <int PARTS>
   __device__ __forceinline__ void stream(Codes &c0, Codes &c1, int first, int last, int s0,
-                                         const char *tok0, const float *sums0,
+                                         const char *tok0, int part, const float *sums0,
                                          float (&acc)[2]) const {
     auto run = [&](const Codes &c, int step) {
-      work(c, step, tok0 + (step - s0) * (2 * kStepK), sums0 + (step - s0) * (kStepK / 32), acc);
+      work<PARTS>(c, step, tok0 + (step - s0) * (2 * kStepK), part,
+                  sums0 + (step - s0) * (kStepK / 32), acc);
     };
     for (int step = first; step < last; step += 2) {
       run(c0, step);
@@ -412,19 +434,22 @@ template <int GS> struct DotRows : ExpertArrays<GS> {
 };
 
 // Token rows into LDS by the whole workgroup: values kb .. kb + klen - 1 of the
-// rows row(0) .. row(n - 1), rowb bytes apart; U loads of a thread in flight.
-template <int U, typename F>
+// rows row(0) .. row(n - 1), rowb bytes apart, 16-byte piece c of row i at place c
+// ^ (i % 8); with PARTS = 2 memory rows 2 row(i) and 2 row(i) + 1 go to LDS rows
+// i and TR + i.  U loads of a thread in flight.
+template <int U, int PARTS, int TR, typename F>
 __device__ __forceinline__ void stage_rows(const Int4Args &g, char *lds, int rowb, int n, int kb,
                                            int klen, F row) {
-  const int np = klen / 8, total = n * np, stride = blockDim.x;
+  const int np = klen / 8, total = PARTS * n * np, stride = blockDim.x;
   for (int i0 = threadIdx.x; i0 < total; i0 += U * stride) {
     int at[U], to[U];
     u32x4_t v[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int i = min(i0 + u * stride, total - 1), x = i / np, c = i - x * np;
-      at[u] = row(x);
-      to[u] = x * rowb + ((c ^ (x & 7)) * 16);
+      const int i = min(i0 + u * stride, total - 1), c = i % np, lo = i / np >= n;
+      const int t = i / np - lo * n;
+      at[u] = PARTS * row(t) + lo;
+      to[u] = (t + lo * TR) * rowb + ((c ^ (t & 7)) * 16);
       v[u][0] = (uint32_t)c;
     }
 #pragma unroll
@@ -452,9 +477,15 @@ __device__ __forceinline__ void finish(const Int4Args &g, int p, int col, float 
     float a = act_val<EPI>(v0, v1, nal, g.prm);
     // the clamps and the rectifier drop a NaN; the token's row shall show it
     if (__builtin_isnan(v0) || __builtin_isnan(v1)) a = __builtin_nanf("");
-    reinterpret_cast<bf16_t *>(g.C)[(size_t)p * g.Nout + col] = bf16_rne(a);
+    const bf16_t hi = bf16_rne(a);
+    bf16_t *c = reinterpret_cast<bf16_t *>(g.C) + (size_t)2 * p * g.Nout + col;
+    c[0] = hi;
+    c[g.Nout] = bf16_rne(a - to_f32(hi));
   }
 }
+
+// Parts of a token row: w2 takes the activation rows as hi and lo.
+template <int EPI> constexpr int parts() { return EPI == EPI_Y || EPI == EPI_OUT ? 2 : 1; }
 
 // GS = G / 32; TR: token rows held at a time.  A wave streams 32 weight rows;
 // ks waves share them and split the steps; the workgroup's waves / ks column
@@ -464,8 +495,10 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void
 expert_int4_kernel(Int4Args g, int ks, int kc) {
   constexpr bool kPlain = EPI == EPI_Y || EPI == EPI_OUT || EPI == EPI_RELU2;
   constexpr int COLS = kPlain ? 32 : 16;  // output columns of a wave's 32 weight rows
+  constexpr int PARTS = parts<EPI>();
   __shared__ int sel[3];
-  extern __shared__ __attribute__((aligned(16))) char lds[];  // [TR][kc] bf16; then the parts
+  // [PARTS][TR][kc] bf16; then the waves' sums
+  extern __shared__ __attribute__((aligned(16))) char lds[];
   int place_x, want;
   place(place_x, want);
   find_expert(g.offsets, g.E, want, sel);
@@ -504,12 +537,12 @@ expert_int4_kernel(Int4Args g, int ks, int kc) {
       if (a0 > 0 || kb > 0) __syncthreads();
       // (four loads in flight: 16 rows 154 -> 147 us on the 64-expert layer; up to
       // four rows are staged in one round anyway, 26.0 -> 26.7 us at one token)
-      stage_rows<TR < 16 ? 1 : 4>(g, lds, rowb, na, kb, klen, [&](int i) {
+      stage_rows<TR < 16 ? 1 : 4, PARTS, TR>(g, lds, rowb, na, kb, klen, [&](int i) {
         const int p = row0 + a0 + i;
         return g.gather ? g.col_sorted[p] / g.topk : p;
       });
       __syncthreads();
-      rows.stream(c0, c1, first, last, s0, lds + x * rowb, x, acc);
+      rows.template stream<PARTS>(c0, c1, first, last, s0, lds + x * rowb, TR * rowb, x & 7, acc);
     }
 
     // the waves' parts, through LDS that the token rows no longer need: lane
@@ -540,10 +573,11 @@ expert_int4_kernel(Int4Args g, int ks, int kc) {
 template <int EPI, int GS>
 __global__ __launch_bounds__(512) void expert_int4_one_kernel(Int4Args g, int ks, int kc) {
   constexpr bool kPlain = EPI == EPI_Y || EPI == EPI_OUT || EPI == EPI_RELU2;
-  constexpr int COLS = kPlain ? 32 : 16;
+  constexpr int COLS = kPlain ? 32 : 16, PARTS = parts<EPI>();
   __shared__ int sel[3];
   __shared__ float red[8][2][16];
-  extern __shared__ __attribute__((aligned(16))) char lds[];  // [kc] bf16, [kc / 32] fp32
+  // [PARTS][kc] bf16, [kc / 32] fp32
+  extern __shared__ __attribute__((aligned(16))) char lds[];
   int place_x, want;
   place(place_x, want);
   find_expert(g.offsets, g.E, want, sel);
@@ -561,7 +595,7 @@ __global__ __launch_bounds__(512) void expert_int4_one_kernel(Int4Args g, int ks
   rows.init(g, e, kPlain ? Nout : 2 * Nout, [&](int t, int x) {
     return kPlain ? n0 + 16 * t + x : g.interleaved ? 2 * (n0 + x) + t : t * Nout + n0 + x;
   });
-  float *sums = reinterpret_cast<float *>(lds + 2 * kc);
+  float *sums = reinterpret_cast<float *>(lds + PARTS * 2 * kc);
   float acc[2] = {0.f, 0.f};
   for (int kb = 0; kb < K; kb += kc) {
     const int klen = min(kc, K - kb);
@@ -573,19 +607,26 @@ __global__ __launch_bounds__(512) void expert_int4_one_kernel(Int4Args g, int ks
     if (kb > 0) __syncthreads();
     const int row = g.gather ? g.col_sorted[p] / g.topk : p;
     for (int c = threadIdx.x; c < klen / 8; c += blockDim.x) {
-      const u32x4_t v = *reinterpret_cast<const u32x4_t *>(
-          reinterpret_cast<const bf16_t *>(g.A) + (size_t)row * K + kb + 8 * c);
-      *reinterpret_cast<u32x4_t *>(lds + 16 * c) = token_order(v);
-      float f[8], s = 0.f;  // sums of 32: four neighbouring lanes
-      unpack(v, f);
+      u32x4_t v[PARTS];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s += f[i];
+      for (int u = 0; u < PARTS; ++u)
+        v[u] = *reinterpret_cast<const u32x4_t *>(reinterpret_cast<const bf16_t *>(g.A) +
+                                                  (size_t)(PARTS * row + u) * K + kb + 8 * c);
+      float s = 0.f;  // sums of 32: four neighbouring lanes
+#pragma unroll
+      for (int u = 0; u < PARTS; ++u) {
+        *reinterpret_cast<u32x4_t *>(lds + u * 2 * kc + 16 * c) = token_order(v[u]);
+        float f[8];
+        unpack(v[u], f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += f[i];
+      }
       s += __shfl_xor(s, 1);
       s += __shfl_xor(s, 2);
       if ((c & 3) == 0) sums[c >> 2] = s;
     }
     __syncthreads();
-    rows.stream(c0, c1, first, last, s0, lds, sums, acc);
+    rows.template stream<PARTS>(c0, c1, first, last, s0, lds, 2 * kc, sums, acc);
   }
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
@@ -661,8 +702,9 @@ void launch_rows(const Int4Args &a, int64_t M, hipStream_t s) {
   const int waves = groups < 2048 ? 4 : 8;
   const int ks = groups < 1024 ? 4 : groups < 4096 ? 2 : 1;
   const int wide = cols * (waves / ks);
-  const int kc = staged_values(a.K, kTokenLds / (2 * TR));
-  const size_t rows = (size_t)TR * kc * 2, red = sizeof(float) * waves * 2 * TR * 17;
+  constexpr int PARTS = parts<EPI>();
+  const int kc = staged_values(a.K, kTokenLds / (2 * TR * PARTS));
+  const size_t rows = (size_t)PARTS * TR * kc * 2, red = sizeof(float) * waves * 2 * TR * 17;
   const dim3 grid((unsigned)((a.Nout + wide - 1) / wide), (unsigned)experts), block(64 * waves);
   if constexpr (TR == 1)
     hipLaunchKernelGGL((expert_int4_one_kernel<EPI, GS>), grid, block,

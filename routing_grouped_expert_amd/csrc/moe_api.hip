@@ -747,10 +747,10 @@ moe_status_t moe_forward_mxfp4(const void *x, const void *logits, moe_dtype_t dt
 namespace {
 bool group_ok(int32_t g) { return g == 32 || g == 64 || g == 128; }
 
-// Scratch of the 4-bit experts: activation rows a[M, inter] bf16, then (topk >
-// 1) the weighted expert rows y[M, hidden] in fp32.
+// Scratch of the 4-bit experts: activation rows a[M, 2, inter] (two bf16 parts
+// of every value), then (topk > 1) the weighted expert rows y[M, hidden] in fp32.
 size_t int4_act_bytes(int64_t n, int32_t k, int32_t inter) {
-  return align256((size_t)n * k * inter * 2);
+  return align256((size_t)n * k * inter * 4);
 }
 size_t int4_ws_bytes(int64_t n, int32_t k, int32_t hidden, int32_t inter) {
   return int4_act_bytes(n, k, inter) + (k > 1 ? align256((size_t)n * k * hidden * 4) : 0);

@@ -146,7 +146,7 @@ hipError_t launch_route_backward(const float *d_topk_w, const int32_t *topk_idx,
 struct Int4Weights {
   const void *q, *s, *z;
 };
-// The expert FFN: act [M, inter] bf16 and y [M, hidden] fp32 (topk > 1) are scratch.
+// The expert FFN: act [M, 2, inter] bf16 and y [M, hidden] fp32 (topk > 1) are scratch.
 hipError_t launch_experts_int4(const Int4Weights &w13, const Int4Weights &w2, const void *x,
                                const moe_routing_t *r, void *out, void *act, void *y,
                                int64_t n_tokens, int topk, int n_experts, int hidden, int inter,
