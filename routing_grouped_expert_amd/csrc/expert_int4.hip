@@ -166,6 +166,7 @@ __device__ __forceinline__ void place(int &x, int &y) {
 }
 
 constexpr int kStepK = 256;  // weights of a row a step: one 128-byte line of codes
+constexpr int kStepBytes = 2 * kStepK;  // a token row's part of a step in LDS
 
 // One expert's weight arrays as a wave reads them.
 template <int GS> struct ExpertArrays {
@@ -247,12 +248,12 @@ template <int GS> struct WaveRows : ExpertArrays<GS> {
   }
 
   // acc[t] += this step's products with the lane's token row, whose part of the
-  // step is at `tok` (16-byte piece c at place c ^ swz); with PARTS = 2 its
-  // second part is `part` bytes further on; with kWhole = false only the groups
+  // step is at `tok` (16-byte piece c at place c ^ swz); with TILES = 2 also with
+  // the row's second part, right behind; with kWhole = false only the groups
   // ahead of K.
-  template <int PARTS, bool kWhole>
-  __device__ __forceinline__ void work(const Codes &c, int step, const char *tok, int part,
-                                       int swz, f32x4_t (&acc)[2]) const {
+  template <int TILES, bool kWhole>
+  __device__ __forceinline__ void work(const Codes &c, int step, const char *tok, int swz,
+                                       f32x4_t (&acc)[2]) const {
     const int h = A::lane >> 4, from = (4 * (A::lane & 15) + h) * 4;
     const int ngroups = kWhole ? 8 / GS : (A::K - step * kStepK) / (32 * GS);
     const bf16x8_t ones = __builtin_bit_cast(
@@ -287,9 +288,9 @@ template <int GS> struct WaveRows : ExpertArrays<GS> {
 #pragma unroll
         for (int t = 0; t < 2; ++t) wv[t] = codes_plus_128(cw[t][j], A::mask, A::magic);
 #pragma unroll
-        for (int u = 0; u < PARTS; ++u) {
+        for (int u = 0; u < TILES; ++u) {
           const bf16x8_t av = *reinterpret_cast<const bf16x8_t *>(
-              tok + u * part + 256 * b + ((eighth<GS>(j, h) ^ swz) * 16));
+              tok + u * kStepBytes + 256 * b + ((eighth<GS>(j, h) ^ swz) * 16));
           const bool begins = j % GS == 0 && u == 0;
           tot = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, ones, begins ? zero : tot, 0, 0, 0);
 #pragma unroll
@@ -297,6 +298,9 @@ template <int GS> struct WaveRows : ExpertArrays<GS> {
             sum[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, wv[t], begins ? zero : sum[t], 0,
                                                              0, 0);
         }
+        // (keeps the second parts' loads from being moved up past the registers: 15-40
+        // spilled without)
+        if constexpr (TILES == 2) __builtin_amdgcn_sched_barrier(0);
         if (j % GS == GS - 1) {
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
@@ -311,15 +315,14 @@ template <int GS> struct WaveRows : ExpertArrays<GS> {
   }
 
   // Steps first .. last - 1, the first two already in c0 and c1, two ahead;
-  // tok0: the lane's token row at step s0.
-  template <int PARTS>
+  // tok0: the lane's token row at step s0, a step every PARTS * kStepBytes.
+  template <int TILES, int PARTS>
   __device__ __forceinline__ void stream(Codes &c0, Codes &c1, int first, int last, int s0,
-                                         const char *tok0, int part, int swz,
-                                         f32x4_t (&acc)[2]) const {
+                                         const char *tok0, int swz, f32x4_t (&acc)[2]) const {
     auto run = [&](const Codes &c, int step) {
-      const char *tok = tok0 + (step - s0) * (2 * kStepK);
-      if ((step + 1) * kStepK <= A::K) work<PARTS, true>(c, step, tok, part, swz, acc);
-      else work<PARTS, false>(c, step, tok, part, swz, acc);
+      const char *tok = tok0 + (step - s0) * (PARTS * kStepBytes);
+      if ((step + 1) * kStepK <= A::K) work<TILES, true>(c, step, tok, swz, acc);
+      else work<TILES, false>(c, step, tok, swz, acc);
     };
     for (int step = first; step < last; step += 2) {
       run(c0, step);
@@ -435,9 +438,9 @@ template <int GS> struct DotRows : ExpertArrays<GS> {
 
 // Token rows into LDS by the whole workgroup: values kb .. kb + klen - 1 of the
 // rows row(0) .. row(n - 1), rowb bytes apart, 16-byte piece c of row i at place c
-// ^ (i % 8); with PARTS = 2 memory rows 2 row(i) and 2 row(i) + 1 go to LDS rows
-// i and TR + i.  U loads of a thread in flight.
-template <int U, int PARTS, int TR, typename F>
+// ^ (i % 8).  With PARTS = 2 row i is memory rows 2 row(i) and 2 row(i) + 1, a step
+// of the second behind each step of the first.  U loads of a thread in flight.
+template <int U, int PARTS, typename F>
 __device__ __forceinline__ void stage_rows(const Int4Args &g, char *lds, int rowb, int n, int kb,
                                            int klen, F row) {
   const int np = klen / 8, total = PARTS * n * np, stride = blockDim.x;
@@ -449,7 +452,7 @@ __device__ __forceinline__ void stage_rows(const Int4Args &g, char *lds, int row
       const int i = min(i0 + u * stride, total - 1), c = i % np, lo = i / np >= n;
       const int t = i / np - lo * n;
       at[u] = PARTS * row(t) + lo;
-      to[u] = (t + lo * TR) * rowb + ((c ^ (t & 7)) * 16);
+      to[u] = t * rowb + (c / 32 * PARTS + lo) * kStepBytes + ((c % 32 ^ (t & 7)) * 16);
       v[u][0] = (uint32_t)c;
     }
 #pragma unroll
@@ -487,17 +490,39 @@ __device__ __forceinline__ void finish(const Int4Args &g, int p, int col, float 
 // Parts of a token row: w2 takes the activation rows as hi and lo.
 template <int EPI> constexpr int parts() { return EPI == EPI_Y || EPI == EPI_OUT ? 2 : 1; }
 
-// GS = G / 32; TR: token rows held at a time.  A wave streams 32 weight rows;
-// ks waves share them and split the steps; the workgroup's waves / ks column
-// groups share the token rows in LDS, kc values of each at a time.
-template <int EPI, int GS, int TR>
+// LDS for token rows: 128 KB for whole rows of 4096 values leaves one workgroup
+// a compute unit (8 experts, 64 tokens: 114 us -> 161; 32 KB: 124).
+constexpr int kTokenLds = 64 * 1024;
+
+// Values of a token row that LDS holds at a time where it holds `rows` rows: all
+// of K, or equal parts of it in whole steps.
+__host__ __device__ inline int staged_values(int K, int rows) {
+  const int most = kTokenLds / (2 * rows);
+  const int nstep = (K + kStepK - 1) / kStepK, parts = (K + most - 1) / most;
+  return (nstep + parts - 1) / parts * kStepK;
+}
+
+// GS = G / 32.  A wave streams 32 weight rows; ks waves share them and split the
+// steps; the workgroup's waves / ks column groups share the token rows in LDS.
+//
+// Up to `most` token rows of the expert are taken at a time, past those its weights
+// are read again.  How many rows LDS is laid out for follows from the expert's own
+// count, not from the average: routing is skewed, and the expert that most tokens
+// take sets the layer's time (128 experts 2880 wide, groups of 64, 33 tokens, Zipf-like
+// routing with exponent 1.1: 389 us, and 595 where all experts hold 4 rows because
+// there are less than two on average; even routing 366 and 352).
+//
+// w2 takes the activation rows as two parts each.  With TILES = 1 the second parts
+// are the other 8 rows of the products (8 token rows a pass, nothing computed
+// twice), with TILES = 2 products of their own (16 token rows a pass).
+template <int EPI, int GS, int TILES>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void
-expert_int4_kernel(Int4Args g, int ks, int kc) {
+expert_int4_kernel(Int4Args g, int ks, int most) {
   constexpr bool kPlain = EPI == EPI_Y || EPI == EPI_OUT || EPI == EPI_RELU2;
   constexpr int COLS = kPlain ? 32 : 16;  // output columns of a wave's 32 weight rows
   constexpr int PARTS = parts<EPI>();
   __shared__ int sel[3];
-  // [PARTS][TR][kc] bf16; then the waves' sums
+  // the token rows, kc values of each; then the waves' sums
   extern __shared__ __attribute__((aligned(16))) char lds[];
   int place_x, want;
   place(place_x, want);
@@ -522,10 +547,13 @@ expert_int4_kernel(Int4Args g, int ks, int kc) {
     return kPlain ? n0 + 16 * t + x : g.interleaved ? 2 * (n0 + x) + t : t * Nout + n0 + x;
   });
 
-  const int rowb = 2 * kc;  // bytes of a token row in LDS (a multiple of 512)
-  const int x = r % TR;     // rows past the expert's last hold anything: their sums are not used
-  for (int a0 = 0; a0 < cnt; a0 += TR) {
-    const int na = min(TR, cnt - a0);
+  for (int a0 = 0; a0 < cnt; a0 += most) {
+    const int na = min(most, cnt - a0);
+    // token rows LDS has room for, rows of a product (the last ones may hold
+    // anything: their sums are not used)
+    const int room = na <= 4 ? 4 : na <= 8 ? 8 : 16, tile = PARTS / TILES * room;
+    const int kc = staged_values(K, PARTS * room), rowb = PARTS * 2 * kc;
+    const int x = r & (room - 1), second = TILES < PARTS && (r & room) ? kStepBytes : 0;
     f32x4_t acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
     for (int kb = 0; kb < K; kb += kc) {
       const int klen = min(kc, K - kb);
@@ -536,31 +564,38 @@ expert_int4_kernel(Int4Args g, int ks, int kc) {
       if (first + 1 < last) rows.load(c1, first + 1);
       if (a0 > 0 || kb > 0) __syncthreads();
       // (four loads in flight: 16 rows 154 -> 147 us on the 64-expert layer; up to
-      // four rows are staged in one round anyway, 26.0 -> 26.7 us at one token)
-      stage_rows<TR < 16 ? 1 : 4, PARTS, TR>(g, lds, rowb, na, kb, klen, [&](int i) {
+      // four rows are staged in one round anyway)
+      auto row = [&](int i) {
         const int p = row0 + a0 + i;
         return g.gather ? g.col_sorted[p] / g.topk : p;
-      });
+      };
+      if (PARTS * room < 16) stage_rows<1, PARTS>(g, lds, rowb, na, kb, klen, row);
+      else stage_rows<4, PARTS>(g, lds, rowb, na, kb, klen, row);
       __syncthreads();
-      rows.template stream<PARTS>(c0, c1, first, last, s0, lds + x * rowb, TR * rowb, x & 7, acc);
+      rows.template stream<TILES, PARTS>(c0, c1, first, last, s0, lds + x * rowb + second, x & 7,
+                                         acc);
     }
 
     // the waves' parts, through LDS that the token rows no longer need: lane
-    // (h, r) holds row r of a tile for token rows 4 h .. 4 h + 3
-    float *red = reinterpret_cast<float *>(lds);  // [wave][tile][TR token rows][17]
+    // (h, r) holds row r of a tile for rows 4 h .. 4 h + 3 of the product
+    float *red = reinterpret_cast<float *>(lds);  // [wave][tile of weights][row][17]
     __syncthreads();
-    if (4 * h < TR) {
+    if (4 * h < tile) {
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) red[((wave * 2 + t) * TR + 4 * h + q) * 17 + r] = acc[t][q];
+        for (int q = 0; q < 4; ++q) red[((wave * 2 + t) * tile + 4 * h + q) * 17 + r] = acc[t][q];
     }
     __syncthreads();
     for (int i = kw * 64 + lane; i < na * COLS && live; i += ks * 64) {
       const int col = i % COLS, trow = i / COLS;
       auto part = [&](int t, int c) {
         float v = 0.f;
-        for (int w = cg * ks; w < cg * ks + ks; ++w) v += red[((w * 2 + t) * TR + trow) * 17 + c];
+        for (int w = cg * ks; w < cg * ks + ks; ++w) {
+          const float *p = red + ((w * 2 + t) * tile + trow) * 17 + c;
+          v += p[0];
+          if (TILES < PARTS) v += p[room * 17];  // the row's second part
+        }
         return v;
       };
       finish<EPI>(g, row0 + a0 + trow, n0 + col, part(kPlain ? col >> 4 : 0, col & 15),
@@ -675,17 +710,6 @@ __global__ __launch_bounds__(256) void sum_slots_kernel(const float *__restrict_
   *reinterpret_cast<u32x4_t *>(out + t * H + c) = pack(acc);
 }
 
-// LDS for token rows: 128 KB for whole rows of 4096 values leaves one workgroup
-// a compute unit (8 experts, 64 tokens: 114 us -> 161; 32 KB: 124).
-constexpr int kTokenLds = 64 * 1024;
-
-// Values of a token row that LDS holds at a time: all of K, or equal parts of
-// it in whole steps, `most` at most.
-int staged_values(int K, int most) {
-  const int nstep = (K + kStepK - 1) / kStepK, parts = (K + most - 1) / most;
-  return (nstep + parts - 1) / parts * kStepK;
-}
-
 // Waves a workgroup and waves that split K, by the number of column groups of
 // all experts (G): fewer waves are left to wait for memory when G is small, and
 // each further wave on the same rows costs its start and a share of the sum at
@@ -695,42 +719,48 @@ int staged_values(int K, int most) {
 // Eight waves share the token rows of one workgroup from 2048 groups on (8
 // experts, 64 tokens: 109 us against 151 with four); with fewer groups four
 // spread over more compute units (one token: 27.6 against 29.6).
-template <int EPI, int GS, int TR>
-void launch_rows(const Int4Args &a, int64_t M, hipStream_t s) {
-  const int cols = EPI == EPI_Y || EPI == EPI_OUT || EPI == EPI_RELU2 ? 32 : 16;
+template <int EPI, int GS>
+void launch_rows(const Int4Args &a, int64_t n_tokens, int64_t M, hipStream_t s) {
+  constexpr int cols = EPI == EPI_Y || EPI == EPI_OUT || EPI == EPI_RELU2 ? 32 : 16;
+  constexpr int PARTS = parts<EPI>();
   const int64_t experts = M < a.E ? M : a.E, groups = (a.Nout / cols) * experts;
   const int waves = groups < 2048 ? 4 : 8;
   const int ks = groups < 1024 ? 4 : groups < 4096 ? 2 : 1;
   const int wide = cols * (waves / ks);
-  constexpr int PARTS = parts<EPI>();
-  const int kc = staged_values(a.K, kTokenLds / (2 * TR * PARTS));
-  const size_t rows = (size_t)PARTS * TR * kc * 2, red = sizeof(float) * waves * 2 * TR * 17;
   const dim3 grid((unsigned)((a.Nout + wide - 1) / wide), (unsigned)experts), block(64 * waves);
-  if constexpr (TR == 1)
+  auto bytes = [&](int rows) { return (size_t)rows * staged_values(a.K, rows) * 2; };
+  if (n_tokens == 1) {
+    const int kc = staged_values(a.K, PARTS);
     hipLaunchKernelGGL((expert_int4_one_kernel<EPI, GS>), grid, block,
-                       rows + (size_t)kc / 32 * sizeof(float), s, a, ks, kc);
-  else
-    hipLaunchKernelGGL((expert_int4_kernel<EPI, GS, TR>), grid, block, rows > red ? rows : red, s,
-                       a, ks, kc);
-}
-
-template <int EPI, int GS>
-void launch_tiles(const Int4Args &a, int64_t n_tokens, int64_t M, hipStream_t s) {
-  // One token has a kernel of its own.  Token rows held at a time: an expert has
-  // at most one a token, and past those held its weights are read again.  Up to
-  // two rows an expert on average four are enough (33 tokens, 128 experts: 350 us against 366 with 16); at
-  // four an expert they are not (64 experts, 32 tokens: 198 against 145).
-  if (n_tokens == 1) launch_rows<EPI, GS, 1>(a, M, s);
-  else if (n_tokens <= 4 || M <= 2 * (int64_t)a.E) launch_rows<EPI, GS, 4>(a, M, s);
-  else launch_rows<EPI, GS, 16>(a, M, s);
+                       bytes(PARTS) + (size_t)kc / 32 * sizeof(float), s, a, ks, kc);
+    return;
+  }
+  auto run = [&](auto tiles) {
+    constexpr int TILES = decltype(tiles)::value;
+    // Token rows a pass: an expert has about one a token at most, and LDS that it
+    // cannot fill keeps other workgroups away.
+    int most = 4;
+    while (most < n_tokens && most < 16 * TILES / PARTS) most *= 2;
+    size_t lds = sizeof(float) * waves * 2 * 16 * 17;
+    for (int rows = 4; rows <= most; rows *= 2)
+      if (bytes(PARTS * rows) > lds) lds = bytes(PARTS * rows);
+    hipLaunchKernelGGL((expert_int4_kernel<EPI, GS, TILES>), grid, block, lds, s, a, ks, most);
+  };
+  // Products of their own for the second parts wherever an expert can have more rows
+  // than a pass holds without: even routing loses up to 2 % by them (33 tokens of 128
+  // experts 359 -> 366 us; groups of 32 427 -> 461), skewed routing and more rows
+  // an expert gain (the same 33 tokens with exponent 1.1 404 -> 389, 128 tokens 912 ->
+  // 773; 8 experts, 64 tokens 141 -> 128).
+  if (PARTS == 2 && n_tokens > 8) run(std::integral_constant<int, PARTS>());
+  else run(std::integral_constant<int, 1>());
 }
 
 template <int EPI>
 hipError_t launch_groups(const Int4Args &a, int group, int64_t n_tokens, int64_t M,
                          hipStream_t s) {
-  if (group == 32) launch_tiles<EPI, 1>(a, n_tokens, M, s);
-  else if (group == 64) launch_tiles<EPI, 2>(a, n_tokens, M, s);
-  else launch_tiles<EPI, 4>(a, n_tokens, M, s);
+  if (group == 32) launch_rows<EPI, 1>(a, n_tokens, M, s);
+  else if (group == 64) launch_rows<EPI, 2>(a, n_tokens, M, s);
+  else launch_rows<EPI, 4>(a, n_tokens, M, s);
   return hipGetLastError();
 }
 
