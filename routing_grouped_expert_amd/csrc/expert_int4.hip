@@ -604,7 +604,8 @@ expert_int4_kernel(Int4Args g, int ks, int most) {
   }
 }
 
-// One token (its expert's only row): as expert_int4_kernel, on DotRows.
+// One token: as expert_int4_kernel, on DotRows.  An expert has one row, or more in a
+// routing of the caller's own that names it in several slots.
 template <int EPI, int GS>
 __global__ __launch_bounds__(512) void expert_int4_one_kernel(Int4Args g, int ks, int kc) {
   constexpr bool kPlain = EPI == EPI_Y || EPI == EPI_OUT || EPI == EPI_RELU2;
@@ -618,7 +619,8 @@ __global__ __launch_bounds__(512) void expert_int4_one_kernel(Int4Args g, int ks
   find_expert(g.offsets, g.E, want, sel);
   const int e = __builtin_amdgcn_readfirstlane(sel[0]);
   if (e < 0) return;  // the whole workgroup
-  const int p = __builtin_amdgcn_readfirstlane(sel[1]);
+  const int row0 = __builtin_amdgcn_readfirstlane(sel[1]);
+  const int cnt = __builtin_amdgcn_readfirstlane(sel[2]);
 
   const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -631,56 +633,58 @@ __global__ __launch_bounds__(512) void expert_int4_one_kernel(Int4Args g, int ks
     return kPlain ? n0 + 16 * t + x : g.interleaved ? 2 * (n0 + x) + t : t * Nout + n0 + x;
   });
   float *sums = reinterpret_cast<float *>(lds + PARTS * 2 * kc);
-  float acc[2] = {0.f, 0.f};
-  for (int kb = 0; kb < K; kb += kc) {
-    const int klen = min(kc, K - kb);
-    const int s0 = kb / kStepK, ns = (klen + kStepK - 1) / kStepK, per = (ns + ks - 1) / ks;
-    const int first = s0 + min(kw * per, ns), last = live ? s0 + min(kw * per + per, ns) : first;
-    typename DotRows<GS>::Codes c0, c1;
-    if (first < last) rows.load(c0, first);
-    if (first + 1 < last) rows.load(c1, first + 1);
-    if (kb > 0) __syncthreads();
-    const int row = g.gather ? g.col_sorted[p] / g.topk : p;
-    for (int c = threadIdx.x; c < klen / 8; c += blockDim.x) {
-      u32x4_t v[PARTS];
+  for (int p = row0; p < row0 + cnt; ++p) {
+    float acc[2] = {0.f, 0.f};
+    for (int kb = 0; kb < K; kb += kc) {
+      const int klen = min(kc, K - kb);
+      const int s0 = kb / kStepK, ns = (klen + kStepK - 1) / kStepK, per = (ns + ks - 1) / ks;
+      const int first = s0 + min(kw * per, ns), last = live ? s0 + min(kw * per + per, ns) : first;
+      typename DotRows<GS>::Codes c0, c1;
+      if (first < last) rows.load(c0, first);
+      if (first + 1 < last) rows.load(c1, first + 1);
+      if (p > row0 || kb > 0) __syncthreads();
+      const int row = g.gather ? g.col_sorted[p] / g.topk : p;
+      for (int c = threadIdx.x; c < klen / 8; c += blockDim.x) {
+        u32x4_t v[PARTS];
 #pragma unroll
-      for (int u = 0; u < PARTS; ++u)
-        v[u] = *reinterpret_cast<const u32x4_t *>(reinterpret_cast<const bf16_t *>(g.A) +
-                                                  (size_t)(PARTS * row + u) * K + kb + 8 * c);
-      float s = 0.f;  // sums of 32: four neighbouring lanes
+        for (int u = 0; u < PARTS; ++u)
+          v[u] = *reinterpret_cast<const u32x4_t *>(reinterpret_cast<const bf16_t *>(g.A) +
+                                                    (size_t)(PARTS * row + u) * K + kb + 8 * c);
+        float s = 0.f;  // sums of 32: four neighbouring lanes
 #pragma unroll
-      for (int u = 0; u < PARTS; ++u) {
-        *reinterpret_cast<u32x4_t *>(lds + u * 2 * kc + 16 * c) = token_order(v[u]);
-        float f[8];
-        unpack(v[u], f);
+        for (int u = 0; u < PARTS; ++u) {
+          *reinterpret_cast<u32x4_t *>(lds + u * 2 * kc + 16 * c) = token_order(v[u]);
+          float f[8];
+          unpack(v[u], f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s += f[i];
+          for (int i = 0; i < 8; ++i) s += f[i];
+        }
+        s += __shfl_xor(s, 1);
+        s += __shfl_xor(s, 2);
+        if ((c & 3) == 0) sums[c >> 2] = s;
       }
-      s += __shfl_xor(s, 1);
-      s += __shfl_xor(s, 2);
-      if ((c & 3) == 0) sums[c >> 2] = s;
+      __syncthreads();
+      rows.template stream<PARTS>(c0, c1, first, last, s0, lds, 2 * kc, sums, acc);
+    }
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      acc[t] += __shfl_xor(acc[t], 1);
+      acc[t] += __shfl_xor(acc[t], 2);
+    }
+    if ((lane & 3) == 0) {
+      red[wave][0][lane >> 2] = acc[0];
+      red[wave][1][lane >> 2] = acc[1];
     }
     __syncthreads();
-    rows.template stream<PARTS>(c0, c1, first, last, s0, lds, 2 * kc, sums, acc);
+    if (kw != 0 || lane >= COLS || !live) continue;
+    auto part = [&](int t, int c) {
+      float v = 0.f;
+      for (int w = wave; w < wave + ks; ++w) v += red[w][t][c];
+      return v;
+    };
+    finish<EPI>(g, p, n0 + lane, part(kPlain ? lane >> 4 : 0, lane & 15),
+                kPlain ? 0.f : part(1, lane & 15));
   }
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    acc[t] += __shfl_xor(acc[t], 1);
-    acc[t] += __shfl_xor(acc[t], 2);
-  }
-  if ((lane & 3) == 0) {
-    red[wave][0][lane >> 2] = acc[0];
-    red[wave][1][lane >> 2] = acc[1];
-  }
-  __syncthreads();
-  if (kw != 0 || lane >= COLS || !live) return;
-  auto part = [&](int t, int c) {
-    float v = 0.f;
-    for (int w = wave; w < wave + ks; ++w) v += red[w][t][c];
-    return v;
-  };
-  finish<EPI>(g, p, n0 + lane, part(kPlain ? lane >> 4 : 0, lane & 15),
-              kPlain ? 0.f : part(1, lane & 15));
 }
 
 // out[t] = sum over the token's slots of its fp32 rows, rounded once.

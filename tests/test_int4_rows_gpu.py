@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import oracle
-from routing_grouped_expert_amd import moe_experts_int4, moe_route
+from routing_grouped_expert_amd import Routing, moe_experts_int4, moe_route
 from tests.test_int4_gpu import _Values
 from tests.test_int4_precision_gpu import _whole_codes
 
@@ -46,3 +46,39 @@ def test_one_expert_takes_every_token(n, group):
     r = moe_route(lg.to(torch.bfloat16).to(DEV), k)
     assert int(r.col_sum[3]) == n and int(r.col_sum[0]) == 0
     _check(_x(n, g), r.topk_idx.cpu().numpy(), r.topk_w.double().cpu().numpy(), w13, w2, r)
+
+
+def _routing_of(idx, e):
+    """Routing metadata for chosen experts idx [N, k] with equal weights."""
+    n, k = idx.shape
+    flat = idx.reshape(-1)
+    col = torch.sort(flat, stable=True)[1]
+    row = torch.empty_like(col)
+    row[col] = torch.arange(n * k)
+    count = torch.bincount(flat, minlength=e)
+    bits = torch.zeros(n, (e + 31) // 32, dtype=torch.int64)
+    for t in range(n):
+        for j in set(idx[t].tolist()):
+            bits[t, j // 32] |= 1 << (j % 32)
+    w = torch.full((n, k), 1.0 / k)
+    i32 = {"topk_idx": idx, "bitmatrix": torch.where(bits >= 2 ** 31, bits - 2 ** 32, bits),
+           "col_sum": count, "offsets": torch.cat([count.new_zeros(1), count.cumsum(0)]),
+           "col_sorted": col, "row_sorted": row}
+    return Routing(**{f: v.int().to(DEV) for f, v in i32.items()}, topk_w=w.to(DEV),
+                   gate_scal=w.reshape(-1).to(DEV))
+
+
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("n,k,picks", [(1, 4, [2, 2, 5, 2]), (1, 2, [0, 0]), (1, 8, [1] * 8),
+                                       (2, 8, [3, 3, 3, 3, 3, 0, 3, 3]), (3, 4, [6, 1, 6, 1])])
+def test_one_expert_in_several_slots_of_a_token(n, k, picks, group):
+    """A routing of the caller's own may name an expert in several slots of a token:
+    every slot counts, also where one token has a kernel of its own."""
+    print(f"[int4-rows] n={n} {picks} G={group}", flush=True)
+    e = 8
+    g = torch.Generator().manual_seed(n + k)
+    idx = torch.tensor([picks] * n)
+    w13 = _whole_codes(g, e, I, H, group, False)
+    w2 = _whole_codes(g, e, H, I, group, True)
+    r = _routing_of(idx, e)
+    _check(_x(n, g), idx.numpy(), r.topk_w.double().cpu().numpy(), w13, w2, r)
