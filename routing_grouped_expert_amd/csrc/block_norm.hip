@@ -278,14 +278,16 @@ __global__ __launch_bounds__(block_threads(TPR)) void block_norm_backward_kernel
     if (g.y) {
       if (g.w_post || g.gate_kind == MOE_GATE_TOKEN) row_sum<TPR>(c2, red2, half2);
       if (g.gate_kind == MOE_GATE_TOKEN && live && lane == 0) g.d_gate[row] = c2[1];
-      const float m2 = g.w_post ? c2[0] * inv_h : 0.f;
+      const float m2 = c2[0] * inv_h;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int c = lane + i * TPR;
-        float yv[CH];
-        unpack(yr[i], yv);
+        if (g.w_post) {  // (without the norm d_y does not depend on y, which may be infinite)
+          float yv[CH];
+          unpack(yr[i], yv);
 #pragma unroll
-        for (int q = 0; q < CH; ++q) dv[i][q] = ry * fmaf(-m2 * ry, yv[q], dv[i][q]);
+          for (int q = 0; q < CH; ++q) dv[i][q] = ry * fmaf(-m2 * ry, yv[q], dv[i][q]);
+        }
         if (live && c < nch) store_chunk<T>(g.d_y, row, H, c, pack(dv[i]));
       }
     }
