@@ -21,7 +21,10 @@
 // A row is read once into registers (TPR threads a row, V 16-byte chunks a
 // thread), summed across its threads in fp32 and written once; the step is
 // bound by HBM: forward 16384 x 4096 bf16 (537 MB) 102 us, 5.2 TB/s, a copy's
-// rate; backward (805 MB) 158 us, 5.1 TB/s; one token 3.2 us.  Loading the next
+// rate; backward (805 MB) 158 us, 5.1 TB/s; one token 3.2 us.  That holds for the
+// backward pass up to 8192 values: the wider kernels pass the 128 registers that
+// 1024 threads leave each, 114 (bf16) and 156 (fp32) of them go through scratch,
+// and 2048 x 16384 takes 368 us in bf16 (1.1 TB/s) and 466 in fp32 (1.7 TB/s).  Loading the next
 // row ahead of the sums measured no faster (backward 164 -> 167 us).  A workgroup
 // takes rows in turn, so that the weights are loaded once and the column sums of
 // the gradient are added up in registers; the workgroups' sums are then added in
@@ -358,25 +361,36 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(const float *__restric
   }
 }
 
-// Calls go(TPR, V) for the number of 16-byte chunks in a row: two chunks a
-// thread up to 512, the backward pass one from there on, where two leave it one
-// wave a SIMD (its row, weights and column sums are 190 registers at V = 2).
-template <bool kBackward, typename F> void by_width(int nch, F go) {
+// Calls go(TPR, V) for the number of 16-byte chunks in a row of T.  V = 2 up to
+// 512 chunks where one wave or 256 threads then cover the row; from there on the
+// backward pass, whose bf16 row, weights and column sums are 190 registers at V = 2
+// (two waves a SIMD) and 110 - 140 at V = 1 (three or four), takes V = 1 as far as
+// 1024 threads reach.  Only what a row of up to kMaxNormHidden values can ask for
+// is built.
+template <bool kBackward, typename T, typename F> void by_width(int nch, F go) {
   using std::integral_constant;
   integral_constant<int, 1> one;
   integral_constant<int, 2> two;
   integral_constant<int, 4> four;
-  if (nch <= 16) go(integral_constant<int, 16>(), one);
-  else if (nch <= 64) go(integral_constant<int, 64>(), one);
-  else if (nch <= 128) go(integral_constant<int, 64>(), two);
-  else if (nch <= 256) go(integral_constant<int, 256>(), one);
-  else if (nch <= 384 && kBackward) go(integral_constant<int, 384>(), one);
-  else if (nch <= 512) go(integral_constant<int, 256>(), two);
-  else if (nch <= 768 && kBackward) go(integral_constant<int, 768>(), one);
-  else if (nch <= 1024 && kBackward) go(integral_constant<int, 1024>(), one);
-  else if (nch <= 1024) go(integral_constant<int, 256>(), four);
-  else if (nch <= 2048) go(integral_constant<int, 1024>(), two);
-  else go(integral_constant<int, 1024>(), four);
+  if (nch <= 16) return go(integral_constant<int, 16>(), one);
+  if (nch <= 64) return go(integral_constant<int, 64>(), one);
+  if (nch <= 128) return go(integral_constant<int, 64>(), two);
+  if (nch <= 256) return go(integral_constant<int, 256>(), one);
+  if constexpr (kBackward) {
+    if (nch <= 384) return go(integral_constant<int, 384>(), one);
+    if (nch <= 512) return go(integral_constant<int, 256>(), two);
+    if (nch <= 768) return go(integral_constant<int, 768>(), one);
+    if (nch <= 1024) return go(integral_constant<int, 1024>(), one);
+  } else {
+    if (nch <= 512) return go(integral_constant<int, 256>(), two);
+    if (nch <= 1024) return go(integral_constant<int, 256>(), four);
+  }
+  if constexpr (kMaxNormHidden / chunk_elems<T>() <= 2048) {
+    go(integral_constant<int, 1024>(), two);
+  } else {
+    if (nch <= 2048) return go(integral_constant<int, 1024>(), two);
+    go(integral_constant<int, 1024>(), four);
+  }
 }
 
 int chunks_of(int hidden, moe_dtype_t dt) { return hidden / (dt == MOE_BF16 ? 8 : 4); }
@@ -406,7 +420,7 @@ hipError_t launch_block_norm(const BlockNormArgs &g, moe_dtype_t dt, hipStream_t
   const dim3 grid((unsigned)norm_blocks(g.n_tokens, nch, kForwardBlocks));
   auto run = [&](auto tag) {
     using T = decltype(tag);
-    by_width<false>(nch, [&](auto tpr, auto v) {
+    by_width<false, T>(nch, [&](auto tpr, auto v) {
       constexpr int TPR = decltype(tpr)::value, V = decltype(v)::value;
       hipLaunchKernelGGL((block_norm_kernel<T, TPR, V>), grid, dim3(block_threads(TPR)), 0, s, g);
     });
@@ -422,7 +436,7 @@ hipError_t launch_block_norm_backward(const BlockNormArgs &g, const ColumnSums &
   if (blocks > 0) {
     auto run = [&](auto tag) {
       using T = decltype(tag);
-      by_width<true>(nch, [&](auto tpr, auto v) {
+      by_width<true, T>(nch, [&](auto tpr, auto v) {
         constexpr int TPR = decltype(tpr)::value, V = decltype(v)::value;
         hipLaunchKernelGGL((block_norm_backward_kernel<T, TPR, V>), dim3(blocks),
                            dim3(block_threads(TPR)), 0, s, g);
