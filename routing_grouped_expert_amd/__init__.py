@@ -52,7 +52,7 @@ weights of 4-bit codes with a scale and a zero point a group, for decoding:
 from __future__ import annotations
 
 import ctypes
-from dataclasses import dataclass, fields
+from dataclasses import dataclass
 from typing import Optional
 
 import torch
@@ -138,7 +138,9 @@ def _shapes(x, w13, w2, act, out=None, logits=None, n_experts=None):
         raise ValueError("logits must be [N, E]")
 
 
-def _check_routing(routing: "Routing", n: int, e: int, k: int):
+def _check_routing(routing: "Routing", n: int, e: int, k: int, fills: Optional[int] = None):
+    """Buffers of the sizes that n tokens, e experts and k slots need.  ``fills``:
+    the call writes the routing, of a layer of that many experts."""
     m = n * k
     want = {"topk_idx": (n, k), "topk_w": (n, k), "bitmatrix": (n, (e + 31) // 32),
             "col_sum": (e,), "offsets": (e + 1,), "col_sorted": (m,), "row_sorted": (m,),
@@ -149,6 +151,8 @@ def _check_routing(routing: "Routing", n: int, e: int, k: int):
             raise ValueError(f"routing.{f} must be contiguous {shp}, got {tuple(t.shape)}")
     if routing.gate_scal.dtype != routing.topk_w.dtype:
         raise TypeError("routing.topk_w and gate_scal must share a dtype")
+    if fills is not None:
+        routing.layer_experts = None if fills == e else fills
 
 
 def _stream(dev, stream) -> ctypes.c_void_p:
@@ -168,6 +172,8 @@ class Routing:
     col_sorted: torch.Tensor  # [N*k] int32
     row_sorted: torch.Tensor  # [N*k] int32
     gate_scal: torch.Tensor   # [N*k] logits dtype
+    # the layer's expert count in the routing of an expert share; None: whole layer
+    layer_experts: Optional[int] = None
 
     @classmethod
     def empty(cls, n_tokens: int, n_experts: int, topk: int, dtype: torch.dtype,
@@ -193,9 +199,12 @@ class Routing:
     def topk(self) -> int:
         return self.topk_idx.shape[1]
 
+    def tensors(self) -> tuple:
+        return (self.topk_idx, self.topk_w, self.bitmatrix, self.col_sum, self.offsets,
+                self.col_sorted, self.row_sorted, self.gate_scal)
+
     def as_c(self) -> N.MoeRouting:
-        return N.MoeRouting(*(getattr(self, f.name).data_ptr() for f in fields(self)),
-                            _dt(self.topk_w))
+        return N.MoeRouting(*(t.data_ptr() for t in self.tensors()), _dt(self.topk_w))
 
 
 def _params(params: Optional[dict]) -> Optional[N.MoeActParams]:
@@ -268,7 +277,7 @@ def prepare_route(logits: torch.Tensor, topk: int, *, routing: Optional[Routing]
     _share(e, lo, nl)
     if routing is None:
         routing = Routing.empty(n, nl, topk, logits.dtype, dev)
-    _check_routing(routing, n, nl, topk)
+    _check_routing(routing, n, nl, topk, fills=e)
     ws = _workspace(workspace, moe_workspace_bytes(n, e, topk, 0, 0, logits.dtype), dev)
     r = routing.as_c()
     if _share_of is None:
@@ -474,7 +483,7 @@ def prepare_forward(x, logits, w13, w2, topk: int, act: str, layout: str = "pack
         raise TypeError("moe_forward takes logits in the layer dtype")
     if routing is None:
         routing = Routing.empty(n, e, topk, logits.dtype, dev)
-    _check_routing(routing, n, e, topk)
+    _check_routing(routing, n, e, topk, fills=e)
     if out is None:
         out = torch.empty_like(x)
     ws = _workspace(workspace, moe_workspace_bytes(n, e, topk, hidden, inter, x.dtype), dev)
@@ -498,7 +507,7 @@ def prepare_forward_noalloc(x, logits, w13, w2, topk: int, act: str, layout: str
         raise TypeError("moe_forward_noalloc takes logits in the layer dtype")
     if routing is None:
         routing = Routing.empty(n, e, topk, logits.dtype, dev)
-    _check_routing(routing, n, e, topk)
+    _check_routing(routing, n, e, topk, fills=e)
     if out is None:
         out = torch.empty_like(x)
     r = routing.as_c()
@@ -535,7 +544,7 @@ def prepare_forward_ep(x, logits, w13, w2, topk: int, local_offset: int, act: st
         raise TypeError("moe_forward_ep takes logits in the layer dtype")
     if routing is None:
         routing = Routing.empty(n, nl, topk, logits.dtype, dev)
-    _check_routing(routing, n, nl, topk)
+    _check_routing(routing, n, nl, topk, fills=e)
     if out is None:
         out = torch.empty_like(x)
     ws = _workspace(workspace, moe_workspace_bytes(n, e, topk, hidden, inter, x.dtype), dev)
@@ -590,7 +599,7 @@ def prepare_gate_route(x: torch.Tensor, w_gate: torch.Tensor, topk: int, *,
     dev, n, e, logits = _gate_args(x, w_gate, logits)
     if routing is None:
         routing = Routing.empty(n, e, topk, x.dtype, dev)
-    _check_routing(routing, n, e, topk)
+    _check_routing(routing, n, e, topk, fills=e)
     ws = _workspace(workspace, moe_workspace_bytes(n, e, topk, x.shape[1], 0, x.dtype), dev)
     r = routing.as_c()
     args = (x.data_ptr(), w_gate.data_ptr(), _dt(x), n, x.shape[1], e, topk, logits.data_ptr(),
@@ -617,7 +626,7 @@ def prepare_gate_forward(x, w_gate, w13, w2, topk: int, act: str, layout: str = 
     hidden, inter = x.shape[1], w2.shape[2]
     if routing is None:
         routing = Routing.empty(n, e, topk, x.dtype, dev)
-    _check_routing(routing, n, e, topk)
+    _check_routing(routing, n, e, topk, fills=e)
     if out is None:
         out = torch.empty_like(x)
     ws = _workspace(workspace, moe_workspace_bytes(n, e, topk, hidden, inter, x.dtype), dev)
@@ -760,7 +769,7 @@ def prepare_forward_mxfp4(x, logits, w13_q, w13_s, w2_q, w2_s, topk: int, act: s
         raise ValueError("logits must be [N, E] in the layer dtype")
     if routing is None:
         routing = Routing.empty(n, e, topk, x.dtype, dev)
-    _check_routing(routing, n, e, topk)
+    _check_routing(routing, n, e, topk, fills=e)
     if out is None:
         out = torch.empty_like(x)
     ws = _workspace(workspace, moe_workspace_bytes(n, e, topk, hidden, inter, x.dtype), dev)
@@ -1286,8 +1295,8 @@ def _block_forward(x, w_gate, w13, w2, topk, act, layout, params, w_pre, w_post,
     logits = _output(logits, x, (n, e), x.dtype, stream, "logits")
     if routing is None:
         routing = _new_routing(n, e, topk, x, stream)
-    _check_routing(routing, n, e, topk)
-    _index(x, *(getattr(routing, f.name) for f in fields(routing)))
+    _check_routing(routing, n, e, topk, fills=e)
+    _index(x, *routing.tensors())
     need = (moe_workspace_bytes(n, e, topk, hidden, inter, x.dtype) + 255) // 256 * 256 \
         + (n * hidden * x.element_size() + 255) // 256 * 256
     ws = _scratch(workspace, x, need, stream)
@@ -1412,6 +1421,9 @@ def _int4_layer(x, w13, w2, act, layout):
 
 
 def _experts_int4(x, w13, w2, routing, act, layout, params, out, workspace, stream) -> _Call:
+    if routing.layer_experts is not None:
+        raise ValueError("moe_experts_int4 takes the whole layer's routing, not an expert share's "
+                         "(moe_route_ep)")
     dev, n, hidden, e, inter, group, c13, c2 = _int4_layer(x, w13, w2, act, layout)
     k = routing.topk
     off, col, row, scal = (routing.offsets, routing.col_sorted, routing.row_sorted,
@@ -1454,7 +1466,8 @@ def moe_experts_int4(x: torch.Tensor, w13_q: torch.Tensor, w13_s: torch.Tensor,
                      workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """moe_experts with 4-bit expert weights (codes, scales and zero points as
     moe_quantize_int4 gives them, zeros None for symmetric codes); bf16 layer,
-    shaped for decode-sized batches (see moe.h)."""
+    shaped for decode-sized batches (see moe.h).  ``routing`` is the whole layer's:
+    one of an expert share is refused."""
     return _experts_int4(x, (w13_q, w13_s, w13_z), (w2_q, w2_s, w2_z), routing, act, layout,
                          params, out, workspace, stream).run()
 
@@ -1467,8 +1480,8 @@ def _forward_int4(x, logits, w13, w2, topk, act, layout, params, out, routing, w
         raise ValueError("logits must be [N, E] in the layer dtype")
     if routing is None:
         routing = _new_routing(n, e, topk, x, stream)
-    _check_routing(routing, n, e, topk)
-    _index(x, *(getattr(routing, f.name) for f in fields(routing)))
+    _check_routing(routing, n, e, topk, fills=e)
+    _index(x, *routing.tensors())
     out = _output(out, x, (n, hidden), x.dtype, stream, "out")
     ws = _scratch(workspace, x, moe_int4_workspace_bytes(n, e, topk, hidden, inter), stream)
     r = routing.as_c()
