@@ -1017,7 +1017,10 @@ def _route_backward(d_topk_w, routing, n_experts, d_logits, stream) -> _Call:
     n, k, w, wdt = _row_routing(routing, dev, order, "topk_idx", True)
     if tuple(d_topk_w.shape) != (n, k) or d_topk_w.dtype != torch.float32:
         raise ValueError("d_topk_w must be fp32 [N, k]")
-    e = routing.n_experts if n_experts is None else n_experts
+    layer = routing.layer_experts
+    e = n_experts if n_experts is not None else routing.n_experts if layer is None else layer
+    if layer is not None and e != layer:
+        raise ValueError(f"the routing is a share's of a layer of {layer} experts, not {e}")
     d_logits = _output(d_logits, d_topk_w, (n, e), routing.topk_w.dtype, stream, "d_logits")
     r = N.MoeRouting(topk_idx=order.data_ptr(), topk_w=w, w_dtype=wdt)
     args = (d_topk_w.data_ptr(), n, e, k, ctypes.byref(r), d_logits.data_ptr(),
@@ -1036,8 +1039,8 @@ def moe_route_backward(d_topk_w: torch.Tensor, routing: Routing,
                        d_logits: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Gradient of the routing weights with respect to the router logits
     ``[N, E]`` (zeros for experts that were not selected).  ``n_experts``: the
-    layer's expert count, needed with the routing of an expert share, whose
-    ``col_sum`` holds the share's experts only."""
+    layer's expert count, by default the routing's own (that of the whole layer also
+    where moe_route_ep or moe_forward_ep filled it for a share)."""
     return _route_backward(d_topk_w, routing, n_experts, d_logits, stream).run()
 
 

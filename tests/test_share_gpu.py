@@ -4,8 +4,8 @@ import pytest
 import torch
 
 from routing_grouped_expert_amd import (Routing, moe_experts_int4, moe_forward_ep, moe_gate_route,
-                                        moe_quantize_int4, moe_route, moe_route_ep,
-                                        prepare_experts_int4)
+                                        moe_quantize_int4, moe_route, moe_route_backward,
+                                        moe_route_ep, prepare_experts_int4, prepare_route_backward)
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -57,3 +57,22 @@ def test_a_routing_that_is_filled_again_is_what_its_last_call_made_it():
     moe_route_ep(wide.contiguous(), 2, 0, 4, routing=r)
     moe_gate_route(x, torch.randn(4, 64, device=DEV).to(x.dtype), 2, routing=r)
     assert r.layer_experts is None
+
+
+@pytest.mark.parametrize("e,lo,nl", [(8, 2, 3), (40, 32, 8), (256, 0, 64)])
+def test_softmax_gradient_of_a_share_covers_the_layer(e, lo, nl):
+    """topk_idx holds the layer's expert ids, so d_logits has the layer's width; the
+    share's own count would drop the gradients of every expert past it."""
+    n, k = 30, 2
+    g = torch.Generator().manual_seed(e)
+    lg = torch.randn(n, e, generator=g).to(DEV)
+    dw = torch.randn(n, k, generator=g).to(DEV)
+    want = moe_route_backward(dw, moe_route(lg, k))
+    r = moe_route_ep(lg, k, lo, nl)
+    for got in (moe_route_backward(dw, r), moe_route_backward(dw, r, e),
+                prepare_route_backward(dw, r)()):
+        assert got.shape == (n, e)
+        assert torch.equal(got, want)
+    for wrong in (nl, e + 8):
+        with pytest.raises(ValueError, match="share"):
+            moe_route_backward(dw, r, wrong)
