@@ -238,7 +238,8 @@ moe_status_t moe_combine(const void *y_sorted, moe_dtype_t dtype, int64_t n_toke
  *   <d_out[t], y_sorted[row_sorted[t*topk + j]]> summed in fp32.
  * moe_route_backward: the gradient of topk_w with respect to the logits:
  *   d_logits [N, n_experts] in routing->w_dtype, d_logits[t][topk_idx[t][j]] =
- *   topk_w[t][j] * (d_topk_w[t][j] - sum_i topk_w[t][i] * d_topk_w[t][i]) and 0
+ *   topk_w[t][j] * (d_topk_w[t][j] - sum_i topk_w[t][i] * d_topk_w[t][i]), summed
+ *   over the slots j that name the expert (one in a routing of moe_route), and 0
  *   for every expert that was not selected (the selection itself has no
  *   gradient).  n_experts is the layer's expert count, an expert share's
  *   included.  Reads routing->topk_idx and topk_w.  It is linear in d_topk_w:

@@ -7,6 +7,7 @@
 //   weighted combine  out[t] = sum_j w[t, j] y[p]       (fp32, slot order, one rounding)
 //   its gradient      d_y[p] = w[t, j] d_out[t];  d_w[t, j] = <d_out[t], y[p]>
 //   softmax gradient  d_logits[t, e_j] = w_j (d_w_j - sum_i w_i d_w_i), 0 elsewhere
+//                     (summed where several slots name one expert)
 //
 // The gradient of the dispatch is the plain combine (combine.hip).  Every
 // kernel walks tokens, not sorted rows: a token's row is then read (or written)
@@ -204,7 +205,7 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
     const int e = topk_idx[t * K + j] - c * C;
     const float d = to_f32(w[t * K + j]) * (dw[t * K + j] - s);
 #pragma unroll
-    for (int i = 0; i < C; ++i) v[i] = e == i ? d : v[i];
+    for (int i = 0; i < C; ++i) v[i] += e == i ? d : 0.f;
   }
   W *out = d_logits + t * E + (int64_t)c * C;
   if constexpr (C == 1) *out = from_f32<W>(v[0]);
