@@ -24,11 +24,11 @@
 // rate; backward (805 MB) 158 us, 5.1 TB/s; one token 3.2 us.  That holds for the
 // backward pass up to 8192 values: the wider kernels pass the 128 registers that
 // 1024 threads leave each, 114 (bf16) and 156 (fp32) of them go through scratch,
-// and 2048 x 16384 takes 368 us in bf16 (1.1 TB/s) and 466 in fp32 (1.7 TB/s).  Loading the next
-// row ahead of the sums measured no faster (backward 164 -> 167 us).  A workgroup
-// takes rows in turn, so that the weights are loaded once and the column sums of
-// the gradient are added up in registers; the workgroups' sums are then added in
-// a fixed order by a second kernel, with no atomics.
+// and 2048 x 16384 takes 368 us in bf16 (1.1 TB/s) and 466 in fp32 (1.7 TB/s).
+// Loading the next row ahead of the sums measured no faster (backward 164 -> 167
+// us).  A workgroup takes rows in turn, so that the weights are loaded once and the
+// column sums of the gradient are added up in registers; the workgroups' sums are
+// then added in a fixed order by a second kernel, with no atomics.
 #include "rows.h"
 
 #include <type_traits>

@@ -37,14 +37,17 @@
 // and, for groups of 32 and 64, lane swaps bring the dwords to the lanes whose
 // product they belong to, so that no product mixes two groups.
 //
-// What bounds it: the rate of the loads, and about 240 vector instructions (of
-// the whole kernel, counted) and 24 products a step of 8192 weights; at one token the
-// start of three kernels and of their loads.  Measured against the bytes of the
-// touched experts: 64 experts (H 4096, I 1536, k 8), 32 tokens, groups of 128:
-// 147 us, 4.2 TB/s; 128 experts (H = I = 2880, k 4), groups of 64 with zero
-// points: 128 tokens 420 us, 4.1 TB/s, 33 tokens 354 us, 3.2 TB/s (rows of 1440
-// bytes straddle cache lines: 2816 wide 3.8 TB/s; the loads alone 319 us), one
-// token 25 us (the loads alone 21, three empty kernels 10).
+// What bounds it: the rate of the loads, and about 235 vector instructions (of
+// the whole kernel, counted) and 24 products a step of 8192 weights in w13, 300 and
+// 48 in w2 with both parts; at one token the start of three kernels and of their
+// loads.  Measured against the bytes of the touched experts: 64 experts (H 4096, I
+// 1536, k 8), 32 tokens, groups of 128: 151 us, 4.1 TB/s; 128 experts (H = I =
+// 2880, k 4), groups of 64 with zero points: 128 tokens 431 us, 4.0 TB/s, 33 tokens
+// 370 us, 3.1 TB/s (rows of 1440 bytes straddle cache lines: 2816 wide 3.6 TB/s;
+// the loads alone 319 us), one token 26.6 us (the loads alone 21, three empty
+// kernels 10).  The second parts cost what w2 has more of: with one part those five
+// took 148, 432, 355, 293 (2816 wide) and 25.3 us, and where experts hold 16 rows and
+// more the whole 15 % less (8 experts, 64 tokens 112 us for 129).
 #include "gemm_common.h"
 #include "lds_dma.h"
 #include "rows.h"
@@ -258,16 +261,7 @@ template <int GS> struct WaveRows : ExpertArrays<GS> {
     const int ngroups = kWhole ? 8 / GS : (A::K - step * kStepK) / (32 * GS);
     const bf16x8_t ones = __builtin_bit_cast(
         bf16x8_t, u32x4_t{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u});
-    uint32_t mt[2][4 * NM];  // scale << 16 | zero point of each group
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int m = 0; m < NM; ++m) {
-        uint32_t v[4];
-        spread_groups(c.s[t][m] << 16 | c.z[t][m], v);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) mt[t][4 * m + q] = v[q];
-      }
+    uint32_t mt[2][4];  // scale << 16 | zero point of the groups (of this half for NM = 2)
     f32x4_t sum[2], tot;
     const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -275,6 +269,10 @@ template <int GS> struct WaveRows : ExpertArrays<GS> {
       u32x4_t cw[2];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
+        if (NM == 2 || b == 0) {
+          const int m = NM == 2 ? b : 0;
+          spread_groups(c.s[t][m] << 16 | c.z[t][m], mt[t]);
+        }
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           cw[t][q] = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)c.w[t][b][q]);
@@ -298,14 +296,14 @@ template <int GS> struct WaveRows : ExpertArrays<GS> {
             sum[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, wv[t], begins ? zero : sum[t], 0,
                                                              0, 0);
         }
-        // (keeps the second parts' loads from being moved up past the registers: 15-40
-        // spilled without)
+        // (keeps the second parts' loads from being moved up past the registers: up to 18
+        // spilled without, 8 for groups of 32 with)
         if constexpr (TILES == 2) __builtin_amdgcn_sched_barrier(0);
         if (j % GS == GS - 1) {
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            const float f = __uint_as_float(mt[t][gr] & 0xffff0000u);
-            const float z = 128.f + (float)(mt[t][gr] & 0xffu);
+            const float f = __uint_as_float(mt[t][gr & 3] & 0xffff0000u);
+            const float z = 128.f + (float)(mt[t][gr & 3] & 0xffu);
 #pragma unroll
             for (int q = 0; q < 4; ++q) acc[t][q] = fmaf(f, fmaf(-z, tot[q], sum[t][q]), acc[t][q]);
           }
@@ -345,8 +343,8 @@ __device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float acc) {
 // row l / 4 of a tile, piece l % 4 of 128 weights) with the token's values at
 // those places, the scale and zero point of the lane's own group, and one sum
 // over the four lanes of a row at the end.  The lanes keep what they load: no
-// permutation, no swaps (one token of 128 experts, groups of 64: 25.9 -> 25.2
-// us; of 32 experts, groups of 32: 29.0 -> 25.0).
+// permutation, no swaps (one token of 128 experts, groups of 64: 28.7 us by the
+// products, 27.1 this way; of 32 experts, groups of 32: 32.1 and 27.2).
 template <int GS> struct DotRows : ExpertArrays<GS> {
   using A = ExpertArrays<GS>;
   struct Codes {  // a step of the rows
@@ -490,8 +488,9 @@ __device__ __forceinline__ void finish(const Int4Args &g, int p, int col, float 
 // Parts of a token row: w2 takes the activation rows as hi and lo.
 template <int EPI> constexpr int parts() { return EPI == EPI_Y || EPI == EPI_OUT ? 2 : 1; }
 
-// LDS for token rows: 128 KB for whole rows of 4096 values leaves one workgroup
-// a compute unit (8 experts, 64 tokens: 114 us -> 161; 32 KB: 124).
+// LDS for token rows: 128 KB leaves one workgroup a compute unit (8 experts, 64
+// tokens 134 -> 173 us, 32 tokens of 64 experts 151 -> 167); 32 KB takes more parts of
+// a row (136 and 159).
 constexpr int kTokenLds = 64 * 1024;
 
 // Values of a token row that LDS holds at a time where it holds `rows` rows: all
@@ -509,8 +508,8 @@ __host__ __device__ inline int staged_values(int K, int rows) {
 // are read again.  How many rows LDS is laid out for follows from the expert's own
 // count, not from the average: routing is skewed, and the expert that most tokens
 // take sets the layer's time (128 experts 2880 wide, groups of 64, 33 tokens, Zipf-like
-// routing with exponent 1.1: 389 us, and 595 where all experts hold 4 rows because
-// there are less than two on average; even routing 366 and 352).
+// routing with exponent 1.1: 389 us, against 595 with 4 rows a pass for all because
+// there are less than two an expert on average; even routing 366 and 352).
 //
 // w2 takes the activation rows as two parts each.  With TILES = 1 the second parts
 // are the other 8 rows of the products (8 token rows a pass, nothing computed
@@ -563,8 +562,8 @@ expert_int4_kernel(Int4Args g, int ks, int most) {
       if (first < last) rows.load(c0, first);
       if (first + 1 < last) rows.load(c1, first + 1);
       if (a0 > 0 || kb > 0) __syncthreads();
-      // (four loads in flight: 16 rows 154 -> 147 us on the 64-expert layer; up to
-      // four rows are staged in one round anyway)
+      // (four loads in flight where rows are many: 8 experts, 64 tokens 138 -> 128 us;
+      // few rows gain nothing by them, one token each of four 71 -> 73)
       auto row = [&](int i) {
         const int p = row0 + a0 + i;
         return g.gather ? g.col_sorted[p] / g.topk : p;
@@ -717,12 +716,12 @@ __global__ __launch_bounds__(256) void sum_slots_kernel(const float *__restrict_
 // Waves a workgroup and waves that split K, by the number of column groups of
 // all experts (G): fewer waves are left to wait for memory when G is small, and
 // each further wave on the same rows costs its start and a share of the sum at
-// the end.  Measured (us, split in 4 / 2 / 1): G = 720, one token of 128
-// experts, 27.2 / 31.5 / 42.6; G = 2880, four tokens, 75.0 / 67.8 / 77.3; G =
-// 2048, 8 experts, 149 / 114 / 133; G = 23040, 33 tokens, 421 / 364 / 349.
-// Eight waves share the token rows of one workgroup from 2048 groups on (8
-// experts, 64 tokens: 109 us against 151 with four); with fewer groups four
-// spread over more compute units (one token: 27.6 against 29.6).
+// the end.  Measured (us a call, split in 4 / 2 / 1): G = 720, one token of 128
+// experts, 26.6 / 27.5 / 31.8; G = 2880, four tokens, 79.5 / 69.0 / 77.4; G =
+// 2048, 8 experts, 64 tokens, 176 / 128 / 142; G = 23040, 33 tokens, 420 / 392 /
+// 368.  Eight waves share the token rows of one workgroup from 2048 groups on (8
+// experts, 64 tokens: 123 us against 161 with four); with fewer groups four spread
+// over more compute units (one token: 26.6 against 30.8).
 template <int EPI, int GS>
 void launch_rows(const Int4Args &a, int64_t n_tokens, int64_t M, hipStream_t s) {
   constexpr int cols = EPI == EPI_Y || EPI == EPI_OUT || EPI == EPI_RELU2 ? 32 : 16;
@@ -752,7 +751,7 @@ void launch_rows(const Int4Args &a, int64_t n_tokens, int64_t M, hipStream_t s) 
   };
   // Products of their own for the second parts wherever an expert can have more rows
   // than a pass holds without: even routing loses up to 2 % by them (33 tokens of 128
-  // experts 359 -> 366 us; groups of 32 427 -> 461), skewed routing and more rows
+  // experts 359 -> 366 us; groups of 32, which spill 8 registers, 427 -> 447), skewed routing and more rows
   // an expert gain (the same 33 tokens with exponent 1.1 404 -> 389, 128 tokens 912 ->
   // 773; 8 experts, 64 tokens 141 -> 128).
   if (PARTS == 2 && n_tokens > 8) run(std::integral_constant<int, PARTS>());
