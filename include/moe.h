@@ -222,8 +222,9 @@ moe_status_t moe_combine(const void *y_sorted, moe_dtype_t dtype, int64_t n_toke
  * add nothing and get a zero weight gradient, and sorted rows that no slot
  * points to are left as they were.  dtype and routing->w_dtype are independent.
  * Deterministic, no atomics, no workspace; limits as moe_combine, and n_tokens *
- * hidden below 2^32 16-byte chunks (moe_combine_weighted_backward: n_tokens
- * below 2^24; moe_route_backward: n_tokens * n_experts below 2^32 - 2^10).
+ * hidden up to 2^32 - 2^10 16-byte chunks (moe_combine_weighted_backward:
+ * n_tokens up to 2^24 - 4; moe_route_backward: n_tokens * n_experts up to 2^32 -
+ * 2^10).
  * Outputs must not overlap inputs.
  *
  * moe_dispatch: x_sorted [N*topk, hidden]; x_sorted[row_sorted[t*topk + j]] =
@@ -520,8 +521,9 @@ typedef struct {
   const void *zeros; /* NULL: 8 */
 } moe_int4_weights_t;
 
-/* moe_quantize_int4: w [n_experts, rows, k] in `dtype` (finite) -> q, scales and
- *   zeros (NULL: symmetric).  Symmetric: scale = max|w| / 7; otherwise scale =
+/* moe_quantize_int4: w [n_experts, rows, k] in `dtype` (finite, as must be the
+ *   difference of any two weights of a group) -> q, scales and zeros (NULL:
+ *   symmetric).  Symmetric: scale = max|w| / 7; otherwise scale =
  *   (max(w, 0) - min(w, 0)) / 15 and zero = round(-min(w, 0) / scale); both
  *   scales rounded to bf16 before they are used, code = round(w / scale) + zero
  *   limited to [0, 15]; IEEE fp32 division, rounding to nearest, ties to even.
@@ -541,13 +543,15 @@ moe_status_t moe_dequantize_int4(const moe_int4_weights_t *w, int32_t n_experts,
  *   scales enter in fp32; the activation rows are kept to 16 bits of mantissa
  *   (moe_experts rounds them to bf16), the weighted expert rows stay fp32 and
  *   the output is rounded once.  x must be finite (an infinity becomes NaN in
- *   its token's row).
+ *   its token's row), and x and the activations below 2^112 in magnitude: sums of
+ *   a group's values times up to 143 stay finite in fp32 then.  A token may name
+ *   an expert in several slots.
  *   Deterministic.
  *   The routing is the whole layer's, not an expert share's.  Any batch is
  *   right; the kernel is shaped for decode-sized ones, a few rows an expert.
  *   From 48 rows an expert on, moe_dequantize_int4 once and moe_experts measured
- *   faster (8 experts, 4096 x 2048, groups of 64: 148 against 124 us at 48 rows,
- *   111 against 153 at 32).  workspace: moe_int4_workspace_bytes(...). */
+ *   faster (8 experts, 4096 x 2048, groups of 64: 176 against 124 us at 48 rows,
+ *   126 against 152 at 32).  workspace: moe_int4_workspace_bytes(...). */
 size_t moe_int4_workspace_bytes(int64_t n_tokens, int32_t n_experts, int32_t topk, int32_t hidden,
                                 int32_t inter);
 moe_status_t moe_experts_int4(const void *x, int64_t n_tokens, int32_t hidden,
