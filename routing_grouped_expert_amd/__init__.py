@@ -52,7 +52,7 @@ weights of 4-bit codes with a scale and a zero point a group, for decoding:
 from __future__ import annotations
 
 import ctypes
-from dataclasses import dataclass
+from dataclasses import InitVar, dataclass
 from typing import Optional
 
 import torch
@@ -151,8 +151,10 @@ def _check_routing(routing: "Routing", n: int, e: int, k: int, fills: Optional[i
             raise ValueError(f"routing.{f} must be contiguous {shp}, got {tuple(t.shape)}")
     if routing.gate_scal.dtype != routing.topk_w.dtype:
         raise TypeError("routing.topk_w and gate_scal must share a dtype")
-    if fills is not None:
-        routing.layer_experts = None if fills == e else fills
+    if fills is not None and fills != e:
+        routing.layer_experts = fills
+    elif fills is not None:
+        vars(routing).pop("layer_experts", None)
 
 
 def _stream(dev, stream) -> ctypes.c_void_p:
@@ -172,8 +174,13 @@ class Routing:
     col_sorted: torch.Tensor  # [N*k] int32
     row_sorted: torch.Tensor  # [N*k] int32
     gate_scal: torch.Tensor   # [N*k] logits dtype
-    # the layer's expert count in the routing of an expert share; None: whole layer
-    layer_experts: Optional[int] = None
+    # the layer's expert count in the routing of an expert share; None: whole layer.
+    # (An attribute of a share's routing only, so that the fields stay all tensors.)
+    layer_experts: InitVar[Optional[int]] = None
+
+    def __post_init__(self, layer_experts):
+        if layer_experts is not None:
+            self.layer_experts = layer_experts
 
     @classmethod
     def empty(cls, n_tokens: int, n_experts: int, topk: int, dtype: torch.dtype,
