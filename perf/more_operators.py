@@ -1,0 +1,521 @@
+"""Measured cases of the operators of a training step of the experts.
+
+Three operators, each in a plain form (elementary torch operations in 32 bits,
+rounded once at the end) and as this package's calls:
+
+* ffn: the forward pass of the expert FFN that keeps the products its gradient
+  needs (``moe_experts_train``);
+* ffn_grad: the gradient of the expert FFN with respect to the token rows, both
+  weight arrays and the routing weights (``moe_experts_backward``);
+* adamw: an AdamW step over many tensors at once, with moments in 32 or in
+  8 bits, clipped by the norm over all gradients (``moe_grad_norm``,
+  ``moe_adamw``).
+"""
+import math
+
+import torch
+
+own = False
+
+DTYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+SIZE = {"bf16": 2, "f32": 4}
+BLOCK = 256          # elements that share a scale in 8-bit moments
+TOP = 448.0          # largest e4m3 value
+STEP, SEED = 100, 20
+BETA1, BETA2, EPS, LR, DECAY = 0.9, 0.999, 1e-8, 1e-3, 0.1
+
+
+# ---------------------------------------------------------------- cases
+
+def _ffn(kind, n, h, i, e, k, dtype, act, layout, zipf):
+    return {"kind": kind, "n": n, "h": h, "i": i, "e": e, "k": k, "dtype": dtype, "act": act,
+            "layout": layout, "zipf": zipf}
+
+
+def _adamw(e, h, i, vectors, odd, p, bits, master, stochastic, clip):
+    """A layer's tensors: w13 and w2 of e experts (none if i is 0), the router's
+    weight and norm vectors; ``odd`` elements are added to each."""
+    return {"kind": "adamw", "e": e, "h": h, "i": i, "vectors": vectors, "odd": odd, "p": p,
+            "bits": bits, "master": master, "stochastic": stochastic, "clip": clip}
+
+
+def listed():
+    def named(name, c):
+        return {"name": name, **c}
+
+    return [
+        # a small fp32 layer: what a call costs when there is next to nothing to compute
+        named("ffn_tiny", _ffn("ffn", 33, 128, 256, 8, 2, "f32", "silu", "packed", 0.0)),
+        # a training batch of a 128-expert top-4 layer with clamped activations
+        named("ffn_clamped", _ffn("ffn", 4096, 2880, 2880, 128, 4, "bf16", "swiglu_oai",
+                                  "interleaved", 0.0)),
+        # a training batch of a 64-expert top-8 layer with skewed routing
+        named("ffn_train", _ffn("ffn", 16384, 4096, 1536, 64, 8, "bf16", "silu", "packed", 1.1)),
+        # the gradients that go with them
+        named("grad_tiny", _ffn("ffn_grad", 33, 128, 256, 8, 2, "f32", "silu", "packed", 0.0)),
+        # a small model's top-1 layer
+        named("grad_small", _ffn("ffn_grad", 4096, 512, 1408, 8, 1, "bf16", "silu", "packed",
+                                 0.0)),
+        # fp32, squared ReLU, odd token count and odd sizes
+        named("grad_odd", _ffn("ffn_grad", 1001, 1416, 712, 40, 6, "f32", "relu2", "packed",
+                               0.5)),
+        named("grad_clamped", _ffn("ffn_grad", 4096, 2880, 2880, 128, 4, "bf16", "swiglu_oai",
+                                   "interleaved", 0.0)),
+        # the largest case
+        named("grad_train", _ffn("ffn_grad", 16384, 4096, 1536, 64, 8, "bf16", "silu", "packed",
+                                 1.1)),
+        # a router and the norm weights of a few blocks: what a step over small tensors costs
+        named("adamw_vectors", _adamw(8, 2880, 0, 12, 0, "f32", 32, False, False, False)),
+        # a small model's layer: bf16 weights with fp32 masters and moments, clipped
+        named("adamw_master", _adamw(8, 512, 1408, 4, 0, "bf16", 32, True, False, True)),
+        # fp32 weights with 8-bit moments, sizes that end inside a block
+        named("adamw_odd", _adamw(5, 1416, 712, 3, 37, "f32", 8, False, True, True)),
+        # the 64-expert layer: bf16 weights, 8-bit moments, stochastic rounding
+        named("adamw_train", _adamw(64, 4096, 1536, 2, 0, "bf16", 8, False, True, True)),
+    ]
+
+
+def _log_int(rng, lo, hi, mult=1):
+    v = math.exp(rng.uniform(math.log(lo), math.log(hi)))
+    return max(lo // mult, round(v / mult)) * mult
+
+
+def draw(rng):
+    kind = rng.choice(["ffn", "ffn_grad", "ffn_grad", "adamw"])
+    while True:
+        e, h, i = _log_int(rng, 2, 128), _log_int(rng, 64, 4096, 8), _log_int(rng, 64, 4096, 8)
+        if kind == "adamw":
+            p = rng.choice(["bf16", "f32"])
+            bits = rng.choice([8, 32])
+            c = _adamw(e, h, rng.choice([0, i, i]), rng.randint(0, 7), rng.choice([0, 0, 1, 37]),
+                       p, bits, p == "bf16" and rng.random() < 0.5, rng.random() < 0.5,
+                       rng.random() < 0.5)
+            if work(c)["bytes"] <= 1.5e10:
+                return c
+            continue
+        dtype = rng.choice(["bf16", "bf16", "bf16", "f32"])
+        k = rng.randint(1, min(e, 8))
+        act = rng.choice(["silu", "swiglu_oai", "relu2"])
+        n = _log_int(rng, 1, 16384)
+        c = _ffn(kind, n, h, i, e, k, dtype, act,
+                 "packed" if act == "relu2" else rng.choice(["packed", "interleaved"]),
+                 rng.choice([0.0, 0.0, 0.5, 1.1]))
+        rows = n * k * SIZE[dtype] * max(_rows13(c), h)
+        if 3 * e * h * i * SIZE[dtype] <= 3e9 and rows < 2 ** 31 and \
+                work(c)["flops"] <= (1e13 if dtype == "bf16" else 1e12):
+            return c
+
+
+def _rows13(c):
+    return c["i"] if c["act"] == "relu2" else 2 * c["i"]
+
+
+def _sizes(c):
+    e, h, i = c["e"], c["h"], c["i"]
+    big = [e * 2 * i * h, e * h * i] if i else []
+    return [v + c["odd"] for v in big + [e * h] + [h] * c["vectors"]]
+
+
+# ---------------------------------------------------------------- inputs
+
+def _gen(seed):
+    return torch.Generator("cuda").manual_seed(seed)
+
+
+def _randn(g, *shape):
+    return torch.randn(*shape, generator=g, device="cuda")
+
+
+def _routing(g, c):
+    """Routing metadata as a routing step leaves it, from random logits (a
+    Zipf-like bias per expert where ``zipf`` is set)."""
+    n, e, k = c["n"], c["e"], c["k"]
+    logits = _randn(g, n, e)
+    if c["zipf"]:
+        rank = torch.randperm(e, generator=g, device="cuda").float() + 1.0
+        logits = logits - c["zipf"] * rank.log()
+    dt = DTYPES[c["dtype"]]
+    val, idx = logits.to(dt).sort(dim=1, descending=True, stable=True)
+    topk_idx = idx[:, :k].to(torch.int32).contiguous()
+    topk_w = torch.softmax(val[:, :k].float(), 1).to(dt).contiguous()
+    flat = topk_idx.reshape(-1).long()
+    col_sorted = flat.sort(stable=True)[1]
+    row_sorted = torch.empty_like(col_sorted)
+    row_sorted[col_sorted] = torch.arange(n * k, device="cuda")
+    col_sum = torch.bincount(flat, minlength=e)
+    offsets = torch.cat([col_sum.new_zeros(1), col_sum.cumsum(0)])
+    words = (e + 31) // 32
+    bits = torch.zeros(n, words * 32, dtype=torch.int64, device="cuda")
+    bits.scatter_(1, topk_idx.long(), 1)
+    bitmatrix = (bits.view(n, words, 32) << torch.arange(32, device="cuda")).sum(2)
+    return {"topk_idx": topk_idx, "topk_w": topk_w,
+            "bitmatrix": torch.where(bitmatrix >= 2 ** 31, bitmatrix - 2 ** 32, bitmatrix)
+            .to(torch.int32),
+            "col_sum": col_sum.to(torch.int32), "offsets": offsets.to(torch.int32),
+            "col_sorted": col_sorted.to(torch.int32), "row_sorted": row_sorted.to(torch.int32),
+            "gate_scal": topk_w.reshape(-1)[col_sorted].contiguous()}
+
+
+def prepare(case, seed):
+    c, g = case, _gen(seed)
+    if c["kind"] == "adamw":
+        return _prepare_adamw(c, g)
+    n, h, i, e, dt = c["n"], c["h"], c["i"], c["e"], DTYPES[c["dtype"]]
+    s = {"case": c, "routing": _routing(g, c)}
+    # bounds of the experts' rows on the host: the plain form takes its slices by them
+    s["bounds"] = s["routing"]["offsets"].tolist()
+    s["params"] = {"alpha": 1.702, "beta": 1.0, "limit": 7.0} if c["act"] == "swiglu_oai" else {}
+    s["x"] = _randn(g, n, h).to(dt)
+
+    def weights(rows, cols, std):
+        w = torch.empty(e, rows, cols, dtype=dt, device="cuda")
+        for j in range(e):
+            w[j] = _randn(g, rows, cols) * std
+        return w
+
+    # products of about N(0, 1); up to N(0, 4) where a clamp is to be met
+    s["w13"] = weights(_rows13(c), h, (4.0 if c["act"] == "swiglu_oai" else 1.0) / h ** 0.5)
+    s["w2"] = weights(h, i, 1.0 / i ** 0.5)
+    if c["kind"] == "ffn_grad":
+        s["d_out"] = (_randn(g, n, h) / 64).to(dt)
+        s["h"] = torch.empty(n * c["k"], _rows13(c), dtype=dt, device="cuda")  # saved by the ffn
+        tok = s["routing"]["col_sorted"].long() // c["k"]
+        for j, (lo, hi) in enumerate(zip(s["bounds"], s["bounds"][1:])):
+            s["h"][lo:hi] = s["x"][tok[lo:hi]] @ s["w13"][j].t()
+    return s
+
+
+def _prepare_adamw(c, g):
+    s = {"case": c, "p": [], "g": [], "m": [], "v": [], "m_scale": [], "v_scale": [],
+         "master": []}
+    for j, size in enumerate(_sizes(c)):
+        vector = j >= len(_sizes(c)) - c["vectors"]
+        w = _randn(g, size) * 0.02 + (1.0 if vector else 0.0)
+        s["p"].append(w.to(DTYPES[c["p"]]))
+        s["master"].append(w if c["master"] else None)
+        # gradients of norm vectors are fp32, those of weights in the weights' type; a few
+        # elements far above the others
+        d = _randn(g, size) * 1e-3
+        d *= 1.0 + 30.0 * (torch.rand(size, generator=g, device="cuda") < 0.002)
+        s["g"].append(d if vector else d.to(DTYPES[c["p"]]))
+        m, v = _randn(g, size) * 3e-4, (_randn(g, size) * 1e-3).square_()
+        if c["bits"] == 8:
+            m, ms = _to_8(m, None, False)
+            v, vs = _to_8(v.sqrt_(), None, True)
+            s["m_scale"].append(ms)
+            s["v_scale"].append(vs)
+        s["m"].append(m)
+        s["v"].append(v)
+    return s
+
+
+# ---------------------------------------------------------------- plain forms
+
+def _act(u, c, p):
+    """Activation of the products u [rows, rows13] and its derivatives with
+    respect to their gate and up parts (up: None if there is none)."""
+    if c["act"] == "relu2":
+        r = torch.relu(u)
+        return r * r, 2 * r, None
+    i = c["i"]
+    gate, up = (u[:, :i], u[:, i:]) if c["layout"] == "packed" else (u[:, 0::2], u[:, 1::2])
+    alpha, beta, limit = p.get("alpha", 1.0), p.get("beta", 0.0), p.get("limit", math.inf)
+    g, v = gate.clamp(max=limit), up.clamp(-limit, limit)
+    s = torch.sigmoid(alpha * g)
+    d_gate = torch.where(gate <= limit, s * (1 + alpha * g * (1 - s)) * (v + beta), 0.0)
+    return g * s * (v + beta), d_gate, torch.where(up.abs() <= limit, g * s, 0.0)
+
+
+def _plain_ffn(s):
+    c, r, dt = s["case"], s["routing"], s["x"].dtype
+    n, k, m = c["n"], c["k"], c["n"] * c["k"]
+    tok = r["col_sorted"].long() // k
+    h = torch.empty(m, _rows13(c), dtype=dt, device="cuda")
+    y = torch.empty(m, c["h"], device="cuda")
+    for e, (lo, hi) in enumerate(zip(s["bounds"], s["bounds"][1:])):
+        u = s["x"][tok[lo:hi]].float() @ s["w13"][e].float().t()
+        h[lo:hi] = u.to(dt)
+        y[lo:hi] = _act(u, c, s["params"])[0] @ s["w2"][e].float().t()
+    y = y[r["row_sorted"].long()].view(n, k, c["h"])
+    return {"out": (y * r["topk_w"].float()[:, :, None]).sum(1).to(dt), "h": h}
+
+
+def _plain_ffn_grad(s):
+    c, r, dt = s["case"], s["routing"], s["x"].dtype
+    n, k, m = c["n"], c["k"], c["n"] * c["k"]
+    tok, w = r["col_sorted"].long() // k, r["gate_scal"].float()[:, None]
+    dx, dw = torch.empty(m, c["h"], device="cuda"), torch.empty(m, device="cuda")
+    d_w13, d_w2 = torch.empty_like(s["w13"]), torch.empty_like(s["w2"])
+    for e, (lo, hi) in enumerate(zip(s["bounds"], s["bounds"][1:])):
+        x, d = s["x"][tok[lo:hi]].float(), s["d_out"][tok[lo:hi]].float()
+        a, d_gate, d_up = _act(s["h"][lo:hi].float(), c, s["params"])
+        u = d @ s["w2"][e].float()
+        dw[lo:hi] = (u * a).sum(1)
+        du = w[lo:hi] * u
+        dh = du * d_gate
+        if d_up is not None:
+            dh = torch.stack([dh, du * d_up], 1 if c["layout"] == "packed" else 2).flatten(1)
+        dx[lo:hi] = dh @ s["w13"][e].float()
+        d_w13[e] = (dh.t() @ x).to(dt)
+        d_w2[e] = ((w[lo:hi] * d).t() @ a).to(dt)
+    row = r["row_sorted"].long()
+    return {"d_x": dx[row].view(n, k, c["h"]).sum(1).to(dt), "d_w13": d_w13, "d_w2": d_w2,
+            "d_topk_w": dw[row].view(n, k)}
+
+
+def _random(n, tensor, device):
+    """The 32 random bits of each element of a tensor in a step: a hash of the
+    seed, the tensor's place in the list, the step and the element's index."""
+    def mix(v):
+        v = (v ^ (v >> 16)) * 0x7FEB352D & 0xFFFFFFFF
+        v = (v ^ (v >> 15)) * 0x846CA68B & 0xFFFFFFFF
+        return v ^ (v >> 16)
+
+    key = mix(mix((SEED + 0x9E3779B9 * (tensor + 1)) & 0xFFFFFFFF) ^ STEP)
+    return mix(torch.arange(n, device=device) ^ key)
+
+
+def _spread(x, dropped, random):
+    """fp32 x as a value that keeps its mantissa but for the lowest ``dropped``
+    bits: rounded up or down by the random bits (10 or, for bf16, 12 of them)."""
+    have = 12 if dropped == 16 else 10
+    r = (random << (dropped - have)) + (1 << (dropped - have - 1))
+    bits = x.contiguous().view(torch.int32) + r.to(torch.int32)
+    return (bits & -(1 << dropped)).view(torch.float32)
+
+
+def _to_8(x, random, root):
+    """e4m3 values of x and the fp32 scale of each block."""
+    n = x.numel()
+    top = torch.nn.functional.pad(x.abs(), (0, -n % BLOCK)).view(-1, BLOCK).amax(1)
+    live = top >= 2.0 ** -100
+    scale = torch.where(live, top * (1 / TOP), 0.0)
+    inverse = torch.where(live, TOP / top, 0.0).repeat_interleave(BLOCK)[:n]
+    u = (x * inverse).clamp(-TOP, TOP)
+    if random is not None:
+        u = _spread(u, 20, random)
+    if root:  # a second moment above zero stays above zero
+        u = torch.where((x > 0) & (inverse > 0), u.clamp(min=2.0 ** -9), u)
+    return u.to(torch.float8_e4m3fn), scale
+
+
+def _from_8(q, scale):
+    return q.float() * scale.repeat_interleave(BLOCK)[:q.numel()]
+
+
+def _norm(grads):
+    return torch.stack([g.float().square().sum(dtype=torch.float64) for g in grads]).sum().sqrt()
+
+
+def _plain_adamw(s):
+    c = s["case"]
+    out = {"p": s["p"], "m": s["m"], "v": s["v"], "m_scale": s["m_scale"],
+           "v_scale": s["v_scale"], "master": s["master"]}
+    coef = 1.0
+    if c["clip"]:
+        norm = _norm(s["g"])
+        out["norm"] = norm.float().view(1)
+        coef = (1.0 / (norm + 1e-6)).clamp(max=1.0).float()
+    c1, c2 = LR / (1 - BETA1 ** STEP), (1 - BETA2 ** STEP) ** -0.5
+    for j in range(len(s["p"])):
+        p, g = s["p"][j], s["g"][j].float() * coef
+        if c["bits"] == 8:
+            m = _from_8(s["m"][j], s["m_scale"][j])
+            v = _from_8(s["v"][j], s["v_scale"][j]).square()
+        else:
+            m, v = s["m"][j], s["v"][j]
+        m = m * BETA1 + g * (1 - BETA1)
+        v = v * BETA2 + g * g * (1 - BETA2)
+        root = v.sqrt()
+        w = (s["master"][j] if c["master"] else p.float())
+        w = w * (1 - LR * DECAY) - c1 * m / (root * c2 + EPS)
+        random = _random(p.numel(), j, p.device) if c["stochastic"] else None
+        if c["master"]:
+            s["master"][j].copy_(w)
+        if random is not None and p.dtype == torch.bfloat16 and not c["master"]:
+            w = _spread(w, 16, random >> 20)
+        p.copy_(w)
+        if c["bits"] == 8:
+            low = (random & 1023, (random >> 10) & 1023) if random is not None else (None, None)
+            q, scale = _to_8(m, low[0], False)
+            s["m"][j].copy_(q)
+            s["m_scale"][j].copy_(scale)
+            q, scale = _to_8(root, low[1], True)
+            s["v"][j].copy_(q)
+            s["v_scale"][j].copy_(scale)
+        else:
+            s["m"][j].copy_(m)
+            s["v"][j].copy_(v)
+    return out
+
+
+# ---------------------------------------------------------------- run
+
+def _own_run(s):
+    import routing_grouped_expert_amd as moe
+
+    c = s["case"]
+    if c["kind"] == "adamw":
+        state = moe.AdamWState(m=s["m"], v=s["v"], m_scale=s["m_scale"] or None,
+                               v_scale=s["v_scale"] or None,
+                               master=s["master"] if c["master"] else None)
+        out = {"p": s["p"], "m": s["m"], "v": s["v"], "m_scale": s["m_scale"],
+               "v_scale": s["v_scale"], "master": s["master"]}
+        norm = None
+        if c["clip"]:
+            out["norm"] = norm = moe.moe_grad_norm(s["g"])
+        moe.moe_adamw(s["p"], s["g"], state, lr=LR, step=STEP, betas=(BETA1, BETA2), eps=EPS,
+                      weight_decay=DECAY, grad_norm=norm, max_norm=1.0 if c["clip"] else None,
+                      seed=SEED if c["stochastic"] else None)
+        return out
+    routing = moe.Routing(**s["routing"])
+    if c["kind"] == "ffn":
+        out, h = moe.moe_experts_train(s["x"], s["w13"], s["w2"], routing, c["act"], c["layout"],
+                                       s["params"])
+        return {"out": out, "h": h}
+    r = moe.moe_experts_backward(s["d_out"], s["x"], s["h"], s["w13"], s["w2"], routing, c["act"],
+                                 c["layout"], s["params"])
+    return {"d_x": r.d_x, "d_w13": r.d_w13, "d_w2": r.d_w2, "d_topk_w": r.d_topk_w}
+
+
+def run(state):
+    if own:
+        return _own_run(state)
+    kind = state["case"]["kind"]
+    if kind == "adamw":
+        return _plain_adamw(state)
+    return _plain_ffn(state) if kind == "ffn" else _plain_ffn_grad(state)
+
+
+# ---------------------------------------------------------------- least work
+
+def work(case):
+    c = case
+    if c["kind"] == "adamw":
+        sizes = _sizes(c)
+        weights = sum(sizes[:len(sizes) - c["vectors"]])
+        vectors = sum(sizes) - weights
+        es = SIZE[c["p"]]
+        moments = 2 * 2 * 4 if c["bits"] == 32 else 2 * 2 * (1 + 4 / BLOCK)
+        kept = 8 + es if c["master"] else 2 * es
+        # (the norm over all gradients is read before the first of them can be used)
+        grads = (es * weights + 4 * vectors) * (2 if c["clip"] else 1)
+        return {"bytes": (moments + kept) * sum(sizes) + grads, "flops": 16 * sum(sizes)}
+    n, h, i, e, m, es = c["n"], c["h"], c["i"], c["e"], c["n"] * c["k"], SIZE[c["dtype"]]
+    rows = _rows13(c)
+    used = e * (1 - (1 - c["k"] / e) ** n)  # experts with a token, expected for even routing
+    one = (rows + i) * h
+    if c["kind"] == "ffn":
+        return {"bytes": es * (2 * n * h + used * one + m * rows), "flops": 2 * m * one}
+    return {"bytes": es * (3 * n * h + m * rows + (used + e) * one) + 4 * m,
+            "flops": 4 * m * one}
+
+
+# ---------------------------------------------------------------- 64 bits
+
+def _act_64(h, c, p):
+    if c["act"] == "relu2":
+        return h.clamp(min=0).square()
+    i = c["i"]
+    gate, up = (h[:, :i], h[:, i:]) if c["layout"] == "packed" else (h[:, ::2], h[:, 1::2])
+    limit = p.get("limit", math.inf)
+    gate, up = gate.clamp(max=limit), up.clamp(min=-limit, max=limit)
+    return gate / (1 + torch.exp(-p.get("alpha", 1.0) * gate)) * (up + p.get("beta", 0.0))
+
+
+def _exact_ffn(c, s):
+    """Expert by expert, the tokens that chose it."""
+    r, dev = s["routing"], "cuda"
+    out = torch.zeros(c["n"], c["h"], dtype=torch.float64, device=dev)
+    h = torch.zeros(c["n"] * c["k"], _rows13(c), dtype=torch.float64, device=dev)
+    row = r["row_sorted"].view(c["n"], c["k"]).long()
+    for e in range(c["e"]):
+        tok, slot = torch.nonzero(r["topk_idx"] == e, as_tuple=True)
+        u = s["x"][tok].double() @ s["w13"][e].double().t()
+        h[row[tok, slot]] = u
+        out[tok] += r["topk_w"][tok, slot].double()[:, None] * \
+            (_act_64(u, c, s["params"]) @ s["w2"][e].double().t())
+    return {"out": out, "h": h}
+
+
+def _exact_ffn_grad(c, s):
+    """Reverse-mode differentiation of sum(out * d_out), expert by expert."""
+    r, f64 = s["routing"], torch.float64
+    d_x = torch.zeros(c["n"], c["h"], dtype=f64, device="cuda")
+    d_topk_w = torch.zeros(c["n"], c["k"], dtype=f64, device="cuda")
+    d_w13, d_w2 = (torch.zeros(s[w].shape, dtype=f64, device="cuda") for w in ("w13", "w2"))
+    row = r["row_sorted"].view(c["n"], c["k"]).long()
+    for e in range(c["e"]):
+        tok, slot = torch.nonzero(r["topk_idx"] == e, as_tuple=True)
+        h = s["h"][row[tok, slot]].double().requires_grad_()
+        w2 = s["w2"][e].double().requires_grad_()
+        w = r["topk_w"][tok, slot].double().requires_grad_()
+        y = _act_64(h, c, s["params"]) @ w2.t()
+        total = (y * w[:, None] * s["d_out"][tok].double()).sum()
+        dh, d_w2[e], d_topk_w[tok, slot] = torch.autograd.grad(total, [h, w2, w])
+        d_x.index_add_(0, tok, dh @ s["w13"][e].double())
+        d_w13[e] = dh.t() @ s["x"][tok].double()
+    return {"d_x": d_x, "d_w13": d_w13, "d_w2": d_w2, "d_topk_w": d_topk_w}
+
+
+def _round_64(u, mantissa, random, bits):
+    """u rounded to ``mantissa`` bits behind the leading one: up where the part
+    cut off and a random number of so many bits together pass one step."""
+    _, ex = torch.frexp(u)
+    step = torch.ldexp(torch.ones_like(u), ex - 1 - mantissa)
+    return torch.floor(u.abs() / step + (random.double() + 0.5) / 2 ** bits) * step * u.sign()
+
+
+def _exact_8(x, random, root):
+    n = x.numel()
+    blocks = torch.cat([x, x.new_zeros(-n % BLOCK)]).view(-1, BLOCK)
+    top = blocks.abs().max(1, keepdim=True)[0]
+    u = torch.where(top > 0, blocks / top * TOP, 0.0).view(-1)[:n]
+    if random is not None:
+        u = _round_64(u, 3, random, 10)
+    if root:
+        u = torch.where(x > 0, u.clamp(min=2.0 ** -9), u)
+    return u.float().to(torch.float8_e4m3fn).double(), (top / TOP).view(-1)
+
+
+def _exact_adamw(c, s):
+    out = {k: [] for k in ("p", "m", "v", "m_scale", "v_scale", "master")}
+    coef = 1.0
+    if c["clip"]:
+        norm = sum(float(g.double().square().sum()) for g in s["g"]) ** 0.5
+        out["norm"] = torch.tensor([norm], dtype=torch.float64)
+        coef = min(1.0, 1.0 / (norm + 1e-6))
+    for j, p in enumerate(s["p"]):
+        g, m, v = s["g"][j].double() * coef, s["m"][j].double(), s["v"][j].double()
+        if c["bits"] == 8:
+            of = torch.arange(p.numel(), device="cuda") // BLOCK
+            m = m * s["m_scale"][j].double()[of]
+            v = (v * s["v_scale"][j].double()[of]) ** 2
+        m = BETA1 * m + (1 - BETA1) * g
+        v = BETA2 * v + (1 - BETA2) * g ** 2
+        w = (s["master"][j] if c["master"] else p).double()
+        w = w - LR * DECAY * w - LR * (m / (1 - BETA1 ** STEP)) / \
+            ((v / (1 - BETA2 ** STEP)).sqrt() + EPS)
+        random = _random(p.numel(), j, "cuda") if c["stochastic"] else None
+        out["master"].append(w if c["master"] else None)
+        if random is not None and p.dtype == torch.bfloat16 and not c["master"]:
+            w = _round_64(w, 7, random >> 20, 12)
+        out["p"].append(w)
+        if c["bits"] == 8:
+            q, scale = _exact_8(m, None if random is None else random & 1023, False)
+            out["m_scale"].append(scale)
+            out["m"].append(q)
+            q, scale = _exact_8(v.sqrt(), None if random is None else (random >> 10) & 1023, True)
+            out["v_scale"].append(scale)
+            out["v"].append(q)
+        else:
+            out["m"].append(m)
+            out["v"].append(v)
+    return out
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    if case["kind"] == "adamw":
+        return _exact_adamw(case, s)
+    return _exact_ffn(case, s) if case["kind"] == "ffn" else _exact_ffn_grad(case, s)
