@@ -260,6 +260,49 @@ moe_status_t moe_route_backward(const float *d_topk_w, int64_t n_tokens, int32_t
                                 int32_t topk, const moe_routing_t *routing, void *d_logits,
                                 void *stream);
 
+/* ---- Training the experts --------------------------------------------------------
+ * moe_experts with what its gradient needs, and that gradient.  The routing is
+ * moe_route's or, for an expert share, moe_route_ep's (then n_experts is the
+ * share's count and the weights hold its experts; n_experts may be smaller than
+ * topk).  Limits as moe_experts; the rows of h (n_tokens * topk * rows of w13)
+ * below 2^31 bytes, too.  Deterministic, no atomics.
+ *
+ * moe_experts_train: moe_experts (a token with no slot in a share gets a zero row)
+ *   that also writes h [n_tokens * topk, rows of w13] in `dtype`: row p holds the
+ *   products W13[e] x[t] of sorted entry p ahead of the activation, in the row
+ *   order of w13, each rounded once.  Rows past the routed ones are left as they
+ *   were.  workspace: moe_workspace_bytes(...) with any n_experts >= topk.
+ * moe_experts_backward: from d_out [N, hidden], the gradient of out, and the
+ *   forward call's x, h, weights and routing, with u[p] = W2[e]^T d_out[t] and
+ *   w[p] = gate_scal[p]:
+ *     d_topk_w [N, topk] fp32   <u[p], act(h[p])>; 0 for a slot outside the share
+ *     dh[p] = w[p] * act'(h[p]) * u[p]                         (not an output)
+ *     d_x [N, hidden]           sum over the token's slots of W13[e]^T dh[p]
+ *     d_w13 (as w13)            sum over the expert's rows of dh[p] x[t]^T
+ *     d_w2 (as w2)              sum over the expert's rows of d_out[t] (w[p] act(h[p]))^T
+ *   An expert without rows gets zeros, and with n_tokens == 0 the weight gradients
+ *   are written as zeros.  Where a clamp holds (gate above limit, up outside
+ *   [-limit, limit]) its derivative is 0, at the limit itself 1.  Sums are fp32;
+ *   dh, w[p] act(h[p]) and the rows of d_x are rounded to `dtype` between the
+ *   products.  The gradient down to the logits goes on with moe_route_backward.
+ *   Outputs must not overlap inputs or one another.  workspace: at least
+ *   moe_experts_backward_workspace_bytes(...). */
+moe_status_t moe_experts_train(const void *x, moe_dtype_t dtype, int64_t n_tokens, int32_t hidden,
+                               const void *w13, const void *w2, int32_t n_experts, int32_t inter,
+                               int32_t topk, moe_act_t act, moe_w13_layout_t layout,
+                               const moe_act_params_t *params, const moe_routing_t *routing,
+                               void *out, void *h, void *workspace, size_t ws_bytes, void *stream);
+size_t moe_experts_backward_workspace_bytes(int64_t n_tokens, int32_t topk, int32_t hidden,
+                                            int32_t inter, moe_dtype_t dtype);
+moe_status_t moe_experts_backward(const void *d_out, const void *x, const void *h,
+                                  moe_dtype_t dtype, int64_t n_tokens, int32_t hidden,
+                                  const void *w13, const void *w2, int32_t n_experts,
+                                  int32_t inter, int32_t topk, moe_act_t act,
+                                  moe_w13_layout_t layout, const moe_act_params_t *params,
+                                  const moe_routing_t *routing, void *d_x, void *d_w13,
+                                  void *d_w2, float *d_topk_w, void *workspace, size_t ws_bytes,
+                                  void *stream);
+
 /* ---- Norms around a block ------------------------------------------------------
  * The RMS norms that a transformer puts around this layer, with the gate and
  * the residual sum, in one pass over the token rows:

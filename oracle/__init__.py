@@ -23,6 +23,8 @@ Python binding, and imports neither.
 * :mod:`oracle.block` -- rows into expert-sorted order and back with the routing
   weights, the norms around a block, and the gradients of both.
 
+* :mod:`oracle.train` -- the gradient of the expert FFN and the AdamW step.
+
 Every function is pinned by ``tests/test_oracle_*.py`` against brute force,
 library routines, closed forms, invariants and the hand-derived fixtures in
 ``tests/golden/``; the one part with no such pin (the SwiGLU-OAI formula relative
@@ -37,6 +39,7 @@ from .block import (block_norm, block_norm_grad, combine_weighted, combine_weigh
                     dispatch, rms_norm, topk_weight_grad)
 from .ffn import (activation, moe_ffn, moe_ffn_share, moe_ffn_sorted,
                   moe_ffn_weighted_input, split_gate_up)
+from .train import activation_grad, join_gate_up, moe_ffn_grad
 
 __all__ = [
     "RoutingRef", "route", "topk_select", "topk_softmax", "bitmatrix", "histogram",
@@ -46,4 +49,5 @@ __all__ = [
     "moe_ffn_weighted_input", "quantize_mxfp4", "dequantize_mxfp4", "e2m1_encode",
     "e2m1_decode", "dispatch", "combine_weighted", "combine_weighted_grad", "topk_weight_grad",
     "rms_norm", "block_norm", "block_norm_grad", "quantize_int4", "dequantize_int4",
+    "activation_grad", "join_gate_up", "moe_ffn_grad",
 ]

@@ -70,7 +70,9 @@ __all__ = ["Routing", "MoeError", "Prepared", "moe_route", "moe_experts", "moe_e
            "prepare_experts_weighted_input", "moe_quantize_mxfp4", "moe_experts_mxfp4",
            "moe_forward_mxfp4", "prepare_experts_mxfp4", "prepare_forward_mxfp4",
            "moe_dispatch", "moe_combine_weighted", "moe_combine_weighted_backward",
-           "moe_route_backward", "prepare_dispatch", "prepare_combine_weighted",
+           "moe_route_backward", "ExpertsGrads", "moe_experts_train", "moe_experts_backward",
+           "prepare_experts_train", "prepare_experts_backward",
+           "moe_experts_backward_workspace_bytes", "prepare_dispatch", "prepare_combine_weighted",
            "prepare_combine_weighted_backward", "prepare_route_backward", "BlockNorm",
            "BlockNormGrads", "moe_block_norm", "moe_block_norm_backward", "prepare_block_norm",
            "prepare_block_norm_backward", "moe_block_norm_workspace_bytes", "moe_block_forward",
@@ -1049,6 +1051,131 @@ def moe_route_backward(d_topk_w: torch.Tensor, routing: Routing,
     layer's expert count, by default the routing's own (that of the whole layer also
     where moe_route_ep or moe_forward_ep filled it for a share)."""
     return _route_backward(d_topk_w, routing, n_experts, d_logits, stream).run()
+
+
+# ------------------------------------------------- training the experts
+
+@dataclass
+class ExpertsGrads:
+    """Outputs of moe_experts_backward."""
+
+    d_x: torch.Tensor       # [N, H]
+    d_w13: torch.Tensor     # as w13
+    d_w2: torch.Tensor      # as w2
+    d_topk_w: torch.Tensor  # [N, k] fp32
+
+
+def _train_layer(x, w13, w2, routing, act, layout):
+    """Checks what both directions take; returns (device, E, inter, k, rows of w13)."""
+    dev = _index(x, w13, w2)
+    _shapes(x, w13, w2, act)
+    if layout not in LAYOUTS:
+        raise ValueError(f"unknown w13 layout {layout!r}")
+    n, k = x.shape[0], routing.topk
+    off, col, row, scal = (routing.offsets, routing.col_sorted, routing.row_sorted,
+                           routing.gate_scal)
+    if _index(off, col, row, scal) != dev:
+        raise ValueError("the routing must be on the GPU of x")
+    e, _, inter = w2.shape
+    if off.numel() != e + 1 or not col.numel() == row.numel() == scal.numel() == n * k:
+        raise ValueError(f"the routing is not one of {n} tokens and {e} experts")
+    if not off.dtype is col.dtype is row.dtype is torch.int32:
+        raise TypeError("the routing's offsets, col_sorted and row_sorted must be int32")
+    r = N.MoeRouting(None, None, None, None, off.data_ptr(), col.data_ptr(), row.data_ptr(),
+                     scal.data_ptr(), _dt(scal))
+    return dev, e, inter, k, w13.shape[1], r
+
+
+def _experts_train(x, w13, w2, routing, act, layout, params, out, h, workspace, stream) -> _Call:
+    dev, e, inter, k, rows13, r = _train_layer(x, w13, w2, routing, act, layout)
+    n, hidden = x.shape
+    out = _output(out, x, (n, hidden), x.dtype, stream, "out")
+    h = _output(h, x, (n * k, rows13), x.dtype, stream, "h")
+    ws = _scratch(workspace, x, moe_workspace_bytes(n, max(e, k), k, hidden, inter, x.dtype),
+                  stream)
+    p = _params(params)
+    args = (x.data_ptr(), _dt(x), n, hidden, w13.data_ptr(), w2.data_ptr(), e, inter, k,
+            ACTS[act], LAYOUTS[layout], ctypes.byref(p) if p else None, ctypes.byref(r),
+            out.data_ptr(), h.data_ptr(), ws.data_ptr(), _nbytes(ws), _raw_stream(dev, stream))
+    return _Call(dev, "moe_experts_train", args, (r, p, x, w13, w2, out, h, ws, routing), (out, h))
+
+
+def prepare_experts_train(x: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor, routing: Routing,
+                          act: str, layout: str = "packed", params: Optional[dict] = None, *,
+                          out: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None, stream=None) -> Prepared:
+    return _experts_train(x, w13, w2, routing, act, layout, params, out, h, workspace,
+                          stream).prepared()
+
+
+def moe_experts_train(x: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor, routing: Routing,
+                      act: str, layout: str = "packed", params: Optional[dict] = None, *,
+                      out: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None, stream=None):
+    """moe_experts that keeps the w13 products its gradient needs: returns ``(out
+    [N, H], h [N*k, rows of w13])``.  The routing is the whole layer's or an expert
+    share's (see moe.h)."""
+    return _experts_train(x, w13, w2, routing, act, layout, params, out, h, workspace,
+                          stream).run()
+
+
+def moe_experts_backward_workspace_bytes(n_tokens: int, topk: int, hidden: int, inter: int,
+                                         dtype: torch.dtype = torch.bfloat16) -> int:
+    b = N.load().moe_experts_backward_workspace_bytes(n_tokens, topk, hidden, inter, _DT[dtype])
+    if b == 0:
+        raise MoeError(N.MOE_ERR_SHAPE, "moe_experts_backward_workspace_bytes")
+    return b
+
+
+def _experts_backward(d_out, x, h, w13, w2, routing, act, layout, params, d_x, d_w13, d_w2,
+                      d_topk_w, workspace, stream) -> _Call:
+    dev, e, inter, k, rows13, r = _train_layer(x, w13, w2, routing, act, layout)
+    n, hidden = x.shape
+    _is(d_out, (n, hidden), x.dtype, dev, "d_out")
+    _is(h, (n * k, rows13), x.dtype, dev, "h")
+    d_x = _output(d_x, x, (n, hidden), x.dtype, stream, "d_x")
+    d_w13 = _output(d_w13, x, w13.shape, x.dtype, stream, "d_w13")
+    d_w2 = _output(d_w2, x, w2.shape, x.dtype, stream, "d_w2")
+    d_topk_w = _output(d_topk_w, x, (n, k), torch.float32, stream, "d_topk_w")
+    ws = _scratch(workspace, x,
+                  moe_experts_backward_workspace_bytes(n, k, hidden, inter, x.dtype), stream)
+    p = _params(params)
+    args = (d_out.data_ptr(), x.data_ptr(), h.data_ptr(), _dt(x), n, hidden, w13.data_ptr(),
+            w2.data_ptr(), e, inter, k, ACTS[act], LAYOUTS[layout],
+            ctypes.byref(p) if p else None, ctypes.byref(r), d_x.data_ptr(), d_w13.data_ptr(),
+            d_w2.data_ptr(), d_topk_w.data_ptr(), ws.data_ptr(), _nbytes(ws),
+            _raw_stream(dev, stream))
+    res = ExpertsGrads(d_x, d_w13, d_w2, d_topk_w)
+    return _Call(dev, "moe_experts_backward", args,
+                 (r, p, d_out, x, h, w13, w2, ws, routing, res), res)
+
+
+def prepare_experts_backward(d_out: torch.Tensor, x: torch.Tensor, h: torch.Tensor,
+                             w13: torch.Tensor, w2: torch.Tensor, routing: Routing, act: str,
+                             layout: str = "packed", params: Optional[dict] = None, *,
+                             d_x: Optional[torch.Tensor] = None,
+                             d_w13: Optional[torch.Tensor] = None,
+                             d_w2: Optional[torch.Tensor] = None,
+                             d_topk_w: Optional[torch.Tensor] = None,
+                             workspace: Optional[torch.Tensor] = None, stream=None) -> Prepared:
+    return _experts_backward(d_out, x, h, w13, w2, routing, act, layout, params, d_x, d_w13, d_w2,
+                             d_topk_w, workspace, stream).prepared()
+
+
+def moe_experts_backward(d_out: torch.Tensor, x: torch.Tensor, h: torch.Tensor,
+                         w13: torch.Tensor, w2: torch.Tensor, routing: Routing, act: str,
+                         layout: str = "packed", params: Optional[dict] = None, *,
+                         d_x: Optional[torch.Tensor] = None,
+                         d_w13: Optional[torch.Tensor] = None,
+                         d_w2: Optional[torch.Tensor] = None,
+                         d_topk_w: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None, stream=None) -> ExpertsGrads:
+    """Gradient of moe_experts_train (or moe_experts) from the gradient of its
+    output, its arguments and its ``h``: the gradients of the token rows, both
+    weight arrays (in the layer dtype) and the routing weights (fp32), which
+    moe_route_backward takes on to the logits (see moe.h)."""
+    return _experts_backward(d_out, x, h, w13, w2, routing, act, layout, params, d_x, d_w13, d_w2,
+                             d_topk_w, workspace, stream).run()
 
 
 # ------------------------------------------------- norms around a block

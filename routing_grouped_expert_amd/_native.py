@@ -91,6 +91,12 @@ SIGNATURES = {
     "moe_combine_weighted_backward": (c_i32, [c_vp, c_vp, c_i32, c_i64, c_i32, c_i32, _P_ROUTING,
                                               c_vp, c_vp, c_vp]),
     "moe_route_backward": (c_i32, [c_vp, c_i64, c_i32, c_i32, _P_ROUTING, c_vp, c_vp]),
+    "moe_experts_train": (c_i32, [c_vp, c_i32, c_i64, c_i32, c_vp, c_vp, c_i32, c_i32, c_i32, c_i32,
+                                  c_i32, _P_PARAMS, _P_ROUTING, c_vp, c_vp, c_vp, c_sz, c_vp]),
+    "moe_experts_backward_workspace_bytes": (c_sz, [c_i64, c_i32, c_i32, c_i32, c_i32]),
+    "moe_experts_backward": (c_i32, [c_vp, c_vp, c_vp, c_i32, c_i64, c_i32, c_vp, c_vp, c_i32,
+                                     c_i32, c_i32, c_i32, c_i32, _P_PARAMS, _P_ROUTING, c_vp, c_vp,
+                                     c_vp, c_vp, c_vp, c_sz, c_vp]),
     "moe_block_norm_workspace_bytes": (c_sz, [c_i64, c_i32, c_i32]),
     "moe_block_norm": (c_i32, [c_vp, c_vp, c_i32, c_i64, c_i32, _P_NORM, c_vp, c_vp, c_vp, c_vp,
                                c_vp]),

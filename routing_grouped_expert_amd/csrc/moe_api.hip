@@ -104,6 +104,20 @@ moe_status_t check_expert_args(moe_dtype_t dtype, int64_t n, int32_t hidden, int
   return check_routing_struct(routing, false, n);
 }
 
+// Checks shared by moe_experts_train and its gradient, of a whole layer or of an
+// expert share: the saved products [n * k, rows of w13] are addressed with 32-bit
+// byte offsets, too.
+moe_status_t check_train(moe_dtype_t dtype, int64_t n, int32_t hidden, int32_t e, int32_t inter,
+                         int32_t k, moe_act_t act, moe_w13_layout_t layout,
+                         const moe_act_params_t *params, const moe_routing_t *routing,
+                         ActParams *prm) {
+  moe_status_t st = check_expert_args(dtype, n, hidden, e, inter, k, act, layout, params, routing,
+                                      prm, true);
+  if (st != MOE_OK) return st;
+  const int64_t rows13 = (act == MOE_ACT_RELU2 ? 1 : 2) * (int64_t)inter;
+  return n * k * rows13 * (int64_t)dsize(dtype) > 0x7fffffff ? MOE_ERR_SHAPE : MOE_OK;
+}
+
 moe_status_t check_ptrs(std::initializer_list<const void *> ptrs) {
   for (const void *p : ptrs) {
     if (!p) return MOE_ERR_NULL;
@@ -365,6 +379,77 @@ moe_status_t moe_experts(const void *x, moe_dtype_t dtype, int64_t n_tokens, int
   if (st != MOE_OK || n_tokens == 0) return st;
   return run_experts(x, dtype, n_tokens, hidden, w13, w2, n_experts, inter, topk, act, layout,
                      prm, routing, out, workspace, (hipStream_t)stream);
+}
+
+moe_status_t moe_experts_train(const void *x, moe_dtype_t dtype, int64_t n_tokens, int32_t hidden,
+                               const void *w13, const void *w2, int32_t n_experts, int32_t inter,
+                               int32_t topk, moe_act_t act, moe_w13_layout_t layout,
+                               const moe_act_params_t *params, const moe_routing_t *routing,
+                               void *out, void *h, void *workspace, size_t ws_bytes,
+                               void *stream) {
+  ActParams prm;
+  moe_status_t st = check_train(dtype, n_tokens, hidden, n_experts, inter, topk, act, layout,
+                                params, routing, &prm);
+  if (st != MOE_OK || n_tokens == 0) return st;
+  if ((st = check_ptrs({x, w13, w2, out, h})) != MOE_OK) return st;
+  st = check_ws(workspace, ws_bytes, experts_ws_bytes(n_tokens, topk, hidden, inter, dtype));
+  if (st != MOE_OK) return st;
+  hipStream_t s = (hipStream_t)stream;
+  // workspace as run_experts
+  void *y = reinterpret_cast<char *>(workspace) +
+            align256((size_t)n_tokens * topk * inter * dsize(dtype));
+  const int32_t rows13 = (act == MOE_ACT_RELU2 ? 1 : 2) * inter;
+  if (moe::launch_gemm1_rows(x, w13, h, routing->offsets, routing->col_sorted, dtype, n_tokens,
+                             topk, n_experts, hidden, rows13, s) != hipSuccess ||
+      moe::launch_activation(h, workspace, routing->offsets, n_experts, dtype, n_tokens * topk,
+                             inter, act, layout, prm, s) != hipSuccess ||
+      run_w2(workspace, dtype, n_tokens, hidden, w2, n_experts, inter, topk, routing, out, y, s,
+             true) != hipSuccess)
+    return MOE_ERR_HIP;
+  return MOE_OK;
+}
+
+size_t moe_experts_backward_workspace_bytes(int64_t n_tokens, int32_t topk, int32_t hidden,
+                                            int32_t inter, moe_dtype_t dtype) {
+  if (check_sizes(n_tokens, kCombineAnyExperts, topk, false) != MOE_OK || !dtype_ok(dtype) ||
+      check_ffn_sizes(hidden, inter) != MOE_OK)
+    return 0;
+  const size_t b = moe::experts_backward_scratch_bytes(n_tokens, topk, hidden, inter, dtype);
+  return b ? b : 256;
+}
+
+moe_status_t moe_experts_backward(const void *d_out, const void *x, const void *h,
+                                  moe_dtype_t dtype, int64_t n_tokens, int32_t hidden,
+                                  const void *w13, const void *w2, int32_t n_experts,
+                                  int32_t inter, int32_t topk, moe_act_t act,
+                                  moe_w13_layout_t layout, const moe_act_params_t *params,
+                                  const moe_routing_t *routing, void *d_x, void *d_w13,
+                                  void *d_w2, float *d_topk_w, void *workspace, size_t ws_bytes,
+                                  void *stream) {
+  moe::ExpertGradArgs a{};
+  moe_status_t st = check_train(dtype, n_tokens, hidden, n_experts, inter, topk, act, layout,
+                                params, routing, &a.prm);
+  if (st != MOE_OK) return st;
+  hipStream_t s = (hipStream_t)stream;
+  const size_t rows13 = (act == MOE_ACT_RELU2 ? 1 : 2) * (size_t)inter;
+  if ((st = check_ptrs({d_w13, d_w2})) != MOE_OK) return st;
+  if (n_tokens == 0) {  // no token: the weights have a gradient of zeros
+    const size_t one = (size_t)n_experts * hidden * dsize(dtype);
+    return moe::launch_zero(d_w13, one * rows13, s) == hipSuccess &&
+                   moe::launch_zero(d_w2, one * inter, s) == hipSuccess
+               ? MOE_OK
+               : MOE_ERR_HIP;
+  }
+  if ((st = check_ptrs({d_out, x, h, w13, w2, d_x, d_topk_w})) != MOE_OK) return st;
+  st = check_ws(workspace, ws_bytes,
+                moe_experts_backward_workspace_bytes(n_tokens, topk, hidden, inter, dtype));
+  if (st != MOE_OK) return st;
+  a.d_out = d_out, a.x = x, a.h = h, a.w13 = w13, a.w2 = w2;
+  a.d_x = d_x, a.d_w13 = d_w13, a.d_w2 = d_w2, a.d_topk_w = d_topk_w;
+  a.routing = routing, a.workspace = workspace;
+  a.n_tokens = n_tokens, a.topk = topk, a.n_experts = n_experts;
+  a.hidden = hidden, a.inter = inter, a.dtype = dtype, a.act = act, a.layout = layout;
+  return moe::launch_experts_backward(a, s) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
 moe_status_t moe_experts_w13(const void *x, moe_dtype_t dtype, int64_t n_tokens, int32_t hidden,

@@ -1,0 +1,160 @@
+"""The expert FFN's forward pass that keeps its products, and its gradient, on the
+GPU against the float64 oracle.
+
+Tolerances are summed up along the computation, element by element.  u = eps / 2
+of the layer dtype (half a step), U32 = 2^-24.  A sum of L fp32 products is off
+by at most 2 (L + 1) U32 times the sum of its terms' magnitudes (the matrix
+instructions may cut off rather than round: a whole step each), errors of the
+factors enter with the other factor's magnitude, and each value that is kept in
+the layer dtype adds u times its own.  The activation and its derivatives come
+from the hardware's exp2 and reciprocal (a step each) of an argument alpha g that
+carries up to two roundings: (16 + 8 |alpha g|) U32 of the product of their
+factors' magnitudes."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from routing_grouped_expert_amd import (Routing, moe_experts, moe_experts_backward,
+                                        moe_experts_backward_workspace_bytes, moe_experts_ep,
+                                        moe_experts_train, moe_route, moe_route_ep,
+                                        prepare_experts_backward, prepare_experts_train)
+from routing_grouped_expert_amd.synth import routing_logits
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+U32 = 2.0 ** -24
+OAI = {"alpha": 1.702, "beta": 1.0, "limit": 1.5}
+
+CASES = [
+    # (N, H, I, E, k, dtype, weights, act, layout, params, zipf)
+    (1, 8, 8, 1, 1, "bf16", "bf16", "silu", "packed", {}, None),
+    (1, 8, 8, 1, 1, "f32", "f32", "relu2", "packed", {}, None),
+    (1, 136, 72, 4, 2, "bf16", "f32", "swiglu_oai", "interleaved", OAI, None),
+    (3, 64, 16, 16, 16, "f32", "f32", "silu", "interleaved", {"limit": 0.5}, None),
+    (33, 128, 256, 8, 2, "f32", "f32", "silu", "packed", {}, None),
+    (33, 128, 256, 8, 2, "bf16", "bf16", "silu", "packed", {}, None),
+    (65, 200, 104, 5, 3, "bf16", "f32", "relu2", "packed", {}, None),
+    (300, 264, 136, 3, 2, "f32", "bf16", "swiglu_oai", "packed", OAI, 1.5),
+    (300, 264, 136, 3, 2, "bf16", "bf16", "swiglu_oai", "interleaved", OAI, 1.5),
+    (700, 520, 392, 2, 2, "bf16", "bf16", "silu", "packed", {}, None),
+    (1000, 328, 1032, 2, 1, "bf16", "f32", "silu", "interleaved", {}, None),
+    (1000, 1032, 328, 4, 1, "f32", "f32", "silu", "packed", {}, None),
+    (2000, 776, 520, 40, 4, "bf16", "bf16", "silu", "packed", {}, 1.1),
+    (600, 2056, 2312, 4, 2, "bf16", "bf16", "swiglu_oai", "interleaved", OAI, None),
+    (1500, 2304, 1288, 2, 2, "f32", "f32", "silu", "packed", {}, None),
+    (40, 72, 264, 256, 4, "bf16", "bf16", "silu", "packed", {}, None),
+]
+
+
+def _np(t):
+    return t.detach().double().cpu().numpy()
+
+
+def layer(n, h, i, e, k, dtype, weights, act, layout, params, zipf, seed=0, share=None):
+    """(routing, x, d_out, w13, w2, local expert ids, sorted rows)."""
+    lg = routing_logits(n, e, weights, seed=seed, zipf_s=zipf).to(DEV)
+    if share is None:
+        r = moe_route(lg, k)
+        idx = r.topk_idx.cpu().numpy()
+    else:
+        r = moe_route_ep(lg, k, *share)
+        idx = r.topk_idx.cpu().numpy() - share[0]
+        idx = np.where((idx >= 0) & (idx < share[1]), idx, -1)
+        e = share[1]
+    g = torch.Generator().manual_seed(seed + 1)
+    rows = i if act == "relu2" else 2 * i
+    dt = DT[dtype]
+    x = torch.randn(n, h, generator=g).to(dt)
+    d = (torch.randn(n, h, generator=g) / 8).to(dt)
+    w13 = (torch.randn(e, rows, h, generator=g) / h ** 0.5).to(dt)
+    w2 = (torch.randn(e, h, i, generator=g) / i ** 0.5).to(dt)
+    return r, x, d, w13, w2, idx, r.row_sorted.cpu().numpy().reshape(n, k)
+
+
+def within(got, want, tol, what):
+    got = _np(got)
+    assert got.shape == want.shape, what
+    err = np.abs(got - want)
+    bad = ~(err <= tol)
+    assert not bad.any(), f"{what}: {int(bad.sum())} values off, worst {err.max():.3g} " \
+                          f"({np.nanmax(err / np.maximum(tol, 1e-300)):.3g} of its tolerance), " \
+                          f"first at {tuple(np.argwhere(bad)[0])}"
+
+
+def _parts(h, act, layout, params):
+    """a, its derivatives joined in w13 order, and the error bounds of both."""
+    if act == "relu2":
+        a, (dg, _) = oracle.activation(act, h), oracle.activation_grad(act, h)
+        return a, dg, 4 * U32 * a, 4 * U32 * dg
+    alpha, beta = (params.get("alpha", 1.0), params.get("beta", 0.0)) if act == "swiglu_oai" \
+        else (1.0, 0.0)
+    lim = params.get("limit", np.inf)
+    g, u = oracle.split_gate_up(h, layout)
+    a, (dg, du) = oracle.activation(act, g, u, params), oracle.activation_grad(act, g, u, params)
+    gc, uc = np.abs(np.minimum(g, lim)), np.minimum(np.abs(u), lim) + abs(beta)
+    c = (16 + 8 * abs(alpha) * gc) * U32
+    s = np.maximum(1 / (1 + np.exp(-alpha * np.minimum(g, lim))), 0)
+    ea = c * gc * s * uc
+    eg, eu = c * s * (1 + abs(alpha) * gc) * uc, c * gc * s
+    join = oracle.join_gate_up
+    return a, join(dg, du, layout), ea, join(eg, eu, layout)
+
+
+def gradient_bounds(d, x, h, idx, w, row, w13, w2, act, layout, params, u):
+    """Error bounds of the four gradients by the rules above."""
+    b = {"d_x": np.zeros_like(x), "d_w13": np.zeros_like(w13), "d_w2": np.zeros_like(w2),
+         "d_topk_w": np.zeros(w.shape)}
+    x, d = np.abs(x), np.abs(d)
+    hidden, inter = w2.shape[1:]
+    for e in range(len(w13)):
+        tok, slot = np.nonzero(idx == e)
+        he, we = h[row[tok, slot]], np.abs(w[tok, slot])[:, None]
+        a, da, ea, eda = (np.abs(v) for v in _parts(he, act, layout, params))
+        sums = d[tok] @ np.abs(w2[e])                       # bounds |u| too
+        eu = 2 * (hidden + 1) * U32 * sums
+        b["d_topk_w"][tok, slot] = (eu * a + sums * ea +
+                                    2 * (inter + 33) * U32 * sums * a).sum(1)
+        two = (lambda v: v) if act == "relu2" else (lambda v: oracle.join_gate_up(v, v, layout))
+        dh = we * two(sums) * (da + eda)
+        edh = we * (two(eu) * da + two(sums) * eda) + (u + 4 * U32) * dh
+        rows = dh @ np.abs(w13[e])
+        erow = edh @ np.abs(w13[e]) + (2 * (len(w13[e]) + 1) * U32 + u) * rows
+        np.add.at(b["d_x"], tok, erow + (u + 17 * U32) * (rows + erow))
+        wa = we * (a + ea)
+        ewa = we * ea + (u + 2 * U32) * wa
+        s13, s2 = dh.T @ x[tok], d[tok].T @ wa
+        c = 2 * (len(tok) + 1) * U32 + u
+        b["d_w13"][e] = edh.T @ x[tok] + c * s13
+        b["d_w2"][e] = d[tok].T @ ewa + c * s2
+    return b
+
+
+def check_gradient(got, d, x, h, idx, w, row, w13, w2, act, layout, params, u):
+    args = (d, x, h, idx, w, row, w13, w2, act, layout, params)
+    want, bound = oracle.moe_ffn_grad(*args), gradient_bounds(*args, u)
+    for name in ("d_topk_w", "d_x", "d_w2", "d_w13"):
+        within(getattr(got, name), want[name], bound[name], name)
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(map(str, c[:9])))
+def test_forward_and_gradient(case):
+    n, hidden, inter, e, k, dtype, weights, act, layout, params, zipf = case
+    r, x, d, w13, w2, idx, row = layer(*case)
+    xg, dg, w13g, w2g = (t.to(DEV) for t in (x, d, w13, w2))
+    out, h = moe_experts_train(xg, w13g, w2g, r, act, layout, params)
+    u = torch.finfo(DT[dtype]).eps / 2
+    xn, dn, w13n, w2n, w = _np(x), _np(d), _np(w13), _np(w2), _np(r.topk_w)
+    want, terms = np.zeros((n * k, len(w13n[0]))), np.zeros((n * k, len(w13n[0])))
+    for t in range(n):
+        for j in range(k):
+            want[row[t, j]] = w13n[idx[t, j]] @ xn[t]
+            terms[row[t, j]] = np.abs(w13n[idx[t, j]]) @ np.abs(xn[t])
+    within(h, want, (2 * (hidden + 1) * U32 + u) * terms, "h")
+    ref = oracle.moe_ffn(x, idx, w, w13, w2, act, layout, params)
+    scale = np.abs(ref).max()
+    assert np.abs(_np(out) - ref).max() <= (1e-4 * scale if dtype == "f32" else
+                                            3e-2 + 3e-2 * scale)
+    got = moe_experts_backward(dg, xg, h, w13g, w2g, r, act, layout, params)
+    check_gradient(got, dn, xn, _np(h), idx, w, row, w13n, w2n, act, layout, params, u)
