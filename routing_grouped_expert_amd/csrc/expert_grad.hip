@@ -75,10 +75,10 @@ template <typename T> __device__ __forceinline__ int col_key(int r) {
 template <typename T, int ROWS, int NW> struct RowTile {
   static constexpr int BYTES = ROWS * RB, J = BYTES / 1024 / NW;
   static_assert(J * NW * 1024 == BYTES, "whole loads a wave");
-  // row and byte inside the row's slice that load j of a wave brings to its lane
-  __device__ static int row(int wave, int lane, int j) { return (wave * J + j) * 8 + (lane >> 3); }
+  // line (here: operand row) and byte inside it that load j of a wave brings to its lane
+  __device__ static int line(int wave, int lane, int j) { return (wave * J + j) * 8 + (lane >> 3); }
   __device__ static int byte(int wave, int lane, int j) {
-    return ((lane & 7) ^ row_key(row(wave, lane, j))) << 4;
+    return ((lane & 7) ^ row_key(line(wave, lane, j))) << 4;
   }
   __device__ static typename Mma<T>::Frag frag(const char *p, int ks, int r, int lane) {
     constexpr int EPL = sizeof(typename Mma<T>::Frag) / sizeof(T);
@@ -95,11 +95,11 @@ template <typename T, int COLS, int NW> struct ColTile {
   static constexpr int ROWB = COLS * (int)sizeof(T), CPR = ROWB / 16;
   static_assert(J * NW * 1024 == BYTES, "whole loads a wave");
   static_assert(CPR >= 16, "a K row spans the banks");
-  __device__ static int krow(int wave, int lane, int j) {
+  __device__ static int line(int wave, int lane, int j) {  // (here: K row)
     return ((wave * J + j) * 64 + lane) / CPR;
   }
-  __device__ static int byte(int wave, int lane, int j) {  // inside the tile's columns
-    return ((lane % CPR) ^ col_key<T>(krow(wave, lane, j))) << 4;
+  __device__ static int byte(int wave, int lane, int j) {
+    return ((lane % CPR) ^ col_key<T>(line(wave, lane, j))) << 4;
   }
   __device__ static typename Mma<T>::Frag frag(const char *p, int ks, int c, int lane) {
     if constexpr (std::is_same<T, bf16_t>::value) {
@@ -133,7 +133,6 @@ struct GradArgs {
   uint32_t a_bytes, b_bytes;    // buffer ranges (b_bytes: of one expert's weights)
   uint32_t c_bytes;             // (of one expert in the weight gradients)
   int E, K, M, N;
-  int gather_a, gather_b;       // the operand's rows are tokens: row p reads col_sorted[p] / topk
   uint32_t div_mul, div_shift;  // f / topk = (f * div_mul) >> div_shift
   // epilogue of the first data gradient
   const void *h;                // [rows, sets * N]
@@ -150,7 +149,8 @@ __device__ __forceinline__ uint32_t token_of(const GradArgs &g, int f) {
   return (uint32_t)(((uint64_t)(uint32_t)f * g.div_mul) >> g.div_shift);
 }
 
-// Gradient kinds.
+// Gradient kinds, and whose rows are gathered: row p of A (1) or B (2) is that of
+// token col_sorted[p] / topk.
 enum { GRAD_ACT = 0, GRAD_ROWS = 1, GRAD_WEIGHT = 2 };
 // Activation kinds of GRAD_ACT.
 enum { ACT_GATED = 0, ACT_RELU2 = 1 };
@@ -249,12 +249,14 @@ __device__ __forceinline__ void expert_units(const GradArgs &g, int least, int *
 // ping-pong schedule: waves 0-3 and 4-7 (one of each a SIMD) alternate between a
 // memory phase (next slice's loads out, this slice's fragments into registers)
 // and an MFMA phase, one group a barrier behind the other.  Four waves read the
-// fragments of the next k-step while the current one multiplies.
+// fragments of the next k-step while the current one multiplies; with 256-row
+// tiles (one wave a SIMD, 128 x 128 each) every memory instruction is placed
+// behind an MFMA by hand.
 //
 // The MFMA takes the N-side fragment first: lane l ends with output row l % 32 of
 // a 32 x 32 sub-tile and, in register group q, columns 8 q + 4 (l / 32) + [0, 4).
-template <typename T, int KIND, int ACT, int BM, int BN, int WM, int WN, int S>
-__global__ __launch_bounds__(64 * WM * WN) void grad_gemm(GradArgs g) {
+template <typename T, int KIND, int ACT, int GATHER, int BM, int BN, int WM, int WN, int S>
+__device__ __forceinline__ void grad_body(const GradArgs &g) {
   using Mm = Mma<T>;
   using Frag = typename Mm::Frag;
   constexpr bool BF = std::is_same<T, bf16_t>::value;
@@ -269,6 +271,8 @@ __global__ __launch_bounds__(64 * WM * WN) void grad_gemm(GradArgs g) {
   constexpr int NPART = BF ? 2 : 4;  // pieces of a sub-tile row a lane
   constexpr int NST = TM * TN * NPART * (KIND == GRAD_ACT ? SETS + 1 : 1);
   constexpr bool PP = NW == 8;
+  constexpr bool BIG = NW == 4 && BM == 256;  // one wave a SIMD
+  static_assert(!BIG || (BF && S == 2 && NKS >= 4), "four-wave tiles");
   static_assert(TM * 32 * WM == BM && TN * 32 * WN == BN && S >= 2 && (S - 2) * PER < 64, "tile");
 
   __shared__ __attribute__((aligned(16))) char smem[S * STAGE];
@@ -328,102 +332,109 @@ __global__ __launch_bounds__(64 * WM * WN) void grad_gemm(GradArgs g) {
   __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<void *>(g.B), (short)0, (int)g.b_bytes, kRsrcWord3);
   const uint32_t arow = (uint32_t)((WG ? g.M : g.K) * ES), brow = (uint32_t)(g.N * ES);
-  uint32_t va[JA], vb[JB];              // a lane's offsets that hold for the whole tile
-  int ia[JA], ib[WG ? JB : 1];          // col_sorted of the rows to load next
+  uint32_t va[JA], vb[JB];  // a lane's offsets that hold for the whole tile
+  uint32_t oa[JA], ob[JB];  // and those of the next slice
+  // col_sorted of the gathered operand's rows in the next slice (weight gradients) or
+  // tile, read ahead of their use (rows past the end read any valid entry)
+  constexpr bool GA = GATHER == 1, GB = GATHER == 2;
+  int ia[GA ? JA : 1], ib[GB ? JB : 1];
   Tile in{};
   int L_in = first, k_in = 0, nk_in = 0, z_in = 0;  // z_in: slices loaded so far
-  // gather indices of slice k_in (weight gradients) or of the tile's rows, read one
-  // slice ahead of their use (rows past the end read any valid entry)
-  auto fetch = [&]() {
-    const int last = in.row0 + in.rows - 1;
-    if (in.rows == 0) return;
-    if constexpr (WG) {
+  auto fetch = [&](const Tile &t, int k0) {
+    const int last = t.row0 + t.rows - 1;
+    if (t.rows == 0) return;
+    if constexpr (GA) {
 #pragma unroll
       for (int j = 0; j < JA; ++j)
-        if (g.gather_a)
-          ia[j] = g.col_sorted[min(in.row0 + k_in * BK + TA::krow(wave, lane, j), last)];
+        ia[j] = g.col_sorted[min(t.row0 + k0 + TA::line(wave, lane, j), last)];
+    }
+    if constexpr (GB) {
 #pragma unroll
       for (int j = 0; j < JB; ++j)
-        if (g.gather_b)
-          ib[j] = g.col_sorted[min(in.row0 + k_in * BK + TB::krow(wave, lane, j), last)];
-    } else if (k_in == 0 && g.gather_a) {
-#pragma unroll
-      for (int j = 0; j < JA; ++j)
-        ia[j] = g.col_sorted[min(in.row0 + TA::row(wave, lane, j), last)];
+        ib[j] = g.col_sorted[min(t.row0 + k0 + TB::line(wave, lane, j), last)];
     }
   };
+  // Offsets of tile L_in, whose gather indices are there.
   auto begin_tile = [&]() {
     in = tile_of(L_in);
     nk_in = slices(in);
-    if constexpr (WG) {
 #pragma unroll
-      for (int j = 0; j < JA; ++j) {
+    for (int j = 0; j < JA; ++j) {
+      if constexpr (WG) {
         const int b = in.m0 * ES + TA::byte(wave, lane, j);
         va[j] = b < (int)arow ? (uint32_t)b : kOOB;
+      } else {
+        const int r = TA::line(wave, lane, j);
+        const uint32_t row = GA ? token_of(g, ia[GA ? j : 0]) : (uint32_t)(in.row0 + r);
+        va[j] = r < in.rows ? row * arow + TA::byte(wave, lane, j) : kOOB;
       }
-    } else {
+    }
+    if constexpr (!WG)
       rb = __builtin_amdgcn_make_buffer_rsrc(
           const_cast<char *>(reinterpret_cast<const char *>(g.B)) + (size_t)in.e * g.b_bytes,
           (short)0, (int)g.b_bytes, kRsrcWord3);
-    }
 #pragma unroll
     for (int j = 0; j < JB; ++j) {
       const int b = in.n0 * ES + TB::byte(wave, lane, j);
       vb[j] = b < (int)brow ? (uint32_t)b : kOOB;
       // (out of range it stays so: an expert's weights are below 2^31 bytes)
-      if constexpr (!WG) vb[j] += (uint32_t)TB::krow(wave, lane, j) * brow;
+      if constexpr (!WG) vb[j] += (uint32_t)TB::line(wave, lane, j) * brow;
     }
-    fetch();
+    if constexpr (GA && !WG)
+      if (L_in + stride < end) fetch(tile_of(L_in + stride), 0);
+  };
+  // Offset of load j of the next slice, A and B; past the last tile out of range.
+  auto prep_a = [&](int j) {
+    if constexpr (WG) {
+      const int k = k_in * BK + TA::line(wave, lane, j);
+      const uint32_t row = GA ? token_of(g, ia[GA ? j : 0]) : (uint32_t)(in.row0 + k);
+      oa[j] = L_in < end && k < in.rows && va[j] != kOOB ? row * arow + va[j] : kOOB;
+    } else {
+      const int kb = k_in * RB;  // (a row is a whole number of 16-byte chunks)
+      const bool past = L_in >= end || kb + TA::byte(wave, lane, j) >= (int)arow;
+      oa[j] = past ? kOOB : va[j] + (uint32_t)kb;
+    }
+  };
+  auto prep_b = [&](int j) {
+    const int k = k_in * BK + TB::line(wave, lane, j);
+    if constexpr (WG) {
+      const uint32_t row = GB ? token_of(g, ib[GB ? j : 0]) : (uint32_t)(in.row0 + k);
+      ob[j] = L_in < end && k < in.rows && vb[j] != kOOB ? row * brow + vb[j] : kOOB;
+    } else {
+      ob[j] = L_in >= end || k >= g.K ? kOOB : vb[j] + (uint32_t)(k_in * BK) * brow;
+    }
+  };
+  auto load_a = [&](char *base, int j) { dma16(ra, base + (wave * JA + j) * 1024, oa[j]); };
+  auto load_b = [&](char *base, int j) {
+    dma16(rb, base + TA::BYTES + (wave * JB + j) * 1024, ob[j]);
+  };
+  // The gather indices of the slice after the next one (the next one's are in use).
+  auto ahead = [&]() {
+    if constexpr (WG && GATHER) {
+      if (k_in + 1 < nk_in) fetch(in, (k_in + 1) * BK);
+      else if (L_in + stride < end) fetch(tile_of(L_in + stride), 0);
+    }
+  };
+  // On to the slice after this one, whose loads are out.
+  auto advance = [&]() {
+    ++z_in;
+    if (++k_in < nk_in) return;
+    k_in = 0;
+    L_in += stride;
+    if (L_in < end) begin_tile();
   };
   auto issue = [&]() {
     char *base = smem + (z_in % S) * STAGE;
-    if constexpr (WG) {
 #pragma unroll
-      for (int j = 0; j < JB; ++j) {
-        const int k = k_in * BK + TB::krow(wave, lane, j);
-        const uint32_t row = g.gather_b ? token_of(g, ib[j]) : (uint32_t)(in.row0 + k);
-        dma16(rb, base + TA::BYTES + (wave * JB + j) * 1024,
-              k < in.rows && vb[j] != kOOB ? row * brow + vb[j] : kOOB);
-      }
+    for (int j = 0; j < JB; ++j) prep_b(j);
 #pragma unroll
-      for (int j = 0; j < JA; ++j) {
-        const int k = k_in * BK + TA::krow(wave, lane, j);
-        const uint32_t row = g.gather_a ? token_of(g, ia[j]) : (uint32_t)(in.row0 + k);
-        dma16(ra, base + (wave * JA + j) * 1024,
-              k < in.rows && va[j] != kOOB ? row * arow + va[j] : kOOB);
-      }
-    } else {
-      if (k_in == 0) {
+    for (int j = 0; j < JA; ++j) prep_a(j);
+    ahead();
 #pragma unroll
-        for (int j = 0; j < JA; ++j) {
-          const int r = TA::row(wave, lane, j);
-          const uint32_t row = g.gather_a ? token_of(g, ia[j]) : (uint32_t)(in.row0 + r);
-          va[j] = r < in.rows ? row * arow + TA::byte(wave, lane, j) : kOOB;
-        }
-      }
-      const int kb = k_in * RB;
-      const bool tail = (k_in + 1) * BK > g.K;
+    for (int j = 0; j < JB; ++j) load_b(base, j);
 #pragma unroll
-      for (int j = 0; j < JB; ++j) {
-        const bool past = tail && k_in * BK + TB::krow(wave, lane, j) >= g.K;
-        dma16(rb, base + TA::BYTES + (wave * JB + j) * 1024,
-              past ? kOOB : vb[j] + (uint32_t)(k_in * BK) * brow);
-      }
-#pragma unroll
-      for (int j = 0; j < JA; ++j) {
-        // (a row is a whole number of 16-byte chunks)
-        const bool past = tail && kb + TA::byte(wave, lane, j) >= (int)arow;
-        dma16(ra, base + (wave * JA + j) * 1024, past ? kOOB : va[j] + (uint32_t)kb);
-      }
-    }
-    ++z_in;
-    if (++k_in == nk_in) {
-      k_in = 0;
-      L_in += stride;
-      if (L_in < end) begin_tile();
-    } else {
-      fetch();
-    }
+    for (int j = 0; j < JA; ++j) load_a(base, j);
+    advance();
   };
 
   // ---- multiplying side ------------------------------------------------------------
@@ -461,6 +472,14 @@ __global__ __launch_bounds__(64 * WM * WN) void grad_gemm(GradArgs g) {
       for (int t = 0; t < 4; ++t) v[t] = acc[i][j][4 * c + t];
     }
   };
+  // (four-wave tiles: the accumulators stay in AGPRs up to their sub-tile, and the
+  // sub-tiles apart: reading them all early would need 256 more registers)
+  auto hold = [&](int i, int j) {
+    if constexpr (BIG) {
+      __builtin_amdgcn_sched_barrier(0);
+      asm volatile("" : "+a"(acc[i][j]));
+    }
+  };
   auto piece_col = [&](int c) { return BF ? 16 * c + 8 * (lane >> 5) : 8 * c + 4 * (lane >> 5); };
   auto put = [&](__amdgpu_buffer_rsrc_t r, uint32_t off, const float (&v)[NV]) {
     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(i32x4_t, pack(v)), r, (int)off, 0, 0);
@@ -484,6 +503,7 @@ __global__ __launch_bounds__(64 * WM * WN) void grad_gemm(GradArgs g) {
         float sum = 0.f;  // this lane's part of d_w
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
+          hold(i, j);
 #pragma unroll
           for (int c = 0; c < NPART; ++c) {
             const int col = t.n0 + wn * WC + j * 32 + piece_col(c);
@@ -549,6 +569,7 @@ __global__ __launch_bounds__(64 * WM * WN) void grad_gemm(GradArgs g) {
         const uint32_t row = (uint32_t)((WG ? t.m0 : t.row0) + m);
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
+          hold(i, j);
 #pragma unroll
           for (int c = 0; c < NPART; ++c) {
             const int col = t.n0 + wn * WC + j * 32 + piece_col(c);
@@ -559,10 +580,12 @@ __global__ __launch_bounds__(64 * WM * WN) void grad_gemm(GradArgs g) {
         }
       }
     }
-    st_until = z + S - 1;
+    st_until = z + S - 1 + (BIG ? 1 : 0);  // (four waves load a slice further ahead)
   };
 
+  if constexpr (GA && !WG) fetch(tile_of(first), 0);
   begin_tile();
+  if constexpr (WG && GATHER) fetch(in, 0);
 #pragma unroll
   for (int s = 0; s < S - 1; ++s)
     if (L_in < end) issue();
@@ -574,6 +597,11 @@ __global__ __launch_bounds__(64 * WM * WN) void grad_gemm(GradArgs g) {
   };
   auto frag_b = [&](const char *p, int ks, int j) {
     return TB::frag(p + TA::BYTES, ks, wn * WC + j * 32, lane);
+  };
+  auto bar = [&]() {  // workgroup barrier; MFMAs may cross it
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
   };
   auto next = [&]() {  // the slice after this one (its tile's first: the next tile)
     if (++kt < nk) return;
@@ -618,6 +646,84 @@ __global__ __launch_bounds__(64 * WM * WN) void grad_gemm(GradArgs g) {
       next();
     }
     if (!grp) barrier();
+  } else if constexpr (BIG) {
+    // One wave a SIMD: nothing else fills the matrix core while this wave issues
+    // other work, so each memory instruction follows an MFMA.
+    //  * k-step 0: the load offsets of slice z + 2; k-step 1: the gather indices of
+    //    slice z + 3 (the wait in k-step NKS - 2 covers them).
+    //  * k-steps before the last: the fragments of the next k-step.
+    //  * k-step NKS - 2, once its reads are out: the wait for slice z + 1 and the
+    //    barrier (after which no wave reads slot z % 2 again), then the first loads
+    //    of slice z + 2 into that slot.
+    //  * last k-step: its other loads, then slice z + 1's first fragments.
+    constexpr int NM = TM * TN, NF = TM + TN, NL = JA + JB;
+    static_assert(!BIG || NL <= NM, "a load offset after each MFMA");
+    Frag fa[2][TM], fb[2][TN];
+    auto read = [&](int buf, const char *p, int ks, int f) {
+      if (f < TM) fa[buf][f] = frag_a(p, ks, f);
+      else fb[buf][f - TM] = frag_b(p, ks, f - TM);
+    };
+    auto load = [&](char *base, int q) {
+      if (q < JB) load_b(base, q);
+      else load_a(base, q - JB);
+    };
+    wait_vm<0>();
+    barrier();
+    issue();  // (past the last slice: zeros)
+#pragma unroll
+    for (int f = 0; f < NF; ++f) read(0, smem, 0, f);
+    int z = 0;
+#pragma nounroll
+    for (;;) {
+      zero_acc();
+#pragma nounroll
+      for (int k = 0; k < nk; ++k, ++z) {
+        char *here = smem + (z & 1) * STAGE, *other = smem + ((z + 1) & 1) * STAGE;
+#pragma unroll
+        for (int ks = 0; ks < NKS; ++ks) {
+          constexpr int D0 = NM - NF - 1;   // loads that k-step NKS - 2 has room for
+          constexpr int NQ = NL - D0 + NF;  // memory instructions of the last k-step
+#pragma unroll
+          for (int m = 0; m < NM; ++m) {
+            const int i = m / TN, j = m % TN;
+            acc[i][j] = Mm::mma(fb[ks & 1][j], fa[ks & 1][i], acc[i][j]);
+            if (ks == 0 && m < NL) {
+              if (m < JB) prep_b(m);
+              else prep_a(m - JB);
+            }
+            if (ks == 1 && m == 0) ahead();
+            if (ks + 2 < NKS) {
+              if (m % 2 == 0) read((ks + 1) & 1, here, ks + 1, m / 2);
+            } else if (ks + 2 == NKS) {
+              if (m < NF) {
+                read((ks + 1) & 1, here, ks + 1, m);
+              } else if (m == NF) {
+                if (!(WG && GATHER) && z + 1 <= st_until) wait_vm<vm_cap(NST)>();
+                else wait_vm<0>();
+                bar();
+              } else {
+                load(here, m - NF - 1);
+              }
+            } else {
+#pragma unroll
+              for (int q = 0; q < NQ; ++q) {
+                if (q * NM / NQ != m) continue;
+                if (q < NL - D0) load(here, D0 + q);
+                else read((ks + 1) & 1, other, 0, q - (NL - D0));
+              }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+        advance();
+      }
+      epilogue(cur, z - 1);
+      L += stride;
+      if (L >= end) break;
+      cur = tile_of(L);
+      nk = slices(cur);
+    }
+    wait_vm<0>();  // the loads past the last slice have landed
   } else {
     for (int z = 0;; ++z) {
       const bool done = kt + 1 == nk && L + stride >= end;
@@ -648,6 +754,19 @@ __global__ __launch_bounds__(64 * WM * WN) void grad_gemm(GradArgs g) {
       next();
     }
   }
+}
+
+template <typename T, int KIND, int ACT, int GATHER, int BM, int BN, int WM, int WN, int S>
+__global__ __launch_bounds__(64 * WM * WN) void grad_gemm(GradArgs g) {
+  grad_body<T, KIND, ACT, GATHER, BM, BN, WM, WN, S>(g);
+}
+
+// The four-wave 256-row tiles: one wave a SIMD, which may then hold the whole
+// register file (256 accumulator registers for its 128 x 128 outputs).
+template <typename T, int KIND, int ACT, int GATHER>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void grad_gemm_w4(
+    GradArgs g) {
+  grad_body<T, KIND, ACT, GATHER, 256, 256, 2, 2, 2>(g);
 }
 
 // d_topk_w of entry f: the column slabs' parts of its sorted row, added in order;
@@ -713,7 +832,7 @@ int device_cus() {
   return cus;
 }
 
-template <typename T, int KIND, int ACT, int BM, int BN, int WM, int WN, int S>
+template <typename T, int KIND, int ACT, int GATHER, int BM, int BN, int WM, int WN, int S>
 hipError_t launch(const GradArgs &g, int64_t tiles, hipStream_t s) {
   constexpr int LDS = S * RB * (BM + BN) + 2 * (kMaxExperts + 1) * 4;
   static_assert(LDS <= 160 * 1024, "LDS budget");
@@ -721,8 +840,12 @@ hipError_t launch(const GradArgs &g, int64_t tiles, hipStream_t s) {
   int64_t grid = (int64_t)device_cus() * per_cu;
   if (grid > tiles) grid = tiles;
   grid = (grid + 7) / 8 * 8;  // whole XCD rounds; surplus workgroups get no tiles
-  hipLaunchKernelGGL((grad_gemm<T, KIND, ACT, BM, BN, WM, WN, S>), dim3((unsigned)grid),
-                     dim3(64 * WM * WN), 0, s, g);
+  if constexpr (BM == 256 && WM * WN == 4)
+    hipLaunchKernelGGL((grad_gemm_w4<T, KIND, ACT, GATHER>), dim3((unsigned)grid), dim3(256), 0, s,
+                       g);
+  else
+    hipLaunchKernelGGL((grad_gemm<T, KIND, ACT, GATHER, BM, BN, WM, WN, S>), dim3((unsigned)grid),
+                       dim3(64 * WM * WN), 0, s, g);
   return hipGetLastError();
 }
 
@@ -731,7 +854,7 @@ inline int64_t cover(int64_t n, int64_t unit) { return (n + unit - 1) / unit; }
 // Data gradients: tiles of 256 rows where they cover the compute units, of 128
 // rows below that, and of 32 rows where experts hold fewer than 48 rows.
 // Returns the columns of a slab of d_w parts in *slab.
-template <typename T, int KIND, int ACT>
+template <typename T, int KIND, int ACT, int GATHER>
 hipError_t launch_rows(const GradArgs &g, hipStream_t s, int *slab) {
   const int64_t cus = device_cus(), most = g.rows < g.E ? g.rows : g.E;
   auto expected = [&](int bm, int bn) {
@@ -740,21 +863,24 @@ hipError_t launch_rows(const GradArgs &g, hipStream_t s, int *slab) {
   auto tiles = [&](int bm, int bn) { return (g.rows / bm + most) * cover(g.N, bn); };
   if (g.rows < 48 * (int64_t)g.E || expected(128, 128) < cus / 2) {
     *slab = 32;
-    return launch<T, KIND, ACT, 32, 128, 1, 4, 4>(g, tiles(32, 128), s);
+    return launch<T, KIND, ACT, GATHER, 32, 128, 1, 4, 4>(g, tiles(32, 128), s);
   }
   if (expected(256, 256) >= cus) {
     *slab = 128;
-    return launch<T, KIND, ACT, 256, 256, 4, 2, 2>(g, tiles(256, 256), s);
+    // (fp32 accumulates at a sixteenth of the rate: nothing to place by hand)
+    constexpr int WM = std::is_same<T, bf16_t>::value ? 2 : 4;
+    return launch<T, KIND, ACT, GATHER, 256, 256, WM, 2, 2>(g, tiles(256, 256), s);
   }
   *slab = 32;
-  return launch<T, KIND, ACT, 128, 128, 2, 4, 3>(g, tiles(128, 128), s);
+  return launch<T, KIND, ACT, GATHER, 128, 128, 2, 4, 3>(g, tiles(128, 128), s);
 }
 
 // Weight gradients: 256 x 256 tiles where they cover the compute units.
-template <typename T> hipError_t launch_weights(const GradArgs &g, hipStream_t s) {
+template <typename T, int GATHER> hipError_t launch_weights(const GradArgs &g, hipStream_t s) {
   const int64_t big = g.E * cover(g.M, 256) * cover(g.N, 256);
-  if (big >= device_cus()) return launch<T, GRAD_WEIGHT, 0, 256, 256, 4, 2, 2>(g, big, s);
-  return launch<T, GRAD_WEIGHT, 0, 128, 128, 2, 4, 3>(
+  constexpr int WM = std::is_same<T, bf16_t>::value ? 2 : 4;
+  if (big >= device_cus()) return launch<T, GRAD_WEIGHT, 0, GATHER, 256, 256, WM, 2, 2>(g, big, s);
+  return launch<T, GRAD_WEIGHT, 0, GATHER, 128, 128, 2, 4, 3>(
       g, g.E * cover(g.M, 128) * cover(g.N, 128), s);
 }
 
@@ -778,12 +904,12 @@ hipError_t run(const ExpertGradArgs &a, GradArgs g, hipStream_t s) {
 
   // u = d_out W2, to dh, w a and the parts of d_w
   GradArgs q = g;
-  q.A = a.d_out, q.a_bytes = token_bytes, q.gather_a = 1, q.K = a.hidden;
+  q.A = a.d_out, q.a_bytes = token_bytes, q.K = a.hidden;
   q.B = a.w2, q.b_bytes = w2_bytes, q.N = a.inter;
   q.h = a.h, q.dh = dh, q.wa = wa, q.part = part, q.h_bytes = h_bytes, q.c_bytes = wa_bytes;
   int slab = 32, unused;
-  err = a.act == MOE_ACT_RELU2 ? launch_rows<T, GRAD_ACT, ACT_RELU2>(q, s, &slab)
-                               : launch_rows<T, GRAD_ACT, ACT_GATED>(q, s, &slab);
+  err = a.act == MOE_ACT_RELU2 ? launch_rows<T, GRAD_ACT, ACT_RELU2, 1>(q, s, &slab)
+                               : launch_rows<T, GRAD_ACT, ACT_GATED, 1>(q, s, &slab);
   if (err != hipSuccess) return err;
   hipLaunchKernelGGL(join_weight_grad, dim3((unsigned)cover(g.rows, 256)), dim3(256), 0, s, part,
                      a.routing->row_sorted, a.d_topk_w, g.rows, (int)cover(a.inter, slab));
@@ -791,25 +917,25 @@ hipError_t run(const ExpertGradArgs &a, GradArgs g, hipStream_t s) {
 
   // dW2 = d_out^T (w a)
   q = g;
-  q.A = a.d_out, q.a_bytes = token_bytes, q.gather_a = 1, q.M = a.hidden;
+  q.A = a.d_out, q.a_bytes = token_bytes, q.M = a.hidden;
   q.B = wa, q.b_bytes = wa_bytes, q.N = a.inter, q.C = a.d_w2, q.c_bytes = w2_bytes;
-  if ((err = launch_weights<T>(q, s)) != hipSuccess) return err;
+  if ((err = launch_weights<T, 1>(q, s)) != hipSuccess) return err;
 
   // rows of d_x = dh W13, added up by token
   q = g;
   q.A = dh, q.a_bytes = h_bytes, q.K = rows13;
   q.B = a.w13, q.b_bytes = w13_bytes, q.N = a.hidden;
   q.C = dx, q.c_bytes = (uint32_t)(m * a.hidden * ES);
-  if ((err = launch_rows<T, GRAD_ROWS, 0>(q, s, &unused)) != hipSuccess) return err;
+  if ((err = launch_rows<T, GRAD_ROWS, 0, 0>(q, s, &unused)) != hipSuccess) return err;
   err = launch_combine(dx, a.routing->row_sorted, a.d_x, a.dtype, a.n_tokens, a.topk, a.hidden, s);
   if (err != hipSuccess) return err;
 
   // dW13 = dh^T x
   q = g;
   q.A = dh, q.a_bytes = h_bytes, q.M = rows13;
-  q.B = a.x, q.b_bytes = token_bytes, q.gather_b = 1, q.N = a.hidden;
+  q.B = a.x, q.b_bytes = token_bytes, q.N = a.hidden;
   q.C = a.d_w13, q.c_bytes = w13_bytes;
-  return launch_weights<T>(q, s);
+  return launch_weights<T, 2>(q, s);
 }
 
 }  // namespace

@@ -45,6 +45,10 @@ CASES = [
     (600, 2056, 2312, 4, 2, "bf16", "bf16", "swiglu_oai", "interleaved", OAI, None),
     (1500, 2304, 1288, 2, 2, "f32", "f32", "silu", "packed", {}, None),
     (40, 72, 264, 256, 4, "bf16", "bf16", "silu", "packed", {}, None),
+    # row tiles of 256 rows (they have to cover the compute units)
+    (4000, 2120, 2072, 3, 2, "bf16", "bf16", "swiglu_oai", "interleaved", OAI, 0.5),
+    (8200, 1048, 4104, 1, 1, "bf16", "f32", "relu2", "packed", {}, None),
+    (5000, 1160, 4104, 2, 1, "f32", "f32", "silu", "packed", {}, None),
 ]
 
 
