@@ -265,7 +265,7 @@ moe_status_t moe_route_backward(const float *d_topk_w, int64_t n_tokens, int32_t
  * moe_route's or, for an expert share, moe_route_ep's (then n_experts is the
  * share's count and the weights hold its experts; n_experts may be smaller than
  * topk).  Limits as moe_experts; the rows of h (n_tokens * topk * rows of w13)
- * below 2^31 bytes, too.  Deterministic, no atomics.
+ * below 2^31 bytes, too, and inter below 2^21.  Deterministic, no atomics.
  *
  * moe_experts_train: moe_experts (a token with no slot in a share gets a zero row)
  *   that also writes h [n_tokens * topk, rows of w13] in `dtype`: row p holds the

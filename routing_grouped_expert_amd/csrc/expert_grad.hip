@@ -8,10 +8,9 @@
 //   dh[p]   = w[p] act'(h[p]) u[p]      dW13[e] = sum_p dh[p] x[t]^T
 //                                       dW2[e]  = sum_p d_out[t] (w[p] a[p])^T
 //
-// Four grouped products in three kernel forms.  Two data gradients run over row
-// tiles as the forward products do, but contract over the weights' row index;
-// the first one's epilogue turns u (never stored) into dh, w a and d_w from the
-// saved h.  The weight gradients contract over an expert's rows, so their K is
+// Four grouped products in two kernel forms, and a pass over rows between them that
+// turns u into dh, w a and d_w.  Two data gradients run over row tiles as the forward
+// products do, but contract over the weights' row index.  The weight gradients contract over an expert's rows, so their K is
 // ragged and an expert without rows gets zeros.
 //
 // An operand that is contracted over its row index lies in LDS as it lies in
@@ -131,29 +130,20 @@ struct GradArgs {
   const int32_t *offsets;       // [E + 1]
   const int32_t *col_sorted;    // [rows]
   uint32_t a_bytes, b_bytes;    // buffer ranges (b_bytes: of one expert's weights)
-  uint32_t c_bytes;             // (of one expert in the weight gradients)
   int E, K, M, N;
-  uint32_t div_mul, div_shift;  // f / topk = (f * div_mul) >> div_shift
-  // epilogue of the first data gradient
-  const void *h;                // [rows, sets * N]
-  void *dh, *wa;                // [rows, sets * N], [rows, N]
-  float *part;                  // [column slabs, rows]: parts of d_w
-  const void *gate_scal;        // [rows]
+  uint32_t div_mul, div_shift;  // f / topk = (2 f * div_mul) >> (32 + div_shift)
   int64_t rows;                 // n_tokens * topk
-  uint32_t h_bytes;
-  int gate_bf16, interleaved;
-  ActParams prm;
 };
 
-__device__ __forceinline__ uint32_t token_of(const GradArgs &g, int f) {
-  return (uint32_t)(((uint64_t)(uint32_t)f * g.div_mul) >> g.div_shift);
+__device__ __forceinline__ uint32_t token_of(const GradArgs &g, uint32_t f) {
+  return __umulhi(2 * f, g.div_mul) >> g.div_shift;
 }
 
-// Gradient kinds, and whose rows are gathered: row p of A (1) or B (2) is that of
-// token col_sorted[p] / topk.
-enum { GRAD_ACT = 0, GRAD_ROWS = 1, GRAD_WEIGHT = 2 };
-// Activation kinds of GRAD_ACT.
-enum { ACT_GATED = 0, ACT_RELU2 = 1 };
+// Gradient kinds (GRAD_U: rows of u, kept in fp32), and whose rows are gathered: row
+// p of A (1) or B (2) is that of token col_sorted[p] / topk.
+enum { GRAD_U = 0, GRAD_ROWS = 1, GRAD_WEIGHT = 2 };
+// Activation kinds (pairs: interleaved w13 rows).
+enum { ACT_GATED = 0, ACT_RELU2 = 1, ACT_GATED_PAIRS = 2 };
 
 // a, and the derivatives of a with respect to the gate and up products.
 template <int ACT>
@@ -214,11 +204,10 @@ __device__ __forceinline__ int find_expert(const int *s, int E, int v) {
   return lo;
 }
 
-// One expert's units (row tiles, or K-slices: at least `least`) summed up to each
-// expert, and the routing offsets, in LDS; one wave, four experts a lane.
-template <int UNIT>
-__device__ __forceinline__ void expert_units(const GradArgs &g, int least, int *s_unit, int *s_off,
-                                             int lane) {
+// Data gradients: the row tiles summed up to each expert, and the routing offsets,
+// in LDS; one wave, four experts a lane.
+template <int BM>
+__device__ __forceinline__ void tile_starts(const GradArgs &g, int *s_unit, int *s_off, int lane) {
   int v[4], s = 0;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
@@ -226,7 +215,7 @@ __device__ __forceinline__ void expert_units(const GradArgs &g, int least, int *
     const int o0 = e < g.E ? g.offsets[e] : 0;
     const int o1 = e < g.E ? g.offsets[e + 1] : 0;
     if (e < g.E) s_off[e] = o0;
-    v[q] = e < g.E ? max(least, (o1 - o0 + UNIT - 1) / UNIT) : 0;
+    v[q] = e < g.E ? (o1 - o0 + BM - 1) / BM : 0;
     s += v[q];
   }
   const int incl = wave_inclusive_sum(s);
@@ -243,6 +232,22 @@ __device__ __forceinline__ void expert_units(const GradArgs &g, int least, int *
   }
 }
 
+// Weight gradients: the experts by their rows, most first, and the routing offsets,
+// in LDS (the whole workgroup).
+__device__ __forceinline__ void expert_order(const GradArgs &g, int *s_order, int *s_off) {
+  for (int e = threadIdx.x; e <= g.E; e += blockDim.x) s_off[e] = g.offsets[e];
+  __syncthreads();
+  for (int e = threadIdx.x; e < g.E; e += blockDim.x) {
+    const int rows = s_off[e + 1] - s_off[e];
+    int rank = 0;
+    for (int f = 0; f < g.E; ++f) {
+      const int r = s_off[f + 1] - s_off[f];
+      rank += r > rows || (r == rows && f < e);
+    }
+    s_order[rank] = e;
+  }
+}
+
 // ---- the kernel --------------------------------------------------------------------
 //
 // Tile of BM x BN outputs, WM x WN waves, S-stage ring.  Eight waves run the
@@ -255,7 +260,7 @@ __device__ __forceinline__ void expert_units(const GradArgs &g, int least, int *
 //
 // The MFMA takes the N-side fragment first: lane l ends with output row l % 32 of
 // a 32 x 32 sub-tile and, in register group q, columns 8 q + 4 (l / 32) + [0, 4).
-template <typename T, int KIND, int ACT, int GATHER, int BM, int BN, int WM, int WN, int S>
+template <typename T, int KIND, int GATHER, int BM, int BN, int WM, int WN, int S>
 __device__ __forceinline__ void grad_body(const GradArgs &g) {
   using Mm = Mma<T>;
   using Frag = typename Mm::Frag;
@@ -265,51 +270,66 @@ __device__ __forceinline__ void grad_body(const GradArgs &g) {
   using TA = typename std::conditional<WG, ColTile<T, BM, NW>, RowTile<T, BM, NW>>::type;
   using TB = ColTile<T, BN, NW>;
   constexpr int STAGE = TA::BYTES + TB::BYTES, JA = TA::J, JB = TB::J, PER = JA + JB;
-  constexpr int TM = BM / WM / 32, TN = BN / WN / 32, WC = BN / WN;
-  constexpr int SETS = KIND == GRAD_ACT && ACT == ACT_GATED ? 2 : 1;
-  // stores a wave's epilogue issues at least (the ring's waits count them)
-  constexpr int NPART = BF ? 2 : 4;  // pieces of a sub-tile row a lane
-  constexpr int NST = TM * TN * NPART * (KIND == GRAD_ACT ? SETS + 1 : 1);
+  constexpr int TM = BM / WM / 32, TN = BN / WN / 32;
+  using Out = typename std::conditional<KIND == GRAD_U, float, T>::type;
+  constexpr bool PACK = std::is_same<Out, bf16_t>::value;
+  constexpr int NPART = PACK ? 2 : 4;      // 16-byte pieces of a sub-tile row a lane
+  constexpr int NST = TM * TN * NPART;     // stores of a wave's epilogue (the waits count them)
   constexpr bool PP = NW == 8;
   constexpr bool BIG = NW == 4 && BM == 256;  // one wave a SIMD
   static_assert(!BIG || (BF && S == 2 && NKS >= 4), "four-wave tiles");
   static_assert(TM * 32 * WM == BM && TN * 32 * WN == BN && S >= 2 && (S - 2) * PER < 64, "tile");
 
   __shared__ __attribute__((aligned(16))) char smem[S * STAGE];
+  // row tiles up to each expert (weight gradients: the experts by their rows), offsets
   __shared__ int s_unit[kMaxExperts + 1], s_off[kMaxExperts + 1];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave % WM, wn = wave / WM;
-  if (wave == 0) expert_units<WG ? BK : BM>(g, WG ? 1 : 0, s_unit, s_off, lane);
-  __syncthreads();
-
-  // this workgroup's tiles: first, first + stride, ... below end.  The tile order
-  // is cut into one run for each XCD (workgroup b runs on XCD b % 8): of equal
-  // tile counts, or in the weight gradients of equal K-slice counts
+  // This workgroup's tiles are those numbered first, first + stride, ... below end
+  // (in the weight gradients: place(first), place(first + stride), ...).
+  //
+  // Data gradients: the tile order is cut into one run of equal length for each XCD
+  // (workgroup b runs on XCD b % 8).
+  //
+  // Weight gradients: a tile takes as many K-slices as its expert's rows give, so
+  // tiles are dealt out in rounds of one a workgroup, the experts with the most rows
+  // first, every other round in reverse, which evens out the workgroups' sums (a
+  // skewed 64-expert layer: the longest 29 % over the mean in runs of equal K-slice
+  // counts an XCD, 2 % dealt out).  An XCD's workgroups get neighbours in a round.
   const int n_nt = (g.N + BN - 1) / BN, n_mt = WG ? (g.M + BM - 1) / BM : 0;
-  const int per_e = n_mt * n_nt, stride = (int)gridDim.x / 8, xcd = (int)blockIdx.x % 8;
-  auto cut = [&](int c) -> int {
-    if constexpr (WG) {
-      if (c == 8) return g.E * per_e;
-      const int64_t want = (int64_t)uniform(s_unit[g.E]) * per_e * c / 8;
-      const int e = find_expert(s_unit, g.E, (int)(want / per_e));
-      const int before = uniform(s_unit[e]), nk = uniform(s_unit[e + 1]) - before;
-      return e * per_e + (int)((want - (int64_t)before * per_e) / nk);
-    } else {
-      const int total = uniform(s_unit[g.E]) * n_nt;
-      return min(total, c * ((total + 7) / 8));
-    }
-  };
-  const int first = cut(xcd) + (int)blockIdx.x / 8, end = cut(xcd + 1);
+  const int per_e = n_mt * n_nt, grid = (int)gridDim.x, xcd = (int)blockIdx.x % 8;
+  const int seat = xcd * (grid / 8) + (int)blockIdx.x / 8;
+  int first, end, stride;
+  if constexpr (WG) {
+    expert_order(g, s_unit, s_off);
+    __syncthreads();
+    first = seat, end = g.E * per_e, stride = grid;
+    // (the last round, if it is a reversed one, may have no tile for this seat)
+    const int rounds = (end + grid - 1) / grid;
+    if (rounds % 2 == 0 && (rounds - 1) * grid + (grid - 1 - seat) >= end) end = (rounds - 1) * grid;
+    else if (rounds % 2 == 0) end = rounds * grid;
+  } else {
+    if (wave == 0) tile_starts<BM>(g, s_unit, s_off, lane);
+    __syncthreads();
+    const int total = uniform(s_unit[g.E]) * n_nt, run = (total + 7) / 8;
+    first = min(total, xcd * run) + (int)blockIdx.x / 8;
+    end = min(total, xcd * run + run), stride = grid / 8;
+  }
   if (first >= end) return;
+  auto place = [&](int L) __attribute__((always_inline)) {  // L = round * grid + seat
+    return (L / grid) % 2 ? L - seat + (grid - 1 - seat) : L;
+  };
 
-  auto tile_of = [&](int L) -> Tile {
+  auto tile_of = [&](int L) __attribute__((always_inline)) -> Tile {
     Tile t;
     int mt, nt;
     if constexpr (WG) {
-      t.e = L / per_e;
-      tile_place(L - t.e * per_e, n_mt, n_nt, mt, nt);
+      L = place(L);
+      const int turn = L / per_e;
+      tile_place(L - turn * per_e, n_mt, n_nt, mt, nt);
+      t.e = uniform(s_unit[turn]);
       t.row0 = uniform(s_off[t.e]);
       t.rows = uniform(s_off[t.e + 1]) - t.row0;
       t.m0 = mt * BM;
@@ -324,7 +344,7 @@ __device__ __forceinline__ void grad_body(const GradArgs &g) {
     t.n0 = nt * BN;
     return t;
   };
-  auto slices = [&](const Tile &t) { return ((WG ? max(t.rows, 1) : g.K) + BK - 1) / BK; };
+  auto slices = [&](const Tile &t) __attribute__((always_inline)) { return ((WG ? max(t.rows, 1) : g.K) + BK - 1) / BK; };
 
   // ---- loading side: slice k_in of tile L_in is the next to load ----------------
   const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
@@ -332,41 +352,45 @@ __device__ __forceinline__ void grad_body(const GradArgs &g) {
   __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<void *>(g.B), (short)0, (int)g.b_bytes, kRsrcWord3);
   const uint32_t arow = (uint32_t)((WG ? g.M : g.K) * ES), brow = (uint32_t)(g.N * ES);
-  uint32_t va[JA], vb[JB];  // a lane's offsets that hold for the whole tile
-  uint32_t oa[JA], ob[JB];  // and those of the next slice
-  // col_sorted of the gathered operand's rows in the next slice (weight gradients) or
-  // tile, read ahead of their use (rows past the end read any valid entry)
+  // A load's address is a lane's offset, which holds for the whole tile, and the
+  // slice's (uniform); a gathered row's offset is added to the lane's.
   constexpr bool GA = GATHER == 1, GB = GATHER == 2;
-  int ia[GA ? JA : 1], ib[GB ? JB : 1];
+  uint32_t va[JA], vb[JB], oa[WG && GA ? JA : 1], ob[GB ? JB : 1];
+  // col_sorted of the gathered operand's rows in the next slice (weight gradients) or
+  // tile, read ahead of their use (past the tile's rows any entry or, past the array, 0)
+  uint32_t ia[GA ? JA : 1], ib[GB ? JB : 1];
+  const __amdgpu_buffer_rsrc_t ri = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<int32_t *>(g.col_sorted), (short)0, (int)(g.rows * 4), kRsrcWord3);
   Tile in{};
   int L_in = first, k_in = 0, nk_in = 0, z_in = 0;  // z_in: slices loaded so far
-  auto fetch = [&](const Tile &t, int k0) {
-    const int last = t.row0 + t.rows - 1;
-    if (t.rows == 0) return;
+  auto fetch = [&](int row) __attribute__((always_inline)) {
     if constexpr (GA) {
 #pragma unroll
       for (int j = 0; j < JA; ++j)
-        ia[j] = g.col_sorted[min(t.row0 + k0 + TA::line(wave, lane, j), last)];
+        ia[j] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(ri, TA::line(wave, lane, j) * 4,
+                                                               row * 4, 0);
     }
     if constexpr (GB) {
 #pragma unroll
       for (int j = 0; j < JB; ++j)
-        ib[j] = g.col_sorted[min(t.row0 + k0 + TB::line(wave, lane, j), last)];
+        ib[j] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(ri, TB::line(wave, lane, j) * 4,
+                                                               row * 4, 0);
     }
   };
-  // Offsets of tile L_in, whose gather indices are there.
-  auto begin_tile = [&]() {
+  // Offsets of tile L_in, whose gather indices are there.  (An offset out of range
+  // stays so whatever is added: every buffer is below 2^31 bytes.)
+  auto begin_tile = [&]() __attribute__((always_inline)) {
     in = tile_of(L_in);
     nk_in = slices(in);
 #pragma unroll
     for (int j = 0; j < JA; ++j) {
+      const int r = TA::line(wave, lane, j), b = TA::byte(wave, lane, j);
       if constexpr (WG) {
-        const int b = in.m0 * ES + TA::byte(wave, lane, j);
-        va[j] = b < (int)arow ? (uint32_t)b : kOOB;
+        const int c = in.m0 * ES + b;
+        va[j] = c < (int)arow ? (GA ? 0u : (uint32_t)(in.row0 + r) * arow) + (uint32_t)c : kOOB;
       } else {
-        const int r = TA::line(wave, lane, j);
         const uint32_t row = GA ? token_of(g, ia[GA ? j : 0]) : (uint32_t)(in.row0 + r);
-        va[j] = r < in.rows ? row * arow + TA::byte(wave, lane, j) : kOOB;
+        va[j] = r < in.rows ? row * arow + (uint32_t)b : kOOB;
       }
     }
     if constexpr (!WG)
@@ -375,71 +399,86 @@ __device__ __forceinline__ void grad_body(const GradArgs &g) {
           (short)0, (int)g.b_bytes, kRsrcWord3);
 #pragma unroll
     for (int j = 0; j < JB; ++j) {
-      const int b = in.n0 * ES + TB::byte(wave, lane, j);
-      vb[j] = b < (int)brow ? (uint32_t)b : kOOB;
-      // (out of range it stays so: an expert's weights are below 2^31 bytes)
-      if constexpr (!WG) vb[j] += (uint32_t)TB::line(wave, lane, j) * brow;
+      const int r = TB::line(wave, lane, j), c = in.n0 * ES + TB::byte(wave, lane, j);
+      const int row = WG ? in.row0 + r : r;
+      vb[j] = c < (int)brow ? (GB ? 0u : (uint32_t)row * brow) + (uint32_t)c : kOOB;
     }
     if constexpr (GA && !WG)
-      if (L_in + stride < end) fetch(tile_of(L_in + stride), 0);
+      if (L_in + stride < end) fetch(tile_of(L_in + stride).row0);
   };
-  // Offset of load j of the next slice, A and B; past the last tile out of range.
-  auto prep_a = [&](int j) {
-    if constexpr (WG) {
-      const int k = k_in * BK + TA::line(wave, lane, j);
-      const uint32_t row = GA ? token_of(g, ia[GA ? j : 0]) : (uint32_t)(in.row0 + k);
-      oa[j] = L_in < end && k < in.rows && va[j] != kOOB ? row * arow + va[j] : kOOB;
-    } else {
-      const int kb = k_in * RB;  // (a row is a whole number of 16-byte chunks)
-      const bool past = L_in >= end || kb + TA::byte(wave, lane, j) >= (int)arow;
-      oa[j] = past ? kOOB : va[j] + (uint32_t)kb;
+  // Ahead of a tile's last slice: its K past the end out of range.
+  auto mask_tail = [&]() __attribute__((always_inline)) {
+    const int k0 = k_in * BK;
+#pragma unroll
+    for (int j = 0; j < JA; ++j) {
+      const bool past = WG ? k0 + TA::line(wave, lane, j) >= in.rows
+                           : k0 * ES + TA::byte(wave, lane, j) >= (int)arow;
+      if (past) va[j] = kOOB;  // (a row is a whole number of 16-byte chunks)
     }
+#pragma unroll
+    for (int j = 0; j < JB; ++j)
+      if (k0 + TB::line(wave, lane, j) >= (WG ? in.rows : g.K)) vb[j] = kOOB;
   };
-  auto prep_b = [&](int j) {
-    const int k = k_in * BK + TB::line(wave, lane, j);
-    if constexpr (WG) {
-      const uint32_t row = GB ? token_of(g, ib[GB ? j : 0]) : (uint32_t)(in.row0 + k);
-      ob[j] = L_in < end && k < in.rows && vb[j] != kOOB ? row * brow + vb[j] : kOOB;
-    } else {
-      ob[j] = L_in >= end || k >= g.K ? kOOB : vb[j] + (uint32_t)(k_in * BK) * brow;
-    }
+  // (an entry past an expert share's rows is -1; its row is masked)
+  auto gather_a = [&](int j) __attribute__((always_inline)) {
+    if constexpr (WG && GA) oa[j] = token_of(g, max((int)ia[j], 0)) * arow + va[j];
   };
-  auto load_a = [&](char *base, int j) { dma16(ra, base + (wave * JA + j) * 1024, oa[j]); };
-  auto load_b = [&](char *base, int j) {
-    dma16(rb, base + TA::BYTES + (wave * JB + j) * 1024, ob[j]);
+  auto gather_b = [&](int j) __attribute__((always_inline)) {
+    if constexpr (GB) ob[j] = token_of(g, max((int)ib[j], 0)) * brow + vb[j];
+  };
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(smem));
+  auto load_a = [&](uint32_t slot, int j) __attribute__((always_inline)) {
+    const uint32_t lds = lds0 + slot * STAGE + (wave * JA + j) * 1024;
+    if constexpr (WG && GA) dma16a(ra, lds, oa[j], 0);
+    else dma16a(ra, lds, va[j], (uint32_t)k_in * (WG ? BK * arow : RB));
+  };
+  auto load_b = [&](uint32_t slot, int j) __attribute__((always_inline)) {
+    const uint32_t lds = lds0 + slot * STAGE + TA::BYTES + (wave * JB + j) * 1024;
+    if constexpr (GB) dma16a(rb, lds, ob[j], 0);
+    else dma16a(rb, lds, vb[j], (uint32_t)k_in * (BK * brow));
   };
   // The gather indices of the slice after the next one (the next one's are in use).
-  auto ahead = [&]() {
+  auto ahead = [&]() __attribute__((always_inline)) {
     if constexpr (WG && GATHER) {
-      if (k_in + 1 < nk_in) fetch(in, (k_in + 1) * BK);
-      else if (L_in + stride < end) fetch(tile_of(L_in + stride), 0);
+      if (k_in + 1 < nk_in) fetch(in.row0 + (k_in + 1) * BK);
+      else if (L_in + stride < end) fetch(tile_of(L_in + stride).row0);
     }
   };
-  // On to the slice after this one, whose loads are out.
-  auto advance = [&]() {
+  // On to the slice after this one, whose loads are out; past the last tile's every
+  // offset is out of range.
+  auto advance = [&]() __attribute__((always_inline)) {
     ++z_in;
-    if (++k_in < nk_in) return;
+    if (L_in >= end || ++k_in < nk_in) return;
     k_in = 0;
     L_in += stride;
-    if (L_in < end) begin_tile();
+    if (L_in < end) {
+      begin_tile();
+    } else {
+      nk_in = 0;
+#pragma unroll
+      for (int j = 0; j < JA; ++j) va[j] = kOOB;
+#pragma unroll
+      for (int j = 0; j < JB; ++j) vb[j] = kOOB;
+    }
   };
-  auto issue = [&]() {
-    char *base = smem + (z_in % S) * STAGE;
+  auto issue = [&]() __attribute__((always_inline)) {
+    if (k_in == nk_in - 1) mask_tail();
 #pragma unroll
-    for (int j = 0; j < JB; ++j) prep_b(j);
+    for (int j = 0; j < JA; ++j) gather_a(j);
 #pragma unroll
-    for (int j = 0; j < JA; ++j) prep_a(j);
+    for (int j = 0; j < JB; ++j) gather_b(j);
     ahead();
+    const uint32_t slot = (uint32_t)z_in % S;
 #pragma unroll
-    for (int j = 0; j < JB; ++j) load_b(base, j);
+    for (int j = 0; j < JB; ++j) load_b(slot, j);
 #pragma unroll
-    for (int j = 0; j < JA; ++j) load_a(base, j);
+    for (int j = 0; j < JA; ++j) load_a(slot, j);
     advance();
   };
 
   // ---- multiplying side ------------------------------------------------------------
   f32x16_t acc[TM][TN];
-  auto zero_acc = [&]() {
+  auto zero_acc = [&]() __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
@@ -449,16 +488,16 @@ __device__ __forceinline__ void grad_body(const GradArgs &g) {
   };
   int st_until = -1;  // last slice whose wait must also cover the latest epilogue's stores
   // slice w is in LDS as far as this wave's loads go (and its LDS reads are done)
-  auto wait_slice = [&](int w) {
+  auto wait_slice = [&](int w) __attribute__((always_inline)) {
     wait_pending<PER, NST, S - 2>(min(S - 2, z_in - 1 - w), w <= st_until);
   };
   // Piece c of a lane's share of sub-tile (i, j): NV consecutive columns of its
-  // row, from column piece_col(c).  In bf16 register groups 2c and 2c + 1 hold 4
+  // row.  For bf16 outputs register groups 2c and 2c + 1 hold 4
   // of 8 + 8 columns each in lanes l and l + 32; exchanging the halves gives
   // each lane 8 consecutive ones, a 16-byte piece.
-  constexpr int NV = 16 / ES;
-  auto piece = [&](int i, int j, int c, float (&v)[NV]) {
-    if constexpr (BF) {
+  constexpr int NV = 16 / (int)sizeof(Out);
+  auto piece = [&](int i, int j, int c, float (&v)[NV]) __attribute__((always_inline)) {
+    if constexpr (PACK) {
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[i][j][8 * c + t]),
@@ -472,138 +511,62 @@ __device__ __forceinline__ void grad_body(const GradArgs &g) {
       for (int t = 0; t < 4; ++t) v[t] = acc[i][j][4 * c + t];
     }
   };
-  // (four-wave tiles: the accumulators stay in AGPRs up to their sub-tile, and the
-  // sub-tiles apart: reading them all early would need 256 more registers)
-  auto hold = [&](int i, int j) {
-    if constexpr (BIG) {
-      __builtin_amdgcn_sched_barrier(0);
-      asm volatile("" : "+a"(acc[i][j]));
-    }
-  };
-  auto piece_col = [&](int c) { return BF ? 16 * c + 8 * (lane >> 5) : 8 * c + 4 * (lane >> 5); };
-  auto put = [&](__amdgpu_buffer_rsrc_t r, uint32_t off, const float (&v)[NV]) {
-    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(i32x4_t, pack(v)), r, (int)off, 0, 0);
-  };
-
-  auto epilogue = [&](const Tile &t, int z) {
-    if constexpr (KIND == GRAD_ACT) {
-      const __amdgpu_buffer_rsrc_t rh = __builtin_amdgcn_make_buffer_rsrc(
-          const_cast<void *>(g.h), (short)0, (int)g.h_bytes, kRsrcWord3);
-      const __amdgpu_buffer_rsrc_t rdh =
-          __builtin_amdgcn_make_buffer_rsrc(g.dh, (short)0, (int)g.h_bytes, kRsrcWord3);
-      const __amdgpu_buffer_rsrc_t rwa =
-          __builtin_amdgcn_make_buffer_rsrc(g.wa, (short)0, (int)g.c_bytes, kRsrcWord3);
-      const int slab = (t.n0 + wn * WC) / WC;
+  auto epilogue = [&](const Tile &t, int z) __attribute__((always_inline)) {
+    // the expert's weights, or the tile's rows
+    const int rows = WG ? g.M - t.m0 : t.rows;
+    const size_t at = WG ? ((size_t)t.e * g.M + t.m0) * g.N : (size_t)t.row0 * g.N;
+    const __amdgpu_buffer_rsrc_t rc = __builtin_amdgcn_make_buffer_rsrc(
+        reinterpret_cast<Out *>(g.C) + at, (short)0,
+        (int)((uint32_t)min(rows, BM) * (uint32_t)g.N * (uint32_t)sizeof(Out)), kRsrcWord3);
 #pragma unroll
-      for (int i = 0; i < TM; ++i) {
-        const int m = wm * (BM / WM) + i * 32 + (lane & 31);
-        const bool ok = m < t.rows;
-        const uint32_t p = (uint32_t)(t.row0 + (ok ? m : 0));
-        const float w = weight_at(g.gate_scal, g.gate_bf16, p);
-        float sum = 0.f;  // this lane's part of d_w
+    for (int i = 0; i < TM; ++i) {
+      const int m = wm * (BM / WM) + i * 32 + (lane & 31);
 #pragma unroll
-        for (int j = 0; j < TN; ++j) {
-          hold(i, j);
-#pragma unroll
-          for (int c = 0; c < NPART; ++c) {
-            const int col = t.n0 + wn * WC + j * 32 + piece_col(c);
-            const bool in_range = ok && col < g.N;
-            const uint32_t row_h = p * (uint32_t)(SETS * g.N);
-            // the gate and up chunks, or the pairs of columns [0, NV / 2) and the rest
-            const uint32_t c0 = SETS == 1 ? (uint32_t)col
-                                : g.interleaved ? (uint32_t)(2 * col) : (uint32_t)col;
-            const uint32_t c1 = g.interleaved ? (uint32_t)(2 * col + NV) : (uint32_t)(g.N + col);
-            const uint32_t o0 = in_range ? (row_h + c0) * ES : kOOB;
-            const uint32_t o1 = in_range ? (row_h + c1) * ES : kOOB;
-            float u[NV], h0[NV], h1[NV], gate[NV], up[NV], a[NV], dg[NV], dv[NV];
-            piece(i, j, c, u);
-            unpack(__builtin_bit_cast(u32x4_t,
-                                      __builtin_amdgcn_raw_buffer_load_b128(rh, (int)o0, 0, 0)), h0);
-            if constexpr (SETS == 2)
-              unpack(__builtin_bit_cast(
-                         u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rh, (int)o1, 0, 0)), h1);
-#pragma unroll
-            for (int q = 0; q < NV; ++q) {
-              gate[q] = h0[q];
-              up[q] = SETS == 2 ? h1[q] : 0.f;
-              if (SETS == 2 && g.interleaved) {
-                gate[q] = q < NV / 2 ? h0[(2 * q) % NV] : h1[(2 * q) % NV];
-                up[q] = q < NV / 2 ? h0[(2 * q + 1) % NV] : h1[(2 * q + 1) % NV];
-              }
-              act_grad<ACT>(gate[q], up[q], g.prm, a[q], dg[q], dv[q]);
-              sum += in_range ? u[q] * a[q] : 0.f;
-              const float wu = w * u[q];
-              a[q] *= w;
-              dg[q] *= wu;
-              dv[q] *= wu;
-            }
-            put(rwa, in_range ? (p * (uint32_t)g.N + (uint32_t)col) * ES : kOOB, a);
-            if constexpr (SETS == 1) {
-              put(rdh, o0, dg);
-            } else {
-#pragma unroll
-              for (int q = 0; q < NV; ++q) {
-                h0[q] = dg[q];
-                h1[q] = dv[q];
-                if (g.interleaved) {
-                  h0[q] = q % 2 ? dv[q / 2] : dg[q / 2];
-                  h1[q] = q % 2 ? dv[NV / 2 + q / 2] : dg[NV / 2 + q / 2];
-                }
-              }
-              put(rdh, o0, h0);
-              put(rdh, o1, h1);
-            }
-          }
+      for (int j = 0; j < TN; ++j) {
+        if constexpr (BIG) {
+          // the accumulators stay in AGPRs up to their sub-tile, and the sub-tiles
+          // apart: reading them all early would need 256 more registers
+          __builtin_amdgcn_sched_barrier(0);
+          asm volatile("" : "+a"(acc[i][j]));
         }
-        sum += __shfl_xor(sum, 32);
-        if (ok && lane < 32 && slab * WC < g.N) g.part[(int64_t)slab * g.rows + p] = sum;
-      }
-    } else {
-      const __amdgpu_buffer_rsrc_t rc = __builtin_amdgcn_make_buffer_rsrc(
-          reinterpret_cast<char *>(g.C) + (WG ? (size_t)t.e * g.c_bytes : 0), (short)0,
-          (int)g.c_bytes, kRsrcWord3);
 #pragma unroll
-      for (int i = 0; i < TM; ++i) {
-        const int m = wm * (BM / WM) + i * 32 + (lane & 31);
-        const bool ok = WG ? t.m0 + m < g.M : m < t.rows;
-        const uint32_t row = (uint32_t)((WG ? t.m0 : t.row0) + m);
-#pragma unroll
-        for (int j = 0; j < TN; ++j) {
-          hold(i, j);
-#pragma unroll
-          for (int c = 0; c < NPART; ++c) {
-            const int col = t.n0 + wn * WC + j * 32 + piece_col(c);
-            float v[NV];
-            piece(i, j, c, v);
-            put(rc, ok && col < g.N ? (row * (uint32_t)g.N + (uint32_t)col) * ES : kOOB, v);
-          }
+        for (int c = 0; c < NPART; ++c) {
+          const int col = t.n0 + wn * (BN / WN) + j * 32 + (PACK ? 16 : 8) * c + NV * (lane >> 5);
+          float v[NV];
+          piece(i, j, c, v);
+          const uint32_t off = m < rows && col < g.N
+                                   ? ((uint32_t)m * (uint32_t)g.N + (uint32_t)col) *
+                                         (uint32_t)sizeof(Out)
+                                   : kOOB;
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(i32x4_t, pack(v)), rc,
+                                                 (int)off, 0, 0);
         }
       }
     }
     st_until = z + S - 1 + (BIG ? 1 : 0);  // (four waves load a slice further ahead)
   };
 
-  if constexpr (GA && !WG) fetch(tile_of(first), 0);
+  if constexpr (GA && !WG) fetch(tile_of(first).row0);
   begin_tile();
-  if constexpr (WG && GATHER) fetch(in, 0);
+  if constexpr (WG && GATHER) fetch(in.row0);
 #pragma unroll
   for (int s = 0; s < S - 1; ++s)
     if (L_in < end) issue();
 
   Tile cur = tile_of(first);
   int nk = slices(cur), kt = 0, L = first;
-  auto frag_a = [&](const char *p, int ks, int i) {
+  auto frag_a = [&](const char *p, int ks, int i) __attribute__((always_inline)) {
     return TA::frag(p, ks, wm * (BM / WM) + i * 32, lane);
   };
-  auto frag_b = [&](const char *p, int ks, int j) {
-    return TB::frag(p + TA::BYTES, ks, wn * WC + j * 32, lane);
+  auto frag_b = [&](const char *p, int ks, int j) __attribute__((always_inline)) {
+    return TB::frag(p + TA::BYTES, ks, wn * (BN / WN) + j * 32, lane);
   };
-  auto bar = [&]() {  // workgroup barrier; MFMAs may cross it
+  auto bar = [&]() __attribute__((always_inline)) {  // workgroup barrier; MFMAs may cross it
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
-  auto next = [&]() {  // the slice after this one (its tile's first: the next tile)
+  auto next = [&]() __attribute__((always_inline)) {  // the slice after this one (its tile's first: the next tile)
     if (++kt < nk) return;
     kt = 0;
     L += stride;
@@ -648,24 +611,27 @@ __device__ __forceinline__ void grad_body(const GradArgs &g) {
     if (!grp) barrier();
   } else if constexpr (BIG) {
     // One wave a SIMD: nothing else fills the matrix core while this wave issues
-    // other work, so each memory instruction follows an MFMA.
-    //  * k-step 0: the load offsets of slice z + 2; k-step 1: the gather indices of
-    //    slice z + 3 (the wait in k-step NKS - 2 covers them).
-    //  * k-steps before the last: the fragments of the next k-step.
+    // other work, so each memory instruction follows an MFMA.  A k-step's first NF
+    // MFMAs carry the reads of the next k-step's fragments, in the order in which
+    // its MFMAs take them, so they have the rest of the k-step to arrive.  Besides:
+    //  * k-step 0: the gathered rows' offsets of slice z + 2; k-step 1: the gather
+    //    indices of slice z + 3 (the wait in k-step NKS - 2 covers them).
     //  * k-step NKS - 2, once its reads are out: the wait for slice z + 1 and the
     //    barrier (after which no wave reads slot z % 2 again), then the first loads
-    //    of slice z + 2 into that slot.
-    //  * last k-step: its other loads, then slice z + 1's first fragments.
+    //    of slice z + 2 into that slot, the others in the last k-step.
     constexpr int NM = TM * TN, NF = TM + TN, NL = JA + JB;
-    static_assert(!BIG || NL <= NM, "a load offset after each MFMA");
+    constexpr int D0 = NM - NF - 1;  // loads that k-step NKS - 2 has room for
+    static_assert(!BIG || (JA <= NM && JB <= NM && NL - D0 <= 2 * (NM - NF)), "room for loads");
     Frag fa[2][TM], fb[2][TN];
-    auto read = [&](int buf, const char *p, int ks, int f) {
-      if (f < TM) fa[buf][f] = frag_a(p, ks, f);
-      else fb[buf][f - TM] = frag_b(p, ks, f - TM);
+    auto read = [&](int buf, const char *p, int ks, int f) __attribute__((always_inline)) {
+      // fa[0], fb[0 ..], fa[1 ..]
+      if (f == 0) fa[buf][0] = frag_a(p, ks, 0);
+      else if (f <= TN) fb[buf][f - 1] = frag_b(p, ks, f - 1);
+      else fa[buf][f - TN] = frag_a(p, ks, f - TN);
     };
-    auto load = [&](char *base, int q) {
-      if (q < JB) load_b(base, q);
-      else load_a(base, q - JB);
+    auto load = [&](uint32_t slot, int q) __attribute__((always_inline)) {
+      if (q < JB) load_b(slot, q);
+      else load_a(slot, q - JB);
     };
     wait_vm<0>();
     barrier();
@@ -678,39 +644,30 @@ __device__ __forceinline__ void grad_body(const GradArgs &g) {
       zero_acc();
 #pragma nounroll
       for (int k = 0; k < nk; ++k, ++z) {
-        char *here = smem + (z & 1) * STAGE, *other = smem + ((z + 1) & 1) * STAGE;
+        const uint32_t slot = (uint32_t)z & 1;
+        const char *here = smem + slot * STAGE, *other = smem + (slot ^ 1) * STAGE;
+        if (k_in == nk_in - 1) mask_tail();
 #pragma unroll
         for (int ks = 0; ks < NKS; ++ks) {
-          constexpr int D0 = NM - NF - 1;   // loads that k-step NKS - 2 has room for
-          constexpr int NQ = NL - D0 + NF;  // memory instructions of the last k-step
+          const int nb = (ks + 1) & 1, nks = (ks + 1) % NKS;
 #pragma unroll
           for (int m = 0; m < NM; ++m) {
             const int i = m / TN, j = m % TN;
             acc[i][j] = Mm::mma(fb[ks & 1][j], fa[ks & 1][i], acc[i][j]);
-            if (ks == 0 && m < NL) {
-              if (m < JB) prep_b(m);
-              else prep_a(m - JB);
+            if (m < NF) read(nb, ks + 1 < NKS ? here : other, nks, m);
+            if (ks == 0 && m < JA) gather_a(m);
+            if (ks == 0 && m < JB) gather_b(m);
+            if (ks == 1 && m == NF) ahead();
+            if (ks + 2 == NKS && m == NF) {
+              if (!(WG && GATHER) && z + 1 <= st_until) wait_vm<vm_cap(NST)>();
+              else wait_vm<0>();
+              bar();
             }
-            if (ks == 1 && m == 0) ahead();
-            if (ks + 2 < NKS) {
-              if (m % 2 == 0) read((ks + 1) & 1, here, ks + 1, m / 2);
-            } else if (ks + 2 == NKS) {
-              if (m < NF) {
-                read((ks + 1) & 1, here, ks + 1, m);
-              } else if (m == NF) {
-                if (!(WG && GATHER) && z + 1 <= st_until) wait_vm<vm_cap(NST)>();
-                else wait_vm<0>();
-                bar();
-              } else {
-                load(here, m - NF - 1);
-              }
-            } else {
+            if (ks + 2 == NKS && m > NF) load(slot, m - NF - 1);
+            if (ks + 1 == NKS && m >= NF) {
 #pragma unroll
-              for (int q = 0; q < NQ; ++q) {
-                if (q * NM / NQ != m) continue;
-                if (q < NL - D0) load(here, D0 + q);
-                else read((ks + 1) & 1, other, 0, q - (NL - D0));
-              }
+              for (int q = D0; q < NL; ++q)
+                if (NF + (q - D0) * (NM - NF) / (NL - D0) == m) load(slot, q);
             }
             __builtin_amdgcn_sched_barrier(0);
           }
@@ -733,7 +690,7 @@ __device__ __forceinline__ void grad_body(const GradArgs &g) {
       if (kt == 0) zero_acc();
       const char *p = smem + (z % S) * STAGE;
       Frag fa[2][TM], fb[2][TN];
-      auto load = [&](int ks) {
+      auto load = [&](int ks) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < TM; ++i) fa[ks & 1][i] = frag_a(p, ks, i);
 #pragma unroll
@@ -756,32 +713,85 @@ __device__ __forceinline__ void grad_body(const GradArgs &g) {
   }
 }
 
-template <typename T, int KIND, int ACT, int GATHER, int BM, int BN, int WM, int WN, int S>
+template <typename T, int KIND, int GATHER, int BM, int BN, int WM, int WN, int S>
 __global__ __launch_bounds__(64 * WM * WN) void grad_gemm(GradArgs g) {
-  grad_body<T, KIND, ACT, GATHER, BM, BN, WM, WN, S>(g);
+  grad_body<T, KIND, GATHER, BM, BN, WM, WN, S>(g);
 }
 
 // The four-wave 256-row tiles: one wave a SIMD, which may then hold the whole
 // register file (256 accumulator registers for its 128 x 128 outputs).
-template <typename T, int KIND, int ACT, int GATHER>
+template <typename T, int KIND, int GATHER>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void grad_gemm_w4(
     GradArgs g) {
-  grad_body<T, KIND, ACT, GATHER, 256, 256, 2, 2, 2>(g);
+  grad_body<T, KIND, GATHER, 256, 256, 2, 2, 2>(g);
 }
 
-// d_topk_w of entry f: the column slabs' parts of its sorted row, added in order;
-// 0 for a slot outside an expert share.
-__global__ __launch_bounds__(256) void join_weight_grad(const float *__restrict__ part,
-                                                        const int32_t *__restrict__ row_sorted,
-                                                        float *__restrict__ d_topk_w, int64_t rows,
-                                                        int slabs) {
-  const int64_t f = (int64_t)blockIdx.x * 256 + threadIdx.x;
+// From u and the saved products: dh, w a and d_w, entry by entry (slot f of a token;
+// its sorted row is p), one wave a row.  Bound by memory: u in fp32 and h are read,
+// dh and w a written.  (In the epilogue of the product, with u never stored, the same
+// work took 1.0 ms of the 64-expert training batch's 2.5 ms: with one wave a SIMD
+// nothing hides the latency of the arithmetic and of the loads of h; here it takes
+// 0.56 ms.)  A slot outside an expert share gets 0.
+template <typename T, int ACT>
+__global__ __launch_bounds__(256) void act_backward_kernel(
+    const float *__restrict__ u, const T *__restrict__ h, const int32_t *__restrict__ row_sorted,
+    const void *__restrict__ gate_scal, int gate_bf16, T *__restrict__ dh, T *__restrict__ wa,
+    float *__restrict__ d_topk_w, int64_t rows, int inter, ActParams prm) {
+  constexpr int NV = 16 / (int)sizeof(T), SETS = ACT == ACT_RELU2 ? 1 : 2;
+  const int64_t f = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
   if (f >= rows) return;
-  const int p = row_sorted[f];
-  float s = 0.f;
-  if (p >= 0)
-    for (int i = 0; i < slabs; ++i) s += part[i * rows + p];
-  d_topk_w[f] = s;
+  const int64_t p = __builtin_amdgcn_readfirstlane(row_sorted[f]);
+  if (p < 0) {
+    if (lane == 0) d_topk_w[f] = 0.f;
+    return;
+  }
+  const float w = weight_at(gate_scal, gate_bf16, p);
+  const int nch = inter / NV;
+  const u32x4_t *uc = reinterpret_cast<const u32x4_t *>(u + p * inter);
+  const u32x4_t *hc = reinterpret_cast<const u32x4_t *>(h + p * SETS * inter);
+  u32x4_t *dc = reinterpret_cast<u32x4_t *>(dh + p * SETS * inter);
+  u32x4_t *ac = reinterpret_cast<u32x4_t *>(wa + p * inter);
+  float sum = 0.f;
+  for (int c = lane; c < nch; c += 64) {
+    // the gate and up chunks, or (pairs) those of the first NV / 2 columns and the others
+    const int c0 = ACT == ACT_GATED_PAIRS ? 2 * c : c, c1 = ACT == ACT_GATED_PAIRS ? 2 * c + 1 : nch + c;
+    float uv[NV], h0[NV], h1[NV], a[NV], d0[NV], d1[NV];
+#pragma unroll
+    for (int q = 0; q < NV / 4; ++q) {
+      const u32x4_t v = __builtin_nontemporal_load(uc + c * (NV / 4) + q);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) uv[4 * q + t] = __uint_as_float(v[t]);
+    }
+    unpack(__builtin_nontemporal_load(hc + c0), h0);
+    if constexpr (SETS == 2) unpack(__builtin_nontemporal_load(hc + c1), h1);
+#pragma unroll
+    for (int q = 0; q < NV; ++q) {
+      float dg, dv;
+      // columns of a pair chunk: gate at 2 q, up at 2 q + 1 of the two chunks in a row
+      const bool low = q < NV / 2;
+      const float gate = ACT != ACT_GATED_PAIRS ? h0[q] : low ? h0[2 * q % NV] : h1[2 * q % NV];
+      const float up = ACT == ACT_RELU2 ? 0.f
+                       : ACT != ACT_GATED_PAIRS ? h1[q]
+                       : low ? h0[(2 * q + 1) % NV] : h1[(2 * q + 1) % NV];
+      act_grad<ACT>(gate, up, prm, a[q], dg, dv);
+      sum += uv[q] * a[q];
+      a[q] *= w;
+      const float wu = w * uv[q];
+      if constexpr (ACT == ACT_GATED_PAIRS) {
+        (low ? d0 : d1)[2 * q % NV] = wu * dg;
+        (low ? d0 : d1)[(2 * q + 1) % NV] = wu * dv;
+      } else {
+        d0[q] = wu * dg;
+        d1[q] = wu * dv;
+      }
+    }
+    ac[c] = pack(a);
+    dc[c0] = pack(d0);
+    if constexpr (SETS == 2) dc[c1] = pack(d1);
+  }
+  sum = wave_sum_f32(sum);
+  if (lane == 0) d_topk_w[f] = sum;
 }
 
 // Weight gradients of a call without tokens.
@@ -796,7 +806,7 @@ template <typename T, int ACT>
 __global__ __launch_bounds__(256) void activation_kernel(const T *__restrict__ h,
                                                          T *__restrict__ act,
                                                          const int32_t *__restrict__ offsets,
-                                                         int E, int inter, int interleaved,
+                                                         int E, int inter,
                                                          int64_t chunks, ActParams prm) {
   constexpr int NV = 16 / (int)sizeof(T);
   const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -807,15 +817,15 @@ __global__ __launch_bounds__(256) void activation_kernel(const T *__restrict__ h
   if (p >= offsets[E]) return;
   const u32x4_t *row = reinterpret_cast<const u32x4_t *>(h + p * (ACT == ACT_RELU2 ? 1 : 2) * inter);
   float h0[NV], h1[NV], a[NV], dg, dv;
-  unpack(row[interleaved ? 2 * c : c], h0);
-  if constexpr (ACT == ACT_GATED) unpack(row[interleaved ? 2 * c + 1 : nch + c], h1);
+  unpack(row[ACT == ACT_GATED_PAIRS ? 2 * c : c], h0);
+  if constexpr (ACT != ACT_RELU2) unpack(row[ACT == ACT_GATED_PAIRS ? 2 * c + 1 : nch + c], h1);
 #pragma unroll
   for (int q = 0; q < NV; ++q) {
-    float gate = h0[q], up = ACT == ACT_GATED ? h1[q] : 0.f;
-    if (ACT == ACT_GATED && interleaved) {
-      gate = q < NV / 2 ? h0[(2 * q) % NV] : h1[(2 * q) % NV];
-      up = q < NV / 2 ? h0[(2 * q + 1) % NV] : h1[(2 * q + 1) % NV];
-    }
+    const bool low = q < NV / 2;
+    const float gate = ACT != ACT_GATED_PAIRS ? h0[q] : low ? h0[2 * q % NV] : h1[2 * q % NV];
+    const float up = ACT == ACT_RELU2 ? 0.f
+                     : ACT != ACT_GATED_PAIRS ? h1[q]
+                     : low ? h0[(2 * q + 1) % NV] : h1[(2 * q + 1) % NV];
     act_grad<ACT>(gate, up, prm, a[q], dg, dv);
   }
   reinterpret_cast<u32x4_t *>(act + p * inter)[c] = pack(a);
@@ -832,7 +842,7 @@ int device_cus() {
   return cus;
 }
 
-template <typename T, int KIND, int ACT, int GATHER, int BM, int BN, int WM, int WN, int S>
+template <typename T, int KIND, int GATHER, int BM, int BN, int WM, int WN, int S>
 hipError_t launch(const GradArgs &g, int64_t tiles, hipStream_t s) {
   constexpr int LDS = S * RB * (BM + BN) + 2 * (kMaxExperts + 1) * 4;
   static_assert(LDS <= 160 * 1024, "LDS budget");
@@ -841,10 +851,10 @@ hipError_t launch(const GradArgs &g, int64_t tiles, hipStream_t s) {
   if (grid > tiles) grid = tiles;
   grid = (grid + 7) / 8 * 8;  // whole XCD rounds; surplus workgroups get no tiles
   if constexpr (BM == 256 && WM * WN == 4)
-    hipLaunchKernelGGL((grad_gemm_w4<T, KIND, ACT, GATHER>), dim3((unsigned)grid), dim3(256), 0, s,
+    hipLaunchKernelGGL((grad_gemm_w4<T, KIND, GATHER>), dim3((unsigned)grid), dim3(256), 0, s,
                        g);
   else
-    hipLaunchKernelGGL((grad_gemm<T, KIND, ACT, GATHER, BM, BN, WM, WN, S>), dim3((unsigned)grid),
+    hipLaunchKernelGGL((grad_gemm<T, KIND, GATHER, BM, BN, WM, WN, S>), dim3((unsigned)grid),
                        dim3(64 * WM * WN), 0, s, g);
   return hipGetLastError();
 }
@@ -853,34 +863,30 @@ inline int64_t cover(int64_t n, int64_t unit) { return (n + unit - 1) / unit; }
 
 // Data gradients: tiles of 256 rows where they cover the compute units, of 128
 // rows below that, and of 32 rows where experts hold fewer than 48 rows.
-// Returns the columns of a slab of d_w parts in *slab.
-template <typename T, int KIND, int ACT, int GATHER>
-hipError_t launch_rows(const GradArgs &g, hipStream_t s, int *slab) {
+template <typename T, int KIND, int GATHER>
+hipError_t launch_rows(const GradArgs &g, hipStream_t s) {
   const int64_t cus = device_cus(), most = g.rows < g.E ? g.rows : g.E;
-  auto expected = [&](int bm, int bn) {
+  auto expected = [&](int bm, int bn) __attribute__((always_inline)) {
     return (g.rows / bm + (most + 1) / 2) * cover(g.N, bn);
   };
-  auto tiles = [&](int bm, int bn) { return (g.rows / bm + most) * cover(g.N, bn); };
+  auto tiles = [&](int bm, int bn) __attribute__((always_inline)) { return (g.rows / bm + most) * cover(g.N, bn); };
   if (g.rows < 48 * (int64_t)g.E || expected(128, 128) < cus / 2) {
-    *slab = 32;
-    return launch<T, KIND, ACT, GATHER, 32, 128, 1, 4, 4>(g, tiles(32, 128), s);
+    return launch<T, KIND, GATHER, 32, 128, 1, 4, 4>(g, tiles(32, 128), s);
   }
   if (expected(256, 256) >= cus) {
-    *slab = 128;
     // (fp32 accumulates at a sixteenth of the rate: nothing to place by hand)
     constexpr int WM = std::is_same<T, bf16_t>::value ? 2 : 4;
-    return launch<T, KIND, ACT, GATHER, 256, 256, WM, 2, 2>(g, tiles(256, 256), s);
+    return launch<T, KIND, GATHER, 256, 256, WM, 2, 2>(g, tiles(256, 256), s);
   }
-  *slab = 32;
-  return launch<T, KIND, ACT, GATHER, 128, 128, 2, 4, 3>(g, tiles(128, 128), s);
+  return launch<T, KIND, GATHER, 128, 128, 2, 4, 3>(g, tiles(128, 128), s);
 }
 
 // Weight gradients: 256 x 256 tiles where they cover the compute units.
 template <typename T, int GATHER> hipError_t launch_weights(const GradArgs &g, hipStream_t s) {
   const int64_t big = g.E * cover(g.M, 256) * cover(g.N, 256);
   constexpr int WM = std::is_same<T, bf16_t>::value ? 2 : 4;
-  if (big >= device_cus()) return launch<T, GRAD_WEIGHT, 0, GATHER, 256, 256, WM, 2, 2>(g, big, s);
-  return launch<T, GRAD_WEIGHT, 0, GATHER, 128, 128, 2, 4, 3>(
+  if (big >= device_cus()) return launch<T, GRAD_WEIGHT, GATHER, 256, 256, WM, 2, 2>(g, big, s);
+  return launch<T, GRAD_WEIGHT, GATHER, 128, 128, 2, 4, 3>(
       g, g.E * cover(g.M, 128) * cover(g.N, 128), s);
 }
 
@@ -892,41 +898,48 @@ hipError_t run(const ExpertGradArgs &a, GradArgs g, hipStream_t s) {
   const int rows13 = (a.act == MOE_ACT_RELU2 ? 1 : 2) * a.inter;
   const size_t m = (size_t)g.rows;
   char *ws = reinterpret_cast<char *>(a.workspace);
-  void *dh = ws;
-  void *wa = ws += align256(m * rows13 * ES);
-  void *dx = ws += align256(m * a.inter * ES);
-  float *part = reinterpret_cast<float *>(ws += align256(m * a.hidden * ES));
+  T *dh = reinterpret_cast<T *>(ws);
+  T *wa = reinterpret_cast<T *>(ws += align256(m * rows13 * ES));
+  void *u = ws += align256(m * a.inter * ES), *dx = u;  // (u is used up when dx is written)
   const uint32_t token_bytes = (uint32_t)(a.n_tokens * a.hidden * ES);
   const uint32_t h_bytes = (uint32_t)(m * rows13 * ES), wa_bytes = (uint32_t)(m * a.inter * ES);
   const uint32_t w13_bytes = (uint32_t)((size_t)rows13 * a.hidden * ES);
   const uint32_t w2_bytes = (uint32_t)((size_t)a.inter * a.hidden * ES);
   hipError_t err;
 
-  // u = d_out W2, to dh, w a and the parts of d_w
+  // u = d_out W2
   GradArgs q = g;
   q.A = a.d_out, q.a_bytes = token_bytes, q.K = a.hidden;
-  q.B = a.w2, q.b_bytes = w2_bytes, q.N = a.inter;
-  q.h = a.h, q.dh = dh, q.wa = wa, q.part = part, q.h_bytes = h_bytes, q.c_bytes = wa_bytes;
-  int slab = 32, unused;
-  err = a.act == MOE_ACT_RELU2 ? launch_rows<T, GRAD_ACT, ACT_RELU2, 1>(q, s, &slab)
-                               : launch_rows<T, GRAD_ACT, ACT_GATED, 1>(q, s, &slab);
+  q.B = a.w2, q.b_bytes = w2_bytes, q.N = a.inter, q.C = u;
+  if ((err = launch_rows<T, GRAD_U, 1>(q, s)) != hipSuccess) return err;
+
+  // dh, w a and d_w
+  auto act = [&](auto kind) {
+    hipLaunchKernelGGL((act_backward_kernel<T, decltype(kind)::value>),
+                       dim3((unsigned)cover(g.rows, 4)), dim3(256), 0, s,
+                       reinterpret_cast<const float *>(u), reinterpret_cast<const T *>(a.h),
+                       a.routing->row_sorted, a.routing->gate_scal,
+                       (int)(a.routing->w_dtype == MOE_BF16), dh, wa, a.d_topk_w, g.rows, a.inter,
+                       a.prm);
+    return hipGetLastError();
+  };
+  err = a.act == MOE_ACT_RELU2 ? act(std::integral_constant<int, ACT_RELU2>())
+        : a.layout == MOE_W13_INTERLEAVED ? act(std::integral_constant<int, ACT_GATED_PAIRS>())
+                                          : act(std::integral_constant<int, ACT_GATED>());
   if (err != hipSuccess) return err;
-  hipLaunchKernelGGL(join_weight_grad, dim3((unsigned)cover(g.rows, 256)), dim3(256), 0, s, part,
-                     a.routing->row_sorted, a.d_topk_w, g.rows, (int)cover(a.inter, slab));
-  if ((err = hipGetLastError()) != hipSuccess) return err;
 
   // dW2 = d_out^T (w a)
   q = g;
   q.A = a.d_out, q.a_bytes = token_bytes, q.M = a.hidden;
-  q.B = wa, q.b_bytes = wa_bytes, q.N = a.inter, q.C = a.d_w2, q.c_bytes = w2_bytes;
+  q.B = wa, q.b_bytes = wa_bytes, q.N = a.inter, q.C = a.d_w2;
   if ((err = launch_weights<T, 1>(q, s)) != hipSuccess) return err;
 
   // rows of d_x = dh W13, added up by token
   q = g;
   q.A = dh, q.a_bytes = h_bytes, q.K = rows13;
   q.B = a.w13, q.b_bytes = w13_bytes, q.N = a.hidden;
-  q.C = dx, q.c_bytes = (uint32_t)(m * a.hidden * ES);
-  if ((err = launch_rows<T, GRAD_ROWS, 0, 0>(q, s, &unused)) != hipSuccess) return err;
+  q.C = dx;
+  if ((err = launch_rows<T, GRAD_ROWS, 0>(q, s)) != hipSuccess) return err;
   err = launch_combine(dx, a.routing->row_sorted, a.d_x, a.dtype, a.n_tokens, a.topk, a.hidden, s);
   if (err != hipSuccess) return err;
 
@@ -934,7 +947,7 @@ hipError_t run(const ExpertGradArgs &a, GradArgs g, hipStream_t s) {
   q = g;
   q.A = dh, q.a_bytes = h_bytes, q.M = rows13;
   q.B = a.x, q.b_bytes = token_bytes, q.N = a.hidden;
-  q.C = a.d_w13, q.c_bytes = w13_bytes;
+  q.C = a.d_w13;
   return launch_weights<T, 2>(q, s);
 }
 
@@ -951,42 +964,40 @@ hipError_t launch_activation(const void *h, void *act, const int32_t *offsets, i
                              moe_dtype_t dt, int64_t rows, int inter, moe_act_t kind,
                              moe_w13_layout_t layout, ActParams prm, hipStream_t s) {
   const int64_t chunks = rows * (inter / (dt == MOE_BF16 ? 8 : 4));
-  auto go = [&](auto t, auto k) {
+  auto go = [&](auto t, auto k) __attribute__((always_inline)) {
     using T = decltype(t);
     hipLaunchKernelGGL((activation_kernel<T, decltype(k)::value>),
                        dim3((unsigned)cover(chunks, 256)), dim3(256), 0, s,
                        reinterpret_cast<const T *>(h), reinterpret_cast<T *>(act), offsets,
-                       n_experts, inter, layout == MOE_W13_INTERLEAVED, chunks, prm);
+                       n_experts, inter, chunks, prm);
+    return hipGetLastError();
   };
-  std::integral_constant<int, ACT_GATED> gated;
-  std::integral_constant<int, ACT_RELU2> relu2;
-  if (dt == MOE_BF16) kind == MOE_ACT_RELU2 ? go(bf16_t(), relu2) : go(bf16_t(), gated);
-  else kind == MOE_ACT_RELU2 ? go(float(), relu2) : go(float(), gated);
-  return hipGetLastError();
+  auto kinds = [&](auto t) {
+    if (kind == MOE_ACT_RELU2) return go(t, std::integral_constant<int, ACT_RELU2>());
+    if (layout == MOE_W13_INTERLEAVED) return go(t, std::integral_constant<int, ACT_GATED_PAIRS>());
+    return go(t, std::integral_constant<int, ACT_GATED>());
+  };
+  return dt == MOE_BF16 ? kinds(bf16_t()) : kinds(float());
 }
 
 size_t experts_backward_scratch_bytes(int64_t n_tokens, int topk, int hidden, int inter,
                                       moe_dtype_t dt) {
   const size_t m = (size_t)n_tokens * topk, es = dt == MOE_BF16 ? 2 : 4;
-  // dh (as for a gated activation), w a, the rows of d_x, the parts of d_w
-  return align256(2 * m * inter * es) + align256(m * inter * es) + align256(m * hidden * es) +
-         align256(m * (size_t)cover(inter, 32) * 4);
+  // dh (as for a gated activation), w a, then u and later the rows of d_x
+  const size_t u = m * inter * 4, dx = m * hidden * es;
+  return align256(2 * m * inter * es) + align256(m * inter * es) + align256(u > dx ? u : dx);
 }
 
 hipError_t launch_experts_backward(const ExpertGradArgs &a, hipStream_t s) {
   GradArgs g{};
   g.offsets = a.routing->offsets;
   g.col_sorted = a.routing->col_sorted;
-  g.gate_scal = a.routing->gate_scal;
-  g.gate_bf16 = a.routing->w_dtype == MOE_BF16;
   g.E = a.n_experts;
   g.rows = a.n_tokens * a.topk;
-  g.interleaved = a.layout == MOE_W13_INTERLEAVED;
-  g.prm = a.prm;
   // exact for f below 2^31: mul = ceil(2^(31 + l) / topk), 2^l >= topk
   int l = 0;
   while ((1 << l) < a.topk) ++l;
-  g.div_shift = 31 + l;
+  g.div_shift = l;
   g.div_mul = (uint32_t)(((1ull << (31 + l)) + a.topk - 1) / a.topk);
   return a.dtype == MOE_BF16 ? run<bf16_t>(a, g, s) : run<float>(a, g, s);
 }

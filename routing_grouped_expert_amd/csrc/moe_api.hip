@@ -106,7 +106,7 @@ moe_status_t check_expert_args(moe_dtype_t dtype, int64_t n, int32_t hidden, int
 
 // Checks shared by moe_experts_train and its gradient, of a whole layer or of an
 // expert share: the saved products [n * k, rows of w13] are addressed with 32-bit
-// byte offsets, too.
+// byte offsets, too, and a 256-row tile of fp32 rows [inter].
 moe_status_t check_train(moe_dtype_t dtype, int64_t n, int32_t hidden, int32_t e, int32_t inter,
                          int32_t k, moe_act_t act, moe_w13_layout_t layout,
                          const moe_act_params_t *params, const moe_routing_t *routing,
@@ -115,6 +115,7 @@ moe_status_t check_train(moe_dtype_t dtype, int64_t n, int32_t hidden, int32_t e
                                       prm, true);
   if (st != MOE_OK) return st;
   const int64_t rows13 = (act == MOE_ACT_RELU2 ? 1 : 2) * (int64_t)inter;
+  if (inter >= (1 << 21)) return MOE_ERR_SHAPE;
   return n * k * rows13 * (int64_t)dsize(dtype) > 0x7fffffff ? MOE_ERR_SHAPE : MOE_OK;
 }
 
