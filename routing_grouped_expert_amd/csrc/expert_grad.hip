@@ -53,14 +53,14 @@ template <> struct Mma<float> {
   }
 };
 
-// ---- LDS tiles of one K-slice (RB bytes of K: 64 bf16 or 32 fp32) -------------
+// ---- LDS tiles of one K-slice (RB bytes of K) -------------------------------------
 
-constexpr int RB = 128;
-template <typename T> constexpr int kBK = RB / (int)sizeof(T);
-
-// Rows of K: operand row r is RB bytes, its 16-byte chunks XOR-swizzled by r / 2
-// so that the 16-byte reads of 16 consecutive rows hit distinct banks.
-__device__ __forceinline__ int row_key(int r) { return (r >> 1) & 7; }
+// Rows of K: operand row r is RB bytes, its 16-byte chunks XOR-swizzled by the row so
+// that the 16-byte reads of 16 consecutive rows hit distinct banks (256 bytes of LDS,
+// or 256 / RB rows, a bank line).
+template <int RB> __device__ __forceinline__ int row_key(int r) {
+  return r / (256 / RB) % (RB / 16);
+}
 
 // Columns of K: K row r is COLS elements.  A bf16 transposing read takes, from
 // each of four K rows, 64 bytes at the same columns (two 16-lane groups), which
@@ -71,25 +71,27 @@ template <typename T> __device__ __forceinline__ int col_key(int r) {
 }
 
 // Operand tile of ROWS rows, K contiguous, NW waves loading.
-template <typename T, int ROWS, int NW> struct RowTile {
+template <typename T, int RB, int ROWS, int NW> struct RowTile {
   static constexpr int BYTES = ROWS * RB, J = BYTES / 1024 / NW;
   static_assert(J * NW * 1024 == BYTES, "whole loads a wave");
   // line (here: operand row) and byte inside it that load j of a wave brings to its lane
-  __device__ static int line(int wave, int lane, int j) { return (wave * J + j) * 8 + (lane >> 3); }
+  __device__ static int line(int wave, int lane, int j) { 
+    return (wave * J + j) * (1024 / RB) + lane / (RB / 16);
+  }
   __device__ static int byte(int wave, int lane, int j) {
-    return ((lane & 7) ^ row_key(line(wave, lane, j))) << 4;
+    return (lane % (RB / 16) ^ row_key<RB>(line(wave, lane, j))) << 4;
   }
   __device__ static typename Mma<T>::Frag frag(const char *p, int ks, int r, int lane) {
     constexpr int EPL = sizeof(typename Mma<T>::Frag) / sizeof(T);
     const int b = (ks * Mma<T>::KS + (lane >> 5) * EPL) * (int)sizeof(T);
     r += lane & 31;
     return *reinterpret_cast<const typename Mma<T>::Frag *>(
-        p + r * RB + (((b >> 4) ^ row_key(r)) << 4) + (b & 15));
+        p + r * RB + (((b >> 4) ^ row_key<RB>(r)) << 4) + (b & 15));
   }
 };
 
 // Operand tile of COLS columns, K rows, NW waves loading.
-template <typename T, int COLS, int NW> struct ColTile {
+template <typename T, int RB, int COLS, int NW> struct ColTile {
   static constexpr int BYTES = COLS * RB, J = BYTES / 1024 / NW;
   static constexpr int ROWB = COLS * (int)sizeof(T), CPR = ROWB / 16;
   static_assert(J * NW * 1024 == BYTES, "whole loads a wave");
@@ -260,16 +262,18 @@ __device__ __forceinline__ void expert_order(const GradArgs &g, int *s_order, in
 //
 // The MFMA takes the N-side fragment first: lane l ends with output row l % 32 of
 // a 32 x 32 sub-tile and, in register group q, columns 8 q + 4 (l / 32) + [0, 4).
-template <typename T, int KIND, int GATHER, int BM, int BN, int WM, int WN, int S>
+template <typename T, int KIND, int GATHER, int BM, int BN, int WM, int WN, int S, int RB>
 __device__ __forceinline__ void grad_body(const GradArgs &g) {
   using Mm = Mma<T>;
   using Frag = typename Mm::Frag;
   constexpr bool BF = std::is_same<T, bf16_t>::value;
-  constexpr int NW = WM * WN, BK = kBK<T>, NKS = BK / Mm::KS, ES = (int)sizeof(T);
+  constexpr int NW = WM * WN, BK = RB / (int)sizeof(T), NKS = BK / Mm::KS, ES = (int)sizeof(T);
   constexpr bool WG = KIND == GRAD_WEIGHT;
-  using TA = typename std::conditional<WG, ColTile<T, BM, NW>, RowTile<T, BM, NW>>::type;
-  using TB = ColTile<T, BN, NW>;
-  constexpr int STAGE = TA::BYTES + TB::BYTES, JA = TA::J, JB = TB::J, PER = JA + JB;
+  using TA = typename std::conditional<WG, ColTile<T, RB, BM, NW>, RowTile<T, RB, BM, NW>>::type;
+  using TB = ColTile<T, RB, BN, NW>;
+  constexpr int STAGE = TA::BYTES + TB::BYTES, JA = TA::J, JB = TB::J;
+  constexpr bool GA = GATHER == 1, GB = GATHER == 2;
+  constexpr int PER = JA + JB + (WG && GATHER);  // loads of a wave a slice
   constexpr int TM = BM / WM / 32, TN = BN / WN / 32;
   using Out = typename std::conditional<KIND == GRAD_U, float, T>::type;
   constexpr bool PACK = std::is_same<Out, bf16_t>::value;
@@ -277,12 +281,15 @@ __device__ __forceinline__ void grad_body(const GradArgs &g) {
   constexpr int NST = TM * TN * NPART;     // stores of a wave's epilogue (the waits count them)
   constexpr bool PP = NW == 8;
   constexpr bool BIG = NW == 4 && BM == 256;  // one wave a SIMD
-  static_assert(!BIG || (BF && S == 2 && NKS >= 4), "four-wave tiles");
+  static_assert(!BIG || (BF && NKS >= 2), "four-wave tiles");
   static_assert(TM * 32 * WM == BM && TN * 32 * WN == BN && S >= 2 && (S - 2) * PER < 64, "tile");
 
   __shared__ __attribute__((aligned(16))) char smem[S * STAGE];
   // row tiles up to each expert (weight gradients: the experts by their rows), offsets
   __shared__ int s_unit[kMaxExperts + 1], s_off[kMaxExperts + 1];
+  // gather indices of a wave's rows: of the slices to come, or of two tiles
+  constexpr int NI = WG ? 2 * S : 2;
+  __shared__ int s_idx[GATHER ? NW : 1][GATHER ? NI : 1][GATHER ? 64 : 1];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -354,34 +361,43 @@ __device__ __forceinline__ void grad_body(const GradArgs &g) {
   const uint32_t arow = (uint32_t)((WG ? g.M : g.K) * ES), brow = (uint32_t)(g.N * ES);
   // A load's address is a lane's offset, which holds for the whole tile, and the
   // slice's (uniform); a gathered row's offset is added to the lane's.
-  constexpr bool GA = GATHER == 1, GB = GATHER == 2;
   uint32_t va[JA], vb[JB], oa[WG && GA ? JA : 1], ob[GB ? JB : 1];
-  // col_sorted of the gathered operand's rows in the next slice (weight gradients) or
-  // tile, read ahead of their use (past the tile's rows any entry or, past the array, 0)
-  uint32_t ia[GA ? JA : 1], ib[GB ? JB : 1];
-  const __amdgpu_buffer_rsrc_t ri = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<int32_t *>(g.col_sorted), (short)0, (int)(g.rows * 4), kRsrcWord3);
   Tile in{};
   int L_in = first, k_in = 0, nk_in = 0, z_in = 0;  // z_in: slices loaded so far
-  auto fetch = [&](int row) __attribute__((always_inline)) {
-    if constexpr (GA) {
-#pragma unroll
-      for (int j = 0; j < JA; ++j)
-        ia[j] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(ri, TA::line(wave, lane, j) * 4,
-                                                               row * 4, 0);
-    }
-    if constexpr (GB) {
-#pragma unroll
-      for (int j = 0; j < JB; ++j)
-        ib[j] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(ri, TB::line(wave, lane, j) * 4,
-                                                               row * 4, 0);
+  // Gather indices come through LDS, too (each wave its own, 64 a load), long before
+  // their use.  As loads into registers their wait would be the compiler's, which does
+  // not know of the loads into LDS and would wait for all of them.
+  const __amdgpu_buffer_rsrc_t ri = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<int32_t *>(g.col_sorted), (short)0, (int)(g.rows * 4), kRsrcWord3);
+  auto load_idx = [&](int slot, int row) __attribute__((always_inline)) {
+    // (past a tile's rows any entry or, past the array, 0)
+    dma4(ri, reinterpret_cast<char *>(s_idx[wave][slot]),
+         row < 0 ? kOOB : (uint32_t)(row + lane) * 4u);
+  };
+  // The place whose indices are loaded next: S slices ahead of the loads.
+  int L_x = first, k_x = 0, nk_x = 0, row_x = 0, z_x = 0;
+  auto next_idx = [&]() __attribute__((always_inline)) {
+    if constexpr (WG && GATHER) {
+      load_idx(z_x % NI, L_x < end ? row_x + k_x * BK : -1);
+      ++z_x;
+      if (L_x < end && ++k_x == nk_x) {
+        k_x = 0;
+        L_x += stride;
+        if (L_x < end) {
+          const Tile t = tile_of(L_x);
+          nk_x = slices(t), row_x = t.row0;
+        }
+      }
     }
   };
   // Offsets of tile L_in, whose gather indices are there.  (An offset out of range
   // stays so whatever is added: every buffer is below 2^31 bytes.)
+  int turn = 0;  // tiles begun
   auto begin_tile = [&]() __attribute__((always_inline)) {
     in = tile_of(L_in);
     nk_in = slices(in);
+    if constexpr (GA && !WG)
+      if (nk_in <= S) wait_vm<0>();  // (else the ring's waits cover the indices)
 #pragma unroll
     for (int j = 0; j < JA; ++j) {
       const int r = TA::line(wave, lane, j), b = TA::byte(wave, lane, j);
@@ -389,7 +405,9 @@ __device__ __forceinline__ void grad_body(const GradArgs &g) {
         const int c = in.m0 * ES + b;
         va[j] = c < (int)arow ? (GA ? 0u : (uint32_t)(in.row0 + r) * arow) + (uint32_t)c : kOOB;
       } else {
-        const uint32_t row = GA ? token_of(g, ia[GA ? j : 0]) : (uint32_t)(in.row0 + r);
+        const uint32_t row =
+            GA ? token_of(g, s_idx[wave][turn % 2][GA ? r - wave * (BM / NW) : 0])
+               : (uint32_t)(in.row0 + r);
         va[j] = r < in.rows ? row * arow + (uint32_t)b : kOOB;
       }
     }
@@ -403,8 +421,11 @@ __device__ __forceinline__ void grad_body(const GradArgs &g) {
       const int row = WG ? in.row0 + r : r;
       vb[j] = c < (int)brow ? (GB ? 0u : (uint32_t)row * brow) + (uint32_t)c : kOOB;
     }
-    if constexpr (GA && !WG)
-      if (L_in + stride < end) fetch(tile_of(L_in + stride).row0);
+    if constexpr (GA && !WG) {
+      ++turn;
+      if (L_in + stride < end)
+        load_idx(turn % 2, tile_of(L_in + stride).row0 + wave * (BM / NW));
+    }
   };
   // Ahead of a tile's last slice: its K past the end out of range.
   auto mask_tail = [&]() __attribute__((always_inline)) {
@@ -419,13 +440,17 @@ __device__ __forceinline__ void grad_body(const GradArgs &g) {
     for (int j = 0; j < JB; ++j)
       if (k0 + TB::line(wave, lane, j) >= (WG ? in.rows : g.K)) vb[j] = kOOB;
   };
-  // (an entry past an expert share's rows is -1; its row is masked)
-  auto gather_a = [&](int j) __attribute__((always_inline)) {
-    if constexpr (WG && GA) oa[j] = token_of(g, max((int)ia[j], 0)) * arow + va[j];
+  // Offsets of the gathered rows in the next slice.  (An entry past an expert share's
+  // rows is -1; its row is masked.)
+  auto gather = [&](int j) __attribute__((always_inline)) {
+    if constexpr (WG && GATHER) {
+      const int line = (GA ? TA::line(wave, lane, j % JA) : TB::line(wave, lane, j % JB));
+      const uint32_t tok = token_of(g, max(s_idx[wave][z_in % NI][line], 0));
+      if constexpr (GA) oa[j] = tok * arow + va[j];
+      else ob[j] = tok * brow + vb[j];
+    }
   };
-  auto gather_b = [&](int j) __attribute__((always_inline)) {
-    if constexpr (GB) ob[j] = token_of(g, max((int)ib[j], 0)) * brow + vb[j];
-  };
+  constexpr int JG = !WG || !GATHER ? 0 : GA ? JA : JB;  // gathered loads a slice
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(smem));
   auto load_a = [&](uint32_t slot, int j) __attribute__((always_inline)) {
     const uint32_t lds = lds0 + slot * STAGE + (wave * JA + j) * 1024;
@@ -436,13 +461,6 @@ __device__ __forceinline__ void grad_body(const GradArgs &g) {
     const uint32_t lds = lds0 + slot * STAGE + TA::BYTES + (wave * JB + j) * 1024;
     if constexpr (GB) dma16a(rb, lds, ob[j], 0);
     else dma16a(rb, lds, vb[j], (uint32_t)k_in * (BK * brow));
-  };
-  // The gather indices of the slice after the next one (the next one's are in use).
-  auto ahead = [&]() __attribute__((always_inline)) {
-    if constexpr (WG && GATHER) {
-      if (k_in + 1 < nk_in) fetch(in.row0 + (k_in + 1) * BK);
-      else if (L_in + stride < end) fetch(tile_of(L_in + stride).row0);
-    }
   };
   // On to the slice after this one, whose loads are out; past the last tile's every
   // offset is out of range.
@@ -464,10 +482,8 @@ __device__ __forceinline__ void grad_body(const GradArgs &g) {
   auto issue = [&]() __attribute__((always_inline)) {
     if (k_in == nk_in - 1) mask_tail();
 #pragma unroll
-    for (int j = 0; j < JA; ++j) gather_a(j);
-#pragma unroll
-    for (int j = 0; j < JB; ++j) gather_b(j);
-    ahead();
+    for (int j = 0; j < JG; ++j) gather(j);
+    next_idx();
     const uint32_t slot = (uint32_t)z_in % S;
 #pragma unroll
     for (int j = 0; j < JB; ++j) load_b(slot, j);
@@ -546,14 +562,21 @@ __device__ __forceinline__ void grad_body(const GradArgs &g) {
     st_until = z + S - 1 + (BIG ? 1 : 0);  // (four waves load a slice further ahead)
   };
 
-  if constexpr (GA && !WG) fetch(tile_of(first).row0);
+  Tile cur = tile_of(first);
+  if constexpr (GATHER) {  // the first indices
+    if constexpr (WG) {
+      nk_x = slices(cur), row_x = cur.row0;
+#pragma unroll
+      for (int s = 0; s < S; ++s) next_idx();
+    } else {
+      load_idx(0, cur.row0 + wave * (BM / NW));
+    }
+    wait_vm<0>();
+  }
   begin_tile();
-  if constexpr (WG && GATHER) fetch(in.row0);
 #pragma unroll
   for (int s = 0; s < S - 1; ++s)
-    if (L_in < end) issue();
-
-  Tile cur = tile_of(first);
+    if (BIG || L_in < end) issue();
   int nk = slices(cur), kt = 0, L = first;
   auto frag_a = [&](const char *p, int ks, int i) __attribute__((always_inline)) {
     return TA::frag(p, ks, wm * (BM / WM) + i * 32, lane);
@@ -614,14 +637,13 @@ __device__ __forceinline__ void grad_body(const GradArgs &g) {
     // other work, so each memory instruction follows an MFMA.  A k-step's first NF
     // MFMAs carry the reads of the next k-step's fragments, in the order in which
     // its MFMAs take them, so they have the rest of the k-step to arrive.  Besides:
-    //  * k-step 0: the gathered rows' offsets of slice z + 2; k-step 1: the gather
-    //    indices of slice z + 3 (the wait in k-step NKS - 2 covers them).
+    //  * k-step 0: the gathered rows' offsets of slice z + S.
     //  * k-step NKS - 2, once its reads are out: the wait for slice z + 1 and the
-    //    barrier (after which no wave reads slot z % 2 again), then the first loads
-    //    of slice z + 2 into that slot, the others in the last k-step.
+    //    barrier (after which no wave reads slot z % S again), then the first loads
+    //    of slice z + S into that slot, the others in the last k-step.
     constexpr int NM = TM * TN, NF = TM + TN, NL = JA + JB;
-    constexpr int D0 = NM - NF - 1;  // loads that k-step NKS - 2 has room for
-    static_assert(!BIG || (JA <= NM && JB <= NM && NL - D0 <= 2 * (NM - NF)), "room for loads");
+    constexpr int D0 = NL < NM - NF - 1 ? NL : NM - NF - 1;  // loads in k-step NKS - 2
+    static_assert(!BIG || (JG <= NF && NL - D0 <= 2 * (NM - NF) && (S & (S - 1)) == 0), "room");
     Frag fa[2][TM], fb[2][TN];
     auto read = [&](int buf, const char *p, int ks, int f) __attribute__((always_inline)) {
       // fa[0], fb[0 ..], fa[1 ..]
@@ -633,9 +655,9 @@ __device__ __forceinline__ void grad_body(const GradArgs &g) {
       if (q < JB) load_b(slot, q);
       else load_a(slot, q - JB);
     };
-    wait_vm<0>();
-    barrier();
     issue();  // (past the last slice: zeros)
+    wait_vm<vm_cap((S - 1) * PER)>();
+    barrier();
 #pragma unroll
     for (int f = 0; f < NF; ++f) read(0, smem, 0, f);
     int z = 0;
@@ -644,8 +666,9 @@ __device__ __forceinline__ void grad_body(const GradArgs &g) {
       zero_acc();
 #pragma nounroll
       for (int k = 0; k < nk; ++k, ++z) {
-        const uint32_t slot = (uint32_t)z & 1;
-        const char *here = smem + slot * STAGE, *other = smem + (slot ^ 1) * STAGE;
+        const uint32_t slot = (uint32_t)z & (S - 1);
+        const char *here = smem + slot * STAGE;
+        const char *other = smem + ((uint32_t)(z + 1) & (S - 1)) * STAGE;
         if (k_in == nk_in - 1) mask_tail();
 #pragma unroll
         for (int ks = 0; ks < NKS; ++ks) {
@@ -655,19 +678,18 @@ __device__ __forceinline__ void grad_body(const GradArgs &g) {
             const int i = m / TN, j = m % TN;
             acc[i][j] = Mm::mma(fb[ks & 1][j], fa[ks & 1][i], acc[i][j]);
             if (m < NF) read(nb, ks + 1 < NKS ? here : other, nks, m);
-            if (ks == 0 && m < JA) gather_a(m);
-            if (ks == 0 && m < JB) gather_b(m);
-            if (ks == 1 && m == NF) ahead();
+            if (ks == 0 && m < JG) gather(m);
             if (ks + 2 == NKS && m == NF) {
-              if (!(WG && GATHER) && z + 1 <= st_until) wait_vm<vm_cap(NST)>();
-              else wait_vm<0>();
+              if (z + 1 <= st_until) wait_vm<vm_cap((S - 2) * PER + NST)>();
+              else wait_vm<vm_cap((S - 2) * PER)>();
               bar();
+              next_idx();
             }
-            if (ks + 2 == NKS && m > NF) load(slot, m - NF - 1);
+            if (ks + 2 == NKS && m > NF && m <= NF + D0) load(slot, m - NF - 1);
             if (ks + 1 == NKS && m >= NF) {
 #pragma unroll
               for (int q = D0; q < NL; ++q)
-                if (NF + (q - D0) * (NM - NF) / (NL - D0) == m) load(slot, q);
+                if (NF + (q - D0) * (NM - NF) / max(NL - D0, 1) == m) load(slot, q);
             }
             __builtin_amdgcn_sched_barrier(0);
           }
@@ -713,17 +735,17 @@ __device__ __forceinline__ void grad_body(const GradArgs &g) {
   }
 }
 
-template <typename T, int KIND, int GATHER, int BM, int BN, int WM, int WN, int S>
+template <typename T, int KIND, int GATHER, int BM, int BN, int WM, int WN, int S, int RB>
 __global__ __launch_bounds__(64 * WM * WN) void grad_gemm(GradArgs g) {
-  grad_body<T, KIND, GATHER, BM, BN, WM, WN, S>(g);
+  grad_body<T, KIND, GATHER, BM, BN, WM, WN, S, RB>(g);
 }
 
 // The four-wave 256-row tiles: one wave a SIMD, which may then hold the whole
 // register file (256 accumulator registers for its 128 x 128 outputs).
-template <typename T, int KIND, int GATHER>
+template <typename T, int KIND, int GATHER, int S, int RB>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void grad_gemm_w4(
     GradArgs g) {
-  grad_body<T, KIND, GATHER, 256, 256, 2, 2, 2>(g);
+  grad_body<T, KIND, GATHER, 256, 256, 2, 2, S, RB>(g);
 }
 
 // From u and the saved products: dh, w a and d_w, entry by entry (slot f of a token;
@@ -842,19 +864,20 @@ int device_cus() {
   return cus;
 }
 
-template <typename T, int KIND, int GATHER, int BM, int BN, int WM, int WN, int S>
+template <typename T, int KIND, int GATHER, int BM, int BN, int WM, int WN, int S, int RB>
 hipError_t launch(const GradArgs &g, int64_t tiles, hipStream_t s) {
-  constexpr int LDS = S * RB * (BM + BN) + 2 * (kMaxExperts + 1) * 4;
+  constexpr int LDS = S * RB * (BM + BN) + 2 * (kMaxExperts + 1) * 4 +
+                      (GATHER ? WM * WN * (KIND == GRAD_WEIGHT ? 2 * S : 2) * 256 : 0);
   static_assert(LDS <= 160 * 1024, "LDS budget");
   constexpr int per_cu = 160 * 1024 / LDS < 2 ? 1 : 2;
   int64_t grid = (int64_t)device_cus() * per_cu;
   if (grid > tiles) grid = tiles;
   grid = (grid + 7) / 8 * 8;  // whole XCD rounds; surplus workgroups get no tiles
   if constexpr (BM == 256 && WM * WN == 4)
-    hipLaunchKernelGGL((grad_gemm_w4<T, KIND, GATHER>), dim3((unsigned)grid), dim3(256), 0, s,
+    hipLaunchKernelGGL((grad_gemm_w4<T, KIND, GATHER, S, RB>), dim3((unsigned)grid), dim3(256), 0, s,
                        g);
   else
-    hipLaunchKernelGGL((grad_gemm<T, KIND, GATHER, BM, BN, WM, WN, S>), dim3((unsigned)grid),
+    hipLaunchKernelGGL((grad_gemm<T, KIND, GATHER, BM, BN, WM, WN, S, RB>), dim3((unsigned)grid),
                        dim3(64 * WM * WN), 0, s, g);
   return hipGetLastError();
 }
@@ -871,22 +894,25 @@ hipError_t launch_rows(const GradArgs &g, hipStream_t s) {
   };
   auto tiles = [&](int bm, int bn) __attribute__((always_inline)) { return (g.rows / bm + most) * cover(g.N, bn); };
   if (g.rows < 48 * (int64_t)g.E || expected(128, 128) < cus / 2) {
-    return launch<T, KIND, GATHER, 32, 128, 1, 4, 4>(g, tiles(32, 128), s);
+    return launch<T, KIND, GATHER, 32, 128, 1, 4, 4, 128>(g, tiles(32, 128), s);
   }
   if (expected(256, 256) >= cus) {
     // (fp32 accumulates at a sixteenth of the rate: nothing to place by hand)
-    constexpr int WM = std::is_same<T, bf16_t>::value ? 2 : 4;
-    return launch<T, KIND, GATHER, 256, 256, WM, 2, 2>(g, tiles(256, 256), s);
+    constexpr bool BF = std::is_same<T, bf16_t>::value;
+    constexpr int WM = BF ? 2 : 4, S = BF ? 4 : 2, RB = BF ? 64 : 128;
+    return launch<T, KIND, GATHER, 256, 256, WM, 2, S, RB>(g, tiles(256, 256), s);
   }
-  return launch<T, KIND, GATHER, 128, 128, 2, 4, 3>(g, tiles(128, 128), s);
+  return launch<T, KIND, GATHER, 128, 128, 2, 4, 3, 128>(g, tiles(128, 128), s);
 }
 
 // Weight gradients: 256 x 256 tiles where they cover the compute units.
 template <typename T, int GATHER> hipError_t launch_weights(const GradArgs &g, hipStream_t s) {
   const int64_t big = g.E * cover(g.M, 256) * cover(g.N, 256);
-  constexpr int WM = std::is_same<T, bf16_t>::value ? 2 : 4;
-  if (big >= device_cus()) return launch<T, GRAD_WEIGHT, GATHER, 256, 256, WM, 2, 2>(g, big, s);
-  return launch<T, GRAD_WEIGHT, GATHER, 128, 128, 2, 4, 3>(
+  constexpr bool BF = std::is_same<T, bf16_t>::value;
+  constexpr int WM = BF ? 2 : 4, S = BF ? 4 : 2, RB = BF ? 64 : 128;
+  if (big >= device_cus())
+    return launch<T, GRAD_WEIGHT, GATHER, 256, 256, WM, 2, S, RB>(g, big, s);
+  return launch<T, GRAD_WEIGHT, GATHER, 128, 128, 2, 4, 3, 128>(
       g, g.E * cover(g.M, 128) * cover(g.N, 128), s);
 }
 
