@@ -182,15 +182,29 @@ struct Tile {
   int e, row0, rows, m0, n0;  // expert, its rows of this tile, output position
 };
 
-__device__ __forceinline__ void tile_place(int l, int mt_all, int nt_all, int &mt, int &nt) {
-  const int nb = l / (GN * mt_all);
+// Division by a number that stays the same for a while.
+struct Divisor {
+  uint32_t d, m;
+  __device__ explicit Divisor(int v) : d((uint32_t)v), m(v > 1 ? 0xffffffffu / (uint32_t)v + 1 : 0) {}
+  __device__ int of(int n) const {  // n / d, 0 <= n
+    if (d == 1) return n;
+    const uint32_t q = __umulhi((uint32_t)n, m);  // the quotient or one more
+    return (int)(q - (q * d > (uint32_t)n));
+  }
+};
+
+// `column`: GN * mt_all
+__device__ __forceinline__ void tile_place(int l, const Divisor &column, int mt_all, int nt_all,
+                                           int &mt, int &nt) {
+  const int nb = column.of(l);
   const int gn = min(GN, nt_all - nb * GN);
-  const int r = l - nb * GN * mt_all;
-  const int mb = r / (GM * gn);
+  const int r = l - nb * (int)column.d;
+  const int mb = gn == GN ? r / (GM * GN) : r / (GM * gn);
   const int gm = min(GM, mt_all - mb * GM);
   const int r2 = r - mb * GM * gn;
-  mt = mb * GM + r2 % gm;
-  nt = nb * GN + r2 / gm;
+  const int n = gm == GM ? r2 / GM : r2 / gm;
+  mt = mb * GM + r2 - n * gm;
+  nt = nb * GN + n;
 }
 
 // A value that every lane holds, in a scalar register.
@@ -325,8 +339,9 @@ __device__ __forceinline__ void grad_body(const GradArgs &g) {
     end = min(total, xcd * run + run), stride = grid / 8;
   }
   if (first >= end) return;
+  const Divisor by_grid(grid), by_expert(WG ? per_e : n_nt), by_column(WG ? GN * n_mt : 1);
   auto place = [&](int L) __attribute__((always_inline)) {  // L = round * grid + seat
-    return (L / grid) % 2 ? L - seat + (grid - 1 - seat) : L;
+    return by_grid.of(L) % 2 ? L - seat + (grid - 1 - seat) : L;
   };
 
   auto tile_of = [&](int L) __attribute__((always_inline)) -> Tile {
@@ -334,16 +349,16 @@ __device__ __forceinline__ void grad_body(const GradArgs &g) {
     int mt, nt;
     if constexpr (WG) {
       L = place(L);
-      const int turn = L / per_e;
-      tile_place(L - turn * per_e, n_mt, n_nt, mt, nt);
+      const int turn = by_expert.of(L);
+      tile_place(L - turn * per_e, by_column, n_mt, n_nt, mt, nt);
       t.e = uniform(s_unit[turn]);
       t.row0 = uniform(s_off[t.e]);
       t.rows = uniform(s_off[t.e + 1]) - t.row0;
       t.m0 = mt * BM;
     } else {
-      t.e = find_expert(s_unit, g.E, L / n_nt);
-      const int before = uniform(s_unit[t.e]);
-      tile_place(L - before * n_nt, uniform(s_unit[t.e + 1]) - before, n_nt, mt, nt);
+      t.e = find_expert(s_unit, g.E, by_expert.of(L));
+      const int before = uniform(s_unit[t.e]), n_mt = uniform(s_unit[t.e + 1]) - before;
+      tile_place(L - before * n_nt, Divisor(GN * n_mt), n_mt, n_nt, mt, nt);
       t.row0 = uniform(s_off[t.e]) + mt * BM;
       t.rows = min(BM, uniform(s_off[t.e + 1]) - t.row0);
       t.m0 = 0;
@@ -507,25 +522,28 @@ __device__ __forceinline__ void grad_body(const GradArgs &g) {
   auto wait_slice = [&](int w) __attribute__((always_inline)) {
     wait_pending<PER, NST, S - 2>(min(S - 2, z_in - 1 - w), w <= st_until);
   };
-  // Piece c of a lane's share of sub-tile (i, j): NV consecutive columns of its
-  // row.  For bf16 outputs register groups 2c and 2c + 1 hold 4
-  // of 8 + 8 columns each in lanes l and l + 32; exchanging the halves gives
-  // each lane 8 consecutive ones, a 16-byte piece.
+  // Piece c of a lane's share of sub-tile (i, j): a 16-byte chunk of NV consecutive
+  // columns of its row.  For bf16 outputs register groups 2c and 2c + 1 hold 4 of 8 + 8
+  // columns each in lanes l and l + 32; exchanging the halves gives each lane 8
+  // consecutive ones.
   constexpr int NV = 16 / (int)sizeof(Out);
-  auto piece = [&](int i, int j, int c, float (&v)[NV]) __attribute__((always_inline)) {
+  auto piece = [&](int i, int j, int c) __attribute__((always_inline)) -> u32x4_t {
+    u32x4_t o;
     if constexpr (PACK) {
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[i][j][8 * c + t]),
-                                                        __float_as_uint(acc[i][j][8 * c + 4 + t]),
-                                                        false, false);
-        v[t] = __uint_as_float(s[0]);
-        v[4 + t] = __uint_as_float(s[1]);
+      for (int t = 0; t < 2; ++t) {
+        const int r = 8 * c + 2 * t;
+        const auto s = __builtin_amdgcn_permlane32_swap(
+            pack_bf16x2(acc[i][j][r], acc[i][j][r + 1]),
+            pack_bf16x2(acc[i][j][r + 4], acc[i][j][r + 5]), false, false);
+        o[t] = s[0];
+        o[2 + t] = s[1];
       }
     } else {
 #pragma unroll
-      for (int t = 0; t < 4; ++t) v[t] = acc[i][j][4 * c + t];
+      for (int t = 0; t < 4; ++t) o[t] = __float_as_uint(acc[i][j][4 * c + t]);
     }
+    return o;
   };
   auto epilogue = [&](const Tile &t, int z) __attribute__((always_inline)) {
     // the expert's weights, or the tile's rows
@@ -534,9 +552,20 @@ __device__ __forceinline__ void grad_body(const GradArgs &g) {
     const __amdgpu_buffer_rsrc_t rc = __builtin_amdgcn_make_buffer_rsrc(
         reinterpret_cast<Out *>(g.C) + at, (short)0,
         (int)((uint32_t)min(rows, BM) * (uint32_t)g.N * (uint32_t)sizeof(Out)), kRsrcWord3);
+    // a chunk's offset is its row's and its columns'; either out of range (the sum
+    // saturates) takes it out of range
+    uint32_t at_col[TN][NPART];
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int c = 0; c < NPART; ++c) {
+        const int col = t.n0 + wn * (BN / WN) + j * 32 + (PACK ? 16 : 8) * c + NV * (lane >> 5);
+        at_col[j][c] = col < g.N ? (uint32_t)col * (uint32_t)sizeof(Out) : kOOB;
+      }
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
       const int m = wm * (BM / WM) + i * 32 + (lane & 31);
+      const uint32_t at_row = m < rows ? (uint32_t)m * (uint32_t)g.N * (uint32_t)sizeof(Out) : kOOB;
 #pragma unroll
       for (int j = 0; j < TN; ++j) {
         if constexpr (BIG) {
@@ -546,17 +575,10 @@ __device__ __forceinline__ void grad_body(const GradArgs &g) {
           asm volatile("" : "+a"(acc[i][j]));
         }
 #pragma unroll
-        for (int c = 0; c < NPART; ++c) {
-          const int col = t.n0 + wn * (BN / WN) + j * 32 + (PACK ? 16 : 8) * c + NV * (lane >> 5);
-          float v[NV];
-          piece(i, j, c, v);
-          const uint32_t off = m < rows && col < g.N
-                                   ? ((uint32_t)m * (uint32_t)g.N + (uint32_t)col) *
-                                         (uint32_t)sizeof(Out)
-                                   : kOOB;
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(i32x4_t, pack(v)), rc,
-                                                 (int)off, 0, 0);
-        }
+        for (int c = 0; c < NPART; ++c)
+          __builtin_amdgcn_raw_buffer_store_b128(
+              __builtin_bit_cast(i32x4_t, piece(i, j, c)), rc,
+              (int)__builtin_elementwise_add_sat(at_row, at_col[j][c]), 0, 0);
       }
     }
     st_until = z + S - 1 + (BIG ? 1 : 0);  // (four waves load a slice further ahead)
@@ -642,7 +664,7 @@ __device__ __forceinline__ void grad_body(const GradArgs &g) {
     //    barrier (after which no wave reads slot z % S again), then the first loads
     //    of slice z + S into that slot, the others in the last k-step.
     constexpr int NM = TM * TN, NF = TM + TN, NL = JA + JB;
-    constexpr int D0 = NL < NM - NF - 1 ? NL : NM - NF - 1;  // loads in k-step NKS - 2
+    constexpr int W0 = NF + 3, D0 = NL < NM - W0 - 1 ? NL : NM - W0 - 1;  // loads in k-step NKS - 2
     static_assert(!BIG || (JG <= NF && NL - D0 <= 2 * (NM - NF) && (S & (S - 1)) == 0), "room");
     Frag fa[2][TM], fb[2][TN];
     auto read = [&](int buf, const char *p, int ks, int f) __attribute__((always_inline)) {
@@ -661,41 +683,45 @@ __device__ __forceinline__ void grad_body(const GradArgs &g) {
 #pragma unroll
     for (int f = 0; f < NF; ++f) read(0, smem, 0, f);
     int z = 0;
+    // slice z; `begin`: the tile's first, whose first k-step starts from zeros
+    auto slice = [&](auto begin) __attribute__((always_inline)) {
+      const uint32_t slot = (uint32_t)z & (S - 1);
+      const char *here = smem + slot * STAGE;
+      const char *other = smem + ((uint32_t)(z + 1) & (S - 1)) * STAGE;
+      if (k_in == nk_in - 1) mask_tail();
+#pragma unroll
+      for (int ks = 0; ks < NKS; ++ks) {
+        const int nb = (ks + 1) & 1, nks = (ks + 1) % NKS;
+#pragma unroll
+        for (int m = 0; m < NM; ++m) {
+          const int i = m / TN, j = m % TN;
+          const f32x16_t c = decltype(begin)::value && ks == 0 ? f32x16_t{} : acc[i][j];
+          acc[i][j] = Mm::mma(fb[ks & 1][j], fa[ks & 1][i], c);
+          if (m < NF) read(nb, ks + 1 < NKS ? here : other, nks, m);
+          if (ks == 0 && m < JG) gather(m);
+          if (ks + 2 == NKS && m == W0) {
+            if (z + 1 <= st_until) wait_vm<vm_cap((S - 2) * PER + NST)>();
+            else wait_vm<vm_cap((S - 2) * PER)>();
+            bar();
+            next_idx();
+          }
+          if (ks + 2 == NKS && m > W0 && m <= W0 + D0) load(slot, m - W0 - 1);
+          if (ks + 1 == NKS && m >= NF) {
+#pragma unroll
+            for (int q = D0; q < NL; ++q)
+              if (NF + (q - D0) * (NM - NF) / max(NL - D0, 1) == m) load(slot, q);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      advance();
+      ++z;
+    };
 #pragma nounroll
     for (;;) {
-      zero_acc();
+      slice(std::true_type());
 #pragma nounroll
-      for (int k = 0; k < nk; ++k, ++z) {
-        const uint32_t slot = (uint32_t)z & (S - 1);
-        const char *here = smem + slot * STAGE;
-        const char *other = smem + ((uint32_t)(z + 1) & (S - 1)) * STAGE;
-        if (k_in == nk_in - 1) mask_tail();
-#pragma unroll
-        for (int ks = 0; ks < NKS; ++ks) {
-          const int nb = (ks + 1) & 1, nks = (ks + 1) % NKS;
-#pragma unroll
-          for (int m = 0; m < NM; ++m) {
-            const int i = m / TN, j = m % TN;
-            acc[i][j] = Mm::mma(fb[ks & 1][j], fa[ks & 1][i], acc[i][j]);
-            if (m < NF) read(nb, ks + 1 < NKS ? here : other, nks, m);
-            if (ks == 0 && m < JG) gather(m);
-            if (ks + 2 == NKS && m == NF) {
-              if (z + 1 <= st_until) wait_vm<vm_cap((S - 2) * PER + NST)>();
-              else wait_vm<vm_cap((S - 2) * PER)>();
-              bar();
-              next_idx();
-            }
-            if (ks + 2 == NKS && m > NF && m <= NF + D0) load(slot, m - NF - 1);
-            if (ks + 1 == NKS && m >= NF) {
-#pragma unroll
-              for (int q = D0; q < NL; ++q)
-                if (NF + (q - D0) * (NM - NF) / max(NL - D0, 1) == m) load(slot, q);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-          }
-        }
-        advance();
-      }
+      for (int k = 1; k < nk; ++k) slice(std::false_type());
       epilogue(cur, z - 1);
       L += stride;
       if (L >= end) break;
@@ -869,7 +895,7 @@ hipError_t launch(const GradArgs &g, int64_t tiles, hipStream_t s) {
   constexpr int LDS = S * RB * (BM + BN) + 2 * (kMaxExperts + 1) * 4 +
                       (GATHER ? WM * WN * (KIND == GRAD_WEIGHT ? 2 * S : 2) * 256 : 0);
   static_assert(LDS <= 160 * 1024, "LDS budget");
-  constexpr int per_cu = 160 * 1024 / LDS < 2 ? 1 : 2;
+  constexpr int fit = 160 * 1024 / LDS, per_cu = fit < 1 ? 1 : fit > 3 ? 3 : fit;
   int64_t grid = (int64_t)device_cus() * per_cu;
   if (grid > tiles) grid = tiles;
   grid = (grid + 7) / 8 * 8;  // whole XCD rounds; surplus workgroups get no tiles
