@@ -303,6 +303,72 @@ moe_status_t moe_experts_backward(const void *d_out, const void *x, const void *
                                   void *d_w2, float *d_topk_w, void *workspace, size_t ws_bytes,
                                   void *stream);
 
+/* ---- AdamW over many tensors -----------------------------------------------------
+ * One step of Adam with decoupled weight decay over any number of tensors in a few
+ * launches (one for every 32 tensors), in place, with t the step:
+ *
+ *   g = grad * coef,  coef = min(1, max_norm / (norm + 1e-6))  (1 without a norm)
+ *   m = beta1 m + (1 - beta1) g;   v = beta2 v + (1 - beta2) g^2
+ *   p = p - lr weight_decay p - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
+ *
+ * in fp32, each result rounded once.  state_bits 32: m and v are fp32 [n].  8: m
+ * and the square root r of v are e4m3 (the OCP 8-bit format, 1-4-3 bits without
+ * infinities) [n], with fp32 scales [ceil(n / 256)], one for each 256 consecutive
+ * elements: value = e4m3 * scale, scale = the block's largest magnitude / 448 (a block
+ * below 2^-100 is held as zeros).  An r above zero stays at least 2^-9 * scale.
+ * Zeroed states are a fresh start.  The moments of a gradient that is not finite are
+ * NaN (in 8 bits the whole block's), unless grad_norm keeps the step from happening.
+ *
+ * master: fp32 [n], or NULL.  With it the step is taken on master and p receives its
+ * rounding to nearest; without it on p itself.
+ *
+ * stochastic: 8-bit values, and p in bf16 without a master, are rounded up or down
+ * with probabilities in proportion (10 and 12 random bits) instead of to nearest.
+ * Small steps then add up where rounding to nearest loses them: 8-bit moments are not
+ * much use without it.  The random bits are a fixed hash of seed, t, the tensor's
+ * place in the list and the element's index, so a call gives the same bits every time.
+ *
+ * The descriptions are read during the call (host memory; free to change after it).
+ * p, grad, m, v, master and the scales 16-byte aligned; n below 2^36; n = 0 is
+ * allowed, with any pointers.  No two tensors of a call may overlap. */
+typedef struct {
+  void *p;
+  const void *grad;
+  void *m;
+  void *v;
+  float *m_scale;   /* state_bits 8 */
+  float *v_scale;   /* state_bits 8 */
+  float *master;    /* or NULL      */
+  int64_t n;
+  int32_t p_dtype;  /* moe_dtype_t  */
+  int32_t grad_dtype;
+} moe_adamw_tensor_t;
+typedef struct {
+  double lr;            /* finite, >= 0                                            */
+  double beta1, beta2;  /* in [0, 1)                                               */
+  double eps;           /* finite, >= 0                                            */
+  double weight_decay;  /* finite, >= 0                                            */
+  int64_t step;         /* t, 1 for the first step; below 2^31                     */
+  const int32_t *step_on_device;  /* t in device memory, read when the step runs (a
+                           captured graph can count it up), or NULL: step is taken */
+  const float *grad_norm;  /* norm over all gradients in device memory, or NULL; if it
+                           is not finite the step changes nothing                  */
+  double max_norm;      /* > 0, with grad_norm                                     */
+  int32_t state_bits;   /* 8 or 32                                                 */
+  int32_t stochastic;   /* 0 or 1                                                  */
+  uint32_t seed;
+} moe_adamw_t;
+moe_status_t moe_adamw(const moe_adamw_tensor_t *tensors, int32_t n_tensors,
+                       const moe_adamw_t *args, void *stream);
+
+/* moe_grad_norm: out [1] fp32, the square root of the sum of the squares of all grad
+ *   (of `tensors` only grad, n and grad_dtype are read), added up in a fixed order in
+ *   fp32 inside pieces of 32768 and in 64 bits over them; 0 for none.  workspace: at
+ *   least moe_grad_norm_workspace_bytes(...). */
+size_t moe_grad_norm_workspace_bytes(const moe_adamw_tensor_t *tensors, int32_t n_tensors);
+moe_status_t moe_grad_norm(const moe_adamw_tensor_t *tensors, int32_t n_tensors, float *out,
+                           void *workspace, size_t ws_bytes, void *stream);
+
 /* ---- Norms around a block ------------------------------------------------------
  * The RMS norms that a transformer puts around this layer, with the gate and
  * the residual sum, in one pass over the token rows:

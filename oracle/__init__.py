@@ -39,7 +39,8 @@ from .block import (block_norm, block_norm_grad, combine_weighted, combine_weigh
                     dispatch, rms_norm, topk_weight_grad)
 from .ffn import (activation, moe_ffn, moe_ffn_share, moe_ffn_sorted,
                   moe_ffn_weighted_input, split_gate_up)
-from .train import activation_grad, join_gate_up, moe_ffn_grad
+from .train import (activation_grad, adamw, block_scale, clip_coefficient, e4m3_values,
+                    join_gate_up, moe_ffn_grad)
 
 __all__ = [
     "RoutingRef", "route", "topk_select", "topk_softmax", "bitmatrix", "histogram",
@@ -49,5 +50,6 @@ __all__ = [
     "moe_ffn_weighted_input", "quantize_mxfp4", "dequantize_mxfp4", "e2m1_encode",
     "e2m1_decode", "dispatch", "combine_weighted", "combine_weighted_grad", "topk_weight_grad",
     "rms_norm", "block_norm", "block_norm_grad", "quantize_int4", "dequantize_int4",
-    "activation_grad", "join_gate_up", "moe_ffn_grad",
+    "activation_grad", "join_gate_up", "moe_ffn_grad", "adamw", "clip_coefficient",
+    "e4m3_values", "block_scale",
 ]

@@ -7,8 +7,8 @@ float64.
   training step saves them rounded); pinned by central differences of that loop
   in ``tests/test_oracle_train.py``.
 * ``adamw`` is the decoupled-weight-decay Adam step with bias correction;
-  ``to_8bit`` and ``from_8bit`` hold a moment as e4m3 values of blocks of 256
-  elements with a scale each.
+  ``e4m3_values`` and ``block_scale`` say what 8-bit moments can hold.  Pinned by
+  torch's optimizer and torch's float8 type.
 """
 from __future__ import annotations
 
@@ -64,3 +64,30 @@ def moe_ffn_grad(d_out, x, h, idx, w, row, w13, w2, act: str, layout: str = "pac
         d_w13[e] = dh.T @ x[tok]
         d_w2[e] = d.T @ (we * a)
     return {"d_x": d_x, "d_w13": d_w13, "d_w2": d_w2, "d_topk_w": d_w}
+
+
+def adamw(p, grad, m, v, *, lr, beta1, beta2, eps, weight_decay, step, coef=1.0):
+    """One step, all arrays float64: ``(p, m, v)`` after it."""
+    g = grad * coef
+    m = beta1 * m + (1.0 - beta1) * g
+    v = beta2 * v + (1.0 - beta2) * g * g
+    update = (m / (1.0 - beta1 ** step)) / (np.sqrt(v / (1.0 - beta2 ** step)) + eps)
+    return p - lr * weight_decay * p - lr * update, m, v
+
+
+def clip_coefficient(norm: float, max_norm: float) -> float:
+    return min(1.0, max_norm / (norm + 1e-6))
+
+
+def e4m3_values() -> np.ndarray:
+    """The values of the codes 0 .. 126 of the OCP e4m3 format (sign bit clear; 127 is
+    NaN): 4 exponent bits with bias 7, 3 mantissa bits, subnormals below 2^-6."""
+    code = np.arange(127)
+    ex, man = code >> 3, code & 7
+    return np.where(ex == 0, man / 8.0 * 2.0 ** -6, (1 + man / 8.0) * 2.0 ** (ex - 7.0))
+
+
+def block_scale(x: np.ndarray) -> np.ndarray:
+    """Scale of each block of 256 elements of the flat array x."""
+    top = np.abs(np.concatenate([x, np.zeros(-len(x) % BLOCK)])).reshape(-1, BLOCK).max(1)
+    return np.where(top >= 2.0 ** -100, top / TOP, 0.0)

@@ -72,7 +72,8 @@ __all__ = ["Routing", "MoeError", "Prepared", "moe_route", "moe_experts", "moe_e
            "moe_dispatch", "moe_combine_weighted", "moe_combine_weighted_backward",
            "moe_route_backward", "ExpertsGrads", "moe_experts_train", "moe_experts_backward",
            "prepare_experts_train", "prepare_experts_backward",
-           "moe_experts_backward_workspace_bytes", "prepare_dispatch", "prepare_combine_weighted",
+           "moe_experts_backward_workspace_bytes", "AdamWState", "moe_adamw_state", "moe_adamw",
+           "moe_grad_norm", "prepare_adamw", "prepare_grad_norm", "prepare_dispatch", "prepare_combine_weighted",
            "prepare_combine_weighted_backward", "prepare_route_backward", "BlockNorm",
            "BlockNormGrads", "moe_block_norm", "moe_block_norm_backward", "prepare_block_norm",
            "prepare_block_norm_backward", "moe_block_norm_workspace_bytes", "moe_block_forward",
@@ -1176,6 +1177,164 @@ def moe_experts_backward(d_out: torch.Tensor, x: torch.Tensor, h: torch.Tensor,
     moe_route_backward takes on to the logits (see moe.h)."""
     return _experts_backward(d_out, x, h, w13, w2, routing, act, layout, params, d_x, d_w13, d_w2,
                              d_topk_w, workspace, stream).run()
+
+
+# ------------------------------------------------- AdamW over many tensors
+
+_F8 = torch.float8_e4m3fn
+_ADAMW_BLOCK = 256  # elements that share a scale in 8-bit moments
+
+
+@dataclass
+class AdamWState:
+    """Moments of moe_adamw, one tensor per parameter and in its shape: fp32, or in
+    8 bits e4m3 values (``v`` then holds the square roots of the second moments) with
+    fp32 scales ``[ceil(numel / 256)]``; and the fp32 masters, if the step keeps any."""
+
+    m: list
+    v: list
+    m_scale: Optional[list] = None
+    v_scale: Optional[list] = None
+    master: Optional[list] = None  # entries may be None
+
+
+def moe_adamw_state(params, bits: int = 32, *, master: bool = False) -> AdamWState:
+    """State of a first step for ``params``: zero moments in 32 or 8 bits and, with
+    ``master``, fp32 copies of the bf16 parameters."""
+    params = list(params)
+    if bits not in (8, 32):
+        raise ValueError("bits must be 8 or 32")
+
+    def zeros(dtype):
+        return [torch.zeros(p.shape, dtype=dtype, device=p.device) for p in params]
+
+    def scales():
+        return [torch.zeros(-(-p.numel() // _ADAMW_BLOCK), dtype=torch.float32, device=p.device)
+                for p in params]
+    s = AdamWState(zeros(_F8), zeros(_F8), scales(), scales()) if bits == 8 \
+        else AdamWState(zeros(torch.float32), zeros(torch.float32))
+    if master:
+        s.master = [p.detach().float() if p.dtype == torch.bfloat16 else None for p in params]
+    return s
+
+
+def _grad_tensors(grads):
+    """Checks the gradients; returns (device, the C array)."""
+    if not grads:
+        raise ValueError("no gradients")
+    dev = _index(*grads)
+    ts = (N.MoeAdamwTensor * len(grads))()
+    for t, g in zip(ts, grads):
+        t.grad, t.n, t.grad_dtype = g.data_ptr(), g.numel(), _dt(g)
+    return dev, ts
+
+
+def _grad_norm(grads, out, workspace, stream) -> _Call:
+    grads = list(grads)
+    dev, ts = _grad_tensors(grads)
+    out = _output(out, grads[0], (1,), torch.float32, stream, "out")
+    need = N.load().moe_grad_norm_workspace_bytes(ts, len(ts))
+    if need == 0:
+        raise MoeError(N.MOE_ERR_SHAPE, "moe_grad_norm")
+    ws = _scratch(workspace, grads[0], need, stream)
+    args = (ts, len(ts), out.data_ptr(), ws.data_ptr(), _nbytes(ws), _raw_stream(dev, stream))
+    return _Call(dev, "moe_grad_norm", args, (ts, grads, ws, out), out)
+
+
+def prepare_grad_norm(grads, *, out: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None, stream=None) -> Prepared:
+    return _grad_norm(grads, out, workspace, stream).prepared()
+
+
+def moe_grad_norm(grads, *, out: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Square root of the sum of the squares of all elements of ``grads`` (fp32 or
+    bf16): an fp32 tensor ``[1]``, for the clipping of moe_adamw."""
+    return _grad_norm(grads, out, workspace, stream).run()
+
+
+def _adamw(params, grads, state, lr, step, betas, eps, weight_decay, grad_norm, max_norm, seed,
+           stream) -> _Call:
+    params, grads = list(params), list(grads)
+    count = len(params)
+    bits = 8 if state.m_scale is not None else 32
+    if (state.m_scale is None) != (state.v_scale is None):
+        raise ValueError("m_scale and v_scale go together")
+    lists = {"grads": grads, "m": state.m, "v": state.v}
+    if bits == 8:
+        lists["m_scale"], lists["v_scale"] = state.m_scale, state.v_scale
+    if state.master is not None:
+        lists["master"] = state.master
+    for name, ts in lists.items():
+        if len(ts) != count:
+            raise ValueError(f"{len(ts)} {name} for {count} parameters")
+    dev, ts = _grad_tensors(grads)
+    moment = _F8 if bits == 8 else torch.float32
+    spans = []
+    for i, (t, p, g) in enumerate(zip(ts, params, grads)):
+        n, shape = p.numel(), p.shape
+        if g.shape != shape:
+            raise ValueError(f"grads[{i}] must have the shape of params[{i}]")
+        _is(p, shape, p.dtype, dev, f"params[{i}]")
+        t.p, t.p_dtype = p.data_ptr(), _dt(p)
+        m, v = state.m[i], state.v[i]
+        _is(m, shape, moment, dev, f"m[{i}]")
+        _is(v, shape, moment, dev, f"v[{i}]")
+        t.m, t.v = m.data_ptr(), v.data_ptr()
+        mine = [p, m, v]
+        if bits == 8:
+            ms, vs = state.m_scale[i], state.v_scale[i]
+            blocks = (-(-n // _ADAMW_BLOCK),)
+            _is(ms, blocks, torch.float32, dev, f"m_scale[{i}]")
+            _is(vs, blocks, torch.float32, dev, f"v_scale[{i}]")
+            t.m_scale, t.v_scale = ms.data_ptr(), vs.data_ptr()
+            mine += [ms, vs]
+        if state.master is not None and state.master[i] is not None:
+            w = state.master[i]
+            _is(w, shape, torch.float32, dev, f"master[{i}]")
+            t.master = w.data_ptr()
+            mine.append(w)
+        if n:
+            spans += [(x.data_ptr(), x.data_ptr() + _nbytes(x)) for x in mine]
+            spans.append((g.data_ptr(), g.data_ptr() + _nbytes(g)))
+    spans.sort()
+    if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+        raise ValueError("parameters, gradients and state must not overlap")
+    if (grad_norm is None) != (max_norm is None):
+        raise ValueError("grad_norm and max_norm go together")
+    if grad_norm is not None:
+        _is(grad_norm, (1,), torch.float32, dev, "grad_norm")
+    on_device = isinstance(step, torch.Tensor)
+    if on_device:
+        _is(step, (1,), torch.int32, dev, "step")
+    c = N.MoeAdamw(lr, *betas, eps, weight_decay, 0 if on_device else step,
+                   step.data_ptr() if on_device else None, _ptr(grad_norm),
+                   0.0 if max_norm is None else max_norm, bits, int(seed is not None),
+                   0 if seed is None else seed & 0xFFFFFFFF)
+    args = (ts, count, ctypes.byref(c), _raw_stream(dev, stream))
+    return _Call(dev, "moe_adamw", args, (ts, c, params, grads, lists, grad_norm, step), None)
+
+
+def prepare_adamw(params, grads, state: AdamWState, *, lr: float, step,
+                  betas: tuple = (0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01,
+                  grad_norm: Optional[torch.Tensor] = None, max_norm: Optional[float] = None,
+                  seed: Optional[int] = None, stream=None) -> Prepared:
+    return _adamw(params, grads, state, lr, step, betas, eps, weight_decay, grad_norm, max_norm,
+                  seed, stream).prepared()
+
+
+def moe_adamw(params, grads, state: AdamWState, *, lr: float, step, betas: tuple = (0.9, 0.999),
+              eps: float = 1e-8, weight_decay: float = 0.01,
+              grad_norm: Optional[torch.Tensor] = None, max_norm: Optional[float] = None,
+              seed: Optional[int] = None, stream=None) -> None:
+    """One AdamW step over all ``params`` (fp32 or bf16) in place, from ``grads`` of
+    their shapes (fp32 or bf16).  ``step``: 1 for the first one, or an int32 tensor
+    ``[1]`` on the GPU that is read when the step runs.  ``grad_norm`` (from
+    moe_grad_norm) with ``max_norm`` clips, and a norm that is not finite skips the
+    step.  ``seed``: 8-bit moments, and bf16 parameters without a master, are rounded
+    stochastically (see moe.h)."""
+    _adamw(params, grads, state, lr, step, betas, eps, weight_decay, grad_norm, max_norm, seed,
+           stream).run()
 
 
 # ------------------------------------------------- norms around a block

@@ -6,8 +6,9 @@ import os
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe.so")
 
-c_i32, c_i64, c_u32, c_sz, c_vp, c_f = (ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32,
-                                        ctypes.c_size_t, ctypes.c_void_p, ctypes.c_float)
+c_i32, c_i64, c_u32, c_sz, c_vp, c_f, c_d = (ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32,
+                                             ctypes.c_size_t, ctypes.c_void_p, ctypes.c_float,
+                                             ctypes.c_double)
 
 # moe_status_t
 MOE_OK, MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_DTYPE = 0, -1, -2, -3
@@ -42,10 +43,24 @@ class MoeInt4Weights(ctypes.Structure):
     _fields_ = [("q", c_vp), ("scales", c_vp), ("zeros", c_vp)]
 
 
+class MoeAdamwTensor(ctypes.Structure):
+    _fields_ = [("p", c_vp), ("grad", c_vp), ("m", c_vp), ("v", c_vp), ("m_scale", c_vp),
+                ("v_scale", c_vp), ("master", c_vp), ("n", c_i64), ("p_dtype", c_i32),
+                ("grad_dtype", c_i32)]
+
+
+class MoeAdamw(ctypes.Structure):
+    _fields_ = [("lr", c_d), ("beta1", c_d), ("beta2", c_d), ("eps", c_d), ("weight_decay", c_d),
+                ("step", c_i64), ("step_on_device", c_vp), ("grad_norm", c_vp), ("max_norm", c_d),
+                ("state_bits", c_i32), ("stochastic", c_i32), ("seed", c_u32)]
+
+
 _P_ROUTING = ctypes.POINTER(MoeRouting)
 _P_INT4 = ctypes.POINTER(MoeInt4Weights)
 _P_NORM = ctypes.POINTER(MoeBlockNorm)
 _P_PARAMS = ctypes.POINTER(MoeActParams)
+_P_TENSORS = ctypes.POINTER(MoeAdamwTensor)
+_P_ADAMW = ctypes.POINTER(MoeAdamw)
 
 # name -> (restype, argtypes); every function include/moe.h declares
 SIGNATURES = {
@@ -97,6 +112,9 @@ SIGNATURES = {
     "moe_experts_backward": (c_i32, [c_vp, c_vp, c_vp, c_i32, c_i64, c_i32, c_vp, c_vp, c_i32,
                                      c_i32, c_i32, c_i32, c_i32, _P_PARAMS, _P_ROUTING, c_vp, c_vp,
                                      c_vp, c_vp, c_vp, c_sz, c_vp]),
+    "moe_adamw": (c_i32, [_P_TENSORS, c_i32, _P_ADAMW, c_vp]),
+    "moe_grad_norm_workspace_bytes": (c_sz, [_P_TENSORS, c_i32]),
+    "moe_grad_norm": (c_i32, [_P_TENSORS, c_i32, c_vp, c_vp, c_sz, c_vp]),
     "moe_block_norm_workspace_bytes": (c_sz, [c_i64, c_i32, c_i32]),
     "moe_block_norm": (c_i32, [c_vp, c_vp, c_i32, c_i64, c_i32, _P_NORM, c_vp, c_vp, c_vp, c_vp,
                                c_vp]),

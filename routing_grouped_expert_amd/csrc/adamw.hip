@@ -1,0 +1,408 @@
+// AdamW over many tensors at once, with moments in 32 or in 8 bits, and the norm over
+// all gradients that its clipping takes.
+//
+//   g = coef * grad,  coef = min(1, max_norm / (norm + 1e-6))
+//   m = b1 m + (1 - b1) g          v = b2 v + (1 - b2) g^2
+//   w = w (1 - lr decay) - c1 m / (c2 sqrt(v) + eps)
+//   c1 = lr / (1 - b1^t),  c2 = 1 / sqrt(1 - b2^t)
+//
+// Both are bound by memory: every value is read and written once.  The tensors of a
+// launch travel in its arguments (no table in device memory, so the call needs no
+// copy and can be captured); a workgroup takes a chunk of one tensor, a lane eight
+// consecutive elements, which are one 16-byte load of bf16 and two of fp32.
+//
+// 8-bit moments: blocks of 256 consecutive elements (half a wave) hold m and
+// r = sqrt(v) as e4m3 values with one fp32 scale, the block's largest magnitude /
+// 448.  r instead of v halves the range that eight bits have to span (the e4m3 values
+// reach down to 2^-18 of the largest: 2^-36 in v).  A step moves a second moment by
+// 0.1 % (b2 = 0.999) where e4m3 values lie 6 to 12 % apart: rounded to nearest most
+// would never move, so with a seed they are rounded up or down at random, in
+// proportion (10 random bits); so are bf16 weights without an fp32 master (12 bits).
+// The bits are a hash of the seed, the step, the tensor's place in the list and the
+// element's index: a call gives the same result every time.  A second moment above
+// zero never becomes zero (its weight's step would be divided by eps alone).
+#include <math.h>
+
+#include <type_traits>
+
+#include "rows.h"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256, kPer = 8;           // elements of a lane at a time
+constexpr int kStep = kThreads * kPer;            // of a workgroup
+constexpr int64_t kChunk = 4 * kStep;             // of a workgroup in all
+constexpr int kBlock = 256;                       // elements that share a scale
+constexpr int64_t kNormChunk = 32768;
+constexpr int kBatch = 32;                        // tensors of a launch
+
+struct Batch {
+  moe_adamw_tensor_t t[kBatch];
+  uint32_t first[kBatch + 1];  // chunks ahead of each tensor
+  int count, base;             // tensors; place of the first in the call's list
+};
+static_assert(sizeof(Batch) + 128 <= 4096, "launch arguments");
+
+struct Hyper {
+  float lr, beta1, beta2, one_beta1, one_beta2, eps, keep;  // keep = 1 - lr * decay
+  float c1, c2, log_beta1, log_beta2;  // c1, c2 of the host's step; logs for the device's
+  const int32_t *step_dev;
+  const float *norm;
+  float max_norm;
+  uint32_t seed, step;
+  int stochastic;
+};
+
+__device__ __forceinline__ uint32_t mix(uint32_t v) {
+  v = (v ^ (v >> 16)) * 0x7feb352du;
+  v = (v ^ (v >> 15)) * 0x846ca68bu;
+  return v ^ (v >> 16);
+}
+
+// Eight elements from index i; past n zeros.
+template <typename T> __device__ __forceinline__ void load8(const T *p, int64_t i, int64_t n, float (&f)[8]) {
+  if (i + 8 <= n) {
+    constexpr int C = 8 * (int)sizeof(T) / 16;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      float v[8 / C];
+      unpack(reinterpret_cast<const u32x4_t *>(p + i)[c], v);
+#pragma unroll
+      for (int q = 0; q < 8 / C; ++q) f[c * (8 / C) + q] = v[q];
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) f[q] = i + q < n ? to_f32(p[i + q]) : 0.f;
+  }
+}
+template <typename T> __device__ __forceinline__ void store8(T *p, int64_t i, int64_t n, const float (&f)[8]) {
+  if (i + 8 <= n) {
+    constexpr int C = 8 * (int)sizeof(T) / 16;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      float v[8 / C];
+#pragma unroll
+      for (int q = 0; q < 8 / C; ++q) v[q] = f[c * (8 / C) + q];
+      reinterpret_cast<u32x4_t *>(p + i)[c] = pack(v);
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (i + q < n) p[i + q] = from_f32<T>(f[q]);
+  }
+}
+
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+
+// Eight e4m3 values times their block's scale; past n zeros.
+__device__ __forceinline__ void load_e4m3(const uint8_t *p, int64_t i, int64_t n, float scale,
+                                          float (&f)[8]) {
+  u32x2_t w = {0u, 0u};
+  if (i + 8 <= n) {
+    w = *reinterpret_cast<const u32x2_t *>(p + i);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (i + q < n) w[q / 4] |= (uint32_t)p[i + q] << (8 * (q % 4));
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const f32x2_t lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[h], false);
+    const f32x2_t hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[h], true);
+    f[4 * h] = lo[0] * scale;
+    f[4 * h + 1] = lo[1] * scale;
+    f[4 * h + 2] = hi[0] * scale;
+    f[4 * h + 3] = hi[1] * scale;
+  }
+}
+
+// The largest of v over each half of the wave, in all its lanes.
+__device__ __forceinline__ uint32_t half_wave_max(uint32_t v) {
+#define MOE_MAX_ROR(n) \
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + n, 0xf, 0xf, false))
+  MOE_MAX_ROR(8);
+  MOE_MAX_ROR(4);
+  MOE_MAX_ROR(2);
+  MOE_MAX_ROR(1);
+#undef MOE_MAX_ROR
+  const auto s = __builtin_amdgcn_permlane16_swap(v, v, false, false);  // rows 0, 1 and 2, 3
+  return max(s[0], s[1]);
+}
+
+// Eight values as e4m3 and their block's scale.  `random`: ten bits of each element
+// from bit `shift`; nullptr: to nearest.  ROOT: values above zero stay above zero.
+// Values that are not finite make the scale NaN, and with it the whole block.
+template <bool ROOT>
+__device__ __forceinline__ void store_e4m3(uint8_t *p, float *scales, int64_t i, int64_t n,
+                                           const float (&f)[8], const uint32_t *random, int shift) {
+  constexpr float kTop = 448.f;
+  uint32_t top_bits = 0;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) top_bits = max(top_bits, __float_as_uint(f[q]) & 0x7fffffffu);
+  top_bits = half_wave_max(top_bits);
+  const float top = __uint_as_float(top_bits);
+  const bool live = top >= 0x1p-100f;  // (below it 448 / top overflows: held as zeros)
+  const float inverse = live ? kTop / top : 0.f;
+  u32x2_t w;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float u[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float x = f[4 * h + q];
+      float y = ROOT ? fminf(x * inverse, kTop) : __builtin_amdgcn_fmed3f(x * inverse, -kTop, kTop);
+      if (random) {
+        const uint32_t r = ((random[4 * h + q] >> shift & 1023u) << 10) | 512u;
+        y = __uint_as_float((__float_as_uint(y) + r) & 0xfff00000u);
+      }
+      if (ROOT) y = x > 0.f && live ? fmaxf(y, 0x1p-9f) : y;
+      u[q] = y;
+    }
+    int v = __builtin_amdgcn_cvt_pk_fp8_f32(u[0], u[1], 0, false);
+    w[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(u[2], u[3], v, true);
+  }
+  if (i + 8 <= n) {
+    *reinterpret_cast<u32x2_t *>(p + i) = w;
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (i + q < n) p[i + q] = (uint8_t)(w[q / 4] >> (8 * (q % 4)));
+  }
+  if (threadIdx.x % (kBlock / kPer) == 0 && i < n)
+    scales[i / kBlock] = top_bits >= 0x7f800000u ? __uint_as_float(0x7fc00000u)
+                         : live                  ? top * (1.f / kTop)
+                                                 : 0.f;
+}
+
+template <typename P, typename G, bool E8>
+__device__ __forceinline__ void update(const moe_adamw_tensor_t &t, int64_t begin, const Hyper &h,
+                                       float coef, float c1, float c2, uint32_t key) {
+  // each operation rounded for itself, as the formulas are written: a moment that is a
+  // hair off lands on the other side of a random rounding now and then, a whole e4m3
+  // step away
+#pragma clang fp contract(off)
+  P *p = reinterpret_cast<P *>(t.p);
+  const G *g = reinterpret_cast<const G *>(t.grad);
+  constexpr bool BF = std::is_same<P, bf16_t>::value;
+#pragma unroll 1
+  for (int64_t s = 0; s < kChunk; s += kStep) {
+    const int64_t i = begin + s + threadIdx.x * kPer;
+    if (begin + s >= t.n) return;
+    float w[8], gr[8], m[8], v[8];
+    load8(g, i, t.n, gr);
+    if (t.master) load8(t.master, i, t.n, w);
+    else load8(p, i, t.n, w);
+    if constexpr (E8) {
+      const bool in = i < t.n;
+      load_e4m3(reinterpret_cast<const uint8_t *>(t.m), i, t.n, in ? t.m_scale[i / kBlock] : 0.f, m);
+      load_e4m3(reinterpret_cast<const uint8_t *>(t.v), i, t.n, in ? t.v_scale[i / kBlock] : 0.f, v);
+    } else {
+      load8(reinterpret_cast<const float *>(t.m), i, t.n, m);
+      load8(reinterpret_cast<const float *>(t.v), i, t.n, v);
+    }
+    uint32_t random[8];
+    if (h.stochastic) {
+      const uint32_t k = key ^ mix((uint32_t)(i >> 32));
+#pragma unroll
+      for (int q = 0; q < 8; ++q) random[q] = mix((uint32_t)(i + q) ^ k);
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const float x = gr[q] * coef;
+      m[q] = m[q] * h.beta1 + x * h.one_beta1;
+      const float old = E8 ? v[q] * v[q] : v[q];
+      v[q] = old * h.beta2 + x * x * h.one_beta2;
+      const float root = sqrtf(v[q]);
+      w[q] = w[q] * h.keep - c1 * m[q] * __builtin_amdgcn_rcpf(root * c2 + h.eps);
+      if (E8) v[q] = root;
+    }
+    if constexpr (E8) {
+      store_e4m3<false>(reinterpret_cast<uint8_t *>(t.m), t.m_scale, i, t.n, m,
+                        h.stochastic ? random : nullptr, 0);
+      store_e4m3<true>(reinterpret_cast<uint8_t *>(t.v), t.v_scale, i, t.n, v,
+                       h.stochastic ? random : nullptr, 10);
+    } else {
+      store8(reinterpret_cast<float *>(t.m), i, t.n, m);
+      store8(reinterpret_cast<float *>(t.v), i, t.n, v);
+    }
+    if (t.master) {
+      store8(t.master, i, t.n, w);
+    } else if (BF && h.stochastic) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const uint32_t b = __float_as_uint(w[q]);
+        // (infinities and NaN stay)
+        if ((b & 0x7f800000u) != 0x7f800000u)
+          w[q] = __uint_as_float((b + ((random[q] >> 20 << 4) | 8u)) & 0xffff0000u);
+      }
+    }
+    store8(p, i, t.n, w);
+  }
+}
+
+// The tensor whose chunk this workgroup takes.
+__device__ __forceinline__ int tensor_of(const Batch &b) {
+  int lo = 0, hi = b.count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (b.first[mid] <= blockIdx.x) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+template <bool E8> __global__ __launch_bounds__(kThreads) void adamw_kernel(Batch b, Hyper h) {
+  const int at = tensor_of(b);
+  const moe_adamw_tensor_t &t = b.t[at];
+  float coef = 1.f, c1 = h.c1, c2 = h.c2;
+  uint32_t step = h.step;
+  if (h.norm) {
+    const float norm = *h.norm;
+    if (!(norm < __builtin_inff())) return;  // not finite: the step changes nothing
+    coef = (float)fmin(1.0, (double)h.max_norm / ((double)norm + 1e-6));
+  }
+  if (h.step_dev) {
+    const int32_t s = *h.step_dev;
+    step = (uint32_t)s;
+    c1 = h.lr / -expm1f((float)s * h.log_beta1);
+    c2 = 1.f / sqrtf(-expm1f((float)s * h.log_beta2));
+  }
+  const uint32_t key = mix(mix(h.seed + 0x9e3779b9u * (uint32_t)(b.base + at + 1)) ^ step);
+  const int64_t begin = (int64_t)(blockIdx.x - b.first[at]) * kChunk;
+  if (t.p_dtype == MOE_BF16) {
+    if (t.grad_dtype == MOE_BF16) update<bf16_t, bf16_t, E8>(t, begin, h, coef, c1, c2, key);
+    else update<bf16_t, float, E8>(t, begin, h, coef, c1, c2, key);
+  } else {
+    if (t.grad_dtype == MOE_BF16) update<float, bf16_t, E8>(t, begin, h, coef, c1, c2, key);
+    else update<float, float, E8>(t, begin, h, coef, c1, c2, key);
+  }
+}
+
+__device__ __forceinline__ float workgroup_sum(float v, float *s) {
+  v = wave_sum_f32(v);
+  if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
+  __syncthreads();
+  float sum = 0.f;
+  for (int w = 0; w < (int)blockDim.x / 64; ++w) sum += s[w];
+  return sum;
+}
+
+// Squares of a chunk, added up in fp32 (128 a lane in eight sums).
+template <typename G>
+__device__ __forceinline__ float squares(const G *g, int64_t begin, int64_t n) {
+  float acc[8] = {};
+  const int64_t end = begin + kNormChunk < n ? begin + kNormChunk : n;
+#pragma unroll 4
+  for (int64_t i = begin + threadIdx.x * kPer; i < end; i += kStep) {
+    float f[8];
+    load8(g, i, n, f);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) acc[q] += f[q] * f[q];
+  }
+  float s = 0.f;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) s += acc[q];
+  return s;
+}
+
+__global__ __launch_bounds__(kThreads) void norm_parts(Batch b, float *__restrict__ parts) {
+  __shared__ float s[kThreads / 64];
+  const int at = tensor_of(b);
+  const int64_t begin = (int64_t)(blockIdx.x - b.first[at]) * kNormChunk;
+  const moe_adamw_tensor_t &t = b.t[at];
+  const float v = t.grad_dtype == MOE_BF16
+                      ? squares(reinterpret_cast<const bf16_t *>(t.grad), begin, t.n)
+                      : squares(reinterpret_cast<const float *>(t.grad), begin, t.n);
+  const float sum = workgroup_sum(v, s);
+  if (threadIdx.x == 0) parts[blockIdx.x] = sum;
+}
+
+// The parts added up in 64 bits, in a fixed order.
+__global__ __launch_bounds__(1024) void norm_join(const float *__restrict__ parts, int64_t n,
+                                                  float *__restrict__ out) {
+  __shared__ double s[1024];
+  double v = 0.0;
+  for (int64_t i = threadIdx.x; i < n; i += 1024) v += (double)parts[i];
+  s[threadIdx.x] = v;
+  for (int d = 512; d > 0; d >>= 1) {
+    __syncthreads();
+    if ((int)threadIdx.x < d) s[threadIdx.x] += s[threadIdx.x + d];
+  }
+  if (threadIdx.x == 0) *out = (float)sqrt(s[0]);
+}
+
+// Launches `go(batch, chunks)` over the tensors that hold elements, up to kBatch (and
+// 2^31 - 1 threads' worth of chunks) at a time.
+template <typename F>
+hipError_t batches(const moe_adamw_tensor_t *t, int n, int64_t chunk, F &&go) {
+  Batch b;
+  int i = 0;
+  while (i < n) {
+    b.count = 0;
+    b.base = i;
+    b.first[0] = 0;
+    // (a batch is a run of the list, empty tensors included: places stay the list's)
+    while (i < n && b.count < kBatch) {
+      const int64_t chunks = (t[i].n + chunk - 1) / chunk;
+      if (b.count && (int64_t)b.first[b.count] + chunks > kMostChunks) break;
+      b.t[b.count] = t[i];
+      b.first[b.count + 1] = b.first[b.count] + (uint32_t)chunks;
+      ++b.count;
+      ++i;
+    }
+    if (b.first[b.count] == 0) continue;
+    const hipError_t err = go(b, b.first[b.count]);
+    if (err != hipSuccess) return err;
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+int64_t grad_norm_parts(const moe_adamw_tensor_t *t, int n) {
+  int64_t parts = 0;
+  for (int i = 0; i < n; ++i) parts += (t[i].n + kNormChunk - 1) / kNormChunk;
+  return parts;
+}
+
+hipError_t launch_grad_norm(const moe_adamw_tensor_t *t, int n, float *parts, float *out,
+                            hipStream_t s) {
+  int64_t done = 0;
+  const hipError_t err = batches(t, n, kNormChunk, [&](const Batch &b, uint32_t chunks) {
+    hipLaunchKernelGGL(norm_parts, dim3(chunks), dim3(kThreads), 0, s, b, parts + done);
+    done += chunks;
+    return hipGetLastError();
+  });
+  if (err != hipSuccess) return err;
+  hipLaunchKernelGGL(norm_join, dim3(1), dim3(1024), 0, s, parts, done, out);
+  return hipGetLastError();
+}
+
+hipError_t launch_adamw(const moe_adamw_tensor_t *t, int n, const moe_adamw_t &a, hipStream_t s) {
+  Hyper h;
+  h.lr = (float)a.lr;
+  h.beta1 = (float)a.beta1, h.one_beta1 = (float)(1.0 - a.beta1);
+  h.beta2 = (float)a.beta2, h.one_beta2 = (float)(1.0 - a.beta2);
+  h.eps = (float)a.eps;
+  h.keep = (float)(1.0 - a.lr * a.weight_decay);
+  h.log_beta1 = (float)log(a.beta1), h.log_beta2 = (float)log(a.beta2);
+  h.c1 = h.c2 = 0.f;
+  if (!a.step_on_device) {
+    h.c1 = (float)(a.lr / -expm1((double)a.step * log(a.beta1)));
+    h.c2 = (float)(1.0 / sqrt(-expm1((double)a.step * log(a.beta2))));
+  }
+  h.step_dev = a.step_on_device;
+  h.step = (uint32_t)a.step;
+  h.norm = a.grad_norm, h.max_norm = (float)a.max_norm;
+  h.seed = a.seed, h.stochastic = a.stochastic;
+  return batches(t, n, kChunk, [&](const Batch &b, uint32_t chunks) {
+    if (a.state_bits == 8)
+      hipLaunchKernelGGL(adamw_kernel<true>, dim3(chunks), dim3(kThreads), 0, s, b, h);
+    else
+      hipLaunchKernelGGL(adamw_kernel<false>, dim3(chunks), dim3(kThreads), 0, s, b, h);
+    return hipGetLastError();
+  });
+}
+
+}  // namespace moe

@@ -183,6 +183,27 @@ moe::BlockNormArgs block_norm_args(const void *x, const void *y, int64_t n, int3
   return g;
 }
 
+// The tensors of an optimizer call: `whole` with all that a step reads and writes,
+// else the gradients alone.
+moe_status_t check_tensors(const moe_adamw_tensor_t *t, int32_t n, bool whole, int32_t bits) {
+  if (n < 0) return MOE_ERR_SHAPE;
+  if (n > 0 && !t) return MOE_ERR_NULL;
+  for (int32_t i = 0; i < n; ++i) {
+    if (t[i].n < 0 || t[i].n > moe::kMostElements) return MOE_ERR_SHAPE;
+    if (!dtype_ok(t[i].grad_dtype) || (whole && !dtype_ok(t[i].p_dtype))) return MOE_ERR_DTYPE;
+    if (t[i].n == 0) continue;
+    if (!t[i].grad || (whole && (!t[i].p || !t[i].m || !t[i].v))) return MOE_ERR_NULL;
+    if (whole && bits == 8 && (!t[i].m_scale || !t[i].v_scale)) return MOE_ERR_NULL;
+    if (!aligned16(t[i].grad)) return MOE_ERR_ALIGN;
+    if (!whole) continue;
+    for (const void *p : {(const void *)t[i].p, (const void *)t[i].m, (const void *)t[i].v,
+                          (const void *)t[i].master})
+      if (!aligned16(p)) return MOE_ERR_ALIGN;
+    if (bits == 8 && (!aligned16(t[i].m_scale) || !aligned16(t[i].v_scale))) return MOE_ERR_ALIGN;
+  }
+  return MOE_OK;
+}
+
 moe_status_t check_ws(const void *ws, size_t have, size_t need) {
   if (need == 0) return MOE_OK;
   if (!ws) return MOE_ERR_WORKSPACE;
@@ -451,6 +472,44 @@ moe_status_t moe_experts_backward(const void *d_out, const void *x, const void *
   a.n_tokens = n_tokens, a.topk = topk, a.n_experts = n_experts;
   a.hidden = hidden, a.inter = inter, a.dtype = dtype, a.act = act, a.layout = layout;
   return moe::launch_experts_backward(a, s) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+moe_status_t moe_adamw(const moe_adamw_tensor_t *tensors, int32_t n_tensors,
+                       const moe_adamw_t *args, void *stream) {
+  if (!args) return MOE_ERR_NULL;
+  const moe_adamw_t &a = *args;
+  if (a.state_bits != 8 && a.state_bits != 32) return MOE_ERR_UNSUPPORTED;
+  if (a.stochastic != 0 && a.stochastic != 1) return MOE_ERR_UNSUPPORTED;
+  auto rate = [](double v) { return v >= 0.0 && isfinite((float)v); };  // (rejects NaN)
+  auto beta = [](double v) { return v >= 0.0 && (float)v < 1.f; };
+  if (!rate(a.lr) || !rate(a.eps) || !rate(a.weight_decay) || !rate(a.lr * a.weight_decay) ||
+      !beta(a.beta1) || !beta(a.beta2))
+    return MOE_ERR_SHAPE;
+  if (!a.step_on_device && (a.step < 1 || a.step > 0x7fffffff)) return MOE_ERR_SHAPE;
+  if (a.grad_norm && !(a.max_norm > 0.0 && isfinite((float)a.max_norm))) return MOE_ERR_SHAPE;
+  if (((uintptr_t)a.step_on_device | (uintptr_t)a.grad_norm) & 3u) return MOE_ERR_ALIGN;
+  const moe_status_t st = check_tensors(tensors, n_tensors, true, a.state_bits);
+  if (st != MOE_OK) return st;
+  return moe::launch_adamw(tensors, n_tensors, a, (hipStream_t)stream) == hipSuccess ? MOE_OK
+                                                                                     : MOE_ERR_HIP;
+}
+
+size_t moe_grad_norm_workspace_bytes(const moe_adamw_tensor_t *tensors, int32_t n_tensors) {
+  if (check_tensors(tensors, n_tensors, false, 0) != MOE_OK) return 0;
+  return align256((size_t)moe::grad_norm_parts(tensors, n_tensors) * sizeof(float)) + 256;
+}
+
+moe_status_t moe_grad_norm(const moe_adamw_tensor_t *tensors, int32_t n_tensors, float *out,
+                           void *workspace, size_t ws_bytes, void *stream) {
+  moe_status_t st = check_tensors(tensors, n_tensors, false, 0);
+  if (st != MOE_OK) return st;
+  if ((st = check_ptrs({out})) != MOE_OK) return st;
+  st = check_ws(workspace, ws_bytes, moe_grad_norm_workspace_bytes(tensors, n_tensors));
+  if (st != MOE_OK) return st;
+  return moe::launch_grad_norm(tensors, n_tensors, reinterpret_cast<float *>(workspace), out,
+                               (hipStream_t)stream) == hipSuccess
+             ? MOE_OK
+             : MOE_ERR_HIP;
 }
 
 moe_status_t moe_experts_w13(const void *x, moe_dtype_t dtype, int64_t n_tokens, int32_t hidden,

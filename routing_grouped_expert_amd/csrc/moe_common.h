@@ -171,6 +171,14 @@ hipError_t launch_activation(const void *h, void *act, const int32_t *offsets, i
                              moe_dtype_t dt, int64_t rows, int inter, moe_act_t kind,
                              moe_w13_layout_t layout, ActParams prm, hipStream_t s);
 
+// AdamW and the gradient norm (adamw.hip).  A launch takes at most kMostChunks
+// workgroups of 256 (a grid's threads are counted in 32 bits) of 8192 elements each.
+constexpr int64_t kMostChunks = (1 << 24) - 1, kMostElements = (int64_t(1) << 36) - 1;
+int64_t grad_norm_parts(const moe_adamw_tensor_t *t, int n);
+hipError_t launch_grad_norm(const moe_adamw_tensor_t *t, int n, float *parts, float *out,
+                            hipStream_t s);
+hipError_t launch_adamw(const moe_adamw_tensor_t *t, int n, const moe_adamw_t &a, hipStream_t s);
+
 // 4-bit weights with group scales (expert_int4.hip): codes [E, rows, K / 2],
 // bf16 scales and byte zero points (NULL: 8) [E, K / group, rows].
 struct Int4Weights {

@@ -1,7 +1,9 @@
 """The oracle's gradient of the expert FFN against central differences of its
-forward loop (CPU)."""
+forward loop, its AdamW step against torch's and its e4m3 values against torch's
+float8 type (CPU)."""
 import numpy as np
 import pytest
+import torch
 
 import oracle
 
@@ -65,3 +67,26 @@ def test_activation_gradient_at_the_limit_is_that_of_the_inside():
     g, u = np.array([2.0, 2.0, 3.0]), np.array([2.0, -2.0, 1.0])
     dg, du = oracle.activation_grad("silu", g, u, {"limit": 2.0})
     assert dg[0] != 0 and dg[2] == 0 and du[0] != 0 and du[1] != 0
+
+
+def test_adamw_is_torchs():
+    rng = np.random.default_rng(4)
+    hyper = {"lr": 3e-3, "beta1": 0.8, "beta2": 0.97, "eps": 1e-7, "weight_decay": 0.2}
+    p = rng.normal(size=50)
+    leaf = torch.tensor(p, requires_grad=True)
+    opt = torch.optim.AdamW([leaf], lr=hyper["lr"], betas=(hyper["beta1"], hyper["beta2"]),
+                            eps=hyper["eps"], weight_decay=hyper["weight_decay"])
+    m, v = np.zeros(50), np.zeros(50)
+    for step in range(1, 8):
+        g = rng.normal(size=50)
+        leaf.grad = torch.tensor(g)
+        opt.step()
+        p, m, v = oracle.adamw(p, g, m, v, step=step, **hyper)
+        # float64 on both sides, in another order of operations
+        assert np.allclose(p, leaf.detach().numpy(), rtol=1e-13, atol=1e-14)
+
+
+def test_e4m3_values_are_torchs():
+    codes = torch.arange(127, dtype=torch.uint8).view(torch.float8_e4m3fn)
+    assert np.array_equal(oracle.e4m3_values(), codes.double().numpy())
+    assert oracle.e4m3_values()[-1] == 448.0
