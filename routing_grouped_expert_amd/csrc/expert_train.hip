@@ -1,4 +1,5 @@
-// Gradient of the grouped expert FFN, MFMA on gfx950.
+// Training the grouped expert FFN, MFMA on gfx950: the forward product that keeps
+// what the gradient needs, and the gradient.
 //
 // With h[p] = W13[e] x[t], a[p] = act(h[p]) and out[t] = sum_p w[p] W2[e] a[p]
 // (p: sorted row, t: its token, e: its expert, w: its routing weight) and
@@ -20,6 +21,9 @@
 // all four rows, so two of them give the eight consecutive K of a lane's MFMA
 // fragment.  No transposed copy of a weight or an activation is ever written.
 // fp32 fragments are single elements and need no transposition.
+//
+// The forward product is that of the plain layer with h as a second output; it shares
+// the loop, with the weights' rows contiguous along K.
 //
 // Loads go straight into LDS (buffer_load ... lds) through an S-stage ring; rows
 // and columns outside an operand get an out-of-range offset, so the hardware
@@ -127,25 +131,38 @@ template <typename T, int RB, int COLS, int NW> struct ColTile {
 
 struct GradArgs {
   const void *A;                // data gradients: rows [.., K]; weight gradients: [rows, M]
-  const void *B;                // data gradients: weights [E, K, N]; weight gradients: [rows, N]
+  const void *B;                // data gradients: weights [E, K, N]; weight gradients: [rows, N];
+                                // forward: weights [E, N or 2 N, K]
   void *C;                      // [rows, N] / [E, M, N]
+  void *H;                      // forward with the activation: h [rows, N or 2 N]
   const int32_t *offsets;       // [E + 1]
   const int32_t *col_sorted;    // [rows]
   uint32_t a_bytes, b_bytes;    // buffer ranges (b_bytes: of one expert's weights)
   int E, K, M, N;
   uint32_t div_mul, div_shift;  // f / topk = (2 f * div_mul) >> (32 + div_shift)
   int64_t rows;                 // n_tokens * topk
+  int interleaved;              // forward: the row order of w13 and h
+  ActParams prm;
 };
 
 __device__ __forceinline__ uint32_t token_of(const GradArgs &g, uint32_t f) {
   return __umulhi(2 * f, g.div_mul) >> g.div_shift;
 }
 
-// Gradient kinds (GRAD_U: rows of u, kept in fp32), and whose rows are gathered: row
-// p of A (1) or B (2) is that of token col_sorted[p] / topk.
-enum { GRAD_U = 0, GRAD_ROWS = 1, GRAD_WEIGHT = 2 };
+// Products.  Gradients: rows of u (kept in fp32), rows of d_x, weights.  Forward: rows
+// of h and of their activation (gated, or ReLU^2).
+enum { GRAD_U, GRAD_ROWS, GRAD_WEIGHT, FWD_GATED, FWD_RELU2 };
+// Whose rows are gathered: row p of A (1) or B (2) is that of token col_sorted[p] / topk.
 // Activation kinds (pairs: interleaved w13 rows).
 enum { ACT_GATED = 0, ACT_RELU2 = 1, ACT_GATED_PAIRS = 2 };
+
+// The clamps of the gate from above and of the up value on both sides (NaN stays).
+__device__ __forceinline__ float clamp_gate(float g, const ActParams &p) {
+  return g > p.limit ? p.limit : g;
+}
+__device__ __forceinline__ float clamp_up(float v, const ActParams &p) {
+  return v > p.limit ? p.limit : v < -p.limit ? -p.limit : v;
+}
 
 // a, and the derivatives of a with respect to the gate and up products.
 template <int ACT>
@@ -158,8 +175,8 @@ __device__ __forceinline__ void act_grad(float g, float v, const ActParams &p, f
     dv = 0.f;
   } else {
     const bool gin = g <= p.limit, vin = fabsf(v) <= p.limit;
-    g = fminf(g, p.limit);
-    v = fminf(fmaxf(v, -p.limit), p.limit);
+    g = clamp_gate(g, p);
+    v = clamp_up(v, p);
     // the logistic function as 1 / (1 + 2^(-alpha log2(e) g)), as the forward pass
     const float ag = p.alpha * g;
     const float s =
@@ -266,13 +283,13 @@ __device__ __forceinline__ void expert_order(const GradArgs &g, int *s_order, in
 
 // ---- the kernel --------------------------------------------------------------------
 //
-// Tile of BM x BN outputs, WM x WN waves, S-stage ring.  Eight waves run the
-// ping-pong schedule: waves 0-3 and 4-7 (one of each a SIMD) alternate between a
-// memory phase (next slice's loads out, this slice's fragments into registers)
-// and an MFMA phase, one group a barrier behind the other.  Four waves read the
-// fragments of the next k-step while the current one multiplies; with 256-row
-// tiles (one wave a SIMD, 128 x 128 each) every memory instruction is placed
-// behind an MFMA by hand.
+// Tile of BM x BN outputs, WM x WN waves (four in all), S-stage ring of RB-byte slices.
+// Each wave reads the fragments of the next k-step while the current one multiplies; in
+// tiles of 192 rows and more (one wave a SIMD, up to 128 x 128 each) every memory
+// instruction is placed behind an MFMA by hand.  Two alternatives measured slower: eight
+// waves in two groups that take turns on memory and the matrix cores (64-expert training
+// batch 15.4 ms against 12.7), and two stages of 128 bytes instead of four of 64 (11.25
+// against 10.2: a gathered row's load has to travel for longer than one slice).
 //
 // The MFMA takes the N-side fragment first: lane l ends with output row l % 32 of
 // a 32 x 32 sub-tile and, in register group q, columns 8 q + 4 (l / 32) + [0, 4).
@@ -284,7 +301,10 @@ __device__ __forceinline__ void grad_body(const GradArgs &g) {
   constexpr int NW = WM * WN, BK = RB / (int)sizeof(T), NKS = BK / Mm::KS, ES = (int)sizeof(T);
   constexpr bool WG = KIND == GRAD_WEIGHT;
   using TA = typename std::conditional<WG, ColTile<T, RB, BM, NW>, RowTile<T, RB, BM, NW>>::type;
-  using TB = ColTile<T, RB, BN, NW>;
+  constexpr bool FWD = KIND == FWD_GATED || KIND == FWD_RELU2;
+  constexpr int SETS = KIND == FWD_GATED ? 2 : 1;  // weight rows of an output column
+  constexpr int BC = BN / SETS;                    // output columns of a tile
+  using TB = typename std::conditional<FWD, RowTile<T, RB, BN, NW>, ColTile<T, RB, BN, NW>>::type;
   constexpr int STAGE = TA::BYTES + TB::BYTES, JA = TA::J, JB = TB::J;
   constexpr bool GA = GATHER == 1, GB = GATHER == 2;
   constexpr int PER = JA + JB + (WG && GATHER);  // loads of a wave a slice
@@ -292,9 +312,9 @@ __device__ __forceinline__ void grad_body(const GradArgs &g) {
   using Out = typename std::conditional<KIND == GRAD_U, float, T>::type;
   constexpr bool PACK = std::is_same<Out, bf16_t>::value;
   constexpr int NPART = PACK ? 2 : 4;      // 16-byte pieces of a sub-tile row a lane
-  constexpr int NST = TM * TN * NPART;     // stores of a wave's epilogue (the waits count them)
-  constexpr bool PP = NW == 8;
-  constexpr bool BIG = NW == 4 && BM == 256;  // one wave a SIMD
+  // stores of a wave's epilogue (the waits count them)
+  constexpr int NST = TM * TN * NPART + (FWD ? TM * TN * NPART / SETS : 0);
+  constexpr bool BIG = NW == 4 && BM >= 192;  // one wave a SIMD
   static_assert(!BIG || (BF && NKS >= 2), "four-wave tiles");
   static_assert(TM * 32 * WM == BM && TN * 32 * WN == BN && S >= 2 && (S - 2) * PER < 64, "tile");
 
@@ -319,7 +339,7 @@ __device__ __forceinline__ void grad_body(const GradArgs &g) {
   // first, every other round in reverse, which evens out the workgroups' sums (a
   // skewed 64-expert layer: the longest 29 % over the mean in runs of equal K-slice
   // counts an XCD, 2 % dealt out).  An XCD's workgroups get neighbours in a round.
-  const int n_nt = (g.N + BN - 1) / BN, n_mt = WG ? (g.M + BM - 1) / BM : 0;
+  const int n_nt = (g.N + BC - 1) / BC, n_mt = WG ? (g.M + BM - 1) / BM : 0;
   const int per_e = n_mt * n_nt, grid = (int)gridDim.x, xcd = (int)blockIdx.x % 8;
   const int seat = xcd * (grid / 8) + (int)blockIdx.x / 8;
   int first, end, stride;
@@ -363,7 +383,7 @@ __device__ __forceinline__ void grad_body(const GradArgs &g) {
       t.rows = min(BM, uniform(s_off[t.e + 1]) - t.row0);
       t.m0 = 0;
     }
-    t.n0 = nt * BN;
+    t.n0 = nt * BC;
     return t;
   };
   auto slices = [&](const Tile &t) __attribute__((always_inline)) { return ((WG ? max(t.rows, 1) : g.K) + BK - 1) / BK; };
@@ -432,8 +452,14 @@ __device__ __forceinline__ void grad_body(const GradArgs &g) {
           (short)0, (int)g.b_bytes, kRsrcWord3);
 #pragma unroll
     for (int j = 0; j < JB; ++j) {
-      const int r = TB::line(wave, lane, j), c = in.n0 * ES + TB::byte(wave, lane, j);
-      const int row = WG ? in.row0 + r : r;
+      const int r = TB::line(wave, lane, j);
+      if constexpr (FWD) {  // a tile's gate rows, then the up rows of the same columns
+        const int set = r / BC, n = in.n0 + r % BC;
+        const int row = SETS == 1 ? n : g.interleaved ? 2 * n + set : set * g.N + n;
+        vb[j] = n < g.N ? (uint32_t)row * arow + (uint32_t)TB::byte(wave, lane, j) : kOOB;
+        continue;
+      }
+      const int c = in.n0 * ES + TB::byte(wave, lane, j), row = WG ? in.row0 + r : r;
       vb[j] = c < (int)brow ? (GB ? 0u : (uint32_t)row * brow) + (uint32_t)c : kOOB;
     }
     if constexpr (GA && !WG) {
@@ -453,7 +479,9 @@ __device__ __forceinline__ void grad_body(const GradArgs &g) {
     }
 #pragma unroll
     for (int j = 0; j < JB; ++j)
-      if (k0 + TB::line(wave, lane, j) >= (WG ? in.rows : g.K)) vb[j] = kOOB;
+      if (FWD ? k0 * ES + TB::byte(wave, lane, j) >= (int)arow
+              : k0 + TB::line(wave, lane, j) >= (WG ? in.rows : g.K))
+        vb[j] = kOOB;
   };
   // Offsets of the gathered rows in the next slice.  (An entry past an expert share's
   // rows is -1; its row is masked.)
@@ -475,7 +503,7 @@ __device__ __forceinline__ void grad_body(const GradArgs &g) {
   auto load_b = [&](uint32_t slot, int j) __attribute__((always_inline)) {
     const uint32_t lds = lds0 + slot * STAGE + TA::BYTES + (wave * JB + j) * 1024;
     if constexpr (GB) dma16a(rb, lds, ob[j], 0);
-    else dma16a(rb, lds, vb[j], (uint32_t)k_in * (BK * brow));
+    else dma16a(rb, lds, vb[j], (uint32_t)k_in * (FWD ? RB : BK * brow));
   };
   // On to the slice after this one, whose loads are out; past the last tile's every
   // offset is out of range.
@@ -545,7 +573,89 @@ __device__ __forceinline__ void grad_body(const GradArgs &g) {
     }
     return o;
   };
+  // h and the activation of a tile, the latter from the unrounded products.
+  auto epilogue_act = [&](const Tile &t) __attribute__((always_inline)) {
+    const uint32_t row_h = (uint32_t)(SETS * g.N) * ES, row_a = (uint32_t)g.N * ES;
+    const __amdgpu_buffer_rsrc_t rh = __builtin_amdgcn_make_buffer_rsrc(
+        reinterpret_cast<char *>(g.H) + (size_t)t.row0 * row_h, (short)0,
+        (int)((uint32_t)t.rows * row_h), kRsrcWord3);
+    const __amdgpu_buffer_rsrc_t rc = __builtin_amdgcn_make_buffer_rsrc(
+        reinterpret_cast<char *>(g.C) + (size_t)t.row0 * row_a, (short)0,
+        (int)((uint32_t)t.rows * row_a), kRsrcWord3);
+    const float nal = -g.prm.alpha * 1.44269504088896341f;
+    auto store = [&](__amdgpu_buffer_rsrc_t r, uint32_t row, uint32_t col, u32x4_t v)
+        __attribute__((always_inline)) {
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(i32x4_t, v), r,
+                                             (int)__builtin_elementwise_add_sat(row, col), 0, 0);
+    };
+    // a chunk of a lane: in fp32 a register group, in bf16 two with their halves
+    // exchanged between lanes l and l + 32 (see piece)
+    auto chunk = [&](const float (&v)[NV]) __attribute__((always_inline)) -> u32x4_t {
+      u32x4_t o = pack(v);
+      if constexpr (BF) {
+        const auto s0 = __builtin_amdgcn_permlane32_swap(o[0], o[2], false, false);
+        const auto s1 = __builtin_amdgcn_permlane32_swap(o[1], o[3], false, false);
+        o = u32x4_t{s0[0], s1[0], s0[1], s1[1]};
+      }
+      return o;
+    };
+    constexpr int UP = SETS == 2 ? TN / 2 : 0;  // the up product of gate product j is j + UP
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const int m = wm * (BM / WM) + i * 32 + (lane & 31);
+      const uint32_t at_h = m < t.rows ? (uint32_t)m * row_h : kOOB;
+      const uint32_t at_a = m < t.rows ? (uint32_t)m * row_a : kOOB;
+#pragma unroll
+      for (int j = 0; j < TN / SETS; ++j) {
+        if constexpr (BIG) {  // (see epilogue)
+          __builtin_amdgcn_sched_barrier(0);
+          asm volatile("" : "+a"(acc[i][j]));
+          if constexpr (SETS == 2) asm volatile("" : "+a"(acc[i][j + UP]));
+        }
+#pragma unroll
+        for (int c = 0; c < NPART; ++c) {
+          const int col0 = t.n0 + wn * (BC / WN) + j * 32 + (BF ? 16 : 8) * c;
+          const int col = col0 + NV * (lane >> 5);
+          const uint32_t at = col < g.N ? (uint32_t)(col * ES) : kOOB;
+          float gv[NV], uv[NV], av[NV];
+#pragma unroll
+          for (int q = 0; q < NV; ++q) {
+            gv[q] = acc[i][j][NV * c + q];
+            uv[q] = acc[i][j + UP][NV * c + q];
+            av[q] = SETS == 1 ? act_val<EPI_RELU2>(gv[q], gv[q], nal, g.prm)
+                              : act_val<EPI_GATED>(clamp_gate(gv[q], g.prm),
+                                                   clamp_up(uv[q], g.prm), nal, g.prm);
+          }
+          store(rc, at_a, at, chunk(av));
+          if (SETS == 2 && g.interleaved) {
+            // gate and up in turn: two chunks without an exchange, in bf16 one for each
+            // group of four columns, in fp32 two columns each
+#pragma unroll
+            for (int d = 0; d < 2; ++d) {
+              const int cd = BF ? col0 + 8 * d + 4 * (lane >> 5) : col + 2 * d;
+              float v[NV];
+#pragma unroll
+              for (int q = 0; q < NV / 2; ++q) {
+                v[2 * q] = gv[NV / 2 * d + q];
+                v[2 * q + 1] = uv[NV / 2 * d + q];
+              }
+              store(rh, at_h, cd < g.N ? (uint32_t)(cd * 2 * ES) : kOOB, pack(v));
+            }
+          } else {
+            store(rh, at_h, at, chunk(gv));
+            if constexpr (SETS == 2)
+              store(rh, at_h, __builtin_elementwise_add_sat(at, row_a), chunk(uv));
+          }
+        }
+      }
+    }
+  };
   auto epilogue = [&](const Tile &t, int z) __attribute__((always_inline)) {
+    if constexpr (FWD) {
+      epilogue_act(t);
+      st_until = z + S - 1 + (BIG ? 1 : 0);
+      return;
+    }
     // the expert's weights, or the tile's rows
     const int rows = WG ? g.M - t.m0 : t.rows;
     const size_t at = WG ? ((size_t)t.e * g.M + t.m0) * g.N : (size_t)t.row0 * g.N;
@@ -604,7 +714,10 @@ __device__ __forceinline__ void grad_body(const GradArgs &g) {
     return TA::frag(p, ks, wm * (BM / WM) + i * 32, lane);
   };
   auto frag_b = [&](const char *p, int ks, int j) __attribute__((always_inline)) {
-    return TB::frag(p + TA::BYTES, ks, wn * (BN / WN) + j * 32, lane);
+    // (two sets: the gate and the up rows of the wave's columns)
+    constexpr int each = TN / SETS;
+    const int c = j / each * BC + wn * (BC / WN) + j % each * 32;
+    return TB::frag(p + TA::BYTES, ks, c, lane);
   };
   auto bar = [&]() __attribute__((always_inline)) {  // workgroup barrier; MFMAs may cross it
     asm volatile("" ::: "memory");
@@ -619,42 +732,7 @@ __device__ __forceinline__ void grad_body(const GradArgs &g) {
     nk = slices(cur);
   };
 
-  if constexpr (PP) {
-    const int grp = wave >> 2;
-    Frag fa[NKS][TM], fb[NKS][TN];
-    wait_slice(0);
-    barrier();
-    if (grp) barrier();  // group 1 runs one phase behind group 0
-    for (int z = 0;; ++z) {
-      const bool done = kt + 1 == nk && L + stride >= end;
-      if (L_in < end) issue();
-      const char *p = smem + (z % S) * STAGE;
-#pragma unroll
-      for (int ks = 0; ks < NKS; ++ks) {
-#pragma unroll
-        for (int i = 0; i < TM; ++i) fa[ks][i] = frag_a(p, ks, i);
-#pragma unroll
-        for (int j = 0; j < TN; ++j) fb[ks][j] = frag_b(p, ks, j);
-      }
-      if (grp && !done) wait_slice(z + 1);
-      barrier();
-      __builtin_amdgcn_s_setprio(1);
-      if (kt == 0) zero_acc();
-#pragma unroll
-      for (int ks = 0; ks < NKS; ++ks)
-#pragma unroll
-        for (int i = 0; i < TM; ++i)
-#pragma unroll
-          for (int j = 0; j < TN; ++j) acc[i][j] = Mm::mma(fb[ks][j], fa[ks][i], acc[i][j]);
-      __builtin_amdgcn_s_setprio(0);
-      if (kt + 1 == nk) epilogue(cur, z);
-      if (!grp && !done) wait_slice(z + 1);
-      barrier();
-      if (done) break;
-      next();
-    }
-    if (!grp) barrier();
-  } else if constexpr (BIG) {
+  if constexpr (BIG) {
     // One wave a SIMD: nothing else fills the matrix core while this wave issues
     // other work, so each memory instruction follows an MFMA.  A k-step's first NF
     // MFMAs carry the reads of the next k-step's fragments, in the order in which
@@ -768,10 +846,10 @@ __global__ __launch_bounds__(64 * WM * WN) void grad_gemm(GradArgs g) {
 
 // The four-wave 256-row tiles: one wave a SIMD, which may then hold the whole
 // register file (256 accumulator registers for its 128 x 128 outputs).
-template <typename T, int KIND, int GATHER, int S, int RB>
+template <typename T, int KIND, int GATHER, int BM, int S, int RB>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void grad_gemm_w4(
     GradArgs g) {
-  grad_body<T, KIND, GATHER, 256, 256, 2, 2, S, RB>(g);
+  grad_body<T, KIND, GATHER, BM, 256, 2, 2, S, RB>(g);
 }
 
 // From u and the saved products: dh, w a and d_w, entry by entry (slot f of a token;
@@ -848,37 +926,6 @@ __global__ __launch_bounds__(256) void zero_kernel(u32x4_t *__restrict__ p, int6
     p[i] = u32x4_t{0u, 0u, 0u, 0u};
 }
 
-// Activation rows of the forward pass from its saved products: one 16-byte chunk
-// of act a thread.
-template <typename T, int ACT>
-__global__ __launch_bounds__(256) void activation_kernel(const T *__restrict__ h,
-                                                         T *__restrict__ act,
-                                                         const int32_t *__restrict__ offsets,
-                                                         int E, int inter,
-                                                         int64_t chunks, ActParams prm) {
-  constexpr int NV = 16 / (int)sizeof(T);
-  const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int nch = inter / NV;
-  if (idx >= chunks) return;
-  const int64_t p = idx / nch;
-  const int c = (int)(idx - p * nch);
-  if (p >= offsets[E]) return;
-  const u32x4_t *row = reinterpret_cast<const u32x4_t *>(h + p * (ACT == ACT_RELU2 ? 1 : 2) * inter);
-  float h0[NV], h1[NV], a[NV], dg, dv;
-  unpack(row[ACT == ACT_GATED_PAIRS ? 2 * c : c], h0);
-  if constexpr (ACT != ACT_RELU2) unpack(row[ACT == ACT_GATED_PAIRS ? 2 * c + 1 : nch + c], h1);
-#pragma unroll
-  for (int q = 0; q < NV; ++q) {
-    const bool low = q < NV / 2;
-    const float gate = ACT != ACT_GATED_PAIRS ? h0[q] : low ? h0[2 * q % NV] : h1[2 * q % NV];
-    const float up = ACT == ACT_RELU2 ? 0.f
-                     : ACT != ACT_GATED_PAIRS ? h1[q]
-                     : low ? h0[(2 * q + 1) % NV] : h1[(2 * q + 1) % NV];
-    act_grad<ACT>(gate, up, prm, a[q], dg, dv);
-  }
-  reinterpret_cast<u32x4_t *>(act + p * inter)[c] = pack(a);
-}
-
 // ---- launches ------------------------------------------------------------------------
 
 int device_cus() {
@@ -899,8 +946,8 @@ hipError_t launch(const GradArgs &g, int64_t tiles, hipStream_t s) {
   int64_t grid = (int64_t)device_cus() * per_cu;
   if (grid > tiles) grid = tiles;
   grid = (grid + 7) / 8 * 8;  // whole XCD rounds; surplus workgroups get no tiles
-  if constexpr (BM == 256 && WM * WN == 4)
-    hipLaunchKernelGGL((grad_gemm_w4<T, KIND, GATHER, S, RB>), dim3((unsigned)grid), dim3(256), 0, s,
+  if constexpr (BM >= 192 && WM * WN == 4)
+    hipLaunchKernelGGL((grad_gemm_w4<T, KIND, GATHER, BM, S, RB>), dim3((unsigned)grid), dim3(256), 0, s,
                        g);
   else
     hipLaunchKernelGGL((grad_gemm<T, KIND, GATHER, BM, BN, WM, WN, S, RB>), dim3((unsigned)grid),
@@ -910,42 +957,55 @@ hipError_t launch(const GradArgs &g, int64_t tiles, hipStream_t s) {
 
 inline int64_t cover(int64_t n, int64_t unit) { return (n + unit - 1) / unit; }
 
-// Data gradients: tiles of 256 rows where they cover the compute units, of 128
-// rows below that, and of 32 rows where experts hold fewer than 48 rows.
-template <typename T, int KIND, int GATHER>
-hipError_t launch_rows(const GradArgs &g, hipStream_t s) {
-  const int64_t cus = device_cus(), most = g.rows < g.E ? g.rows : g.E;
-  auto expected = [&](int bm, int bn) __attribute__((always_inline)) {
-    return (g.rows / bm + (most + 1) / 2) * cover(g.N, bn);
-  };
-  auto tiles = [&](int bm, int bn) __attribute__((always_inline)) { return (g.rows / bm + most) * cover(g.N, bn); };
-  if (g.rows < 48 * (int64_t)g.E || expected(128, 128) < cus / 2) {
-    return launch<T, KIND, GATHER, 32, 128, 1, 4, 4, 128>(g, tiles(32, 128), s);
-  }
-  if (expected(256, 256) >= cus) {
-    // (fp32 accumulates at a sixteenth of the rate: nothing to place by hand)
-    constexpr bool BF = std::is_same<T, bf16_t>::value;
-    constexpr int WM = BF ? 2 : 4, S = BF ? 4 : 2, RB = BF ? 64 : 128;
-    return launch<T, KIND, GATHER, 256, 256, WM, 2, S, RB>(g, tiles(256, 256), s);
-  }
-  return launch<T, KIND, GATHER, 128, 128, 2, 4, 3, 128>(g, tiles(128, 128), s);
+// Row tiles: how many of bm rows and bn output columns there can be, and are to be
+// expected (an expert's last row tile is half full on average).
+inline int64_t most_tiles(const GradArgs &g, int bm, int bn) {
+  return (g.rows / bm + (g.rows < g.E ? g.rows : g.E)) * cover(g.N, bn);
+}
+inline int64_t expected_tiles(const GradArgs &g, int bm, int bn) {
+  return (g.rows / bm + ((g.rows < g.E ? g.rows : g.E) + 1) / 2) * cover(g.N, bn);
+}
+// Experts with few rows (the weights are streamed), or too few tiles of 128 rows.
+inline bool few_rows(const GradArgs &g) {
+  return g.rows < 48 * (int64_t)g.E || expected_tiles(g, 128, 128) < device_cus() / 2;
 }
 
-// Weight gradients: 256 x 256 tiles where they cover the compute units.
-template <typename T, int GATHER> hipError_t launch_weights(const GradArgs &g, hipStream_t s) {
-  const int64_t big = g.E * cover(g.M, 256) * cover(g.N, 256);
+// Rows of u and of d_x: tiles of 256 rows where they cover the compute units, of 128
+// rows below that, and of 32 rows where experts hold few.  fp32, which multiplies at a
+// sixteenth of the rate, takes 128 rows throughout, in rings of two slices so that two
+// workgroups share a unit (1001 tokens x 6 of 40 experts, 712 x 1416: u 224 us with four
+// slices, 190 with two; d_x 413 us with 256 rows, 204 with 128).
+template <typename T, int KIND, int GATHER>
+hipError_t launch_rows(const GradArgs &g, hipStream_t s) {
   constexpr bool BF = std::is_same<T, bf16_t>::value;
-  constexpr int WM = BF ? 2 : 4, S = BF ? 4 : 2, RB = BF ? 64 : 128;
-  if (big >= device_cus())
-    return launch<T, GRAD_WEIGHT, GATHER, 256, 256, WM, 2, S, RB>(g, big, s);
-  return launch<T, GRAD_WEIGHT, GATHER, 128, 128, 2, 4, 3, 128>(
+  if (few_rows(g))
+    return launch<T, KIND, GATHER, 32, 128, 1, 4, 4, 128>(g, most_tiles(g, 32, 128), s);
+  if constexpr (BF) {
+    if (expected_tiles(g, 256, 256) >= device_cus())
+      return launch<T, KIND, GATHER, 256, 256, 2, 2, 4, 64>(g, most_tiles(g, 256, 256), s);
+  }
+  return launch<T, KIND, GATHER, 128, 128, 2, 2, BF ? 4 : 2, 128>(g, most_tiles(g, 128, 128), s);
+}
+
+// Weight gradients: tiles of 256 x 256 in bf16, where they cover half the compute units
+// (the 2816 x 512 weights of 8 experts, 176 tiles: 40 us with 128 x 128, 25 with these;
+// also with few rows an expert, where the writes count: 128 experts of 5760 x 2880 and
+// 128 rows, 1990 us with 128 x 128, 1500 with these).
+template <typename T, int GATHER> hipError_t launch_weights(const GradArgs &g, hipStream_t s) {
+  constexpr bool BF = std::is_same<T, bf16_t>::value;
+  if constexpr (BF) {
+    const int64_t big = g.E * cover(g.M, 256) * cover(g.N, 256);
+    if (big >= device_cus() / 2)
+      return launch<T, GRAD_WEIGHT, GATHER, 256, 256, 2, 2, 4, 64>(g, big, s);
+  }
+  return launch<T, GRAD_WEIGHT, GATHER, 128, 128, 2, 2, BF ? 4 : 2, 128>(
       g, g.E * cover(g.M, 128) * cover(g.N, 128), s);
 }
 
 inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 template <typename T>
-hipError_t run(const ExpertGradArgs &a, GradArgs g, hipStream_t s) {
+hipError_t run(const ExpertGradArgs &a, const GradArgs &g, hipStream_t s) {
   constexpr size_t ES = sizeof(T);
   const int rows13 = (a.act == MOE_ACT_RELU2 ? 1 : 2) * a.inter;
   const size_t m = (size_t)g.rows;
@@ -1012,24 +1072,57 @@ hipError_t launch_zero(void *p, size_t bytes, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_activation(const void *h, void *act, const int32_t *offsets, int n_experts,
-                             moe_dtype_t dt, int64_t rows, int inter, moe_act_t kind,
-                             moe_w13_layout_t layout, ActParams prm, hipStream_t s) {
-  const int64_t chunks = rows * (inter / (dt == MOE_BF16 ? 8 : 4));
-  auto go = [&](auto t, auto k) __attribute__((always_inline)) {
-    using T = decltype(t);
-    hipLaunchKernelGGL((activation_kernel<T, decltype(k)::value>),
-                       dim3((unsigned)cover(chunks, 256)), dim3(256), 0, s,
-                       reinterpret_cast<const T *>(h), reinterpret_cast<T *>(act), offsets,
-                       n_experts, inter, chunks, prm);
-    return hipGetLastError();
-  };
-  auto kinds = [&](auto t) {
-    if (kind == MOE_ACT_RELU2) return go(t, std::integral_constant<int, ACT_RELU2>());
-    if (layout == MOE_W13_INTERLEAVED) return go(t, std::integral_constant<int, ACT_GATED_PAIRS>());
-    return go(t, std::integral_constant<int, ACT_GATED>());
-  };
-  return dt == MOE_BF16 ? kinds(bf16_t()) : kinds(float());
+namespace {
+// Tiles as launch_rows takes them, gated ones with half the output columns; and in bf16
+// one of 192 rows where it holds most experts' rows at once (a gpt-oss-sized layer at
+// 4096 tokens, 128 rows an expert: 1126 -> 1081 us; the data gradients, which do nothing
+// but stream weights there, gain nothing by it: 957 and 977 us).
+template <typename T, int KIND> hipError_t forward_tiles(const GradArgs &g, hipStream_t s) {
+  constexpr int half = KIND == FWD_GATED ? 2 : 1, BIG = 256 / half, SMALL = 128 / half;
+  const int64_t cus = device_cus();
+  if (few_rows(g))  // (a wave needs the gate and the up product of a column)
+    return launch<T, KIND, 1, 32, 128, 1, 4 / half, 4, 128>(g, most_tiles(g, 32, SMALL), s);
+  if constexpr (std::is_same<T, bf16_t>::value) {
+    if (g.rows >= 96 * (int64_t)g.E && g.rows <= 176 * (int64_t)g.E &&
+        expected_tiles(g, 192, BIG) >= cus)
+      return launch<T, KIND, 1, 192, 256, 2, 2, 4, 64>(g, most_tiles(g, 192, BIG), s);
+    if (expected_tiles(g, 256, BIG) >= cus)
+      return launch<T, KIND, 1, 256, 256, 2, 2, 4, 64>(g, most_tiles(g, 256, BIG), s);
+  }
+  constexpr int S = std::is_same<T, bf16_t>::value ? 4 : 2;  // (see launch_rows)
+  return launch<T, KIND, 1, 128, 128, 2, 2, S, 128>(g, most_tiles(g, 128, SMALL), s);
+}
+
+template <typename T> hipError_t forward(const ExpertFwdArgs &a, GradArgs g, hipStream_t s) {
+  constexpr size_t ES = sizeof(T);
+  const int rows13 = (a.act == MOE_ACT_RELU2 ? 1 : 2) * a.inter;
+  g.A = a.x, g.a_bytes = (uint32_t)(a.n_tokens * a.hidden * ES), g.K = a.hidden;
+  g.B = a.w13, g.b_bytes = (uint32_t)((size_t)rows13 * a.hidden * ES);
+  g.N = a.inter, g.H = a.h, g.C = a.act_out;
+  if (a.act == MOE_ACT_RELU2) return forward_tiles<T, FWD_RELU2>(g, s);
+  return forward_tiles<T, FWD_GATED>(g, s);
+}
+
+GradArgs common_args(const moe_routing_t *r, int n_experts, int64_t n_tokens, int topk) {
+  GradArgs g{};
+  g.offsets = r->offsets;
+  g.col_sorted = r->col_sorted;
+  g.E = n_experts;
+  g.rows = n_tokens * topk;
+  // exact for f below 2^31: mul = ceil(2^(31 + l) / topk), 2^l >= topk
+  int l = 0;
+  while ((1 << l) < topk) ++l;
+  g.div_shift = l;
+  g.div_mul = (uint32_t)(((1ull << (31 + l)) + topk - 1) / topk);
+  return g;
+}
+}  // namespace
+
+hipError_t launch_experts_forward(const ExpertFwdArgs &a, hipStream_t s) {
+  GradArgs g = common_args(a.routing, a.n_experts, a.n_tokens, a.topk);
+  g.interleaved = a.layout == MOE_W13_INTERLEAVED;
+  g.prm = a.prm;
+  return a.dtype == MOE_BF16 ? forward<bf16_t>(a, g, s) : forward<float>(a, g, s);
 }
 
 size_t experts_backward_scratch_bytes(int64_t n_tokens, int topk, int hidden, int inter,
@@ -1041,16 +1134,7 @@ size_t experts_backward_scratch_bytes(int64_t n_tokens, int topk, int hidden, in
 }
 
 hipError_t launch_experts_backward(const ExpertGradArgs &a, hipStream_t s) {
-  GradArgs g{};
-  g.offsets = a.routing->offsets;
-  g.col_sorted = a.routing->col_sorted;
-  g.E = a.n_experts;
-  g.rows = a.n_tokens * a.topk;
-  // exact for f below 2^31: mul = ceil(2^(31 + l) / topk), 2^l >= topk
-  int l = 0;
-  while ((1 << l) < a.topk) ++l;
-  g.div_shift = l;
-  g.div_mul = (uint32_t)(((1ull << (31 + l)) + a.topk - 1) / a.topk);
+  const GradArgs g = common_args(a.routing, a.n_experts, a.n_tokens, a.topk);
   return a.dtype == MOE_BF16 ? run<bf16_t>(a, g, s) : run<float>(a, g, s);
 }
 

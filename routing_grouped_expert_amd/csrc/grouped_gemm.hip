@@ -1422,18 +1422,6 @@ hipError_t launch_gemm1(const void *x, const void *w13, void *act_out, const int
                  : launch_t<float, 2, EPI_GATED>(a, M, n_experts, s);
 }
 
-hipError_t launch_gemm1_rows(const void *x, const void *w13, void *h, const int32_t *offsets,
-                             const int32_t *col_sorted, moe_dtype_t dt, int64_t n_tokens, int topk,
-                             int n_experts, int hidden, int rows13, hipStream_t s) {
-  const int64_t M = n_tokens * topk;
-  const size_t es = dt == MOE_BF16 ? 2 : 4;
-  GemmArgs a{x, w13, h, offsets, col_sorted, nullptr, (uint32_t)(n_tokens * hidden * es),
-             (uint32_t)(M * rows13 * es), 0, n_experts, hidden, rows13, topk, 1, 0, 0,
-             ActParams{1.f, 0.f, 0.f}};
-  return dt == MOE_BF16 ? launch_t<bf16_t, 1, EPI_Y>(a, M, n_experts, s)
-                        : launch_t<float, 1, EPI_Y>(a, M, n_experts, s);
-}
-
 hipError_t launch_gemm2(const void *act_in, const void *w2, void *y, const int32_t *offsets,
                         const int32_t *col_sorted, const void *gate_scal, moe_dtype_t gate_dt,
                         moe_dtype_t dt, int64_t n_tokens, int topk, int n_experts, int hidden,

@@ -420,11 +420,13 @@ moe_status_t moe_experts_train(const void *x, moe_dtype_t dtype, int64_t n_token
   // workspace as run_experts
   void *y = reinterpret_cast<char *>(workspace) +
             align256((size_t)n_tokens * topk * inter * dsize(dtype));
-  const int32_t rows13 = (act == MOE_ACT_RELU2 ? 1 : 2) * inter;
-  if (moe::launch_gemm1_rows(x, w13, h, routing->offsets, routing->col_sorted, dtype, n_tokens,
-                             topk, n_experts, hidden, rows13, s) != hipSuccess ||
-      moe::launch_activation(h, workspace, routing->offsets, n_experts, dtype, n_tokens * topk,
-                             inter, act, layout, prm, s) != hipSuccess ||
+  moe::ExpertFwdArgs a{};
+  a.x = x, a.w13 = w13, a.h = h, a.act_out = workspace, a.routing = routing;
+  a.n_tokens = n_tokens, a.topk = topk, a.n_experts = n_experts;
+  a.hidden = hidden, a.inter = inter, a.dtype = dtype, a.act = act, a.layout = layout;
+  a.prm = prm;
+  // (with one slot a token a share may leave tokens out: their rows are zeroed)
+  if (moe::launch_experts_forward(a, s) != hipSuccess ||
       run_w2(workspace, dtype, n_tokens, hidden, w2, n_experts, inter, topk, routing, out, y, s,
              true) != hipSuccess)
     return MOE_ERR_HIP;

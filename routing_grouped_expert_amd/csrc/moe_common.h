@@ -84,10 +84,6 @@ hipError_t launch_gemm1(const void *x, const void *w13, void *act_out, const int
                         int n_experts, int hidden, int inter, moe_act_t act,
                         moe_w13_layout_t layout, ActParams p, hipStream_t s,
                         bool sorted_rows = false, const uint8_t *w13_scale = nullptr);
-// The products of GEMM1 ahead of the activation: h[M, rows13] = xs . W13[e]^T.
-hipError_t launch_gemm1_rows(const void *x, const void *w13, void *h, const int32_t *offsets,
-                             const int32_t *col_sorted, moe_dtype_t dt, int64_t n_tokens, int topk,
-                             int n_experts, int hidden, int rows13, hipStream_t s);
 // GEMM2: y = gate_scal[p] * (a[p] . W2[e]^T) (gate_scal NULL: weight 1); stored
 // to y_sorted[M, hidden], or (topk == 1) straight to out[token(p)].
 hipError_t launch_gemm2(const void *act_in, const void *w2, void *y, const int32_t *offsets,
@@ -145,7 +141,22 @@ hipError_t launch_route_backward(const float *d_topk_w, const int32_t *topk_idx,
                                  const void *topk_w, void *d_logits, moe_dtype_t w_dt,
                                  int64_t n_tokens, int n_experts, int topk, hipStream_t s);
 
-// Gradient of the expert FFN (expert_grad.hip): d_x [n_tokens, hidden], d_w13 and
+// Training the expert FFN (expert_train.hip).  Forward: h [n_tokens * topk, rows of
+// w13], the products W13[e] x[t] of the sorted rows, and act_out [n_tokens * topk,
+// inter], their activation.
+struct ExpertFwdArgs {
+  const void *x, *w13;
+  void *h, *act_out;
+  const moe_routing_t *routing;
+  int64_t n_tokens;
+  int topk, n_experts, hidden, inter;
+  moe_dtype_t dtype;
+  moe_act_t act;
+  moe_w13_layout_t layout;
+  ActParams prm;
+};
+hipError_t launch_experts_forward(const ExpertFwdArgs &a, hipStream_t s);
+// Gradient: d_x [n_tokens, hidden], d_w13 and
 // d_w2 as the weights, d_topk_w [n_tokens, topk], from d_out, x, the w13 products
 // h [n_tokens * topk, rows of w13] and the weights.
 struct ExpertGradArgs {
@@ -166,10 +177,6 @@ size_t experts_backward_scratch_bytes(int64_t n_tokens, int topk, int hidden, in
 hipError_t launch_experts_backward(const ExpertGradArgs &a, hipStream_t s);
 // `bytes` (a multiple of 16) of zeros.
 hipError_t launch_zero(void *p, size_t bytes, hipStream_t s);
-// act[p] = act(h[p]) of the routed rows p < offsets[n_experts].
-hipError_t launch_activation(const void *h, void *act, const int32_t *offsets, int n_experts,
-                             moe_dtype_t dt, int64_t rows, int inter, moe_act_t kind,
-                             moe_w13_layout_t layout, ActParams prm, hipStream_t s);
 
 // AdamW and the gradient norm (adamw.hip).  A launch takes at most kMostChunks
 // workgroups of 256 (a grid's threads are counted in 32 bits) of 8192 elements each.
