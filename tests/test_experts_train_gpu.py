@@ -162,3 +162,195 @@ def test_forward_and_gradient(case):
                                             3e-2 + 3e-2 * scale)
     got = moe_experts_backward(dg, xg, h, w13g, w2g, r, act, layout, params)
     check_gradient(got, dn, xn, _np(h), idx, w, row, w13n, w2n, act, layout, params, u)
+
+
+def _layer_on_gpu(case, **kw):
+    r, x, d, w13, w2, idx, row = layer(*case, **kw)
+    return r, idx, row, [t.to(DEV) for t in (x, d, w13, w2)]
+
+
+SMALL = (33, 128, 72, 6, 3, "bf16", "f32", "swiglu_oai", "interleaved", OAI, 0.5)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("k,share", [(3, (2, 3)), (3, (5, 1)), (1, (1, 2)), (6, (0, 2))])
+def test_expert_share(dtype, k, share):
+    case = (70, 136, 72, 6, k, dtype, "f32", "silu", "packed", {}, 0.5)
+    r, idx, row, (x, d, w13, w2) = _layer_on_gpu(case, share=share)
+    n, hidden = x.shape
+    routed = int(r.offsets[-1])
+    fill = torch.full((n * k, w13.shape[1]), 7.0, dtype=x.dtype, device=DEV)
+    out, h = moe_experts_train(x, w13, w2, r, "silu", h=fill.clone())
+    assert torch.equal(h[routed:], fill[routed:])  # rows past the routed ones stay
+    ref = oracle.moe_ffn(_np(x), idx, _np(r.topk_w), _np(w13), _np(w2), "silu")
+    assert np.abs(_np(out) - ref).max() <= (1e-4 if dtype == "f32" else 6e-2) * np.abs(ref).max()
+    assert not out[torch.from_numpy((idx < 0).all(1)).to(DEV)].any()
+    h[routed:] = float("nan")  # and are not read
+    got = moe_experts_backward(d, x, h, w13, w2, r, "silu")
+    hn = np.nan_to_num(_np(h))
+    check_gradient(got, _np(d), _np(x), hn, idx, _np(r.topk_w), row, _np(w13), _np(w2), "silu",
+                   "packed", {}, torch.finfo(DT[dtype]).eps / 2)
+    assert not got.d_topk_w[torch.from_numpy(idx < 0).to(DEV)].any()
+
+
+def test_experts_without_rows_get_zeros_and_no_tokens_give_zeros():
+    case = (3, 64, 40, 32, 2, "bf16", "bf16", "silu", "packed", {}, 1.5)
+    r, idx, row, (x, d, w13, w2) = _layer_on_gpu(case)
+    out, h = moe_experts_train(x, w13, w2, r, "silu")
+    dirty = [torch.full_like(w, float("nan")) for w in (w13, w2)]
+    got = moe_experts_backward(d, x, h, w13, w2, r, "silu", d_w13=dirty[0], d_w2=dirty[1])
+    unused = [e for e in range(32) if e not in set(idx.reshape(-1).tolist())]
+    assert unused and not got.d_w13[unused].any() and not got.d_w2[unused].any()
+    assert torch.isfinite(got.d_w13).all() and torch.isfinite(got.d_w2).all()
+    empty = Routing.empty(0, 32, 2, torch.bfloat16, DEV)
+    x0, h0 = x[:0], h[:0]
+    out, h = moe_experts_train(x0, w13, w2, empty, "silu")
+    assert tuple(out.shape) == (0, 64) and tuple(h.shape) == (0, 80)
+    got = moe_experts_backward(x0, x0, h0, w13, w2, empty, "silu",
+                               d_w13=torch.full_like(w13, 3.0), d_w2=torch.full_like(w2, 3.0))
+    assert not got.d_w13.any() and not got.d_w2.any() and got.d_x.numel() == 0
+
+
+def test_infinities_and_nan_stay_with_their_token_and_its_experts():
+    case = (64, 128, 72, 16, 2, "bf16", "bf16", "silu", "packed", {}, None)
+    r, idx, row, (x, d, w13, w2) = _layer_on_gpu(case)
+    clean_out, h = moe_experts_train(x, w13, w2, r, "silu")
+    clean = moe_experts_backward(d, x, h, w13, w2, r, "silu")
+    x2, d2 = x.clone(), d.clone()
+    x2[5, 3], x2[9, 1], d2[21, 7] = float("nan"), float("inf"), float("-inf")
+    out, h2 = moe_experts_train(x2, w13, w2, r, "silu")
+    bad = [5, 9]
+    rest = [t for t in range(64) if t not in bad]
+    assert torch.equal(out[rest], clean_out[rest]) and not torch.isfinite(out[bad]).all(1).any()
+    got = moe_experts_backward(d2, x2, h2, w13, w2, r, "silu")
+    rest = [t for t in range(64) if t not in (5, 9, 21)]
+    assert torch.equal(got.d_x[rest], clean.d_x[rest])
+    assert torch.equal(got.d_topk_w[rest], clean.d_topk_w[rest])
+    touched = set(idx[[5, 9, 21]].reshape(-1).tolist())
+    keep = [e for e in range(16) if e not in touched]
+    assert keep and torch.equal(got.d_w13[keep], clean.d_w13[keep])
+    assert torch.equal(got.d_w2[keep], clean.d_w2[keep])
+
+
+def test_clamp_borders():
+    """Products exactly at the limit pass a gradient, those beyond pass none."""
+    case = (4, 8, 8, 1, 1, "f32", "f32", "swiglu_oai", "interleaved", {}, None)
+    r, idx, row, (x, d, w13, w2) = _layer_on_gpu(case)
+    params = {"alpha": 1.25, "beta": 0.5, "limit": 2.0}
+    h = torch.tensor([[2.0, 2.0, 2.0, -2.0, 2.25, 1.0, 1.0, 2.25, -50.0, -2.25, 0.0, 0.0,
+                       -2.0, 0.5, 100.0, -100.0]] * 4, device=DEV)
+    got = moe_experts_backward(d, x, h, w13, w2, r, "swiglu_oai", "interleaved", params)
+    check_gradient(got, _np(d), _np(x), _np(h), idx, _np(r.topk_w), row, _np(w13), _np(w2),
+                   "swiglu_oai", "interleaved", params, U32)
+
+
+def test_gradient_of_the_call_itself_by_differences():
+    """moe_experts_backward against central differences of moe_experts_train (fp32)."""
+    case = (5, 16, 8, 3, 2, "f32", "f32", "silu", "packed", {}, None)
+    r, idx, row, (x, d, w13, w2) = _layer_on_gpu(case)
+    _, h = moe_experts_train(x, w13, w2, r, "silu")
+    got = moe_experts_backward(d, x, h, w13, w2, r, "silu")
+
+    def total():
+        return float((moe_experts_train(x, w13, w2, r, "silu")[0].double() * d.double()).sum())
+    g = torch.Generator().manual_seed(3)
+    for t, grad in ((x, got.d_x), (w13, got.d_w13), (w2, got.d_w2)):
+        v = torch.randn(t.shape, generator=g).to(DEV)
+        step = 2.0 ** -7
+        keep = t.clone()
+        t.copy_(keep + step * v)
+        up = total()
+        t.copy_(keep - step * v)
+        down = total()
+        t.copy_(keep)
+        want = float((grad.double() * v.double()).sum())
+        # truncation: step^2 / 6 of third derivatives of O(|v|^3); rounding: 2^-24 of sums of
+        # O(100) over the step
+        assert abs((up - down) / (2 * step) - want) <= 2e-2 * max(1.0, abs(want))
+
+
+@pytest.mark.parametrize("case", [SMALL, (600, 520, 392, 2, 2, "bf16", "bf16", "silu", "packed",
+                                          {}, None)], ids=["small", "medium"])
+def test_the_same_bits_prepared_on_another_stream_and_replayed(case):
+    act, layout, params = case[7:10]
+    r, idx, row, (x, d, w13, w2) = _layer_on_gpu(case)
+    n, hidden = x.shape
+    k, inter = r.topk, w2.shape[2]
+    out, h = moe_experts_train(x, w13, w2, r, act, layout, params)
+    want = moe_experts_backward(d, x, h, w13, w2, r, act, layout, params)
+
+    def same(a, b):
+        assert torch.equal(a[0], out) and torch.equal(a[1], h)
+        for f in ("d_x", "d_w13", "d_w2", "d_topk_w"):
+            assert torch.equal(getattr(b, f), getattr(want, f)), f
+    fwd = prepare_experts_train(x, w13, w2, r, act, layout, params)
+    bwd = prepare_experts_backward(d, x, h, w13, w2, r, act, layout, params)
+    for _ in range(2):
+        a, b = fwd(), bwd()
+        same(a, b)
+    # two calls at once on two streams, each with a workspace of its own
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    res = [(moe_experts_train(x, w13, w2, r, act, layout, params, stream=s),
+            moe_experts_backward(d, x, h, w13, w2, r, act, layout, params, stream=s))
+           for s in streams]
+    torch.cuda.synchronize()
+    for a, b in res:
+        same(a, b)
+    # captured with given buffers; what the workspace held does not matter
+    ws = torch.empty(moe_experts_backward_workspace_bytes(n, k, hidden, inter, x.dtype),
+                     dtype=torch.uint8, device=DEV)
+    o2, h2 = torch.empty_like(out), torch.empty_like(h)
+    b2 = type(want)(*(torch.empty_like(t) for t in (want.d_x, want.d_w13, want.d_w2,
+                                                    want.d_topk_w)))
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        moe_experts_train(x, w13, w2, r, act, layout, params, out=o2, h=h2)
+        moe_experts_backward(d, x, h2, w13, w2, r, act, layout, params, d_x=b2.d_x,
+                             d_w13=b2.d_w13, d_w2=b2.d_w2, d_topk_w=b2.d_topk_w, workspace=ws)
+    for fill in (0, 255, 17):
+        ws.fill_(fill)
+        for t in (o2, h2, b2.d_x, b2.d_w13, b2.d_w2, b2.d_topk_w):
+            t.fill_(float("nan"))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        same((o2, h2), b2)
+
+
+def test_forward_is_that_of_moe_experts():
+    for case in (SMALL, (300, 264, 136, 3, 2, "f32", "f32", "silu", "packed", {}, None)):
+        act, layout, params = case[7:10]
+        r, idx, row, (x, d, w13, w2) = _layer_on_gpu(case)
+        want = moe_experts(x, w13, w2, r, act, layout, params)
+        out, _ = moe_experts_train(x, w13, w2, r, act, layout, params)
+        # the same roundings (activation rows, expert rows, output) of sums in another
+        # order: a half step of each may fall the other way
+        scale = float(want.abs().max())
+        assert float((out.float() - want.float()).abs().max()) <= \
+            (1e-5 if case[5] == "f32" else 4 * 2.0 ** -8) * scale
+
+
+def test_refusals():
+    r, idx, row, (x, d, w13, w2) = _layer_on_gpu(SMALL)
+    act, layout, params = SMALL[7:10]
+    out, h = moe_experts_train(x, w13, w2, r, act, layout, params)
+    ok = (d, x, h, w13, w2, r, act, layout, params)
+
+    def swapped(i, v):
+        return ok[:i] + (v,) + ok[i + 1:]
+    for bad in (swapped(0, d[:-1]), swapped(0, d.float()), swapped(1, x.cpu()),
+                swapped(2, h[:, :-8]), swapped(2, h.t().contiguous().t()),
+                swapped(3, w13[:, :-8].contiguous()), swapped(4, w2[:-1].contiguous()),
+                swapped(6, "gelu"), swapped(7, "columns"), swapped(8, {"gamma": 1.0})):
+        with pytest.raises((ValueError, TypeError)):
+            moe_experts_backward(*bad)
+    other = moe_route(routing_logits(34, 6, "f32").to(DEV), 3)
+    with pytest.raises(ValueError):
+        moe_experts_backward(*swapped(5, other))
+    with pytest.raises(ValueError):
+        moe_experts_train(x, w13, w2, r, act, layout, params, h=h[:-1])
+    with pytest.raises(Exception):
+        moe_experts_backward(*ok, workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
