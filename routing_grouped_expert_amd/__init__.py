@@ -1182,6 +1182,7 @@ def moe_experts_backward(d_out: torch.Tensor, x: torch.Tensor, h: torch.Tensor,
 # ------------------------------------------------- AdamW over many tensors
 
 _F8 = torch.float8_e4m3fn
+_SIZE = {torch.float32: 4, torch.bfloat16: 2}
 _ADAMW_BLOCK = 256  # elements that share a scale in 8-bit moments
 
 
@@ -1253,6 +1254,19 @@ def moe_grad_norm(grads, *, out: Optional[torch.Tensor] = None,
     return _grad_norm(grads, out, workspace, stream).run()
 
 
+def _adamw_wrong(i, p, g, m, v, moment, dev):
+    """Says what is wrong with tensor i of a step."""
+    _dt(p), _dt(g)
+    if g.shape != p.shape:
+        raise ValueError(f"grads[{i}] must have the shape of params[{i}]")
+    for name, t, dtype in (("params", p, p.dtype), ("grads", g, g.dtype), ("m", m, moment),
+                           ("v", v, moment)):
+        if dev < 0 or t.get_device() != dev:
+            raise ValueError(f"{name}[{i}] must be on the GPU of the parameters")
+        _is(t, p.shape, dtype, dev, f"{name}[{i}]")
+    raise AssertionError("unreachable")
+
+
 def _adamw(params, grads, state, lr, step, betas, eps, weight_decay, grad_norm, max_norm, seed,
            stream) -> _Call:
     params, grads = list(params), list(grads)
@@ -1265,41 +1279,47 @@ def _adamw(params, grads, state, lr, step, betas, eps, weight_decay, grad_norm, 
         lists["m_scale"], lists["v_scale"] = state.m_scale, state.v_scale
     if state.master is not None:
         lists["master"] = state.master
+    moment = _F8 if bits == 8 else torch.float32
     for name, ts in lists.items():
         if len(ts) != count:
             raise ValueError(f"{len(ts)} {name} for {count} parameters")
-    dev, ts = _grad_tensors(grads)
-    moment = _F8 if bits == 8 else torch.float32
-    spans = []
-    for i, (t, p, g) in enumerate(zip(ts, params, grads)):
-        n, shape = p.numel(), p.shape
-        if g.shape != shape:
-            raise ValueError(f"grads[{i}] must have the shape of params[{i}]")
-        _is(p, shape, p.dtype, dev, f"params[{i}]")
-        t.p, t.p_dtype = p.data_ptr(), _dt(p)
-        m, v = state.m[i], state.v[i]
-        _is(m, shape, moment, dev, f"m[{i}]")
-        _is(v, shape, moment, dev, f"v[{i}]")
-        t.m, t.v = m.data_ptr(), v.data_ptr()
-        mine = [p, m, v]
+    if not count:
+        raise ValueError("no parameters")
+    dev = params[0].get_device()
+    words, spans, wide = [], [], 1 if bits == 8 else 4
+    for i, (p, g, m, v) in enumerate(zip(params, grads, state.m, state.v)):
+        shape, n, pd, gd = p.shape, p.numel(), p.dtype, g.dtype
+        if not (g.shape == m.shape == v.shape == shape and m.dtype is v.dtype is moment and
+                dev == p.get_device() == g.get_device() == m.get_device() == v.get_device() and
+                dev >= 0 and p.is_contiguous() and g.is_contiguous() and m.is_contiguous() and
+                v.is_contiguous() and pd in _DT and gd in _DT):
+            _adamw_wrong(i, p, g, m, v, moment, dev)
+        at = (p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr())
+        ms = vs = w = None
+        if n:
+            spans += ((at[0], n * _SIZE[pd]), (at[1], n * _SIZE[gd]), (at[2], n * wide),
+                      (at[3], n * wide))
         if bits == 8:
             ms, vs = state.m_scale[i], state.v_scale[i]
             blocks = (-(-n // _ADAMW_BLOCK),)
             _is(ms, blocks, torch.float32, dev, f"m_scale[{i}]")
             _is(vs, blocks, torch.float32, dev, f"v_scale[{i}]")
-            t.m_scale, t.v_scale = ms.data_ptr(), vs.data_ptr()
-            mine += [ms, vs]
+            ms, vs = ms.data_ptr(), vs.data_ptr()
+            if n:
+                spans += ((ms, 4 * blocks[0]), (vs, 4 * blocks[0]))
         if state.master is not None and state.master[i] is not None:
-            w = state.master[i]
-            _is(w, shape, torch.float32, dev, f"master[{i}]")
-            t.master = w.data_ptr()
-            mine.append(w)
-        if n:
-            spans += [(x.data_ptr(), x.data_ptr() + _nbytes(x)) for x in mine]
-            spans.append((g.data_ptr(), g.data_ptr() + _nbytes(g)))
+            _is(state.master[i], shape, torch.float32, dev, f"master[{i}]")
+            w = state.master[i].data_ptr()
+            if n:
+                spans.append((w, 4 * n))
+        words += (*at, ms or 0, vs or 0, w or 0, n, _DT[pd] | _DT[gd] << 32)
     spans.sort()
-    if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
-        raise ValueError("parameters, gradients and state must not overlap")
+    end = 0
+    for begin, size in spans:
+        if begin < end:
+            raise ValueError("parameters, gradients and state must not overlap")
+        end = begin + size
+    ts = ctypes.cast((ctypes.c_int64 * len(words))(*words), ctypes.POINTER(N.MoeAdamwTensor))
     if (grad_norm is None) != (max_norm is None):
         raise ValueError("grad_norm and max_norm go together")
     if grad_norm is not None:
