@@ -22,7 +22,9 @@
  * moe_block_norm_backward) and moe_block_forward (the block from its residual
  * stream).  Around expert products that run elsewhere: moe_dispatch and
  * moe_combine_weighted with moe_combine_weighted_backward, and
- * moe_route_backward.  With 4-bit expert weights: moe_quantize_int4,
+ * moe_route_backward.  Training the experts: moe_experts_train and
+ * moe_experts_backward, and the optimizer's step over all tensors, moe_adamw with
+ * moe_grad_norm.  With 4-bit expert weights: moe_quantize_int4,
  * moe_dequantize_int4, moe_experts_int4 and moe_forward_int4.
  *
  * Sources of the operations (the pages are cited by title and section):
@@ -54,7 +56,8 @@
  *  - Arguments are checked before anything is enqueued; on error a negative
  *    moe_status_t is returned and nothing is written.  A launch failure returns
  *    MOE_ERR_HIP.  Asynchronous device faults surface at the caller's next sync.
- *  - n_tokens == 0 is valid: MOE_OK, nothing enqueued.
+ *  - n_tokens == 0 is valid: MOE_OK, nothing enqueued (gradients that sum over tokens
+ *    are written as zeros).
  *  - Limits: 1 <= n_experts <= 256, 1 <= topk <= min(n_experts, 16),
  *    n_tokens * topk < 2^31, hidden and inter positive multiples of 8.
  *    moe_experts* and moe_forward also need each of these below 2^31 bytes:

@@ -25,9 +25,19 @@ outputs over the group's shares gives the layer output:
     out = moe_experts_ep(x, w13, w2, routing, act="silu")
     out, routing = moe_forward_ep(x, logits, w13, w2, topk, lo, act="silu")
 
-Expert products that run elsewhere (a training step) take their rows from
-``moe_dispatch`` and give them back to ``moe_combine_weighted``; the gradients
-are calls of their own (this package registers nothing with autograd):
+A training step of the experts keeps the w13 products, takes the gradients of rows,
+weights and routing weights from them, and steps all tensors at once (the gradients
+are calls of their own; this package registers nothing with autograd):
+
+    out, h = moe_experts_train(x, w13, w2, routing, act="silu")
+    g = moe_experts_backward(d_out, x, h, w13, w2, routing, act="silu")
+    d_logits = moe_route_backward(g.d_topk_w, routing)
+    state = moe_adamw_state(params, bits=8)              # once
+    moe_adamw(params, grads, state, lr=1e-4, step=t, grad_norm=moe_grad_norm(grads),
+              max_norm=1.0, seed=t)
+
+Expert products that run elsewhere (experts with adapters) take their rows from
+``moe_dispatch`` and give them back to ``moe_combine_weighted``:
 
     x_sorted = moe_dispatch(x, routing)                  # rows by expert
     out = moe_combine_weighted(y_sorted, routing)        # topk_w applied

@@ -151,10 +151,10 @@ def test_forward_and_gradient(case):
     u = torch.finfo(DT[dtype]).eps / 2
     xn, dn, w13n, w2n, w = _np(x), _np(d), _np(w13), _np(w2), _np(r.topk_w)
     want, terms = np.zeros((n * k, len(w13n[0]))), np.zeros((n * k, len(w13n[0])))
-    for t in range(n):
-        for j in range(k):
-            want[row[t, j]] = w13n[idx[t, j]] @ xn[t]
-            terms[row[t, j]] = np.abs(w13n[idx[t, j]]) @ np.abs(xn[t])
+    for i in range(e):
+        tok, slot = np.nonzero(idx == i)
+        want[row[tok, slot]] = xn[tok] @ w13n[i].T
+        terms[row[tok, slot]] = np.abs(xn[tok]) @ np.abs(w13n[i]).T
     within(h, want, (2 * (hidden + 1) * U32 + u) * terms, "h")
     ref = oracle.moe_ffn(x, idx, w, w13, w2, act, layout, params)
     scale = np.abs(ref).max()
