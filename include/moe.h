@@ -354,7 +354,7 @@ typedef struct {
   int64_t step;         /* t, 1 for the first step; below 2^31                     */
   const int32_t *step_on_device;  /* t in device memory, read when the step runs (a
                            captured graph can count it up), or NULL: step is taken */
-  const float *grad_norm;  /* norm over all gradients in device memory, or NULL; if it
+  const double *grad_norm; /* norm over all gradients in device memory, or NULL; if it
                            is not finite the step changes nothing                  */
   double max_norm;      /* > 0, with grad_norm                                     */
   int32_t state_bits;   /* 8 or 32                                                 */
@@ -364,12 +364,12 @@ typedef struct {
 moe_status_t moe_adamw(const moe_adamw_tensor_t *tensors, int32_t n_tensors,
                        const moe_adamw_t *args, void *stream);
 
-/* moe_grad_norm: out [1] fp32, the square root of the sum of the squares of all grad
- *   (of `tensors` only grad, n and grad_dtype are read), added up in a fixed order in
- *   fp32 inside pieces of 32768 and in 64 bits over them; 0 for none.  workspace: at
- *   least moe_grad_norm_workspace_bytes(...). */
+/* moe_grad_norm: out [1] fp64, the square root of the sum of the squares of all grad
+ *   (of `tensors` only grad, n and grad_dtype are read; squares in fp32, added up in
+ *   64 bits in a fixed order); 0 for none.  workspace: at least
+ *   moe_grad_norm_workspace_bytes(...). */
 size_t moe_grad_norm_workspace_bytes(const moe_adamw_tensor_t *tensors, int32_t n_tensors);
-moe_status_t moe_grad_norm(const moe_adamw_tensor_t *tensors, int32_t n_tensors, float *out,
+moe_status_t moe_grad_norm(const moe_adamw_tensor_t *tensors, int32_t n_tensors, double *out,
                            void *workspace, size_t ws_bytes, void *stream);
 
 /* ---- Norms around a block ------------------------------------------------------

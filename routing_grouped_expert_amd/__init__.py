@@ -1243,7 +1243,7 @@ def _grad_tensors(grads):
 def _grad_norm(grads, out, workspace, stream) -> _Call:
     grads = list(grads)
     dev, ts = _grad_tensors(grads)
-    out = _output(out, grads[0], (1,), torch.float32, stream, "out")
+    out = _output(out, grads[0], (1,), torch.float64, stream, "out")
     need = N.load().moe_grad_norm_workspace_bytes(ts, len(ts))
     if need == 0:
         raise MoeError(N.MOE_ERR_SHAPE, "moe_grad_norm")
@@ -1260,7 +1260,7 @@ def prepare_grad_norm(grads, *, out: Optional[torch.Tensor] = None,
 def moe_grad_norm(grads, *, out: Optional[torch.Tensor] = None,
                   workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Square root of the sum of the squares of all elements of ``grads`` (fp32 or
-    bf16): an fp32 tensor ``[1]``, for the clipping of moe_adamw."""
+    bf16): a float64 tensor ``[1]``, for the clipping of moe_adamw."""
     return _grad_norm(grads, out, workspace, stream).run()
 
 
@@ -1333,7 +1333,7 @@ def _adamw(params, grads, state, lr, step, betas, eps, weight_decay, grad_norm, 
     if (grad_norm is None) != (max_norm is None):
         raise ValueError("grad_norm and max_norm go together")
     if grad_norm is not None:
-        _is(grad_norm, (1,), torch.float32, dev, "grad_norm")
+        _is(grad_norm, (1,), torch.float64, dev, "grad_norm")
     on_device = isinstance(step, torch.Tensor)
     if on_device:
         _is(step, (1,), torch.int32, dev, "step")
@@ -1360,7 +1360,7 @@ def moe_adamw(params, grads, state: AdamWState, *, lr: float, step, betas: tuple
     """One AdamW step over all ``params`` (fp32 or bf16) in place, from ``grads`` of
     their shapes (fp32 or bf16).  ``step``: 1 for the first one, or an int32 tensor
     ``[1]`` on the GPU that is read when the step runs.  ``grad_norm`` (from
-    moe_grad_norm) with ``max_norm`` clips, and a norm that is not finite skips the
+    moe_grad_norm, float64) with ``max_norm`` clips, and a norm that is not finite skips the
     step.  ``seed``: 8-bit moments, and bf16 parameters without a master, are rounded
     stochastically (see moe.h)."""
     _adamw(params, grads, state, lr, step, betas, eps, weight_decay, grad_norm, max_norm, seed,

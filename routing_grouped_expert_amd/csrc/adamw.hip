@@ -50,8 +50,8 @@ struct Hyper {
   float lr, beta1, beta2, one_beta1, one_beta2, eps, keep;  // keep = 1 - lr * decay
   float c1, c2, log_beta1, log_beta2;  // c1, c2 of the host's step; logs for the device's
   const int32_t *step_dev;
-  const float *norm;
-  float max_norm;
+  const double *norm;
+  double max_norm;
   uint32_t seed, step;
   int stochastic;
 };
@@ -146,7 +146,7 @@ __device__ __forceinline__ void store_e4m3(uint8_t *p, float *scales, int64_t i,
   top_bits = half_wave_max(top_bits);
   const float top = __uint_as_float(top_bits);
   const bool live = top >= 0x1p-100f;  // (below it 448 / top overflows: held as zeros)
-  const float inverse = live ? kTop / top : 0.f;
+  const float inverse = live ? kTop * (1.f / top) : 0.f;
   u32x2_t w;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -260,9 +260,9 @@ template <bool E8> __global__ __launch_bounds__(kThreads) void adamw_kernel(Batc
   float coef = 1.f, c1 = h.c1, c2 = h.c2;
   uint32_t step = h.step;
   if (h.norm) {
-    const float norm = *h.norm;
-    if (!(norm < __builtin_inff())) return;  // not finite: the step changes nothing
-    coef = (float)fmin(1.0, (double)h.max_norm / ((double)norm + 1e-6));
+    const double norm = *h.norm;
+    if (!(norm < __builtin_inf())) return;  // not finite: the step changes nothing
+    coef = (float)fmin(1.0, h.max_norm / (norm + 1e-6));
   }
   if (h.step_dev) {
     const int32_t s = *h.step_dev;
@@ -281,57 +281,56 @@ template <bool E8> __global__ __launch_bounds__(kThreads) void adamw_kernel(Batc
   }
 }
 
-__device__ __forceinline__ float workgroup_sum(float v, float *s) {
-  v = wave_sum_f32(v);
-  if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
-  __syncthreads();
-  float sum = 0.f;
-  for (int w = 0; w < (int)blockDim.x / 64; ++w) sum += s[w];
-  return sum;
+// The sum of v over the workgroup's N threads, in a fixed order, for thread 0.
+template <int N> __device__ __forceinline__ double workgroup_sum(double v, double *s) {
+  s[threadIdx.x] = v;
+  for (int d = N / 2; d > 0; d >>= 1) {
+    __syncthreads();
+    if ((int)threadIdx.x < d) s[threadIdx.x] += s[threadIdx.x + d];
+  }
+  return s[0];
 }
 
-// Squares of a chunk, added up in fp32 (128 a lane, in eight sums).
+// Squares of a chunk, each rounded to fp32 and added up in 64 bits: what is left of
+// their roundings in the sum of many is far below an fp32 step, so the coefficient is
+// the formula's to its last bit (a coefficient one step off turns a random rounding of
+// an 8-bit moment over now and then, a whole e4m3 step).  The loads still set the time.
 template <typename G>
-__device__ __forceinline__ float squares(const G *g, int64_t begin, int64_t n) {
-  float acc[8] = {};
+__device__ __forceinline__ double squares(const G *g, int64_t begin, int64_t n) {
+  double acc[8] = {};
   const int64_t end = begin + kNormChunk < n ? begin + kNormChunk : n;
 #pragma unroll 4
   for (int64_t i = begin + threadIdx.x * kPer; i < end; i += kStep) {
     float f[8];
     load8(g, i, n, f);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) acc[q] += f[q] * f[q];
+    for (int q = 0; q < 8; ++q) acc[q] += (double)(f[q] * f[q]);
   }
-  float s = 0.f;
+  double s = 0.0;
 #pragma unroll
   for (int q = 0; q < 8; ++q) s += acc[q];
   return s;
 }
 
-__global__ __launch_bounds__(kThreads) void norm_parts(Batch b, float *__restrict__ parts) {
-  __shared__ float s[kThreads / 64];
+__global__ __launch_bounds__(kThreads) void norm_parts(Batch b, double *__restrict__ parts) {
+  __shared__ double s[kThreads];
   const int at = tensor_of(b);
   const int64_t begin = (int64_t)(blockIdx.x - b.first[at]) * kNormChunk;
   const moe_adamw_tensor_t &t = b.t[at];
-  const float v = t.grad_dtype == MOE_BF16
-                      ? squares(reinterpret_cast<const bf16_t *>(t.grad), begin, t.n)
-                      : squares(reinterpret_cast<const float *>(t.grad), begin, t.n);
-  const float sum = workgroup_sum(v, s);
+  const double v = t.grad_dtype == MOE_BF16
+                       ? squares(reinterpret_cast<const bf16_t *>(t.grad), begin, t.n)
+                       : squares(reinterpret_cast<const float *>(t.grad), begin, t.n);
+  const double sum = workgroup_sum<kThreads>(v, s);
   if (threadIdx.x == 0) parts[blockIdx.x] = sum;
 }
 
-// The parts added up in 64 bits, in a fixed order.
-__global__ __launch_bounds__(1024) void norm_join(const float *__restrict__ parts, int64_t n,
-                                                  float *__restrict__ out) {
+__global__ __launch_bounds__(1024) void norm_join(const double *__restrict__ parts, int64_t n,
+                                                  double *__restrict__ out) {
   __shared__ double s[1024];
   double v = 0.0;
-  for (int64_t i = threadIdx.x; i < n; i += 1024) v += (double)parts[i];
-  s[threadIdx.x] = v;
-  for (int d = 512; d > 0; d >>= 1) {
-    __syncthreads();
-    if ((int)threadIdx.x < d) s[threadIdx.x] += s[threadIdx.x + d];
-  }
-  if (threadIdx.x == 0) *out = (float)sqrt(s[0]);
+  for (int64_t i = threadIdx.x; i < n; i += 1024) v += parts[i];
+  v = workgroup_sum<1024>(v, s);
+  if (threadIdx.x == 0) *out = sqrt(v);
 }
 
 // Launches `go(batch, chunks)` over the tensors that hold elements, up to kBatch (and
@@ -368,7 +367,7 @@ int64_t grad_norm_parts(const moe_adamw_tensor_t *t, int n) {
   return parts;
 }
 
-hipError_t launch_grad_norm(const moe_adamw_tensor_t *t, int n, float *parts, float *out,
+hipError_t launch_grad_norm(const moe_adamw_tensor_t *t, int n, double *parts, double *out,
                             hipStream_t s) {
   int64_t done = 0;
   const hipError_t err = batches(t, n, kNormChunk, [&](const Batch &b, uint32_t chunks) {
@@ -396,7 +395,7 @@ hipError_t launch_adamw(const moe_adamw_tensor_t *t, int n, const moe_adamw_t &a
   }
   h.step_dev = a.step_on_device;
   h.step = (uint32_t)a.step;
-  h.norm = a.grad_norm, h.max_norm = (float)a.max_norm;
+  h.norm = a.grad_norm, h.max_norm = a.max_norm;
   h.seed = a.seed, h.stochastic = a.stochastic;
   return batches(t, n, kChunk, [&](const Batch &b, uint32_t chunks) {
     if (a.state_bits == 8)

@@ -488,8 +488,8 @@ moe_status_t moe_adamw(const moe_adamw_tensor_t *tensors, int32_t n_tensors,
       !beta(a.beta1) || !beta(a.beta2))
     return MOE_ERR_SHAPE;
   if (!a.step_on_device && (a.step < 1 || a.step > 0x7fffffff)) return MOE_ERR_SHAPE;
-  if (a.grad_norm && !(a.max_norm > 0.0 && isfinite((float)a.max_norm))) return MOE_ERR_SHAPE;
-  if (((uintptr_t)a.step_on_device | (uintptr_t)a.grad_norm) & 3u) return MOE_ERR_ALIGN;
+  if (a.grad_norm && !(a.max_norm > 0.0 && isfinite(a.max_norm))) return MOE_ERR_SHAPE;
+  if (((uintptr_t)a.step_on_device & 3u) || ((uintptr_t)a.grad_norm & 7u)) return MOE_ERR_ALIGN;
   const moe_status_t st = check_tensors(tensors, n_tensors, true, a.state_bits);
   if (st != MOE_OK) return st;
   return moe::launch_adamw(tensors, n_tensors, a, (hipStream_t)stream) == hipSuccess ? MOE_OK
@@ -498,17 +498,17 @@ moe_status_t moe_adamw(const moe_adamw_tensor_t *tensors, int32_t n_tensors,
 
 size_t moe_grad_norm_workspace_bytes(const moe_adamw_tensor_t *tensors, int32_t n_tensors) {
   if (check_tensors(tensors, n_tensors, false, 0) != MOE_OK) return 0;
-  return align256((size_t)moe::grad_norm_parts(tensors, n_tensors) * sizeof(float)) + 256;
+  return align256((size_t)moe::grad_norm_parts(tensors, n_tensors) * sizeof(double)) + 256;
 }
 
-moe_status_t moe_grad_norm(const moe_adamw_tensor_t *tensors, int32_t n_tensors, float *out,
+moe_status_t moe_grad_norm(const moe_adamw_tensor_t *tensors, int32_t n_tensors, double *out,
                            void *workspace, size_t ws_bytes, void *stream) {
   moe_status_t st = check_tensors(tensors, n_tensors, false, 0);
   if (st != MOE_OK) return st;
   if ((st = check_ptrs({out})) != MOE_OK) return st;
   st = check_ws(workspace, ws_bytes, moe_grad_norm_workspace_bytes(tensors, n_tensors));
   if (st != MOE_OK) return st;
-  return moe::launch_grad_norm(tensors, n_tensors, reinterpret_cast<float *>(workspace), out,
+  return moe::launch_grad_norm(tensors, n_tensors, reinterpret_cast<double *>(workspace), out,
                                (hipStream_t)stream) == hipSuccess
              ? MOE_OK
              : MOE_ERR_HIP;

@@ -182,7 +182,7 @@ hipError_t launch_zero(void *p, size_t bytes, hipStream_t s);
 // workgroups of 256 (a grid's threads are counted in 32 bits) of 8192 elements each.
 constexpr int64_t kMostChunks = (1 << 24) - 1, kMostElements = (int64_t(1) << 36) - 1;
 int64_t grad_norm_parts(const moe_adamw_tensor_t *t, int n);
-hipError_t launch_grad_norm(const moe_adamw_tensor_t *t, int n, float *parts, float *out,
+hipError_t launch_grad_norm(const moe_adamw_tensor_t *t, int n, double *parts, double *out,
                             hipStream_t s);
 hipError_t launch_adamw(const moe_adamw_tensor_t *t, int n, const moe_adamw_t &a, hipStream_t s);
 

@@ -140,8 +140,8 @@ def test_steps(bits, p, g, master, seed):
         grads = [t.to(DEV) for t in grads]
         norm = moe_grad_norm(grads)
         exact = np.sqrt(sum(float((_np(t) ** 2).sum()) for t in grads))
-        # 128 squares a lane in eight sums, then 6 + 4 + 2 pairwise levels
-        assert abs(float(norm) - exact) <= (17 + 8 + 12) * U * exact
+        # each square is rounded to fp32 once, the sum and the root are in 64 bits
+        assert norm.dtype == torch.float64 and abs(float(norm) - exact) <= U * exact
         clip = 0.5 * exact if step == 2 else None
         coef = 1.0 if clip is None else oracle.clip_coefficient(float(norm), clip)
         _check_step(params, grads, state, step, coef, seed, lambda: moe_adamw(
@@ -155,7 +155,7 @@ def test_more_tensors_than_a_launch_takes():
     params, grads = [t.to(DEV) for t in params], [t.to(DEV) for t in grads]
     state = moe_adamw_state(params, 8)
     exact = np.sqrt(sum(float((_np(t) ** 2).sum()) for t in grads))
-    assert abs(float(moe_grad_norm(grads)) - exact) <= 37 * U * exact
+    assert abs(float(moe_grad_norm(grads)) - exact) <= U * exact
     _check_step(params, grads, state, 1, 1.0, 5, lambda: moe_adamw(
         params, grads, state, step=1, seed=5, **HYPER))
     # the same bits every time, and others with another seed, step or place
@@ -234,7 +234,7 @@ def test_capture_counts_the_step_on_the_device():
     graphed = [t.clone() for t in eager]
     se, sg = moe_adamw_state(eager, 8), moe_adamw_state(graphed, 8)
     step = torch.zeros(1, dtype=torch.int32, device=DEV)
-    norm = torch.empty(1, device=DEV)
+    norm = torch.empty(1, dtype=torch.float64, device=DEV)
     call_norm = prepare_grad_norm(grads, out=norm)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
@@ -293,7 +293,9 @@ def test_refusals():
     with pytest.raises(ValueError):
         moe_adamw([p], [g], AdamWState(s.m, [t.half() for t in s.v]), **ok)
     with pytest.raises(ValueError):
-        moe_adamw([p], [g], s, grad_norm=torch.ones(1, device=DEV), **ok)
+        moe_adamw([p], [g], s, grad_norm=torch.ones(1, device=DEV, dtype=torch.float64), **ok)
+    with pytest.raises((ValueError, TypeError)):  # not in 64 bits
+        moe_adamw([p], [g], s, grad_norm=torch.ones(1, device=DEV), max_norm=1.0, **ok)
     for bad in ({"step": 0}, {"step": 1 << 31}, {"lr": -1.0}, {"lr": float("nan")},
                 {"betas": (1.0, 0.9)}, {"betas": (0.9, -0.1)}, {"eps": float("inf")},
                 {"weight_decay": -0.1}):

@@ -108,7 +108,8 @@ def test_adamw(lib):
                 {"grad_norm": FAKE}, {"grad_norm": FAKE, "max_norm": -1.0},
                 {"grad_norm": FAKE, "max_norm": nan}):
         assert call(**bad) == N.MOE_ERR_SHAPE, bad
-    assert call(grad_norm=FAKE + 2, max_norm=1.0) == N.MOE_ERR_ALIGN
+    for off in (2, 4):
+        assert call(grad_norm=FAKE + off, max_norm=1.0) == N.MOE_ERR_ALIGN
     assert call(step_on_device=FAKE + 1) == N.MOE_ERR_ALIGN
     for bad in ({"state_bits": 16}, {"stochastic": 2}):
         assert call(**bad) == N.MOE_ERR_UNSUPPORTED, bad
@@ -136,7 +137,7 @@ def test_grad_norm(lib):
     assert call(ws=None) == N.MOE_ERR_WORKSPACE and call(size=0) == N.MOE_ERR_WORKSPACE
     assert lib.moe_grad_norm_workspace_bytes(_tensor(n=-1), 1) == 0
     many = lib.moe_grad_norm_workspace_bytes(_tensor(n=1 << 30), 1)
-    assert many >= (1 << 30) // 32768 * 4
+    assert many >= (1 << 30) // 32768 * 8
 
 
 def test_python_side_refuses_tensors_off_the_gpu():
