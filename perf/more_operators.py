@@ -363,7 +363,8 @@ def _own_run(s):
                "v_scale": s["v_scale"], "master": s["master"]}
         norm = None
         if c["clip"]:
-            out["norm"] = norm = moe.moe_grad_norm(s["g"])
+            norm = moe.moe_grad_norm(s["g"])
+            out["norm"] = norm.float()
         moe.moe_adamw(s["p"], s["g"], state, lr=LR, step=STEP, betas=(BETA1, BETA2), eps=EPS,
                       weight_decay=DECAY, grad_norm=norm, max_norm=1.0 if c["clip"] else None,
                       seed=SEED if c["stochastic"] else None)
