@@ -133,12 +133,15 @@ __device__ __forceinline__ uint32_t half_wave_max(uint32_t v) {
   return max(s[0], s[1]);
 }
 
-// Eight values as e4m3 and their block's scale.  `random`: ten bits of each element
-// from bit `shift`; nullptr: to nearest.  ROOT: values above zero stay above zero.
-// Values that are not finite make the scale NaN, and with it the whole block.
+// Eight values as e4m3 and their block's scale.  Stochastic: by the ten bits of each
+// element of `random` from bit `shift`; else to nearest (a flag and an array that is
+// always there: with a pointer that may be null the array went to scratch memory and
+// the kernel took twice as long).  ROOT: values above zero stay above zero.  Values that
+// are not finite make the scale NaN, and with it the whole block.
 template <bool ROOT>
 __device__ __forceinline__ void store_e4m3(uint8_t *p, float *scales, int64_t i, int64_t n,
-                                           const float (&f)[8], const uint32_t *random, int shift) {
+                                           const float (&f)[8], const uint32_t (&random)[8],
+                                           bool stochastic, int shift) {
   constexpr float kTop = 448.f;
   uint32_t top_bits = 0;
 #pragma unroll
@@ -155,7 +158,7 @@ __device__ __forceinline__ void store_e4m3(uint8_t *p, float *scales, int64_t i,
     for (int q = 0; q < 4; ++q) {
       const float x = f[4 * h + q];
       float y = ROOT ? fminf(x * inverse, kTop) : __builtin_amdgcn_fmed3f(x * inverse, -kTop, kTop);
-      if (random) {
+      if (stochastic) {
         const uint32_t r = ((random[4 * h + q] >> shift & 1023u) << 10) | 512u;
         y = __uint_as_float((__float_as_uint(y) + r) & 0xfff00000u);
       }
@@ -204,7 +207,7 @@ __device__ __forceinline__ void update(const moe_adamw_tensor_t &t, int64_t begi
       load8(reinterpret_cast<const float *>(t.m), i, t.n, m);
       load8(reinterpret_cast<const float *>(t.v), i, t.n, v);
     }
-    uint32_t random[8];
+    uint32_t random[8] = {};
     if (h.stochastic) {
       const uint32_t k = key ^ mix((uint32_t)(i >> 32));
 #pragma unroll
@@ -222,9 +225,9 @@ __device__ __forceinline__ void update(const moe_adamw_tensor_t &t, int64_t begi
     }
     if constexpr (E8) {
       store_e4m3<false>(reinterpret_cast<uint8_t *>(t.m), t.m_scale, i, t.n, m,
-                        h.stochastic ? random : nullptr, 0);
+                        random, h.stochastic, 0);
       store_e4m3<true>(reinterpret_cast<uint8_t *>(t.v), t.v_scale, i, t.n, v,
-                       h.stochastic ? random : nullptr, 10);
+                       random, h.stochastic, 10);
     } else {
       store8(reinterpret_cast<float *>(t.m), i, t.n, m);
       store8(reinterpret_cast<float *>(t.v), i, t.n, v);
