@@ -977,9 +977,12 @@ inline bool few_rows(const GradArgs &g) {
 
 // Rows of u and of d_x: tiles of 256 rows where they cover the compute units, of 128
 // rows below that, and of 32 rows where experts hold few.  fp32, which multiplies at a
-// sixteenth of the rate, takes 128 rows throughout, in rings of two slices so that two
+// sixteenth of the rate, takes at most 128 rows, in rings of two slices so that two
 // workgroups share a unit (1001 tokens x 6 of 40 experts, 712 x 1416: u 224 us with four
-// slices, 190 with two; d_x 413 us with 256 rows, 204 with 128).
+// slices, 190 with two; d_x 413 us with 256 rows, 204 with 128), and 64 rows where that
+// leaves out a quarter of the tiles' rows at even routing (the same, 150 rows an expert:
+// the whole gradient 691 -> 645 us; 64 rows of 16 experts, 1024 x 1024: 244 -> 189; where
+// less is left out it costs: 614 rows an expert 1996 -> 2083, 105 rows 466 -> 479).
 template <typename T, int KIND, int GATHER>
 hipError_t launch_rows(const GradArgs &g, hipStream_t s) {
   constexpr bool BF = std::is_same<T, bf16_t>::value;
@@ -988,6 +991,8 @@ hipError_t launch_rows(const GradArgs &g, hipStream_t s) {
   if constexpr (BF) {
     if (expected_tiles(g, 256, 256) >= device_cus())
       return launch<T, KIND, GATHER, 256, 256, 2, 2, 4, 64>(g, most_tiles(g, 256, 256), s);
+  } else if (const int64_t even = g.rows / g.E; 2 * cover(even, 64) <= 3 * cover(even, 128)) {
+    return launch<T, KIND, GATHER, 64, 128, 2, 2, 2, 128>(g, most_tiles(g, 64, 128), s);
   }
   return launch<T, KIND, GATHER, 128, 128, 2, 2, BF ? 4 : 2, 128>(g, most_tiles(g, 128, 128), s);
 }

@@ -49,6 +49,9 @@ CASES = [
     (4000, 2120, 2072, 3, 2, "bf16", "bf16", "swiglu_oai", "interleaved", OAI, 0.5),
     (8200, 1048, 4104, 1, 1, "bf16", "f32", "relu2", "packed", {}, None),
     (5000, 1160, 4104, 2, 1, "f32", "f32", "silu", "packed", {}, None),
+    # fp32 row tiles of 64 rows: 60 and 140 rows an expert
+    (320, 1160, 1096, 16, 3, "f32", "f32", "swiglu_oai", "interleaved", OAI, None),
+    (420, 1672, 1608, 6, 2, "f32", "bf16", "relu2", "packed", {}, 0.5),
 ]
 
 
